@@ -144,7 +144,7 @@ def _cache(case, pages, dev, gen):
         if case["cache"] != "e4m3":
             return torch.randn(shape, device=dev, generator=gen, dtype=TYPES[case["cache"]])
         # calibrated: the largest value met is a little below the format's largest
-        return (torch.randn(shape, device=dev, generator=gen, dtype=torch.bfloat16) * 80.0).to(torch.float8_e4m3fn)
+        return (torch.randn(shape, device=dev, generator=gen, dtype=torch.bfloat16) * 80.0).clamp_(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
 
     def scale():
         return 0.01 + 0.004 * torch.rand(heads, device=dev, generator=gen) if case["cache"] == "e4m3" else None
