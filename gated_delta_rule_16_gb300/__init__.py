@@ -1,4 +1,5 @@
-"""GB300-native chunkwise Gated Delta Network prefill core (dense and event-sparse).
+"""GB300-native chunkwise Gated Delta Network prefill core (dense and event-sparse), and the decode
+step of the softmax-attention layers beside it (paged cache, one-token attention, sampling).
 
 The compute path is libgdn.so (hand-written CUDA for sm_103a behind the C ABI
 in include/gdn.h); this package is its thin ctypes binding.
@@ -7,6 +8,7 @@ from ._binding import (  # noqa: F401
     EXPORTS,
     GdnError,
     GdnEvents,
+    GdnKvCache,
     GdnOptions,
     GdnShape,
     STAGES,
@@ -31,4 +33,11 @@ from ._binding import (  # noqa: F401
     gdn_workspace_status,
     load,
     shape_of,
+)
+from .paged import (  # noqa: F401
+    gdn_kv_append,
+    gdn_page_tables,
+    gdn_page_tables_status,
+    gdn_paged_decode,
+    gdn_sample,
 )

@@ -16,7 +16,7 @@ import torch
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libgdn.so")
 
-GDN_BF16, GDN_F32 = 0, 1
+GDN_BF16, GDN_F32, GDN_E4M3 = 0, 1, 2
 SOLVERS = {"exact": 0, "block_adj": 1}
 STATUS = {0: "GDN_OK", 1: "GDN_ERR_NULL", 2: "GDN_ERR_SHAPE", 3: "GDN_ERR_DTYPE", 4: "GDN_ERR_ALIGN",
           5: "GDN_ERR_WORKSPACE", 6: "GDN_ERR_UNSUPPORTED", 7: "GDN_ERR_CUDA", 8: "GDN_ERR_DEVICE",
@@ -27,7 +27,8 @@ EXPORTS = ("gdn_workspace_bytes", "gdn_select_events", "gdn_events_status", "gdn
            "gdn_prefill_sparse_online", "gdn_select_events_scored", "gdn_select_scored_workspace_bytes",
            "gdn_prefill_host", "gdn_prefill_host_workspace_bytes", "gdn_decode_step", "gdn_prefill_ex",
            "gdn_workspace_bytes_ex", "gdn_events_bytes", "gdn_events_carve", "gdn_noalloc_status",
-           "gdn_select_events_gamma")
+           "gdn_select_events_gamma", "gdn_page_tables", "gdn_page_tables_status", "gdn_kv_append",
+           "gdn_paged_decode", "gdn_paged_decode_workspace_bytes", "gdn_sample", "gdn_sample_workspace_bytes")
 STAGES = ("select", "prefix", "intra", "wbuild", "scan_runs", "scan_chain", "scan", "output", "selector")
 
 
@@ -55,6 +56,13 @@ class GdnEvents(ctypes.Structure):
     _fields_ = [("row_pair", ctypes.c_void_p), ("row_ptr", ctypes.c_void_p), ("ev_chunk", ctypes.c_void_p),
                 ("grp_pred", ctypes.c_void_p), ("snap_slot", ctypes.c_void_p), ("counts", ctypes.c_void_p),
                 ("capacity", ctypes.c_int32)]
+
+
+class GdnKvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("stride_page", ctypes.c_int64),
+                ("stride_token", ctypes.c_int64), ("stride_head", ctypes.c_int64), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -117,6 +125,22 @@ def load(path: str | None = None):
             lib.gdn_workspace_status.restype = i32
             lib.gdn_status_string.argtypes = [i32]
             lib.gdn_status_string.restype = ctypes.c_char_p
+            i64, kvp = ctypes.c_int64, ctypes.POINTER(GdnKvCache)
+            lib.gdn_page_tables.argtypes = [i32, i32, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp, i32, vp, vp]
+            lib.gdn_page_tables.restype = i32
+            lib.gdn_page_tables_status.argtypes = [vp, vp]
+            lib.gdn_page_tables_status.restype = i32
+            lib.gdn_kv_append.argtypes = [kvp, i32, i32, vp, i64, i64, vp, i64, i64, vp, vp]
+            lib.gdn_kv_append.restype = i32
+            lib.gdn_paged_decode_workspace_bytes.argtypes = [kvp, i32]
+            lib.gdn_paged_decode_workspace_bytes.restype = sz
+            lib.gdn_paged_decode.argtypes = [kvp, i32, i32, i32, vp, i64, i64, vp, i64, i32, vp, i32, ctypes.c_float,
+                                             vp, vp, vp, sz, vp]
+            lib.gdn_paged_decode.restype = i32
+            lib.gdn_sample_workspace_bytes.argtypes = [i32, i32]
+            lib.gdn_sample_workspace_bytes.restype = sz
+            lib.gdn_sample.argtypes = [i32, i32, i32, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+            lib.gdn_sample.restype = i32
             lib.gdn_version.argtypes = []
             lib.gdn_version.restype = ctypes.c_int32
             lib.gdn_profile_enable.argtypes = [i32]

@@ -8,6 +8,22 @@
 #include "gdn_internal.cuh"
 
 namespace gdn {
+
+int device_ok() {
+    // cache per device: 0 unknown, 1 ok, 2 not a compute-capability 10.3 part
+    static int state[64] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (state[dev] == 0) {
+        int major = 0, minor = 0;
+        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+            return 0;
+        state[dev] = (major == 10 && minor == 3) ? 1 : 2;
+    }
+    return state[dev] == 1;
+}
+
 namespace {
 
 constexpr size_t kAlign = 256;
@@ -35,21 +51,6 @@ Profiler g_prof;
 cudaEvent_t *prof_slot() {
     if (g_prof.mode != 1 || g_prof.used >= kProfSlots) return nullptr;
     return g_prof.ev[g_prof.used++];
-}
-
-int device_ok() {
-    // cache per device: 0 unknown, 1 ok, 2 not a compute-capability 10.3 part
-    static int state[64] = {0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if (state[dev] == 0) {
-        int major = 0, minor = 0;
-        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-            return 0;
-        state[dev] = (major == 10 && minor == 3) ? 1 : 2;
-    }
-    return state[dev] == 1;
 }
 
 gdn_status check_shape(const gdn_shape *s) {
@@ -687,11 +688,12 @@ const char *gdn_status_string(gdn_status status) {
         case GDN_ERR_SHAPE: return "unsupported or inconsistent sizes";
         case GDN_ERR_DTYPE: return "unknown dtype or solver";
         case GDN_ERR_ALIGN: return "pointer not 16-byte aligned (workspace: 256-byte)";
-        case GDN_ERR_WORKSPACE: return "workspace smaller than gdn_workspace_bytes()";
-        case GDN_ERR_UNSUPPORTED: return "request not implemented by this library (needs d == dv == 128, ceil(T/64) <= 16384)";
+        case GDN_ERR_WORKSPACE: return "workspace smaller than the call's workspace query reports";
+        case GDN_ERR_UNSUPPORTED: return "request not implemented by this library (prefill: d == dv == 128, ceil(T/64) <= 16384; "
+                                          "paged cache: d 64, 128 or 256)";
         case GDN_ERR_CUDA: return "CUDA runtime call or kernel launch failed";
         case GDN_ERR_DEVICE: return "current device is not a compute-capability 10.3 (GB300) GPU";
-        case GDN_ERR_CAPACITY: return "device-side event or snapshot capacity exceeded";
+        case GDN_ERR_CAPACITY: return "device-side event, snapshot, page or slot capacity exceeded";
         case GDN_ERR_TIMEOUT: return "a kernel gave up waiting after its time limit (device-latched)";
     }
     return "unknown status";

@@ -121,6 +121,9 @@ struct Workspace {
     int64_t ev_cap, snap_cap;
 };
 
+// 1 if the current device is a compute-capability 10.3 GPU (cached per device).
+int device_ok();
+
 size_t workspace_layout(const Problem &pb, void *base, Workspace *ws);
 
 // gdn_prefill_sparse with every kernel on the caller's stream (no library-owned streams).

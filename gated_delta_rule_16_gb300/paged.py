@@ -1,0 +1,244 @@
+"""Decode step over a paged key-value cache: ctypes binding of the entry points of the same names.
+
+A cache is a pair of tensors indexed [page, cell, kv_head, dim] whose last
+dimension is contiguous; head-major storage [pages, kv_heads, page, dim] is
+passed as its ``transpose(1, 2)`` view.  An 8-bit cache is a pair of
+``torch.float8_e4m3fn`` tensors with one fp32 scale per KV head.
+
+These calls run once per layer and token, so the marshalling is kept short:
+each check reads a tensor's attributes once, and the default workspace belongs
+to one device and stream.  Every call is enqueued on `stream` (default: the
+current stream of the tensors' device) and returns without waiting.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from ._binding import GDN_BF16, GDN_E4M3, GDN_F32, GdnKvCache, Workspace, _check, load
+
+_CODES = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
+_CACHE_CODES = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32, torch.float8_e4m3fn: GDN_E4M3}
+_ws = {}
+
+
+def _want(t, name, dtype, shape, device):
+    """A contiguous tensor of this type, shape and device; returns its address."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, is on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _cuda(t, name):
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+class _On:
+    """The call's device and stream.  Memory that torch hands out for another stream than the
+    current one is recorded on it, so that it is not reused while the call still runs."""
+
+    def __init__(self, dev, stream):
+        self.dev = dev
+        self.other = False
+        if stream is None:
+            self.stream = None
+            self.handle = torch._C._cuda_getCurrentRawStream(dev.index)
+        else:
+            self.stream = stream
+            self.handle = stream.cuda_stream
+            self.other = self.handle != torch._C._cuda_getCurrentRawStream(dev.index)
+
+    def empty(self, shape, dtype):
+        t = torch.empty(shape, dtype=dtype, device=self.dev)
+        if self.other:
+            t.record_stream(self.stream)
+        return t
+
+    def workspace(self, ws, nbytes):
+        """(address, bytes) of the caller's workspace, or of this device and stream's own."""
+        if ws is None:
+            key = (self.dev.index, self.handle)
+            buf = _ws.get(key)
+            if buf is None or buf.numel() < nbytes:
+                buf = _ws[key] = self.empty((nbytes,), torch.uint8)
+            return buf.data_ptr(), buf.numel()
+        if isinstance(ws, Workspace):
+            ws = ws.get(nbytes, self.dev)
+        if ws.device != self.dev:
+            raise ValueError(f"workspace must be on {self.dev}, is on {ws.device}")
+        return ws.data_ptr(), ws.numel() * ws.element_size()
+
+    def call(self, name, *args):
+        fn = getattr(load(), name)
+        if torch._C._cuda_getDevice() == self.dev.index:
+            rc = fn(*args, self.handle)
+        else:
+            with torch.cuda.device(self.dev):
+                rc = fn(*args, self.handle)
+        if rc:
+            _check(name, rc)
+
+
+def _cache(k, v, k_scale, v_scale, dev):
+    """The C description of a cache, checked."""
+    if k.dim() != 4:
+        raise ValueError(f"k_cache must have 4 dimensions [pages, page, kv_heads, dim], got {k.dim()}")
+    shape, stride = k.shape, k.stride()
+    code = _CACHE_CODES.get(k.dtype)
+    if code is None:
+        raise TypeError(f"k_cache must be bfloat16, float32 or float8_e4m3fn, got {k.dtype}")
+    if v.dtype is not k.dtype or v.shape != shape or v.stride() != stride:
+        raise ValueError("v_cache must have k_cache's dtype, shape and strides")
+    if k.device != dev or v.device != dev:
+        raise ValueError(f"the cache must be on {dev}")
+    pages, page, heads, d = shape
+    if stride[3] != 1:
+        raise ValueError("the cache's last dimension must be contiguous")
+    ks = vs = None
+    if code == GDN_E4M3:
+        if k_scale is None or v_scale is None:
+            raise ValueError("an 8-bit cache needs k_scale and v_scale")
+        ks, vs = (_want(t, n, torch.float32, (heads,), dev) for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")))
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("k_scale and v_scale belong to an 8-bit cache")
+    return GdnKvCache(k.data_ptr(), v.data_ptr(), stride[0], stride[1], stride[2], ks, vs, pages, page, heads, d, code)
+
+
+def gdn_page_tables(new_lens, free_pages, block_table, *, page, cached_lens=None, n_slots=None, slots=None,
+                    positions=None, seq_lens=None, cu_new=None, counts=None, stream=None):
+    """Block tables and slot maps of one step, from the requests' lengths.
+
+    new_lens [B] and cached_lens [B] (default 0) int32: tokens that each request adds and has;
+    free_pages int32: ids of free pages, taken in order; block_table [B, max_pages] int32, updated
+    in place (entries of pages held already are kept).  n_slots: length of the slot map (at least
+    the number of new tokens; a captured step keeps it fixed), or pass `slots` and `positions`.
+    Returns (slots int64, positions int32, seq_lens int32 [B], cu_new int32 [B+1], counts int32 [4] =
+    {tokens, pages taken, status bits, longest sequence}); gdn_page_tables_status reads the status."""
+    dev = _cuda(block_table, "block_table")
+    B, max_pages = block_table.shape
+    if n_slots is None:
+        if slots is None:
+            raise ValueError("gdn_page_tables needs n_slots or slots")
+        n_slots = slots.numel()
+    i32 = torch.int32
+    on = _On(dev, stream)
+    cached = None if cached_lens is None else _want(cached_lens, "cached_lens", i32, (B,), dev)
+    if slots is None:
+        slots = on.empty((n_slots,), torch.int64)
+    if positions is None:
+        positions = on.empty((n_slots,), i32)
+    if seq_lens is None:
+        seq_lens = on.empty((B,), i32)
+    if cu_new is None:
+        cu_new = on.empty((B + 1,), i32)
+    if counts is None:
+        counts = on.empty((4,), i32)
+    on.call("gdn_page_tables", B, page, max_pages, cached, _want(new_lens, "new_lens", i32, (B,), dev),
+            _want(free_pages, "free_pages", i32, (free_pages.numel(),), dev), free_pages.numel(),
+            _want(block_table, "block_table", i32, (B, max_pages), dev), _want(seq_lens, "seq_lens", i32, (B,), dev),
+            _want(cu_new, "cu_new", i32, (B + 1,), dev), _want(slots, "slots", torch.int64, (n_slots,), dev),
+            _want(positions, "positions", i32, (n_slots,), dev), n_slots, _want(counts, "counts", i32, (4,), dev))
+    return slots, positions, seq_lens, cu_new, counts
+
+
+def gdn_page_tables_status(counts, stream=None) -> int:
+    """Status of a gdn_page_tables call from its counts (synchronises the stream): 0, or
+    9 (GDN_ERR_CAPACITY) if the free list, the table or the slot map was too short."""
+    dev = _cuda(counts, "counts")
+    return int(load().gdn_page_tables_status(_want(counts, "counts", torch.int32, (4,), dev), _On(dev, stream).handle))
+
+
+def gdn_kv_append(k, v, slots, k_cache, v_cache, *, k_scale=None, v_scale=None, stream=None):
+    """Write new tokens' keys and values, k and v [n, kv_heads, dim], to slots [n] (int64; -1 is skipped)
+    of a cache in place.  k and v have the cache's dtype, or bfloat16 / float32 with an 8-bit cache."""
+    dev = _cuda(k_cache, "k_cache")
+    c = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    code = _CODES.get(k.dtype)
+    if code is None or v.dtype is not k.dtype:
+        raise TypeError(f"k and v must both be bfloat16 or float32, got {k.dtype} and {v.dtype}")
+    n = slots.numel()
+    if k.shape != (n, c.Hkv, c.d) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [{n}, {c.Hkv}, {c.d}], got {tuple(k.shape)} and {tuple(v.shape)}")
+    if k.device != dev or v.device != dev:
+        raise ValueError(f"k and v must be on {dev}")
+    ks, vs = k.stride(), v.stride()
+    if ks[2] != 1 or vs[2] != 1:
+        raise ValueError("the last dimension of k and v must be contiguous")
+    _On(dev, stream).call("gdn_kv_append", c, n, code, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+                          _want(slots, "slots", torch.int64, (n,), dev))
+
+
+def gdn_paged_decode(q, k_cache, v_cache, block_table, seq_lens, *, k_scale=None, v_scale=None, scale=None, window=0,
+                     o=None, lse=None, workspace=None, stream=None):
+    """Softmax attention of one new token per request, q [B, heads, dim], over its cached tokens.
+
+    block_table [B, max_pages] int32 (its row stride may be 0: all requests share one row); seq_lens
+    [B] int32, the new token included; window: only the last `window` tokens (0: all); scale:
+    default dim ** -0.5.  Returns (o [B, heads, dim] in q's dtype, lse [B, heads] fp32)."""
+    dev = _cuda(q, "q")
+    c = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    code = _CODES.get(q.dtype)
+    if code is None or (c.dtype != GDN_E4M3 and c.dtype != code):
+        raise TypeError(f"q must have the cache's dtype (bfloat16 with an 8-bit cache), got {q.dtype}")
+    B, heads, d = q.shape
+    if d != c.d:
+        raise ValueError(f"q has dim {d}, the cache {c.d}")
+    qs, ts = q.stride(), block_table.stride()
+    if qs[2] != 1:
+        raise ValueError("the last dimension of q must be contiguous")
+    if block_table.dtype is not torch.int32:
+        raise TypeError(f"block_table must be int32, got {block_table.dtype}")
+    if block_table.device != dev:
+        raise ValueError(f"block_table must be on {dev}, is on {block_table.device}")
+    rows, max_pages = block_table.shape
+    if rows != B or (ts[1] != 1 and max_pages > 1):
+        raise ValueError(f"block_table must be [{B}, max_pages] with contiguous rows, got {tuple(block_table.shape)}")
+    on = _On(dev, stream)
+    if o is None:
+        o = on.empty((B, heads, d), q.dtype)
+    if lse is None:
+        lse = on.empty((B, heads), torch.float32)
+    ws, ws_bytes = on.workspace(workspace, load().gdn_paged_decode_workspace_bytes(c, heads))
+    on.call("gdn_paged_decode", c, B, heads, code, q.data_ptr(), qs[0], qs[1], block_table.data_ptr(), ts[0], max_pages,
+            _want(seq_lens, "seq_lens", torch.int32, (B,), dev), window, d ** -0.5 if scale is None else scale,
+            _want(o, "o", q.dtype, (B, heads, d), dev), _want(lse, "lse", torch.float32, (B, heads), dev), ws, ws_bytes)
+    return o, lse
+
+
+def gdn_sample(logits, noise, *, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, logprobs=None,
+               workspace=None, stream=None):
+    """The next token of every row of logits [B, V] (bfloat16 or float32), from uniform random numbers
+    noise [B, V] (fp32).  temperature, top_p, min_p [B] fp32 and top_k [B] int32: include/gdn.h has the
+    order of the filters; None leaves one out.  Returns (tokens int32 [B], logprobs fp32 [B])."""
+    dev = _cuda(logits, "logits")
+    code = _CODES.get(logits.dtype)
+    if code is None:
+        raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
+    B, V = logits.shape
+    if noise.dtype is not torch.float32 or noise.shape != logits.shape or noise.device != dev:
+        raise ValueError(f"noise must be float32 {tuple(logits.shape)} on {dev}")
+    ls, ns = logits.stride(), noise.stride()
+    if V > 1 and (ls[1] != 1 or ns[1] != 1):
+        raise ValueError("the rows of logits and noise must be contiguous")
+    on = _On(dev, stream)
+    opt = [None if t is None else _want(t, n, torch.int32 if n == "top_k" else torch.float32, (B,), dev)
+           for t, n in ((temperature, "temperature"), (top_k, "top_k"), (top_p, "top_p"), (min_p, "min_p"))]
+    if tokens is None:
+        tokens = on.empty((B,), torch.int32)
+    if logprobs is None:
+        logprobs = on.empty((B,), torch.float32)
+    ws, ws_bytes = on.workspace(workspace, load().gdn_sample_workspace_bytes(B, V))
+    on.call("gdn_sample", B, V, code, logits.data_ptr(), ls[0], noise.data_ptr(), ns[0], *opt,
+            _want(tokens, "tokens", torch.int32, (B,), dev), _want(logprobs, "logprobs", torch.float32, (B,), dev),
+            ws, ws_bytes)
+    return tokens, logprobs

@@ -86,7 +86,9 @@ typedef enum {
     GDN_ERR_TIMEOUT = 10     /* (device-latched) a kernel wait exceeded its 2 s limit and was abandoned */
 } gdn_status;
 
-typedef enum { GDN_BF16 = 0, GDN_F32 = 1 } gdn_dtype;
+/* GDN_E4M3 (8-bit floating point: 4 exponent bits, 3 fraction bits, largest
+ * finite value 448) is a storage type of the paged key-value cache only. */
+typedef enum { GDN_BF16 = 0, GDN_F32 = 1, GDN_E4M3 = 2 } gdn_dtype;
 
 /* Intra-chunk solver for M = I + A_Delta (Sec. 2.3).
  * EXACT ("Full64"): C = M^-1.  BLOCK_ADJ: only the four diagonal and three
@@ -305,6 +307,116 @@ GDN_API gdn_status gdn_prefill_ex(const gdn_shape *shape, gdn_mode mode,
  * Enqueues one kernel on `stream`; no workspace. */
 GDN_API gdn_status gdn_decode_step(const gdn_shape *shape, const void *q, const void *k, const void *v,
                                    const float *beta, const float *a, float *state, void *o, void *stream);
+
+/* ---- Decode step of the softmax-attention layers ---------------------------
+ * A hybrid decoder interleaves the gated delta layers above with softmax
+ * attention layers.  Their keys and values grow with the sequence, so they are
+ * kept in pages of `page` tokens that requests take from one pool.  Request b
+ * holds its tokens in order in the pages its row of the block table names:
+ * token j lies in page table[b][j / page], cell j % page, and its slot is
+ * table[b][j / page] * page + j % page.  None of these calls waits for the
+ * GPU or allocates; all of them may be captured in a CUDA graph.
+ *
+ * gdn_kv_cache describes one layer's cache.  Element (page, cell, head, i) of
+ * both k and v lies at page * stride_page + cell * stride_token +
+ * head * stride_head + i elements, so both storage orders (token-major
+ * [pages, page, Hkv, d] and head-major [pages, Hkv, page, d]) are taken as they
+ * are.  k, v and every stride are multiples of 16 bytes; d is 64, 128 or 256.
+ * k_scale, v_scale [Hkv] (GDN_E4M3 only, else NULL): a stored value x stands
+ * for x * scale[head]. */
+typedef struct {
+    void *k, *v;
+    int64_t stride_page, stride_token, stride_head; /* in elements */
+    const float *k_scale, *v_scale;
+    int64_t pages;      /* pages in the pool */
+    int32_t page;       /* tokens per page, >= 1 */
+    int32_t Hkv, d;
+    gdn_dtype dtype;    /* GDN_BF16, GDN_F32 or GDN_E4M3 */
+} gdn_kv_cache;
+
+/* Block tables and slot maps of one step, from the requests' lengths.  Request
+ * b has c = cached_lens[b] tokens in the cache (cached_lens NULL: 0) and adds
+ * new_lens[b] (negative lengths count as 0).  With old = ceil(c / page) and
+ * need = min(ceil((c + new) / page), max_pages):
+ *   block_table [B][max_pages]  entries below old are kept, entries old..need-1
+ *                take the next ids of free_pages [n_free], requests in order
+ *                (-1 once the list is used up), entries from need on become -1;
+ *   seq_lens [B] c + new;  cu_new [B+1] running sum of the new tokens;
+ *   slots [n_slots] (int64) the slot of every new token, requests in order, -1
+ *                where it has no page and behind the last token;
+ *   positions [n_slots] the token's position in its sequence, 0 behind the last;
+ *   counts [4] {new tokens, pages taken, status bits, longest sequence}.
+ * Status bits: 1 the free list was too short, 2 a sequence needs more than
+ * max_pages pages, 4 more new tokens than n_slots.  Calling again with the same
+ * lengths and free list writes the same values. */
+GDN_API gdn_status gdn_page_tables(int32_t B, int32_t page, int32_t max_pages, const int32_t *cached_lens,
+                                   const int32_t *new_lens, const int32_t *free_pages, int32_t n_free,
+                                   int32_t *block_table, int32_t *seq_lens, int32_t *cu_new, int64_t *slots,
+                                   int32_t *positions, int32_t n_slots, int32_t *counts, void *stream);
+
+/* Synchronises `stream` and reports the status bits of counts
+ * (GDN_ERR_CAPACITY if any is set). */
+GDN_API gdn_status gdn_page_tables_status(const int32_t *counts, void *stream);
+
+/* Writes the keys and values of n new tokens into the cache: row t of k and v
+ * ([Hkv][d] at t * k_stride_token + head * k_stride_head elements, multiples of
+ * 16 bytes; v alike) goes to slot slots[t]; slots outside [0, pages * page) are
+ * skipped.  Rows of dtype (GDN_BF16 or GDN_F32) are copied into a cache of the
+ * same dtype, or stored in a GDN_E4M3 cache as x / scale[head], rounded to
+ * nearest even and saturated at +-448 (NaN stays NaN).  Two rows with the same
+ * slot: either is kept. */
+GDN_API gdn_status gdn_kv_append(const gdn_kv_cache *cache, int32_t n, gdn_dtype dtype, const void *k,
+                                 int64_t k_stride_token, int64_t k_stride_head, const void *v,
+                                 int64_t v_stride_token, int64_t v_stride_head, const int64_t *slots, void *stream);
+
+/* Softmax attention of one new token per request over its cached tokens:
+ *   o[b,h] = sum_j p_j v_j,  p = softmax_j(scale * <q[b,h], k_j>),
+ *   lse[b,h] = log sum_j exp(scale * <q[b,h], k_j>)        (lse may be NULL)
+ * over the tokens j in [max(0, L - window), L), L = seq_lens[b] (window 0: from
+ * 0 on; L is cut at max_pages * page), whose table entry lies in [0, pages).
+ * Query head h reads KV head h / (Hq / Hkv).  A request left without a token
+ * gets o = 0 and lse = -inf.  What the cache holds outside those tokens is
+ * never used, whatever its bits.
+ * q [B][Hq][d] at b * q_stride_request + h * q_stride_head elements (multiples of
+ * 16 bytes); o [B][Hq][d] contiguous; lse [B][Hq] fp32; q and o have the cache's
+ * dtype, or GDN_BF16 with a GDN_E4M3 cache.  Row b of the block table starts at
+ * b * table_stride (0: all requests share one row, as the rows of a prompt chunk
+ * do with seq_lens c+1, c+2, ...).
+ * Sums are held in fp32; a row's tokens are summed in an order that depends on
+ * the lengths of all requests of the call, never on timing: the same call gives
+ * the same bits.
+ * Workspace: gdn_paged_decode_workspace_bytes(cache, Hq), 256-byte aligned; its
+ * contents need no set-up and do not outlive the call. */
+GDN_API size_t gdn_paged_decode_workspace_bytes(const gdn_kv_cache *cache, int32_t Hq);
+GDN_API gdn_status gdn_paged_decode(const gdn_kv_cache *cache, int32_t B, int32_t Hq, gdn_dtype dtype, const void *q,
+                                    int64_t q_stride_request, int64_t q_stride_head, const int32_t *block_table,
+                                    int64_t table_stride, int32_t max_pages, const int32_t *seq_lens, int32_t window,
+                                    float scale, void *o, float *lse, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+
+/* The next token of every row of logits [B][V] (row b at b * logits_stride
+ * elements; GDN_BF16 or GDN_F32; V <= 2^22).  With m the row's largest logit,
+ * T = temperature[b], y_i = (x_i - m) / T and w_i = exp(y_i):
+ *   K  the top_k[b] largest logits (ties: lowest index first; <= 0 or >= V: all);
+ *   P  the shortest prefix of K, in that descending order, whose mass is at least
+ *      top_p[b] of K's (>= 1: all of K; at least one token);
+ *   the tokens of P with 0 < w_i and w_i >= min_p[b] stay (at least the largest);
+ *   tokens[b] = argmax over them of y_i - log(-log u_i), u = noise[b] [V] uniform
+ *   random numbers in (0, 1) (clamped to [2^-32, 1 - 2^-24]; ties: lowest index),
+ *   which is a draw from the kept weights.
+ * logprobs[b] (logprobs may be NULL) = log(w_token / sum_i w_i), over the whole
+ * row.  T <= 0: the largest logit (ties: lowest index), logprob 0.  A NULL array
+ * stands for T = 1, top_k = 0, top_p = 1, min_p = 0.  Logits of -inf and NaN are
+ * never chosen, +inf counts as the largest finite number; a row with neither a
+ * finite logit nor +inf gets token -1 and logprob -inf.  Masses are held as 64-bit
+ * whole numbers in units of 2^-40 of the largest weight, so the result does not
+ * depend on the order of any sum.  Workspace: gdn_sample_workspace_bytes(B, V),
+ * 256-byte aligned, no set-up. */
+GDN_API size_t gdn_sample_workspace_bytes(int32_t B, int32_t V);
+GDN_API gdn_status gdn_sample(int32_t B, int32_t V, gdn_dtype dtype, const void *logits, int64_t logits_stride,
+                              const float *noise, int64_t noise_stride, const float *temperature,
+                              const int32_t *top_k, const float *top_p, const float *min_p, int32_t *tokens,
+                              float *logprobs, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Prefill with HOST inputs and outputs: the same computation as
  * gdn_prefill_sparse (mask != NULL) or gdn_prefill_dense (mask == NULL), with
