@@ -1,81 +1,118 @@
-// k_paged_decode.cu -- softmax attention of one new token per request over the paged cache.
+// k_paged_decode.cu -- one-token attention over the paged cache: the launch, and the join of
+// rows that were cut between CTAs (paged_decode.cuh has the main kernel).
 //
-// First form: one CTA per (request, query head), one warp per token in turn, with
-// a running maximum and sum per warp, joined in shared memory.
-#include "paged.cuh"
+// A row cut into parts (m_i, l_i, o_i) is o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i, M = max m_i.  One
+// CTA per (CTA edge, query head): the first edge inside a row joins all of the row's parts, in the order of
+// the tokens, so the result does not depend on which part was done first.  At most 2 x 304 parts of up to 16
+// heads, read back from L2: latency, hidden in part by a programmatic dependent launch.
+#include "paged_decode.cuh"
 
 namespace gdn {
+namespace paged {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kThreads = 128;
 
-template <typename T> __device__ __forceinline__ float ld(const T *p) { return io<T>::ld(p); }
-template <> __device__ __forceinline__ float ld(const __nv_fp8_e4m3 *p) { return (float)*p; }
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) join_kernel(AttendArgs a, int grid, int heads) {
+    __shared__ float weight[kMaxCtas + 1];
+    __shared__ float2 red[kThreads / 32];
+    __shared__ float4 acc[kThreads];
+    pdl_wait();
+    const WsView ws = ws_view(a.ws, heads);
+    const int64_t total = *ws.total;
+    const int ctas = (int)min((int64_t)grid, total), i = blockIdx.x + 1;
+    if (i >= ctas) return;
+    const int4 at = ws.first[i];
+    const int group = a.Hq / a.c.Hkv, passes = (group + heads - 1) / heads;
+    const int h = at.y / passes, hh = at.y % passes * heads + blockIdx.y;
+    if (at.z == 0 || hh >= group) return;  // the row begins with CTA i
+    const int64_t row0 = split_at(total, ctas, i) - at.z, row1 = row0 + at.w, before = split_at(total, ctas, i - 1);
+    if (before > row0) return;             // an edge before this one lies inside the row too
+    // parts: CTA i - 1's (its last row, or its only one), then the first of every CTA up to the row's end
+    const int last = (int)min((int64_t)ctas - 1, (row1 * ctas + total - 1) / total - 1), parts = last - i + 2;
+    const int p0 = 2 * (i - 1) + (before < row0);
+    auto part = [&](int k) { return k == 0 ? p0 : 2 * (i + k - 1); };
 
-template <typename Q, typename T, int D>
-__global__ void __launch_bounds__(32 * kWarps) decode_kernel(AttendArgs a) {
-    constexpr int N = D / 32;
-    __shared__ float sm[kWarps], sl[kWarps], so[kWarps][D];
-    const int b = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq, hk = h / (a.Hq / a.c.Hkv);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t len = min((int64_t)max(a.lens[b], 0), (int64_t)a.max_pages * a.c.page);
-    const int64_t start = a.window > 0 ? max((int64_t)0, len - a.window) : 0;
-    const float ks = a.c.k_scale ? a.c.k_scale[hk] : 1.f, vs = a.c.v_scale ? a.c.v_scale[hk] : 1.f;
-    float q[N], o[N], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        q[i] = io<Q>::ld((const Q *)a.q + b * a.q_req + h * a.q_head + lane + 32 * i) * (a.scale * ks);
-        o[i] = 0.f;
-    }
-    for (int64_t j = start + warp; j < len; j += kWarps) {
-        const int64_t page = a.table[b * a.table_stride + j / a.c.page];
-        if (page < 0 || page >= a.c.pages) continue;
-        const int64_t at = page * a.c.stride_page + (j % a.c.page) * a.c.stride_token + hk * a.c.stride_head + lane;
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) s += q[i] * ld((const T *)a.c.k + at + 32 * i);
-#pragma unroll
-        for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn;
-        const float f = expf(m - ref), p = expf(s - ref);
-        l = l * f + p;
-#pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = o[i] * f + p * ld((const T *)a.c.v + at + 32 * i);
-        m = mn;
-    }
-    if (lane == 0) sm[warp] = m, sl[warp] = l;
-#pragma unroll
-    for (int i = 0; i < N; ++i) so[warp][lane + 32 * i] = o[i];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float top = -INFINITY;
+    for (int k = tid; k < parts; k += kThreads) top = fmaxf(top, ws.ml[(int64_t)part(k) * heads + blockIdx.y].x);
+    for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    if (lane == 0) red[warp].x = top;
     __syncthreads();
-    float M = -INFINITY, L = 0.f;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w]);
-    const float ref = M == -INFINITY ? 0.f : M;
-    for (int w = 0; w < kWarps; ++w) L += sl[w] * expf(sm[w] - ref);
-    for (int i = threadIdx.x; i < D; i += 32 * kWarps) {
-        float x = 0.f;
-        for (int w = 0; w < kWarps; ++w) x += so[w][i] * expf(sm[w] - ref);
-        io<Q>::st((Q *)a.o + ((int64_t)b * a.Hq + h) * D + i, L == 0.f ? 0.f : x * vs / L);
+    for (int w = 0; w < kThreads / 32; ++w) top = fmaxf(top, red[w].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+    for (int k = tid; k < parts; k += kThreads) {
+        const float2 x = ws.ml[(int64_t)part(k) * heads + blockIdx.y];
+        const float f = exp2_fast(x.x - ref);
+        weight[k] = f;
+        sum += f * x.y;
     }
-    if (threadIdx.x == 0 && a.lse) a.lse[(int64_t)b * a.Hq + h] = L == 0.f ? -INFINITY : ref + logf(L);
+    for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (lane == 0) red[warp].y = sum;
+    __syncthreads();
+    sum = 0.f;
+    for (int w = 0; w < kThreads / 32; ++w) sum += red[w].y;
+
+    constexpr int kLanes = D / 4, kGroups = kThreads / kLanes;
+    const int d4 = tid % kLanes * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = tid / kLanes; k < parts; k += kGroups) {
+        const float4 y = *(const float4 *)(ws.o + ((int64_t)part(k) * heads + blockIdx.y) * D + d4);
+        const float f = weight[k];
+        x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w;
+    }
+    acc[tid] = x;
+    __syncthreads();
+    if (tid >= kLanes) return;
+    for (int gr = 1; gr < kGroups; ++gr) {
+        const float4 y = acc[gr * kLanes + tid];
+        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+    }
+    float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (a.c.v_scale) inv *= a.c.v_scale[h];
+    const int64_t out = (int64_t)at.x * a.Hq + h * group + hh;
+    io<T>::st((T *)a.o + out * D + d4, x.x * inv);
+    io<T>::st((T *)a.o + out * D + d4 + 1, x.y * inv);
+    io<T>::st((T *)a.o + out * D + d4 + 2, x.z * inv);
+    io<T>::st((T *)a.o + out * D + d4 + 3, x.w * inv);
+    if (tid == 0 && a.lse) a.lse[out] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
 }
 
-template <typename Q, typename T>
-void launch(const AttendArgs &a, cudaStream_t stream) {
-    const unsigned grid = (unsigned)(a.B * a.Hq);
-    if (a.c.d == 64) decode_kernel<Q, T, 64><<<grid, 32 * kWarps, 0, stream>>>(a);
-    else if (a.c.d == 128) decode_kernel<Q, T, 128><<<grid, 32 * kWarps, 0, stream>>>(a);
-    else decode_kernel<Q, T, 256><<<grid, 32 * kWarps, 0, stream>>>(a);
+template <typename T>
+cudaError_t join(const AttendArgs &a, int grid, int heads, cudaStream_t stream) {
+    const dim3 g(grid - 1, heads);
+    switch (a.c.d) {
+        case 64: return launch_kernel(true, join_kernel<T, 64>, g, kThreads, 0, stream, a, grid, heads);
+        case 128: return launch_kernel(true, join_kernel<T, 128>, g, kThreads, 0, stream, a, grid, heads);
+        default: return launch_kernel(true, join_kernel<T, 256>, g, kThreads, 0, stream, a, grid, heads);
+    }
 }
 
 }  // namespace
+}  // namespace paged
 
-size_t paged_decode_workspace_bytes(const gdn_kv_cache &, int) { return 0; }
+size_t paged_decode_workspace_bytes(const gdn_kv_cache &c, int Hq) {
+    return paged::ws_bytes(paged::pass_heads(Hq / c.Hkv), c.d);
+}
 
-cudaError_t launch_paged_decode(const AttendArgs &a, cudaStream_t stream) {
-    if (a.c.dtype == GDN_BF16) launch<__nv_bfloat16, __nv_bfloat16>(a, stream);
-    else if (a.c.dtype == GDN_E4M3) launch<__nv_bfloat16, __nv_fp8_e4m3>(a, stream);
-    else launch<float, float>(a, stream);
-    return cudaGetLastError();
+cudaError_t launch_paged_decode(const AttendArgs &args, cudaStream_t stream) {
+    AttendArgs a = args;
+    if (a.max_pages == 0) a.c.k = a.c.v = (void *)a.q;  // an address for copies of no bytes
+    // slices of 16 tokens of a row as long as the table or the window (whose first slice it need not fill)
+    int64_t tokens = (int64_t)a.max_pages * a.c.page;
+    if (a.window > 0) tokens = min(tokens, (int64_t)a.window + 15);
+    const int64_t slices = max((int64_t)1, (tokens + 15) / 16);
+    int grid = 0;
+    cudaError_t e;
+    if (a.c.dtype == GDN_BF16) e = paged::launch_kind<GDN_BF16>(a, slices, stream, &grid);
+    else if (a.c.dtype == GDN_E4M3) e = paged::launch_kind<GDN_E4M3>(a, slices, stream, &grid);
+    else e = paged::launch_kind<GDN_F32>(a, slices, stream, &grid);
+    if (e != cudaSuccess || grid < 2) return e;
+    const int heads = paged::pass_heads(a.Hq / a.c.Hkv);
+    return a.c.dtype == GDN_F32 ? paged::join<float>(a, grid, heads, stream) : paged::join<__nv_bfloat16>(a, grid, heads, stream);
 }
 
 }  // namespace gdn

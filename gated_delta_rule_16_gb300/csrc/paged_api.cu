@@ -108,6 +108,7 @@ gdn_status gdn_paged_decode(const gdn_kv_cache *cache, int32_t B, int32_t Hq, gd
     if (B < 0 || Hq <= 0 || Hq % cache->Hkv || max_pages < 0 || window < 0 || table_stride < 0) return GDN_ERR_SHAPE;
     if (dtype != (cache->dtype == GDN_E4M3 ? GDN_BF16 : cache->dtype)) return GDN_ERR_DTYPE;
     if ((int64_t)B * Hq > INT32_MAX) return GDN_ERR_SHAPE;
+    if ((int64_t)max_pages * cache->page > INT32_MAX - 127) return GDN_ERR_UNSUPPORTED;  // token positions are int32
     if (B == 0) return GDN_OK;
     // with no page in the pool or no column in the table every request is empty, but o and lse are still written
     if (cache->pages > 0 && max_pages > 0) {

@@ -1,0 +1,683 @@
+// paged_decode.cuh -- one-token attention over the paged cache: the kernel template that
+// k_paged_decode_{bf16,e4m3,f32}.cu instantiate.
+//
+// o = sum_j p_j v_j / sum_j p_j with p_j = 2^(z_j - max z), z_j = scale log2(e) <q, k_j>: one pass over K and V
+// with a running maximum, sum and output per (request, query head).
+//
+// What bounds it: every cached byte is read once and used for 2 G operations (G query heads per KV head; at most
+// 16 to a pass), so HBM, as long as tensor and issue slots keep up.  The design follows from that:
+//   - Work is cut by cached tokens, not by requests.  All (request, KV head) rows are laid end to end in tiles of
+//     16 tokens per warp and the CTAs of one wave get equal runs of tiles.  A row inside one CTA is written out
+//     directly; a row cut by a CTA's edge leaves unnormalised fp32 parts that a second, dependent launch joins in a
+//     fixed order.  Lengths are only known on the GPU, so each CTA finds its run from a scan over them.
+//   - Each warp streams its own 16-token slices of K and V through a ring of shared-memory stages by 16-byte
+//     cp.async, whose source address is free per token: any page size, any storage order.  No CTA barrier inside a
+//     row: the warps keep their own maxima and meet at the row's end.
+//   - Products on warp MMAs with the cached tokens as M and 8 query heads as N: S^T = K Q^T (16 tokens x 8 heads) and
+//     O^T += V^T P^T (16 dims x 8 heads), so 8 heads waste nothing (heads as M would pad them to 16), and K and V
+//     are the A operands straight from shared memory.  The tensor cores' tcgen05 form wants 64 rows of M or more and
+//     both operands in shared memory; at 2 G flops a byte the warp form has the rate needed, and P stays in registers.
+//     P^T comes from the S^T fragment by transposing 8x8 tiles between registers (movmatrix).
+//   - Rounding: scores, maxima, sums and outputs are fp32.  P enters the second product as two bf16 terms (16 bits
+//     together) for a bf16 cache, as f16 (11 bits) for an 8-bit cache, where K and V are converted exactly to f16 and
+//     q, scaled by a power of two to below 2, loses nothing unless it is 2^14 times smaller than the row's largest.  A
+//     32-bit cache splits every operand into two tf32 terms, drops the product of the low ones (2^-22) and adds each
+//     8-wide product to its sum outside the tensor core, whose own accumulation cuts instead of rounding: that
+//     drift alone put scores of thousands past 1e-5.
+//   - Tokens outside [max(0, L - window), L) or on a page outside the pool are zero-filled, never read, and their
+//     scores set to -inf, so that what the cache holds there cannot reach a product.
+#pragma once
+
+#include "paged.cuh"
+
+namespace gdn {
+namespace paged {
+
+constexpr int kSMs = 152;
+constexpr int kMaxCtas = 2 * kSMs;   // one wave at two CTAs per SM
+constexpr int kMergeDims = 64;       // output dims joined per round at a row's end
+
+// Workspace: tiles in all, each CTA's first tile as {request, row in request, tile in row, tiles of the row}, then two
+// parts per CTA (one where its first row began before it, one where its last row ends after it).
+struct WsView {
+    int64_t *total;
+    int4 *first;
+    float2 *ml;   // [2 * kMaxCtas][heads] {maximum, sum}
+    float *o;     // [2 * kMaxCtas][heads][d]
+};
+__host__ __device__ inline WsView ws_view(void *ws, int heads) {
+    char *p = (char *)ws;
+    WsView w;
+    w.total = (int64_t *)p;
+    w.first = (int4 *)(p + 256);
+    w.ml = (float2 *)(p + 256 + kMaxCtas * sizeof(int4));
+    w.o = (float *)(p + 256 + kMaxCtas * sizeof(int4) + (size_t)2 * kMaxCtas * heads * sizeof(float2));
+    return w;
+}
+inline size_t ws_bytes(int heads, int d) {
+    return 256 + kMaxCtas * sizeof(int4) + (size_t)2 * kMaxCtas * heads * (sizeof(float2) + (size_t)d * sizeof(float));
+}
+
+// Query heads per pass over a KV head's tokens: 8 or 16 (a larger group takes several passes, as rows of their own).
+__host__ __device__ constexpr int pass_heads(int group) { return group <= 8 ? 8 : 16; }
+
+template <gdn_dtype KIND, int D, int NT>
+struct Cfg {
+    static constexpr int kBytes = KIND == GDN_BF16 ? 2 : (KIND == GDN_E4M3 ? 1 : 4);
+    static constexpr int kRow = D * kBytes;           // bytes of a cached row
+    static constexpr int kChunks = kRow / 16;
+    static constexpr int kWarps = kRow > 512 ? 2 : 4;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kTile = 16 * kWarps;         // tokens
+    static constexpr int kSlice = 16 * kRow;          // bytes of one warp's K (or V) slice
+    static constexpr int kStage = kWarps * 2 * kSlice;
+    // two CTAs per SM where three stages of a tile fit twice, else one
+    static constexpr int kOcc = kStage <= 32 * 1024 ? 2 : 1;
+    static constexpr int kStages = kStage <= 16 * 1024 ? 6 : 3;
+    static constexpr int kMerge = kWarps * 8 * (kMergeDims + 4) * 4;
+    static constexpr int kQ = KIND == GDN_F32 ? NT * (D / 8) * 32 * 8 : 0;
+    static constexpr int kSmem = kStages * kStage + kMerge + kWarps * NT * 8 * 8 + kQ + kWarps * kStages * 4;
+    static_assert((kSmem + 1024) * kOcc <= 228 * 1024, "shared memory of an SM");
+};
+
+// ---- instructions -----------------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t r;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
+    return r;
+}
+__device__ __forceinline__ void lds128(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// x = hi + lo to 2^-22 of x, both representable in tf32
+__device__ __forceinline__ void split_tf32(uint32_t x, uint32_t &hi, uint32_t &lo) {
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(__uint_as_float(x)));
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(__uint_as_float(x) - __uint_as_float(hi)));
+}
+// both 8-bit values of x's low (high) half as f16: exact
+__device__ __forceinline__ uint32_t f16_lo(uint32_t x) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)x));
+    return r;
+}
+__device__ __forceinline__ uint32_t f16_hi(uint32_t x) { return f16_lo(x >> 16); }
+__device__ __forceinline__ float exp2_fast(float x) {  // 2^-22 relative
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// ---- a place in the list of tiles -------------------------------------------------------------------
+struct Cursor {
+    int b, row, tile, tiles;  // request, row in request, tile in row, tiles of the row
+    int start, len;           // tokens attended: [start, len)
+
+    template <int TILE> __device__ __forceinline__ void load(const AttendArgs &a) {
+        tiles = 1;
+        start = len = 0;
+        if (b >= a.B) return;
+        const int64_t room = (int64_t)a.max_pages * a.c.page;
+        len = (int)min((int64_t)max(a.lens[b], 0), room);
+        start = a.window > 0 ? max(0, len - a.window) : 0;
+        tiles = max(1, (len - (start & ~15) + TILE - 1) / TILE);  // an empty request keeps one, to be written
+    }
+    template <int TILE> __device__ __forceinline__ void next(const AttendArgs &a, int rows) {
+        if (++tile < tiles) return;
+        tile = 0;
+        if (++row < rows) return;
+        row = 0;
+        ++b;
+        load<TILE>(a);
+    }
+};
+
+__device__ __forceinline__ int64_t split_at(int64_t total, int ctas, int i) { return total * i / ctas; }
+
+template <int THREADS>
+__device__ int64_t block_sum(int64_t x, int64_t *buf) {
+#pragma unroll
+    for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) x += buf[w];
+    __syncthreads();
+    return x;
+}
+
+template <gdn_dtype KIND, int D, int NT>
+__global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::kOcc) paged_decode_kernel(AttendArgs a) {
+    using C = Cfg<KIND, D, NT>;
+    constexpr int W = C::kWarps, STAGES = C::kStages, TILE = C::kTile;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, q4 = lane & 3;  // fragment row, fragment column pair
+    uint8_t *ring = smem + warp * (STAGES * 2 * C::kSlice);
+    float *merge = (float *)(smem + STAGES * C::kStage);
+    float2 *ml = (float2 *)(smem + STAGES * C::kStage + C::kMerge);
+    float2 *qs = (float2 *)((uint8_t *)ml + W * NT * 8 * 8);                         // 32-bit storage: q by fragment
+    uint32_t *real = (uint32_t *)((uint8_t *)qs + C::kQ) + warp * STAGES;            // bit t: token t of the slice is real
+    const uint32_t ring_addr = smem_addr(ring);
+    const int group = a.Hq / a.c.Hkv, passes = (group + NT * 8 - 1) / (NT * 8), rows = a.c.Hkv * passes;
+    const WsView ws = ws_view(a.ws, NT * 8);
+    pdl_trigger();
+
+    // ---- this CTA's run of tiles
+    __shared__ int64_t scan[W];
+    __shared__ int4 found;
+    Cursor cur;
+    int64_t sum = 0;
+    for (int b = tid; b < a.B; b += C::kThreads) {
+        cur.b = b;
+        cur.load<TILE>(a);
+        sum += cur.tiles;
+    }
+    const int64_t per_row = block_sum<C::kThreads>(sum, scan), total = per_row * rows;
+    const int ctas = (int)min((int64_t)gridDim.x, total), cta = blockIdx.x;
+    if (cta >= ctas) return;
+    const int64_t t0 = split_at(total, ctas, cta), n = split_at(total, ctas, cta + 1) - t0;
+    {
+        // the request whose tiles hold t0: requests lie one after the other, `rows` rows each
+        const int64_t want = t0 / rows;
+        int64_t before = 0;
+        for (int b0 = 0; b0 < a.B; b0 += C::kThreads) {
+            cur.b = b0 + tid;
+            cur.load<TILE>(a);
+            const int64_t mine = cur.b < a.B ? cur.tiles : 0;
+            int64_t incl = mine;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += x;
+            }
+            if (lane == 31) scan[warp] = incl;
+            __syncthreads();
+            int64_t base = before, step = 0;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                if (w < warp) base += scan[w];
+                step += scan[w];
+            }
+            const int64_t excl = base + incl - mine;
+            if (mine > 0 && excl <= want && want < excl + mine) {
+                const int64_t at = t0 - excl * rows;
+                found = make_int4(cur.b, (int)(at / mine), (int)(at % mine), (int)mine);
+            }
+            before += step;
+            __syncthreads();
+            if (before > want) break;
+        }
+        if (tid == 0) {
+            ws.first[cta] = found;
+            if (cta == 0) *ws.total = total;
+        }
+        cur.b = found.x;
+        cur.load<TILE>(a);
+        cur.row = found.y;
+        cur.tile = found.z;
+    }
+
+    // ---- loads: a lane finds the cached row of token (lane & 15) of its warp's slice; -1 where there is none
+    const bool pow2 = (a.c.page & (a.c.page - 1)) == 0;
+    const int shift = 31 - __clz(a.c.page);
+    auto find_row = [&](const Cursor &c) -> int64_t {
+        const int t = (c.start & ~15) + c.tile * TILE + warp * 16 + (lane & 15);
+        if (t < c.start || t >= c.len) return -1;
+        const int slot = pow2 ? t >> shift : t / a.c.page;
+        const int id = a.table[c.b * a.table_stride + slot];
+        if (id < 0 || id >= a.c.pages) return -1;
+        return id * a.c.stride_page + (int64_t)(t - slot * a.c.page) * a.c.stride_token + (c.row / passes) * a.c.stride_head;
+    };
+    auto swizzled = [](int row, int chunk) -> uint32_t {
+        const int x = C::kChunks >= 8 ? row & 7 : (row >> 1) & 3;
+        return (uint32_t)(row * C::kRow + ((chunk ^ x) << 4));
+    };
+    auto issue = [&](int stage, int64_t row_off) {
+        const uint32_t mask = __ballot_sync(0xffffffffu, row_off >= 0) & 0xffffu;
+        if (lane == 0) real[stage] = mask;
+        const uint32_t dst = ring_addr + stage * (2 * C::kSlice);
+#pragma unroll
+        for (int i = 0; i < 16 * C::kChunks / 32; ++i) {
+            const int idx = i * 32 + lane, row = idx / C::kChunks, chunk = idx % C::kChunks;
+            const int64_t off = __shfl_sync(0xffffffffu, row_off, row);
+            const int64_t byte = (off < 0 ? 0 : off) * C::kBytes + chunk * 16;
+            const uint32_t d = dst + swizzled(row, chunk);
+            cp16(d, (const char *)a.c.k + byte, off >= 0);
+            cp16(d + C::kSlice, (const char *)a.c.v + byte, off >= 0);
+        }
+    };
+
+    // ---- a row's state
+    uint32_t qf[KIND == GDN_F32 ? 1 : D / 16][NT][2];
+    float z_scale[NT][2];                       // per query head 2 q4 + j of tile nt
+    float m[NT][2], l[NT][2], o[D / 16][NT][4];
+    auto begin_row = [&](const Cursor &c) {
+        const int h = c.row / passes, first = (c.row % passes) * NT * 8;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int hh = first + nt * 8 + g;
+            const bool have = hh < group;
+            const int64_t off = c.b * a.q_req + (int64_t)(h * group + (have ? hh : 0)) * a.q_head;
+            float unit = 1.f;
+            if constexpr (KIND == GDN_BF16) {
+                const __nv_bfloat16 *q = (const __nv_bfloat16 *)a.q + off;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        qf[kk][nt][i] = have ? *(const uint32_t *)(q + 16 * kk + 8 * i + 2 * q4) : 0u;
+            } else if constexpr (KIND == GDN_E4M3) {
+                // K's bytes 4 q4 .. 4 q4 + 3 of a 16-byte piece are this lane's k indices 2 q4, 2 q4 + 1, 2 q4 + 8, 2 q4 + 9
+                const __nv_bfloat16 *q = (const __nv_bfloat16 *)a.q + off;
+                float top = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint2 x = have ? *(const uint2 *)(q + 16 * kk + 4 * q4) : make_uint2(0u, 0u);
+                    qf[kk][nt][0] = x.x;
+                    qf[kk][nt][1] = x.y;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[kk][nt][i] << 16)),
+                                               fabsf(__uint_as_float(qf[kk][nt][i] & 0xffff0000u))));
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int e = (int)(__float_as_uint(top) >> 23);        // top = 2^(e-127) * [1, 2); 0 or infinite: left as it is
+                float down = 1.f;
+                if (e > 0 && e < 255) {
+                    unit = __uint_as_float((uint32_t)e << 23);
+                    down = e < 254 ? __uint_as_float((uint32_t)(254 - e) << 23) : __uint_as_float(1u << 22);
+                }
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        qf[kk][nt][i] = pack_f16(__uint_as_float(qf[kk][nt][i] << 16) * down,
+                                                 __uint_as_float(qf[kk][nt][i] & 0xffff0000u) * down);
+            } else {
+                const float *q = (const float *)a.q + off;
+                for (int kk = warp; kk < D / 8; kk += W)
+                    qs[(nt * (D / 8) + kk) * 32 + lane] = have ? make_float2(q[8 * kk + q4], q[8 * kk + q4 + 4]) : make_float2(0.f, 0.f);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float f = a.scale * 1.4426950408889634f;
+                if constexpr (KIND == GDN_E4M3) f *= a.c.k_scale ? a.c.k_scale[h] : 1.f;
+                z_scale[nt][j] = f * (KIND == GDN_E4M3 ? __shfl_sync(0xffffffffu, unit, (2 * q4 + j) * 4) : 1.f);
+                m[nt][j] = -INFINITY;
+                l[nt][j] = 0.f;
+            }
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[mt][nt][i] = 0.f;
+        }
+        if constexpr (KIND == GDN_F32) __syncthreads();
+    };
+
+    // ---- one slice: 16 tokens
+    auto slice = [&](int stage) {
+        const uint32_t mask = real[stage];
+        if (mask == 0) return;
+        const uint32_t kb = ring_addr + stage * (2 * C::kSlice), vb = kb + C::kSlice;
+        const int mrow = lane & 7, mid = lane >> 3;  // ldmatrix: row in matrix, matrix
+        float s[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
+        if constexpr (KIND == GDN_BF16) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                uint32_t k[4];
+                ldsm4(k, kb + swizzled(mrow + (mid & 1) * 8, 2 * kk + (mid >> 1)));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma_bf16(s[nt], k, qf[kk][nt][0], qf[kk][nt][1]);
+            }
+        } else if constexpr (KIND == GDN_E4M3) {
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk) {
+                uint32_t k[4];  // rows 0-7 and 8-15 of one 16-byte piece, then of the next
+                ldsm4(k, kb + swizzled(mrow + (mid & 1) * 8, 2 * kk + (mid >> 1)));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t a0 = f16_lo(k[2 * i]), a1 = f16_lo(k[2 * i + 1]), a2 = f16_hi(k[2 * i]), a3 = f16_hi(k[2 * i + 1]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt], a0, a1, a2, a3, qf[2 * kk + i][nt][0], qf[2 * kk + i][nt][1]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int kk = 0; kk < D / 8; ++kk) {
+                uint32_t k[4], kh[4], kl[4];
+                ldsm4(k, kb + swizzled(mrow + (mid & 1) * 8, 2 * kk + (mid >> 1)));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) split_tf32(k[i], kh[i], kl[i]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float2 x = qs[(nt * (D / 8) + kk) * 32 + lane];
+                    uint32_t h0, l0, h1, l1;
+                    split_tf32(__float_as_uint(x.x), h0, l0);
+                    split_tf32(__float_as_uint(x.y), h1, l1);
+                    float t[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma_tf32(t, kl, h0, h1);
+                    mma_tf32(t, kh, l0, l1);
+                    mma_tf32(t, kh, h0, h1);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[nt][i] += t[i];
+                }
+            }
+        }
+
+        // running softmax; token g (rows 0-7) in s[.][0..1], token g + 8 in s[.][2..3], heads 2 q4 and 2 q4 + 1
+        const bool real0 = mask >> g & 1, real1 = mask >> (g + 8) & 1;
+        bool moved = false;
+        float f[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float x0 = real0 ? s[nt][j] * z_scale[nt][j] : -INFINITY;
+                const float x1 = real1 ? s[nt][2 + j] * z_scale[nt][j] : -INFINITY;
+                float top = fmaxf(x0, x1);
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                top = fmaxf(top, m[nt][j]);
+                const float ref = top == -INFINITY ? 0.f : top;
+                moved |= top != m[nt][j];
+                f[nt][j] = exp2_fast(m[nt][j] - ref);
+                m[nt][j] = top;
+                s[nt][j] = exp2_fast(x0 - ref);
+                s[nt][2 + j] = exp2_fast(x1 - ref);
+                l[nt][j] = l[nt][j] * f[nt][j] + (s[nt][j] + s[nt][2 + j]);
+            }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[mt][nt][i] *= f[nt][i & 1];
+        }
+
+        if constexpr (KIND == GDN_BF16) {
+            uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float p0 = s[nt][2 * i], p1 = s[nt][2 * i + 1];
+                    // cut, not rounded, so that both terms of a weight are positive: an infinite value stays infinite
+                    const uint32_t h = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+                    const uint32_t r = pack_bf16(fmaxf(p0 - __uint_as_float(h << 16), 1.17549435e-38f),
+                                                 fmaxf(p1 - __uint_as_float(h & 0xffff0000u), 1.17549435e-38f));
+                    hi[nt][i] = transpose8x8(h);
+                    lo[nt][i] = transpose8x8(r);
+                }
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt) {
+                uint32_t v[4];
+                ldsm4t(v, vb + swizzled(mrow + (mid >> 1) * 8, 2 * mt + (mid & 1)));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma_bf16(o[mt][nt], v, lo[nt][0], lo[nt][1]);
+                    mma_bf16(o[mt][nt], v, hi[nt][0], hi[nt][1]);
+                }
+            }
+        } else if constexpr (KIND == GDN_E4M3) {
+            uint32_t p[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) p[nt][i] = transpose8x8(pack_f16(s[nt][2 * i], s[nt][2 * i + 1]));
+            // a lane's 4 bytes of a token are dims 4 g .. 4 g + 3 of a block of 32; bytes of neighbouring tokens are
+            // paired into the A fragments of two 16-row tiles whose rows g, g + 8 are dims 4 g, 4 g + 1 and 4 g + 2, 4 g + 3
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] = lds32(vb + swizzled(2 * q4 + (i & 1) + (i >> 1) * 8, 2 * kk + (g >> 2)) + (g & 3) * 4);
+                const uint32_t t01 = __byte_perm(w[0], w[1], 0x5140), t23 = __byte_perm(w[2], w[3], 0x5140);
+                const uint32_t u01 = __byte_perm(w[0], w[1], 0x7362), u23 = __byte_perm(w[2], w[3], 0x7362);
+                const uint32_t ta[4] = {f16_lo(t01), f16_hi(t01), f16_lo(t23), f16_hi(t23)};
+                const uint32_t ua[4] = {f16_lo(u01), f16_hi(u01), f16_lo(u23), f16_hi(u23)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma_f16(o[2 * kk][nt], ta[0], ta[1], ta[2], ta[3], p[nt][0], p[nt][1]);
+                    mma_f16(o[2 * kk + 1][nt], ua[0], ua[1], ua[2], ua[3], p[nt][0], p[nt][1]);
+                }
+            }
+        } else {
+            // k index q4 of step i is token 8 i + 2 q4, k index q4 + 4 is token 8 i + 2 q4 + 1; rows as for 8 bits
+            uint32_t ph[NT][2][2], pl[NT][2][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t x = __float_as_uint(s[nt][2 * i]), y = __float_as_uint(s[nt][2 * i + 1]);
+                    const uint32_t top = transpose8x8(__byte_perm(x, y, 0x7632)), low = transpose8x8(__byte_perm(x, y, 0x5410));
+                    split_tf32(__byte_perm(low, top, 0x5410), ph[nt][i][0], pl[nt][i][0]);
+                    split_tf32(__byte_perm(low, top, 0x7632), ph[nt][i][1], pl[nt][i][1]);
+                }
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t x[4], y[4];
+                    lds128(x, vb + swizzled(8 * i + 2 * q4, 8 * kk + g));
+                    lds128(y, vb + swizzled(8 * i + 2 * q4 + 1, 8 * kk + g));
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const uint32_t v[4] = {x[2 * t], x[2 * t + 1], y[2 * t], y[2 * t + 1]};
+                        uint32_t vh[4], vl[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) split_tf32(v[e], vh[e], vl[e]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float r[4] = {0.f, 0.f, 0.f, 0.f};
+                            mma_tf32(r, vl, ph[nt][i][0], ph[nt][i][1]);
+                            mma_tf32(r, vh, pl[nt][i][0], pl[nt][i][1]);
+                            mma_tf32(r, vh, ph[nt][i][0], ph[nt][i][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[2 * kk + t][nt][e] += r[e];
+                        }
+                    }
+                }
+        }
+    };
+
+    // ---- a row's (or part's) end: the warps' sums meet
+    auto end_row = [&](const Cursor &c, bool whole, int part) {
+        const int h = c.row / passes, first = (c.row % passes) * NT * 8;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float x = l[nt][j];
+                x += __shfl_xor_sync(0xffffffffu, x, 4);
+                x += __shfl_xor_sync(0xffffffffu, x, 8);
+                x += __shfl_xor_sync(0xffffffffu, x, 16);
+                if (g == 0) ml[warp * NT * 8 + nt * 8 + 2 * q4 + j] = make_float2(m[nt][j], x);
+            }
+        __syncthreads();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float f[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < W; ++w) top = fmaxf(top, ml[w * NT * 8 + nt * 8 + 2 * q4 + j].x);
+                f[j] = exp2_fast(m[nt][j] - (top == -INFINITY ? 0.f : top));
+            }
+#pragma unroll
+            for (int r = 0; r < D / kMergeDims; ++r) {
+                float *mine = merge + warp * 8 * (kMergeDims + 4);
+#pragma unroll
+                for (int mt = 0; mt < kMergeDims / 16; ++mt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        // dim of fragment row g + 8 (i / 2) of tile mt: in order for bf16, else two tiles interleave by 4
+                        const int dim = KIND == GDN_BF16 ? 16 * mt + g + 8 * (i >> 1) : 32 * (mt >> 1) + 4 * g + 2 * (mt & 1) + (i >> 1);
+                        mine[(2 * q4 + (i & 1)) * (kMergeDims + 4) + dim] = o[r * (kMergeDims / 16) + mt][nt][i] * f[i & 1];
+                    }
+                __syncthreads();
+                for (int idx = tid; idx < 8 * kMergeDims / 4; idx += C::kThreads) {
+                    const int head = idx / (kMergeDims / 4), d4 = idx % (kMergeDims / 4) * 4, hh = first + nt * 8 + head;
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                    float top = -INFINITY, sum = 0.f;
+#pragma unroll
+                    for (int w = 0; w < W; ++w) {
+                        const float4 y = *(const float4 *)(merge + (w * 8 + head) * (kMergeDims + 4) + d4);
+                        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+                        top = fmaxf(top, ml[w * NT * 8 + nt * 8 + head].x);
+                    }
+                    const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+                    for (int w = 0; w < W; ++w) {
+                        const float2 y = ml[w * NT * 8 + nt * 8 + head];
+                        sum += y.y * exp2_fast(y.x - ref);
+                    }
+                    if (hh >= group) continue;
+                    const int d = r * kMergeDims + d4;
+                    if (whole) {
+                        float inv = sum == 0.f ? 0.f : 1.f / sum;
+                        if constexpr (KIND == GDN_E4M3) inv *= a.c.v_scale ? a.c.v_scale[h] : 1.f;
+                        const int64_t at = (int64_t)c.b * a.Hq + h * group + hh;
+                        if constexpr (KIND == GDN_F32)
+                            *(float4 *)((float *)a.o + at * D + d) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+                        else
+                            *(uint2 *)((__nv_bfloat16 *)a.o + at * D + d) = make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+                        if (d == 0 && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+                    } else {
+                        const int64_t at = (int64_t)part * NT * 8 + nt * 8 + head;
+                        *(float4 *)(ws.o + at * D + d) = x;
+                        if (d == 0) ws.ml[at] = make_float2(top, sum);
+                    }
+                }
+                __syncthreads();
+            }
+        }
+    };
+
+    Cursor ahead = cur;  // the tile whose loads go out next
+    int64_t issued = 0, row_off = find_row(ahead);
+    auto feed = [&](int stage) {
+        if (issued < n) {
+            issue(stage, row_off);
+            if (++issued < n) {
+                ahead.next<TILE>(a, rows);
+                row_off = find_row(ahead);
+            }
+        }
+        cp_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) feed(s);
+    bool open = false, began_here = false;
+    int segment = 0, stage = 0;
+    for (int64_t it = 0; it < n; ++it) {
+        if (!open) {
+            begin_row(cur);
+            open = true;
+            began_here = cur.tile == 0;
+        }
+        cp_wait<STAGES - 2>();
+        __syncwarp();  // every lane's copies into this stage have landed, and the stage before is read
+        feed(stage == 0 ? STAGES - 1 : stage - 1);
+        slice(stage);
+        stage = stage == STAGES - 1 ? 0 : stage + 1;
+        const bool row_ends = cur.tile == cur.tiles - 1;
+        if (row_ends || it == n - 1) {
+            end_row(cur, began_here && row_ends, 2 * cta + (segment > 0));
+            open = false;
+            ++segment;
+        }
+        cur.next<TILE>(a, rows);
+    }
+}
+
+template <gdn_dtype KIND, int D, int NT>
+cudaError_t launch_one(const AttendArgs &a, int64_t most_tiles16, cudaStream_t stream, int *grid_out) {
+    using C = Cfg<KIND, D, NT>;
+    auto kern = paged_decode_kernel<KIND, D, NT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    const int64_t most = (most_tiles16 + C::kWarps - 1) / C::kWarps;  // tiles of a row, were it as long as the table
+    const int group = a.Hq / a.c.Hkv, rows = a.c.Hkv * ((group + NT * 8 - 1) / (NT * 8));
+    const int64_t wave = (int64_t)kSMs * C::kOcc;
+    int64_t ctas = (int64_t)a.B * rows;
+    ctas = ctas >= wave || most >= wave ? wave : min(ctas * most, wave);
+    *grid_out = (int)ctas;
+    kern<<<(unsigned)ctas, C::kThreads, C::kSmem, stream>>>(a);
+    return cudaGetLastError();
+}
+
+// Launches the kernel of one storage type; defined in k_paged_decode_{bf16,e4m3,f32}.cu.
+template <gdn_dtype KIND>
+cudaError_t launch_kind(const AttendArgs &a, int64_t most_tiles16, cudaStream_t stream, int *grid);
+
+template <gdn_dtype KIND>
+cudaError_t dispatch(const AttendArgs &a, int64_t most_tiles16, cudaStream_t stream, int *grid) {
+    const bool one = pass_heads(a.Hq / a.c.Hkv) == 8;
+    switch (a.c.d) {
+        case 64: return one ? launch_one<KIND, 64, 1>(a, most_tiles16, stream, grid) : launch_one<KIND, 64, 2>(a, most_tiles16, stream, grid);
+        case 128: return one ? launch_one<KIND, 128, 1>(a, most_tiles16, stream, grid) : launch_one<KIND, 128, 2>(a, most_tiles16, stream, grid);
+        default: return one ? launch_one<KIND, 256, 1>(a, most_tiles16, stream, grid) : launch_one<KIND, 256, 2>(a, most_tiles16, stream, grid);
+    }
+}
+
+}  // namespace paged
+}  // namespace gdn

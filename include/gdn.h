@@ -373,10 +373,11 @@ GDN_API gdn_status gdn_kv_append(const gdn_kv_cache *cache, int32_t n, gdn_dtype
  *   o[b,h] = sum_j p_j v_j,  p = softmax_j(scale * <q[b,h], k_j>),
  *   lse[b,h] = log sum_j exp(scale * <q[b,h], k_j>)        (lse may be NULL)
  * over the tokens j in [max(0, L - window), L), L = seq_lens[b] (window 0: from
- * 0 on; L is cut at max_pages * page), whose table entry lies in [0, pages).
+ * 0 on; L is cut at max_pages * page, which is at most 2^31 - 128), whose table entry lies in [0, pages).
  * Query head h reads KV head h / (Hq / Hkv).  A request left without a token
  * gets o = 0 and lse = -inf.  What the cache holds outside those tokens is
- * never used, whatever its bits.
+ * never used, whatever its bits; a non-finite value inside them reaches only the
+ * rows and elements that read it (as infinity or NaN).
  * q [B][Hq][d] at b * q_stride_request + h * q_stride_head elements (multiples of
  * 16 bytes); o [B][Hq][d] contiguous; lse [B][Hq] fp32; q and o have the cache's
  * dtype, or GDN_BF16 with a GDN_E4M3 cache.  Row b of the block table starts at

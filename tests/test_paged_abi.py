@@ -93,6 +93,7 @@ def test_decode_refusals(lib):
     for kw in (dict(q=FAKE + 8), dict(o=FAKE + 4), dict(qs=(2047, 128)), dict(table=FAKE + 2), dict(lens=FAKE + 1), dict(lse=FAKE + 2),
                dict(ws=FAKE + 64)):
         assert decode(lib, **kw) == ALIGN, kw
+    assert decode(lib, pages=1 << 27) == UNSUPPORTED   # 2^31 token positions
     c = cache()
     need = lib.gdn_paged_decode_workspace_bytes(c, 16)
     assert need > 0 and decode(lib, nbytes=need - 1) == WORKSPACE and decode(lib, nbytes=need) == DEVICE
