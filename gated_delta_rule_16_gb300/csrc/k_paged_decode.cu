@@ -14,25 +14,21 @@ namespace {
 constexpr int kThreads = 128;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) join_kernel(AttendArgs a, int grid, int heads) {
-    __shared__ float weight[kMaxCtas + 1];
+__global__ void __launch_bounds__(kThreads) join_kernel(AttendArgs a, int heads) {
+    __shared__ float weight[kMaxCtas];
     __shared__ float2 red[kThreads / 32];
     __shared__ float4 acc[kThreads];
-    pdl_wait();
     const WsView ws = ws_view(a.ws, heads);
-    const int64_t total = *ws.total;
-    const int ctas = (int)min((int64_t)grid, total), i = blockIdx.x + 1;
-    if (i >= ctas) return;
-    const int4 at = ws.first[i];
+    const int i = blockIdx.x + 1;
+    pdl_wait();
+    const int4 at = ws.joins[i];
+    const int parts = at.w;
+    if (parts == 0) return;
     const int group = a.Hq / a.c.Hkv, passes = (group + heads - 1) / heads;
     const int h = at.y / passes, hh = at.y % passes * heads + blockIdx.y;
-    if (at.z == 0 || hh >= group) return;  // the row begins with CTA i
-    const int64_t row0 = split_at(total, ctas, i) - at.z, row1 = row0 + at.w, before = split_at(total, ctas, i - 1);
-    if (before > row0) return;             // an edge before this one lies inside the row too
-    // parts: CTA i - 1's (its last row, or its only one), then the first of every CTA up to the row's end
-    const int last = (int)min((int64_t)ctas - 1, (row1 * ctas + total - 1) / total - 1), parts = last - i + 2;
-    const int p0 = 2 * (i - 1) + (before < row0);
-    auto part = [&](int k) { return k == 0 ? p0 : 2 * (i + k - 1); };
+    if (hh >= group) return;
+    // the row's last in CTA i - 1 (or its only one), then the first of each CTA up to the row's end
+    auto part = [&](int k) { return k == 0 ? at.z : 2 * (i + k - 1); };
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     float top = -INFINITY;
@@ -83,11 +79,11 @@ __global__ void __launch_bounds__(kThreads) join_kernel(AttendArgs a, int grid, 
 
 template <typename T>
 cudaError_t join(const AttendArgs &a, int grid, int heads, cudaStream_t stream) {
-    const dim3 g(grid - 1, heads);
+    const dim3 g(grid - 1, min(heads, a.Hq / a.c.Hkv));
     switch (a.c.d) {
-        case 64: return launch_kernel(true, join_kernel<T, 64>, g, kThreads, 0, stream, a, grid, heads);
-        case 128: return launch_kernel(true, join_kernel<T, 128>, g, kThreads, 0, stream, a, grid, heads);
-        default: return launch_kernel(true, join_kernel<T, 256>, g, kThreads, 0, stream, a, grid, heads);
+        case 64: return launch_kernel(true, join_kernel<T, 64>, g, kThreads, 0, stream, a, heads);
+        case 128: return launch_kernel(true, join_kernel<T, 128>, g, kThreads, 0, stream, a, heads);
+        default: return launch_kernel(true, join_kernel<T, 256>, g, kThreads, 0, stream, a, heads);
     }
 }
 
@@ -110,7 +106,8 @@ cudaError_t launch_paged_decode(const AttendArgs &args, cudaStream_t stream) {
     if (a.c.dtype == GDN_BF16) e = paged::launch_kind<GDN_BF16>(a, slices, stream, &grid);
     else if (a.c.dtype == GDN_E4M3) e = paged::launch_kind<GDN_E4M3>(a, slices, stream, &grid);
     else e = paged::launch_kind<GDN_F32>(a, slices, stream, &grid);
-    if (e != cudaSuccess || grid < 2) return e;
+    // a row of one tile (64 tokens; 32 where rows are wider than 512 bytes) cannot be cut
+    if (e != cudaSuccess || grid < 2 || slices <= paged::least_tile(a.c) / 16) return e;
     const int heads = paged::pass_heads(a.Hq / a.c.Hkv);
     return a.c.dtype == GDN_F32 ? paged::join<float>(a, grid, heads, stream) : paged::join<__nv_bfloat16>(a, grid, heads, stream);
 }

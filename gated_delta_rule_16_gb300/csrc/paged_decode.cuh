@@ -10,7 +10,7 @@
 //     16 tokens per warp and the CTAs of one wave get equal runs of tiles.  A row inside one CTA is written out
 //     directly; a row cut by a CTA's edge leaves unnormalised fp32 parts that a second, dependent launch joins in a
 //     fixed order.  Lengths are only known on the GPU, so each CTA finds its run from a scan over them.
-//   - Each warp streams its own 16-token slices of K and V through a ring of shared-memory stages by 16-byte
+//   - Each warp streams its own 16-token slices of K and V through a ring of shared-memory slots by 16-byte
 //     cp.async, whose source address is free per token: any page size, any storage order.  No CTA barrier inside a
 //     row: the warps keep their own maxima and meet at the row's end.
 //   - Products on warp MMAs with the cached tokens as M and 8 query heads as N: S^T = K Q^T (16 tokens x 8 heads) and
@@ -34,28 +34,26 @@ namespace gdn {
 namespace paged {
 
 constexpr int kSMs = 152;
-constexpr int kMaxCtas = 2 * kSMs;   // one wave at two CTAs per SM
-constexpr int kMergeDims = 64;       // output dims joined per round at a row's end
+constexpr int kMaxCtas = 4 * kSMs;   // one wave
 
-// Workspace: tiles in all, each CTA's first tile as {request, row in request, tile in row, tiles of the row}, then two
-// parts per CTA (one where its first row began before it, one where its last row ends after it).
+// Workspace: for each CTA, if it is the second of those that share a row, {request, row in request, first part, parts}
+// of that row (parts 0 otherwise); then two parts per CTA (one where its first row began before it, one where its last row
+// ends after it).
 struct WsView {
-    int64_t *total;
-    int4 *first;
+    int4 *joins;
     float2 *ml;   // [2 * kMaxCtas][heads] {maximum, sum}
     float *o;     // [2 * kMaxCtas][heads][d]
 };
 __host__ __device__ inline WsView ws_view(void *ws, int heads) {
     char *p = (char *)ws;
     WsView w;
-    w.total = (int64_t *)p;
-    w.first = (int4 *)(p + 256);
-    w.ml = (float2 *)(p + 256 + kMaxCtas * sizeof(int4));
-    w.o = (float *)(p + 256 + kMaxCtas * sizeof(int4) + (size_t)2 * kMaxCtas * heads * sizeof(float2));
+    w.joins = (int4 *)p;
+    w.ml = (float2 *)(p + kMaxCtas * sizeof(int4));
+    w.o = (float *)(p + kMaxCtas * sizeof(int4) + (size_t)2 * kMaxCtas * heads * sizeof(float2));
     return w;
 }
 inline size_t ws_bytes(int heads, int d) {
-    return 256 + kMaxCtas * sizeof(int4) + (size_t)2 * kMaxCtas * heads * (sizeof(float2) + (size_t)d * sizeof(float));
+    return kMaxCtas * sizeof(int4) + (size_t)2 * kMaxCtas * heads * (sizeof(float2) + (size_t)d * sizeof(float));
 }
 
 // Query heads per pass over a KV head's tokens: 8 or 16 (a larger group takes several passes, as rows of their own).
@@ -68,17 +66,22 @@ struct Cfg {
     static constexpr int kChunks = kRow / 16;
     static constexpr int kWarps = kRow > 512 ? 2 : 4;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kTile = 16 * kWarps;         // tokens
-    static constexpr int kSlice = 16 * kRow;          // bytes of one warp's K (or V) slice
-    static constexpr int kStage = kWarps * 2 * kSlice;
-    // two CTAs per SM where three stages of a tile fit twice, else one
-    static constexpr int kOcc = kStage <= 32 * 1024 ? 2 : 1;
-    static constexpr int kStages = kStage <= 16 * 1024 ? 6 : 3;
+    static constexpr int kTile = 16 * kWarps;         // tokens (least_tile below)
+    static constexpr int kHalf = 16 * kRow;           // bytes of one warp's K (or V) slice
+    // CTAs per SM and ring slots of half a slice (K or V) per warp.  Warps hide each other's waits, so as many CTAs as
+    // shared memory holds with three slots and the registers allow (8 more heads or 256 dims of output per warp take
+    // twice the registers); what is left deepens the ring.
+    static constexpr int kOcc = kHalf > 8192 && NT == 2 ? 1 : NT == 2 || D == 256 || kHalf > 4096 ? 2 : kHalf > 2048 ? 3 : 4;
+    static constexpr int kSlots = kOcc == 1 ? 6 : kHalf > 4096 ? 3 : kOcc == 2 ? (kHalf > 2048 ? 6 : 8) : kOcc == 3 ? 4 : kHalf > 1024 ? 5 : 8;
+    static constexpr int kRing = kSlots * kHalf;      // per warp
+    static constexpr int kMergeDims = KIND == GDN_F32 && NT == 2 ? 32 : 64;  // output dims joined per round at a row's end
     static constexpr int kMerge = kWarps * 8 * (kMergeDims + 4) * 4;
     static constexpr int kQ = KIND == GDN_F32 ? NT * (D / 8) * 32 * 8 : 0;
-    static constexpr int kSmem = kStages * kStage + kMerge + kWarps * NT * 8 * 8 + kQ + kWarps * kStages * 4;
+    static constexpr int kSmem = kWarps * kRing + kMerge + kWarps * NT * 8 * 8 + kQ + kWarps * kSlots * 4;
     static_assert((kSmem + 1024) * kOcc <= 228 * 1024, "shared memory of an SM");
 };
+
+inline int least_tile(const gdn_kv_cache &c) { return c.dtype == GDN_F32 && c.d == 256 ? 32 : 64; }
 
 // ---- instructions -----------------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -180,7 +183,9 @@ struct Cursor {
     }
 };
 
-__device__ __forceinline__ int64_t split_at(int64_t total, int ctas, int i) { return total * i / ctas; }
+__device__ __forceinline__ int64_t split_at(int64_t total, int ctas, int i) {
+    return total < (1 << 22) ? (int64_t)((uint32_t)total * (uint32_t)i / (uint32_t)ctas) : total * i / ctas;  // ctas < 2^10
+}
 
 template <int THREADS>
 __device__ int64_t block_sum(int64_t x, int64_t *buf) {
@@ -198,16 +203,15 @@ __device__ int64_t block_sum(int64_t x, int64_t *buf) {
 template <gdn_dtype KIND, int D, int NT>
 __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::kOcc) paged_decode_kernel(AttendArgs a) {
     using C = Cfg<KIND, D, NT>;
-    constexpr int W = C::kWarps, STAGES = C::kStages, TILE = C::kTile;
+    constexpr int W = C::kWarps, TILE = C::kTile, kMergeDims = C::kMergeDims;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, q4 = lane & 3;  // fragment row, fragment column pair
-    uint8_t *ring = smem + warp * (STAGES * 2 * C::kSlice);
-    float *merge = (float *)(smem + STAGES * C::kStage);
-    float2 *ml = (float2 *)(smem + STAGES * C::kStage + C::kMerge);
+    float *merge = (float *)(smem + W * C::kRing);
+    float2 *ml = (float2 *)(smem + W * C::kRing + C::kMerge);
     float2 *qs = (float2 *)((uint8_t *)ml + W * NT * 8 * 8);                         // 32-bit storage: q by fragment
-    uint32_t *real = (uint32_t *)((uint8_t *)qs + C::kQ) + warp * STAGES;            // bit t: token t of the slice is real
-    const uint32_t ring_addr = smem_addr(ring);
+    uint32_t *real = (uint32_t *)((uint8_t *)qs + C::kQ) + warp * C::kSlots;         // of the slice in a slot: bit t: token t is real
+    const uint32_t ring = smem_addr(smem) + warp * C::kRing;
     const int group = a.Hq / a.c.Hkv, passes = (group + NT * 8 - 1) / (NT * 8), rows = a.c.Hkv * passes;
     const WsView ws = ws_view(a.ws, NT * 8);
     pdl_trigger();
@@ -224,7 +228,10 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
     }
     const int64_t per_row = block_sum<C::kThreads>(sum, scan), total = per_row * rows;
     const int ctas = (int)min((int64_t)gridDim.x, total), cta = blockIdx.x;
-    if (cta >= ctas) return;
+    if (cta >= ctas) {
+        if (tid == 0) ws.joins[cta] = make_int4(0, 0, 0, 0);
+        return;
+    }
     const int64_t t0 = split_at(total, ctas, cta), n = split_at(total, ctas, cta + 1) - t0;
     {
         // the request whose tiles hold t0: requests lie one after the other, `rows` rows each
@@ -257,43 +264,60 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
             __syncthreads();
             if (before > want) break;
         }
-        if (tid == 0) {
-            ws.first[cta] = found;
-            if (cta == 0) *ws.total = total;
-        }
         cur.b = found.x;
         cur.load<TILE>(a);
         cur.row = found.y;
         cur.tile = found.z;
     }
 
-    // ---- loads: a lane finds the cached row of token (lane & 15) of its warp's slice; -1 where there is none
-    const bool pow2 = (a.c.page & (a.c.page - 1)) == 0;
+    // ---- loads.  Where a page holds whole slices (page a multiple of 16, as slices are aligned to 16 tokens) one table
+    // entry and one address serve the warp: its lanes' pieces lie at fixed distances.  Else lane l finds the row of token
+    // l & 15 and the lanes pass them on.  `off`: of the slice's first token, or of the lane's; `mask`: the real tokens.
+    const bool whole_pages = (a.c.page & 15) == 0, pow2 = (a.c.page & (a.c.page - 1)) == 0;
     const int shift = 31 - __clz(a.c.page);
-    auto find_row = [&](const Cursor &c) -> int64_t {
-        const int t = (c.start & ~15) + c.tile * TILE + warp * 16 + (lane & 15);
-        if (t < c.start || t >= c.len) return -1;
-        const int slot = pow2 ? t >> shift : t / a.c.page;
-        const int id = a.table[c.b * a.table_stride + slot];
-        if (id < 0 || id >= a.c.pages) return -1;
-        return id * a.c.stride_page + (int64_t)(t - slot * a.c.page) * a.c.stride_token + (c.row / passes) * a.c.stride_head;
+    struct Next { int64_t off; uint32_t mask; };
+    auto find = [&](const Cursor &c) -> Next {
+        const int t0 = (c.start & ~15) + c.tile * TILE + warp * 16, t = whole_pages ? t0 : t0 + (lane & 15);
+        const int lo = max(c.start - t0, 0), hi = min(c.len - t0, 16);
+        if (hi <= lo) return {0, 0u};
+        uint32_t mask = (0xffffu >> (16 - hi)) & (0xffffu << lo);
+        int id = -1, cell = 0;
+        if (whole_pages || (mask >> (lane & 15) & 1)) {
+            const int slot = pow2 ? t >> shift : t / a.c.page;
+            cell = t - slot * a.c.page;
+            id = a.table[c.b * a.table_stride + slot];
+        }
+        const bool real = id >= 0 && id < a.c.pages;
+        if (whole_pages) mask = real ? mask : 0u;
+        else mask &= __ballot_sync(0xffffffffu, real);
+        return {real ? id * a.c.stride_page + cell * a.c.stride_token + (c.row / passes) * a.c.stride_head : 0, mask};
     };
     auto swizzled = [](int row, int chunk) -> uint32_t {
         const int x = C::kChunks >= 8 ? row & 7 : (row >> 1) & 3;
         return (uint32_t)(row * C::kRow + ((chunk ^ x) << 4));
     };
-    auto issue = [&](int stage, int64_t row_off) {
-        const uint32_t mask = __ballot_sync(0xffffffffu, row_off >= 0) & 0xffffu;
-        if (lane == 0) real[stage] = mask;
-        const uint32_t dst = ring_addr + stage * (2 * C::kSlice);
+    const int64_t token_bytes = a.c.stride_token * C::kBytes;
+    const int64_t lane_bytes = (lane / C::kChunks) * token_bytes + lane % C::kChunks * 16;
+    auto issue = [&](int slot, const Next &x, const void *cache) {
+        if (lane == 0) real[slot] = x.mask;
+        const uint32_t dst = ring + slot * C::kHalf;
+        if (whole_pages && C::kChunks <= 32) {
+            constexpr int kRows = C::kChunks <= 32 ? 32 / C::kChunks : 1;  // per instruction
+            const char *src = (const char *)cache + (x.off * C::kBytes + lane_bytes);
 #pragma unroll
-        for (int i = 0; i < 16 * C::kChunks / 32; ++i) {
-            const int idx = i * 32 + lane, row = idx / C::kChunks, chunk = idx % C::kChunks;
-            const int64_t off = __shfl_sync(0xffffffffu, row_off, row);
-            const int64_t byte = (off < 0 ? 0 : off) * C::kBytes + chunk * 16;
-            const uint32_t d = dst + swizzled(row, chunk);
-            cp16(d, (const char *)a.c.k + byte, off >= 0);
-            cp16(d + C::kSlice, (const char *)a.c.v + byte, off >= 0);
+            for (int i = 0; i < 16 / kRows; ++i) {
+                const int row = i * kRows + lane / C::kChunks;
+                cp16(dst + swizzled(row, lane % C::kChunks), src, x.mask >> row & 1);
+                src += kRows * token_bytes;
+            }
+        } else {
+#pragma unroll 4
+            for (int i = 0; i < 16 * C::kChunks / 32; ++i) {
+                const int idx = i * 32 + lane, row = idx / C::kChunks, chunk = idx % C::kChunks;
+                const int64_t at = whole_pages ? x.off + row * a.c.stride_token : __shfl_sync(0xffffffffu, x.off, row);
+                const bool have = x.mask >> row & 1;
+                cp16(dst + swizzled(row, chunk), (const char *)cache + (have ? at : 0) * C::kBytes + chunk * 16, have);
+            }
         }
     };
 
@@ -365,13 +389,10 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
         if constexpr (KIND == GDN_F32) __syncthreads();
     };
 
-    // ---- one slice: 16 tokens
-    auto slice = [&](int stage) {
-        const uint32_t mask = real[stage];
-        if (mask == 0) return;
-        const uint32_t kb = ring_addr + stage * (2 * C::kSlice), vb = kb + C::kSlice;
-        const int mrow = lane & 7, mid = lane >> 3;  // ldmatrix: row in matrix, matrix
-        float s[NT][4];
+    // ---- one slice: 16 tokens.  Scores and the running softmax, from the K slice at kb
+    const int mrow = lane & 7, mid = lane >> 3;  // ldmatrix: row in matrix, matrix
+    float s[NT][4];
+    auto scores = [&](uint32_t kb, uint32_t mask) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -451,6 +472,9 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
                     for (int i = 0; i < 4; ++i) o[mt][nt][i] *= f[nt][i & 1];
         }
 
+    };
+    // The weighted sum, from the V slice at vb
+    auto values = [&](uint32_t vb) {
         if constexpr (KIND == GDN_BF16) {
             uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
@@ -613,32 +637,57 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
     };
 
     Cursor ahead = cur;  // the tile whose loads go out next
-    int64_t issued = 0, row_off = find_row(ahead);
-    auto feed = [&](int stage) {
-        if (issued < n) {
-            issue(stage, row_off);
-            if (++issued < n) {
+    int64_t issued = 0;  // halves
+    Next next = find(ahead);
+    int feed_slot = 0;
+    auto feed = [&]() {
+        if (issued < 2 * n) {
+            const bool second = issued & 1;
+            issue(feed_slot, next, second ? a.c.v : a.c.k);
+            if (++issued < 2 * n && second) {
                 ahead.next<TILE>(a, rows);
-                row_off = find_row(ahead);
+                next = find(ahead);
             }
         }
+        feed_slot = feed_slot == C::kSlots - 1 ? 0 : feed_slot + 1;
         cp_commit();
     };
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) feed(s);
+#pragma unroll 1
+    for (int i = 0; i < C::kSlots - 1; ++i) feed();
+    if (tid == 32) {  // beside the first loads
+        // The row that this CTA begins in: it is the second of the row's CTAs if the row began in the one before
+        int4 join = make_int4(cur.b, cur.row, 0, 0);
+        const int64_t row0 = t0 - cur.tile, row1 = row0 + cur.tiles, before = cta > 0 ? split_at(total, ctas, cta - 1) : 0;
+        if (cur.tile > 0 && before <= row0) {
+            // the row's last CTA: the last i with floor(total i / ctas) < row1
+            const int last = min(ctas, total < (1 << 22) ? (int)(((uint32_t)row1 * ctas + (uint32_t)total - 1) / (uint32_t)total)
+                                                         : (int)((row1 * ctas + total - 1) / total)) - 1;
+            join.z = 2 * (cta - 1) + (before < row0);
+            join.w = last - cta + 2;
+        }
+        ws.joins[cta] = join;
+    }
     bool open = false, began_here = false;
-    int segment = 0, stage = 0;
+    int segment = 0, slot = 0;
+    auto arrive = [&]() -> uint32_t {  // at the next half
+        cp_wait<C::kSlots - 2>();
+        __syncwarp();  // every lane's copies into this slot have landed, and the slot before is read
+        feed();
+        const uint32_t at = ring + slot * C::kHalf;
+        slot = slot == C::kSlots - 1 ? 0 : slot + 1;
+        return at;
+    };
     for (int64_t it = 0; it < n; ++it) {
         if (!open) {
             begin_row(cur);
             open = true;
             began_here = cur.tile == 0;
         }
-        cp_wait<STAGES - 2>();
-        __syncwarp();  // every lane's copies into this stage have landed, and the stage before is read
-        feed(stage == 0 ? STAGES - 1 : stage - 1);
-        slice(stage);
-        stage = stage == STAGES - 1 ? 0 : stage + 1;
+        const int k_slot = slot;
+        const uint32_t kb = arrive(), mask = real[k_slot];
+        if (mask) scores(kb, mask);
+        const uint32_t vb = arrive();
+        if (mask) values(vb);
         const bool row_ends = cur.tile == cur.tiles - 1;
         if (row_ends || it == n - 1) {
             end_row(cur, began_here && row_ends, 2 * cta + (segment > 0));
