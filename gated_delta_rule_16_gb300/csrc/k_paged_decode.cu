@@ -106,8 +106,7 @@ cudaError_t launch_paged_decode(const AttendArgs &args, cudaStream_t stream) {
     if (a.c.dtype == GDN_BF16) e = paged::launch_kind<GDN_BF16>(a, slices, stream, &grid);
     else if (a.c.dtype == GDN_E4M3) e = paged::launch_kind<GDN_E4M3>(a, slices, stream, &grid);
     else e = paged::launch_kind<GDN_F32>(a, slices, stream, &grid);
-    // a row of one tile (64 tokens; 32 where rows are wider than 512 bytes) cannot be cut
-    if (e != cudaSuccess || grid < 2 || slices <= paged::least_tile(a.c) / 16) return e;
+    if (e != cudaSuccess || grid < 2 || slices <= paged::tile_of(a.c) / 16) return e;  // a row of one tile cannot be cut
     const int heads = paged::pass_heads(a.Hq / a.c.Hkv);
     return a.c.dtype == GDN_F32 ? paged::join<float>(a, grid, heads, stream) : paged::join<__nv_bfloat16>(a, grid, heads, stream);
 }

@@ -59,15 +59,22 @@ inline size_t ws_bytes(int heads, int d) {
 // Query heads per pass over a KV head's tokens: 8 or 16 (a larger group takes several passes, as rows of their own).
 __host__ __device__ constexpr int pass_heads(int group) { return group <= 8 ? 8 : 16; }
 
+// By the bytes of a cached row: warps per CTA (rows wider than 512 bytes leave room for two warps' rings), and 16-token
+// parts of a warp's slice (narrow rows take two at a time: half the waits, maxima and addresses per token).
+__host__ __device__ constexpr int warps_of(int row) { return row > 512 ? 2 : 4; }
+__host__ __device__ constexpr int sub_slices(int row) { return row <= 128 ? 2 : 1; }
+
 template <gdn_dtype KIND, int D, int NT>
 struct Cfg {
     static constexpr int kBytes = KIND == GDN_BF16 ? 2 : (KIND == GDN_E4M3 ? 1 : 4);
     static constexpr int kRow = D * kBytes;           // bytes of a cached row
     static constexpr int kChunks = kRow / 16;
-    static constexpr int kWarps = kRow > 512 ? 2 : 4;
+    static constexpr int kWarps = warps_of(kRow);
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kTile = 16 * kWarps;         // tokens (least_tile below)
-    static constexpr int kHalf = 16 * kRow;           // bytes of one warp's K (or V) slice
+    static constexpr int kSub = sub_slices(kRow);     // 16-token parts of a slice
+    static constexpr int kTok = 16 * kSub;            // tokens of a warp's slice
+    static constexpr int kTile = kTok * kWarps;       // tokens of a tile
+    static constexpr int kHalf = kTok * kRow;          // bytes of one warp's K (or V) slice
     // CTAs per SM and ring slots of half a slice (K or V) per warp.  Warps hide each other's waits, so as many CTAs as
     // shared memory holds with three slots and the registers allow (8 more heads or 256 dims of output per warp take
     // twice the registers); what is left deepens the ring.
@@ -78,10 +85,14 @@ struct Cfg {
     static constexpr int kMerge = kWarps * 8 * (kMergeDims + 4) * 4;
     static constexpr int kQ = KIND == GDN_F32 ? NT * (D / 8) * 32 * 8 : 0;
     static constexpr int kSmem = kWarps * kRing + kMerge + kWarps * NT * 8 * 8 + kQ + kWarps * kSlots * 4;
+    static_assert(KIND != GDN_F32 || kSub == 1, "the fp32 products take one part");
     static_assert((kSmem + 1024) * kOcc <= 228 * 1024, "shared memory of an SM");
 };
 
-inline int least_tile(const gdn_kv_cache &c) { return c.dtype == GDN_F32 && c.d == 256 ? 32 : 64; }
+inline int tile_of(const gdn_kv_cache &c) {  // Cfg::kTile
+    const int row = c.d * (c.dtype == GDN_BF16 ? 2 : c.dtype == GDN_E4M3 ? 1 : 4);
+    return 16 * sub_slices(row) * warps_of(row);
+}
 
 // ---- instructions -----------------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -203,7 +214,7 @@ __device__ int64_t block_sum(int64_t x, int64_t *buf) {
 template <gdn_dtype KIND, int D, int NT>
 __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::kOcc) paged_decode_kernel(AttendArgs a) {
     using C = Cfg<KIND, D, NT>;
-    constexpr int W = C::kWarps, TILE = C::kTile, kMergeDims = C::kMergeDims;
+    constexpr int W = C::kWarps, TILE = C::kTile, SUB = C::kSub, kMergeDims = C::kMergeDims;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, q4 = lane & 3;  // fragment row, fragment column pair
@@ -270,27 +281,36 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
         cur.tile = found.z;
     }
 
-    // ---- loads.  Where a page holds whole slices (page a multiple of 16, as slices are aligned to 16 tokens) one table
-    // entry and one address serve the warp: its lanes' pieces lie at fixed distances.  Else lane l finds the row of token
-    // l & 15 and the lanes pass them on.  `off`: of the slice's first token, or of the lane's; `mask`: the real tokens.
+    // ---- loads, in parts of 16 tokens.  Where a page holds whole parts (page a multiple of 16, as parts are aligned to 16
+    // tokens) one table entry and one address serve the warp: its lanes' pieces lie at fixed distances.  Else lane l finds
+    // the row of token l & 15 and the lanes pass them on.  `off`: of the part's first token, or of the lane's; `mask`: the
+    // real tokens of the slice.
     const bool whole_pages = (a.c.page & 15) == 0, pow2 = (a.c.page & (a.c.page - 1)) == 0;
     const int shift = 31 - __clz(a.c.page);
-    struct Next { int64_t off; uint32_t mask; };
+    struct Next { int64_t off[SUB]; uint32_t mask; };
     auto find = [&](const Cursor &c) -> Next {
-        const int t0 = (c.start & ~15) + c.tile * TILE + warp * 16, t = whole_pages ? t0 : t0 + (lane & 15);
-        const int lo = max(c.start - t0, 0), hi = min(c.len - t0, 16);
-        if (hi <= lo) return {0, 0u};
-        uint32_t mask = (0xffffu >> (16 - hi)) & (0xffffu << lo);
-        int id = -1, cell = 0;
-        if (whole_pages || (mask >> (lane & 15) & 1)) {
-            const int slot = pow2 ? t >> shift : t / a.c.page;
-            cell = t - slot * a.c.page;
-            id = a.table[c.b * a.table_stride + slot];
+        Next x;
+        x.mask = 0u;
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+            const int t0 = (c.start & ~15) + c.tile * TILE + warp * C::kTok + 16 * u, t = whole_pages ? t0 : t0 + (lane & 15);
+            const int lo = max(c.start - t0, 0), hi = min(c.len - t0, 16);
+            x.off[u] = 0;
+            if (hi <= lo) continue;
+            uint32_t mask = (0xffffu >> (16 - hi)) & (0xffffu << lo);
+            int id = -1, cell = 0;
+            if (whole_pages || (mask >> (lane & 15) & 1)) {
+                const int slot = pow2 ? t >> shift : t / a.c.page;
+                cell = t - slot * a.c.page;
+                id = a.table[c.b * a.table_stride + slot];
+            }
+            const bool real = id >= 0 && id < a.c.pages;
+            if (whole_pages) mask = real ? mask : 0u;
+            else mask &= __ballot_sync(0xffffffffu, real);
+            if (real) x.off[u] = id * a.c.stride_page + cell * a.c.stride_token + (c.row / passes) * a.c.stride_head;
+            x.mask |= mask << (16 * u);
         }
-        const bool real = id >= 0 && id < a.c.pages;
-        if (whole_pages) mask = real ? mask : 0u;
-        else mask &= __ballot_sync(0xffffffffu, real);
-        return {real ? id * a.c.stride_page + cell * a.c.stride_token + (c.row / passes) * a.c.stride_head : 0, mask};
+        return x;
     };
     auto swizzled = [](int row, int chunk) -> uint32_t {
         const int x = C::kChunks >= 8 ? row & 7 : (row >> 1) & 3;
@@ -300,23 +320,26 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
     const int64_t lane_bytes = (lane / C::kChunks) * token_bytes + lane % C::kChunks * 16;
     auto issue = [&](int slot, const Next &x, const void *cache) {
         if (lane == 0) real[slot] = x.mask;
-        const uint32_t dst = ring + slot * C::kHalf;
-        if (whole_pages && C::kChunks <= 32) {
-            constexpr int kRows = C::kChunks <= 32 ? 32 / C::kChunks : 1;  // per instruction
-            const char *src = (const char *)cache + (x.off * C::kBytes + lane_bytes);
 #pragma unroll
-            for (int i = 0; i < 16 / kRows; ++i) {
-                const int row = i * kRows + lane / C::kChunks;
-                cp16(dst + swizzled(row, lane % C::kChunks), src, x.mask >> row & 1);
-                src += kRows * token_bytes;
-            }
-        } else {
+        for (int u = 0; u < SUB; ++u) {
+            const uint32_t dst = ring + slot * C::kHalf + u * (16 * C::kRow), mask = x.mask >> (16 * u);
+            if (whole_pages && C::kChunks <= 32) {
+                constexpr int kRows = C::kChunks <= 32 ? 32 / C::kChunks : 1;  // per instruction
+                const char *src = (const char *)cache + (x.off[u] * C::kBytes + lane_bytes);
+#pragma unroll
+                for (int i = 0; i < 16 / kRows; ++i) {
+                    const int row = i * kRows + lane / C::kChunks;
+                    cp16(dst + swizzled(row, lane % C::kChunks), src, mask >> row & 1);
+                    src += kRows * token_bytes;
+                }
+            } else {
 #pragma unroll 4
-            for (int i = 0; i < 16 * C::kChunks / 32; ++i) {
-                const int idx = i * 32 + lane, row = idx / C::kChunks, chunk = idx % C::kChunks;
-                const int64_t at = whole_pages ? x.off + row * a.c.stride_token : __shfl_sync(0xffffffffu, x.off, row);
-                const bool have = x.mask >> row & 1;
-                cp16(dst + swizzled(row, chunk), (const char *)cache + (have ? at : 0) * C::kBytes + chunk * 16, have);
+                for (int i = 0; i < 16 * C::kChunks / 32; ++i) {
+                    const int idx = i * 32 + lane, row = idx / C::kChunks, chunk = idx % C::kChunks;
+                    const int64_t at = whole_pages ? x.off[u] + row * a.c.stride_token : __shfl_sync(0xffffffffu, x.off[u], row);
+                    const bool have = mask >> row & 1;
+                    cp16(dst + swizzled(row, chunk), (const char *)cache + (have ? at : 0) * C::kBytes + chunk * 16, have);
+                }
             }
         }
     };
@@ -389,39 +412,47 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
         if constexpr (KIND == GDN_F32) __syncthreads();
     };
 
-    // ---- one slice: 16 tokens.  Scores and the running softmax, from the K slice at kb
+    // ---- one slice.  Scores and the running softmax, from the K slice at kb
     const int mrow = lane & 7, mid = lane >> 3;  // ldmatrix: row in matrix, matrix
-    float s[NT][4];
+    float p[SUB][NT][4];  // scores, then weights
     auto scores = [&](uint32_t kb, uint32_t mask) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int u = 0; u < SUB; ++u)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) p[u][nt][i] = 0.f;
         if constexpr (KIND == GDN_BF16) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                uint32_t k[4];
-                ldsm4(k, kb + swizzled(mrow + (mid & 1) * 8, 2 * kk + (mid >> 1)));
+            for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma_bf16(s[nt], k, qf[kk][nt][0], qf[kk][nt][1]);
+            for (int u = 0; u < SUB; ++u) {
+                uint32_t k[4];
+                ldsm4(k, kb + u * (16 * C::kRow) + swizzled(mrow + (mid & 1) * 8, 2 * kk + (mid >> 1)));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma_bf16(p[u][nt], k, qf[kk][nt][0], qf[kk][nt][1]);
             }
         } else if constexpr (KIND == GDN_E4M3) {
 #pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk) {
+            for (int kk = 0; kk < D / 32; ++kk)
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
                 uint32_t k[4];  // rows 0-7 and 8-15 of one 16-byte piece, then of the next
-                ldsm4(k, kb + swizzled(mrow + (mid & 1) * 8, 2 * kk + (mid >> 1)));
+                ldsm4(k, kb + u * (16 * C::kRow) + swizzled(mrow + (mid & 1) * 8, 2 * kk + (mid >> 1)));
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const uint32_t a0 = f16_lo(k[2 * i]), a1 = f16_lo(k[2 * i + 1]), a2 = f16_hi(k[2 * i]), a3 = f16_hi(k[2 * i + 1]);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt], a0, a1, a2, a3, qf[2 * kk + i][nt][0], qf[2 * kk + i][nt][1]);
+                    for (int nt = 0; nt < NT; ++nt) mma_f16(p[u][nt], a0, a1, a2, a3, qf[2 * kk + i][nt][0], qf[2 * kk + i][nt][1]);
                 }
             }
         } else {
 #pragma unroll
-            for (int kk = 0; kk < D / 8; ++kk) {
+            for (int kk = 0; kk < D / 8; ++kk)
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
                 uint32_t k[4], kh[4], kl[4];
-                ldsm4(k, kb + swizzled(mrow + (mid & 1) * 8, 2 * kk + (mid >> 1)));
+                ldsm4(k, kb + u * (16 * C::kRow) + swizzled(mrow + (mid & 1) * 8, 2 * kk + (mid >> 1)));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) split_tf32(k[i], kh[i], kl[i]);
 #pragma unroll
@@ -435,22 +466,27 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
                     mma_tf32(t, kh, l0, l1);
                     mma_tf32(t, kh, h0, h1);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) s[nt][i] += t[i];
+                    for (int i = 0; i < 4; ++i) p[u][nt][i] += t[i];
                 }
             }
         }
 
-        // running softmax; token g (rows 0-7) in s[.][0..1], token g + 8 in s[.][2..3], heads 2 q4 and 2 q4 + 1
-        const bool real0 = mask >> g & 1, real1 = mask >> (g + 8) & 1;
+        // running softmax; token g of a part in p[u][.][0..1], token g + 8 in p[u][.][2..3], heads 2 q4 and 2 q4 + 1
         bool moved = false;
         float f[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float x0 = real0 ? s[nt][j] * z_scale[nt][j] : -INFINITY;
-                const float x1 = real1 ? s[nt][2 + j] * z_scale[nt][j] : -INFINITY;
-                float top = fmaxf(x0, x1);
+                float top = -INFINITY;
+#pragma unroll
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float &x = p[u][nt][2 * i + j];
+                        x = mask >> (16 * u + 8 * i + g) & 1 ? x * z_scale[nt][j] : -INFINITY;
+                        top = fmaxf(top, x);
+                    }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -459,9 +495,16 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
                 moved |= top != m[nt][j];
                 f[nt][j] = exp2_fast(m[nt][j] - ref);
                 m[nt][j] = top;
-                s[nt][j] = exp2_fast(x0 - ref);
-                s[nt][2 + j] = exp2_fast(x1 - ref);
-                l[nt][j] = l[nt][j] * f[nt][j] + (s[nt][j] + s[nt][2 + j]);
+                float sum = 0.f;
+#pragma unroll
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float &x = p[u][nt][2 * i + j];
+                        x = exp2_fast(x - ref);
+                        sum += x;
+                    }
+                l[nt][j] = l[nt][j] * f[nt][j] + sum;
             }
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -476,53 +519,61 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
     // The weighted sum, from the V slice at vb
     auto values = [&](uint32_t vb) {
         if constexpr (KIND == GDN_BF16) {
-            uint32_t hi[NT][2], lo[NT][2];
+            uint32_t hi[SUB][NT][2], lo[SUB][NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int u = 0; u < SUB; ++u)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float p0 = s[nt][2 * i], p1 = s[nt][2 * i + 1];
-                    // cut, not rounded, so that both terms of a weight are positive: an infinite value stays infinite
-                    const uint32_t h = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
-                    const uint32_t r = pack_bf16(fmaxf(p0 - __uint_as_float(h << 16), 1.17549435e-38f),
-                                                 fmaxf(p1 - __uint_as_float(h & 0xffff0000u), 1.17549435e-38f));
-                    hi[nt][i] = transpose8x8(h);
-                    lo[nt][i] = transpose8x8(r);
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float p0 = p[u][nt][2 * i], p1 = p[u][nt][2 * i + 1];
+                        // cut, not rounded, so that both terms of a weight are positive: an infinite value stays infinite
+                        const uint32_t h = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+                        const uint32_t r = pack_bf16(fmaxf(p0 - __uint_as_float(h << 16), 1.17549435e-38f),
+                                                     fmaxf(p1 - __uint_as_float(h & 0xffff0000u), 1.17549435e-38f));
+                        hi[u][nt][i] = transpose8x8(h);
+                        lo[u][nt][i] = transpose8x8(r);
+                    }
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
+                    uint32_t v[4];
+                    ldsm4t(v, vb + u * (16 * C::kRow) + swizzled(mrow + (mid >> 1) * 8, 2 * mt + (mid & 1)));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_bf16(o[mt][nt], v, lo[u][nt][0], lo[u][nt][1]);
+                        mma_bf16(o[mt][nt], v, hi[u][nt][0], hi[u][nt][1]);
+                    }
                 }
-#pragma unroll
-            for (int mt = 0; mt < D / 16; ++mt) {
-                uint32_t v[4];
-                ldsm4t(v, vb + swizzled(mrow + (mid >> 1) * 8, 2 * mt + (mid & 1)));
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma_bf16(o[mt][nt], v, lo[nt][0], lo[nt][1]);
-                    mma_bf16(o[mt][nt], v, hi[nt][0], hi[nt][1]);
-                }
-            }
         } else if constexpr (KIND == GDN_E4M3) {
-            uint32_t p[NT][2];
+            uint32_t b[SUB][NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int u = 0; u < SUB; ++u)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) p[nt][i] = transpose8x8(pack_f16(s[nt][2 * i], s[nt][2 * i + 1]));
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) b[u][nt][i] = transpose8x8(pack_f16(p[u][nt][2 * i], p[u][nt][2 * i + 1]));
             // a lane's 4 bytes of a token are dims 4 g .. 4 g + 3 of a block of 32; bytes of neighbouring tokens are
             // paired into the A fragments of two 16-row tiles whose rows g, g + 8 are dims 4 g, 4 g + 1 and 4 g + 2, 4 g + 3
 #pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk) {
-                uint32_t w[4];
+            for (int kk = 0; kk < D / 32; ++kk)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    w[i] = lds32(vb + swizzled(2 * q4 + (i & 1) + (i >> 1) * 8, 2 * kk + (g >> 2)) + (g & 3) * 4);
-                const uint32_t t01 = __byte_perm(w[0], w[1], 0x5140), t23 = __byte_perm(w[2], w[3], 0x5140);
-                const uint32_t u01 = __byte_perm(w[0], w[1], 0x7362), u23 = __byte_perm(w[2], w[3], 0x7362);
-                const uint32_t ta[4] = {f16_lo(t01), f16_hi(t01), f16_lo(t23), f16_hi(t23)};
-                const uint32_t ua[4] = {f16_lo(u01), f16_hi(u01), f16_lo(u23), f16_hi(u23)};
+                for (int u = 0; u < SUB; ++u) {
+                    uint32_t w[4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma_f16(o[2 * kk][nt], ta[0], ta[1], ta[2], ta[3], p[nt][0], p[nt][1]);
-                    mma_f16(o[2 * kk + 1][nt], ua[0], ua[1], ua[2], ua[3], p[nt][0], p[nt][1]);
+                    for (int i = 0; i < 4; ++i)
+                        w[i] = lds32(vb + u * (16 * C::kRow) + swizzled(2 * q4 + (i & 1) + (i >> 1) * 8, 2 * kk + (g >> 2)) + (g & 3) * 4);
+                    const uint32_t t01 = __byte_perm(w[0], w[1], 0x5140), t23 = __byte_perm(w[2], w[3], 0x5140);
+                    const uint32_t u01 = __byte_perm(w[0], w[1], 0x7362), u23 = __byte_perm(w[2], w[3], 0x7362);
+                    const uint32_t ta[4] = {f16_lo(t01), f16_hi(t01), f16_lo(t23), f16_hi(t23)};
+                    const uint32_t ua[4] = {f16_lo(u01), f16_hi(u01), f16_lo(u23), f16_hi(u23)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_f16(o[2 * kk][nt], ta[0], ta[1], ta[2], ta[3], b[u][nt][0], b[u][nt][1]);
+                        mma_f16(o[2 * kk + 1][nt], ua[0], ua[1], ua[2], ua[3], b[u][nt][0], b[u][nt][1]);
+                    }
                 }
-            }
         } else {
             // k index q4 of step i is token 8 i + 2 q4, k index q4 + 4 is token 8 i + 2 q4 + 1; rows as for 8 bits
             uint32_t ph[NT][2][2], pl[NT][2][2];
@@ -530,7 +581,7 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint32_t x = __float_as_uint(s[nt][2 * i]), y = __float_as_uint(s[nt][2 * i + 1]);
+                    const uint32_t x = __float_as_uint(p[0][nt][2 * i]), y = __float_as_uint(p[0][nt][2 * i + 1]);
                     const uint32_t top = transpose8x8(__byte_perm(x, y, 0x7632)), low = transpose8x8(__byte_perm(x, y, 0x5410));
                     split_tf32(__byte_perm(low, top, 0x5410), ph[nt][i][0], pl[nt][i][0]);
                     split_tf32(__byte_perm(low, top, 0x7632), ph[nt][i][1], pl[nt][i][1]);
@@ -704,7 +755,7 @@ cudaError_t launch_one(const AttendArgs &a, int64_t most_tiles16, cudaStream_t s
     auto kern = paged_decode_kernel<KIND, D, NT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    const int64_t most = (most_tiles16 + C::kWarps - 1) / C::kWarps;  // tiles of a row, were it as long as the table
+    const int64_t most = (most_tiles16 + C::kSub * C::kWarps - 1) / (C::kSub * C::kWarps);  // tiles of a row, were it as long as the table
     const int group = a.Hq / a.c.Hkv, rows = a.c.Hkv * ((group + NT * 8 - 1) / (NT * 8));
     const int64_t wave = (int64_t)kSMs * C::kOcc;
     int64_t ctas = (int64_t)a.B * rows;
