@@ -2,88 +2,101 @@
 // rows that were cut between CTAs (paged_decode.cuh has the main kernel).
 //
 // A row cut into parts (m_i, l_i, o_i) is o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i, M = max m_i.  One
-// CTA per (CTA edge, query head): the first edge inside a row joins all of the row's parts, in the order of
-// the tokens, so the result does not depend on which part was done first.  At most 2 x 304 parts of up to 16
-// heads, read back from L2: latency, hidden in part by a programmatic dependent launch.
+// CTA per (cut row, query head), in the order of the tokens, so the result does not depend on which part was done
+// first.  Latency is all there is to it: the parts lie in L2, so a thread has its first four loads of outputs in
+// flight beside those of maxima and sums.  With 8 CTAs or more to a row (few long rows, up to 608 parts each) there is an
+// entry per row and 512 threads to each; else one per CTA edge, of a few parts, and 128 threads.
 #include "paged_decode.cuh"
 
 namespace gdn {
 namespace paged {
 namespace {
 
-constexpr int kThreads = 128;
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) join_kernel(AttendArgs a, int heads) {
-    __shared__ float weight[kMaxCtas];
-    __shared__ float2 red[kThreads / 32];
-    __shared__ float4 acc[kThreads];
+template <typename T, int D, int THREADS>
+__global__ void __launch_bounds__(THREADS) join_kernel(AttendArgs a, int heads) {
+    constexpr int kLanes = D / 4, kGroups = THREADS / kLanes, kFirst = 4;
+    __shared__ float2 ml[kMaxCtas];
+    __shared__ float2 red[THREADS / 32];
+    __shared__ float4 acc[THREADS];
     const WsView ws = ws_view(a.ws, heads);
-    const int i = blockIdx.x + 1;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
-    const int4 at = ws.joins[i];
+    const int4 at = ws.joins[blockIdx.x];
     const int parts = at.w;
     if (parts == 0) return;
     const int group = a.Hq / a.c.Hkv, passes = (group + heads - 1) / heads;
     const int h = at.y / passes, hh = at.y % passes * heads + blockIdx.y;
     if (hh >= group) return;
-    // the row's last in CTA i - 1 (or its only one), then the first of each CTA up to the row's end
-    auto part = [&](int k) { return k == 0 ? at.z : 2 * (i + k - 1); };
-
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // the row's last in its first CTA (or that CTA's only one), then the first of each CTA up to the row's end
+    auto part = [&](int k) { return (int64_t)(k == 0 ? at.z : 2 * ((at.z >> 1) + k)) * heads + blockIdx.y; };
+    const int own = tid / kLanes, d4 = tid % kLanes * 4;
+    float4 y[kFirst];
+#pragma unroll
+    for (int e = 0; e < kFirst; ++e)
+        if (own + e * kGroups < parts) y[e] = *(const float4 *)(ws.o + part(own + e * kGroups) * D + d4);
     float top = -INFINITY;
-    for (int k = tid; k < parts; k += kThreads) top = fmaxf(top, ws.ml[(int64_t)part(k) * heads + blockIdx.y].x);
+    for (int k = tid; k < parts; k += THREADS) {
+        ml[k] = ws.ml[part(k)];
+        top = fmaxf(top, ml[k].x);
+    }
+#pragma unroll
     for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
     if (lane == 0) red[warp].x = top;
     __syncthreads();
-    for (int w = 0; w < kThreads / 32; ++w) top = fmaxf(top, red[w].x);
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) top = fmaxf(top, red[w].x);
     const float ref = top == -INFINITY ? 0.f : top;
     float sum = 0.f;
-    for (int k = tid; k < parts; k += kThreads) {
-        const float2 x = ws.ml[(int64_t)part(k) * heads + blockIdx.y];
-        const float f = exp2_fast(x.x - ref);
-        weight[k] = f;
-        sum += f * x.y;
-    }
+    for (int k = tid; k < parts; k += THREADS) sum += exp2_fast(ml[k].x - ref) * ml[k].y;
+#pragma unroll
     for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     if (lane == 0) red[warp].y = sum;
-    __syncthreads();
-    sum = 0.f;
-    for (int w = 0; w < kThreads / 32; ++w) sum += red[w].y;
 
-    constexpr int kLanes = D / 4, kGroups = kThreads / kLanes;
-    const int d4 = tid % kLanes * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](int k, const float4 &z) {
+        const float f = exp2_fast(ml[k].x - ref);
+        x.x += f * z.x, x.y += f * z.y, x.z += f * z.z, x.w += f * z.w;
+    };
+#pragma unroll
+    for (int e = 0; e < kFirst; ++e)
+        if (own + e * kGroups < parts) add(own + e * kGroups, y[e]);
 #pragma unroll 4
-    for (int k = tid / kLanes; k < parts; k += kGroups) {
-        const float4 y = *(const float4 *)(ws.o + ((int64_t)part(k) * heads + blockIdx.y) * D + d4);
-        const float f = weight[k];
-        x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w;
-    }
+    for (int k = own + kFirst * kGroups; k < parts; k += kGroups) add(k, *(const float4 *)(ws.o + part(k) * D + d4));
     acc[tid] = x;
     __syncthreads();
     if (tid >= kLanes) return;
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) sum += red[w].y;
+#pragma unroll
     for (int gr = 1; gr < kGroups; ++gr) {
-        const float4 y = acc[gr * kLanes + tid];
-        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+        const float4 z = acc[gr * kLanes + tid];
+        x.x += z.x, x.y += z.y, x.z += z.z, x.w += z.w;
     }
     float inv = sum == 0.f ? 0.f : 1.f / sum;
     if (a.c.v_scale) inv *= a.c.v_scale[h];
     const int64_t out = (int64_t)at.x * a.Hq + h * group + hh;
-    io<T>::st((T *)a.o + out * D + d4, x.x * inv);
-    io<T>::st((T *)a.o + out * D + d4 + 1, x.y * inv);
-    io<T>::st((T *)a.o + out * D + d4 + 2, x.z * inv);
-    io<T>::st((T *)a.o + out * D + d4 + 3, x.w * inv);
+    if constexpr (sizeof(T) == 4)
+        *(float4 *)((float *)a.o + out * D + d4) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    else
+        *(uint2 *)((__nv_bfloat16 *)a.o + out * D + d4) = make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
     if (tid == 0 && a.lse) a.lse[out] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
 }
 
+template <typename T, int D>
+cudaError_t join(const AttendArgs &a, int grid, int heads, cudaStream_t stream) {
+    const int group = a.Hq / a.c.Hkv;
+    const int64_t rows = (int64_t)a.B * a.c.Hkv * ((group + heads - 1) / heads);
+    if (join_by_row(rows, grid))
+        return launch_kernel(true, join_kernel<T, D, 512>, dim3((unsigned)rows, min(heads, group)), 512, 0, stream, a, heads);
+    return launch_kernel(true, join_kernel<T, D, 128>, dim3(grid - 1, min(heads, group)), 128, 0, stream, a, heads);
+}
 template <typename T>
 cudaError_t join(const AttendArgs &a, int grid, int heads, cudaStream_t stream) {
-    const dim3 g(grid - 1, min(heads, a.Hq / a.c.Hkv));
     switch (a.c.d) {
-        case 64: return launch_kernel(true, join_kernel<T, 64>, g, kThreads, 0, stream, a, heads);
-        case 128: return launch_kernel(true, join_kernel<T, 128>, g, kThreads, 0, stream, a, heads);
-        default: return launch_kernel(true, join_kernel<T, 256>, g, kThreads, 0, stream, a, heads);
+        case 64: return join<T, 64>(a, grid, heads, stream);
+        case 128: return join<T, 128>(a, grid, heads, stream);
+        default: return join<T, 256>(a, grid, heads, stream);
     }
 }
 

@@ -36,9 +36,9 @@ namespace paged {
 constexpr int kSMs = 152;
 constexpr int kMaxCtas = 4 * kSMs;   // one wave
 
-// Workspace: for each CTA, if it is the second of those that share a row, {request, row in request, first part, parts}
-// of that row (parts 0 otherwise); then two parts per CTA (one where its first row began before it, one where its last row
-// ends after it).
+// Workspace.  A row cut between CTAs is described by one entry {request, row in request, first part, parts}: entry r of row
+// r = request * rows + row if rows are few (join_by_row; parts 0: not cut), else entry i - 1 of the
+// CTA i that is the second of the row's.  Then two parts per CTA: 2 i of CTA i's first row, 2 i + 1 of its last.
 struct WsView {
     int4 *joins;
     float2 *ml;   // [2 * kMaxCtas][heads] {maximum, sum}
@@ -55,6 +55,8 @@ __host__ __device__ inline WsView ws_view(void *ws, int heads) {
 inline size_t ws_bytes(int heads, int d) {
     return kMaxCtas * sizeof(int4) + (size_t)2 * kMaxCtas * heads * (sizeof(float2) + (size_t)d * sizeof(float));
 }
+
+inline bool join_by_row(int64_t rows, int grid) { return rows * 8 <= grid; }
 
 // Query heads per pass over a KV head's tokens: 8 or 16 (a larger group takes several passes, as rows of their own).
 __host__ __device__ constexpr int pass_heads(int group) { return group <= 8 ? 8 : 16; }
@@ -212,7 +214,7 @@ __device__ int64_t block_sum(int64_t x, int64_t *buf) {
 }
 
 template <gdn_dtype KIND, int D, int NT>
-__global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::kOcc) paged_decode_kernel(AttendArgs a) {
+__global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::kOcc) paged_decode_kernel(AttendArgs a, bool by_row) {
     using C = Cfg<KIND, D, NT>;
     constexpr int W = C::kWarps, TILE = C::kTile, SUB = C::kSub, kMergeDims = C::kMergeDims;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -240,7 +242,7 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
     const int64_t per_row = block_sum<C::kThreads>(sum, scan), total = per_row * rows;
     const int ctas = (int)min((int64_t)gridDim.x, total), cta = blockIdx.x;
     if (cta >= ctas) {
-        if (tid == 0) ws.joins[cta] = make_int4(0, 0, 0, 0);
+        if (tid == 0 && !by_row) ws.joins[cta - 1] = make_int4(0, 0, 0, 0);
         return;
     }
     const int64_t t0 = split_at(total, ctas, cta), n = split_at(total, ctas, cta + 1) - t0;
@@ -705,18 +707,15 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
     };
 #pragma unroll 1
     for (int i = 0; i < C::kSlots - 1; ++i) feed();
-    if (tid == 32) {  // beside the first loads
-        // The row that this CTA begins in: it is the second of the row's CTAs if the row began in the one before
-        int4 join = make_int4(cur.b, cur.row, 0, 0);
-        const int64_t row0 = t0 - cur.tile, row1 = row0 + cur.tiles, before = cta > 0 ? split_at(total, ctas, cta - 1) : 0;
-        if (cur.tile > 0 && before <= row0) {
-            // the row's last CTA: the last i with floor(total i / ctas) < row1
-            const int last = min(ctas, total < (1 << 22) ? (int)(((uint32_t)row1 * ctas + (uint32_t)total - 1) / (uint32_t)total)
-                                                         : (int)((row1 * ctas + total - 1) / total)) - 1;
-            join.z = 2 * (cta - 1) + (before < row0);
-            join.w = last - cta + 2;
-        }
-        ws.joins[cta] = join;
+    // the number of CTAs that a row's tiles [t0, t1) are spread over, if its first is in CTA i
+    auto spread = [&](int i, int64_t t1) {  // its last CTA: the last j with floor(total j / ctas) < t1
+        const int64_t j = total < (1 << 22) ? ((uint32_t)t1 * (uint32_t)ctas + (uint32_t)total - 1) / (uint32_t)total : (t1 * ctas + total - 1) / total;
+        return min(ctas, (int)j) - i;
+    };
+    if (tid == 32 && !by_row && cta > 0) {  // beside the first loads
+        const int64_t row0 = t0 - cur.tile, before = split_at(total, ctas, cta - 1);
+        const bool second = cur.tile > 0 && before <= row0;
+        ws.joins[cta - 1] = make_int4(cur.b, cur.row, 2 * (cta - 1) + (before < row0), second ? spread(cta - 1, row0 + cur.tiles) : 0);
     }
     bool open = false, began_here = false;
     int segment = 0, slot = 0;
@@ -733,6 +732,10 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
             begin_row(cur);
             open = true;
             began_here = cur.tile == 0;
+            if (by_row && began_here && tid == 32) {
+                const int parts = n - it < cur.tiles ? spread(cta, t0 + it + cur.tiles) : 0;
+                ws.joins[cur.b * rows + cur.row] = make_int4(cur.b, cur.row, 2 * cta + (segment > 0), parts);
+            }
         }
         const int k_slot = slot;
         const uint32_t kb = arrive(), mask = real[k_slot];
@@ -761,7 +764,7 @@ cudaError_t launch_one(const AttendArgs &a, int64_t most_tiles16, cudaStream_t s
     int64_t ctas = (int64_t)a.B * rows;
     ctas = ctas >= wave || most >= wave ? wave : min(ctas * most, wave);
     *grid_out = (int)ctas;
-    kern<<<(unsigned)ctas, C::kThreads, C::kSmem, stream>>>(a);
+    kern<<<(unsigned)ctas, C::kThreads, C::kSmem, stream>>>(a, join_by_row((int64_t)a.B * rows, (int)ctas));
     return cudaGetLastError();
 }
 
