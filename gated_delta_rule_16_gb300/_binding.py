@@ -28,7 +28,7 @@ EXPORTS = ("gdn_workspace_bytes", "gdn_select_events", "gdn_events_status", "gdn
            "gdn_prefill_host", "gdn_prefill_host_workspace_bytes", "gdn_decode_step", "gdn_prefill_ex",
            "gdn_workspace_bytes_ex", "gdn_events_bytes", "gdn_events_carve", "gdn_noalloc_status",
            "gdn_select_events_gamma", "gdn_page_tables", "gdn_page_tables_status", "gdn_kv_append",
-           "gdn_paged_decode", "gdn_paged_decode_workspace_bytes", "gdn_sample", "gdn_sample_workspace_bytes")
+           "gdn_paged_decode", "gdn_paged_decode_workspace_bytes", "gdn_sample")
 STAGES = ("select", "prefix", "intra", "wbuild", "scan_runs", "scan_chain", "scan", "output", "selector")
 
 
@@ -137,9 +137,7 @@ def load(path: str | None = None):
             lib.gdn_paged_decode.argtypes = [kvp, i32, i32, i32, vp, i64, i64, vp, i64, i32, vp, i32, ctypes.c_float,
                                              vp, vp, vp, sz, vp]
             lib.gdn_paged_decode.restype = i32
-            lib.gdn_sample_workspace_bytes.argtypes = [i32, i32]
-            lib.gdn_sample_workspace_bytes.restype = sz
-            lib.gdn_sample.argtypes = [i32, i32, i32, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+            lib.gdn_sample.argtypes = [i32, i32, i32, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp]
             lib.gdn_sample.restype = i32
             lib.gdn_version.argtypes = []
             lib.gdn_version.restype = ctypes.c_int32

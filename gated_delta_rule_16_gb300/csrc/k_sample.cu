@@ -761,8 +761,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
 
 }  // namespace
 
-size_t sample_workspace_bytes(int, int) { return 0; }
-
 cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream) {
     // CTAs per row: double while all rows' CTAs fit the GPU at once (152 SMs, two CTAs each) and a CTA has 4096 tokens
     // left.  Past one wave it costs: 256 rows of 100003 with top_k 50 and top_p 0.9 take 43 us on one CTA each, 59 on

@@ -51,14 +51,12 @@ struct SampleArgs {
     const int32_t *top_k;                      // may be NULL
     int32_t *tokens;
     float *logprobs;  // may be NULL
-    void *ws;
 };
 
 cudaError_t launch_page_tables(const TablesArgs &a, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream);
 size_t paged_decode_workspace_bytes(const gdn_kv_cache &c, int Hq);
 cudaError_t launch_paged_decode(const AttendArgs &a, cudaStream_t stream);
-size_t sample_workspace_bytes(int B, int V);
 cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream);
 
 }  // namespace gdn

@@ -127,28 +127,21 @@ gdn_status gdn_paged_decode(const gdn_kv_cache *cache, int32_t B, int32_t Hq, gd
     return launch_paged_decode(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
-size_t gdn_sample_workspace_bytes(int32_t B, int32_t V) {
-    if (B < 0 || V <= 0) return 0;
-    return sample_workspace_bytes(B, V) + kWsAlign;
-}
-
 gdn_status gdn_sample(int32_t B, int32_t V, gdn_dtype dtype, const void *logits, int64_t logits_stride,
                       const float *noise, int64_t noise_stride, const float *temperature, const int32_t *top_k,
-                      const float *top_p, const float *min_p, int32_t *tokens, float *logprobs, void *workspace,
-                      size_t workspace_bytes, void *stream) {
+                      const float *top_p, const float *min_p, int32_t *tokens, float *logprobs, void *stream) {
     if (dtype != GDN_BF16 && dtype != GDN_F32) return GDN_ERR_DTYPE;
     if (B < 0 || V <= 0 || logits_stride < 0 || noise_stride < 0) return GDN_ERR_SHAPE;
     if (V > (1 << 22)) return GDN_ERR_UNSUPPORTED;  // 2^22 weights of at most 2^40 units: sums stay below 2^63
     if (B == 0) return GDN_OK;
-    if (!logits || !noise || !tokens || !workspace) return GDN_ERR_NULL;
+    if (!logits || !noise || !tokens) return GDN_ERR_NULL;
     if ((uintptr_t)logits % (unsigned)bytes_of(dtype) ||
         (((uintptr_t)noise | (uintptr_t)temperature | (uintptr_t)top_k | (uintptr_t)top_p | (uintptr_t)min_p |
-          (uintptr_t)tokens | (uintptr_t)logprobs) & 3u) || (uintptr_t)workspace % kWsAlign)
+          (uintptr_t)tokens | (uintptr_t)logprobs) & 3u))
         return GDN_ERR_ALIGN;
-    if (workspace_bytes < gdn_sample_workspace_bytes(B, V)) return GDN_ERR_WORKSPACE;
     if (!device_ok()) return GDN_ERR_DEVICE;
     const SampleArgs a = {B, V, dtype, logits, logits_stride, noise, noise_stride, temperature, top_p, min_p, top_k,
-                          tokens, logprobs, workspace};
+                          tokens, logprobs};
     return launch_sample(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

@@ -16,11 +16,15 @@ import ctypes
 
 import torch
 
+from . import _binding
 from ._binding import GDN_BF16, GDN_E4M3, GDN_F32, GdnKvCache, Workspace, _check, load
 
 _CODES = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
 _CACHE_CODES = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32, torch.float8_e4m3fn: GDN_E4M3}
-_ws = {}
+_ws = {}        # the default workspaces, by device and stream
+_ws_bytes = {}  # answers of gdn_paged_decode_workspace_bytes
+_current_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _want(t, name, dtype, shape, device):
@@ -43,50 +47,46 @@ def _cuda(t, name):
     return dev
 
 
-class _On:
-    """The call's device and stream.  Memory that torch hands out for another stream than the
-    current one is recorded on it, so that it is not reused while the call still runs."""
+def _handle(dev, stream):
+    """The call's stream as an address, and that stream if it is not the device's current one: memory that torch
+    hands out for the current stream is then recorded on it, so that it is not reused while the call still runs."""
+    current = _current_stream(dev.index)
+    if stream is None or stream.cuda_stream == current:
+        return current, None
+    return stream.cuda_stream, stream
 
-    def __init__(self, dev, stream):
-        self.dev = dev
-        self.other = False
-        if stream is None:
-            self.stream = None
-            self.handle = torch._C._cuda_getCurrentRawStream(dev.index)
-        else:
-            self.stream = stream
-            self.handle = stream.cuda_stream
-            self.other = self.handle != torch._C._cuda_getCurrentRawStream(dev.index)
 
-    def empty(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.dev)
-        if self.other:
-            t.record_stream(self.stream)
-        return t
+def _empty(shape, dtype, dev, other):
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    if other is not None:
+        t.record_stream(other)
+    return t
 
-    def workspace(self, ws, nbytes):
-        """(address, bytes) of the caller's workspace, or of this device and stream's own."""
-        if ws is None:
-            key = (self.dev.index, self.handle)
-            buf = _ws.get(key)
-            if buf is None or buf.numel() < nbytes:
-                buf = _ws[key] = self.empty((nbytes,), torch.uint8)
-            return buf.data_ptr(), buf.numel()
-        if isinstance(ws, Workspace):
-            ws = ws.get(nbytes, self.dev)
-        if ws.device != self.dev:
-            raise ValueError(f"workspace must be on {self.dev}, is on {ws.device}")
-        return ws.data_ptr(), ws.numel() * ws.element_size()
 
-    def call(self, name, *args):
-        fn = getattr(load(), name)
-        if torch._C._cuda_getDevice() == self.dev.index:
-            rc = fn(*args, self.handle)
-        else:
-            with torch.cuda.device(self.dev):
-                rc = fn(*args, self.handle)
-        if rc:
-            _check(name, rc)
+def _workspace(ws, nbytes, dev, handle, other):
+    """(address, bytes) of the caller's workspace, or of this device and stream's own."""
+    if ws is None:
+        key = (dev.index, handle)
+        buf = _ws.get(key)
+        if buf is None or buf.numel() < nbytes:
+            buf = _ws[key] = _empty((nbytes,), torch.uint8, dev, other)
+        return buf.data_ptr(), buf.numel()
+    if isinstance(ws, Workspace):
+        ws = ws.get(nbytes, dev)
+    if ws.device != dev:
+        raise ValueError(f"workspace must be on {dev}, is on {ws.device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _call(name, dev, *args):
+    fn = getattr(_binding._lib or load(), name)
+    if _current_device() == dev.index:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args)
+    if rc:
+        _check(name, rc)
 
 
 def _cache(k, v, k_scale, v_scale, dev):
@@ -131,23 +131,31 @@ def gdn_page_tables(new_lens, free_pages, block_table, *, page, cached_lens=None
             raise ValueError("gdn_page_tables needs n_slots or slots")
         n_slots = slots.numel()
     i32 = torch.int32
-    on = _On(dev, stream)
+    handle, other = _handle(dev, stream)
     cached = None if cached_lens is None else _want(cached_lens, "cached_lens", i32, (B,), dev)
-    if slots is None:
-        slots = on.empty((n_slots,), torch.int64)
-    if positions is None:
-        positions = on.empty((n_slots,), i32)
-    if seq_lens is None:
-        seq_lens = on.empty((B,), i32)
-    if cu_new is None:
-        cu_new = on.empty((B + 1,), i32)
-    if counts is None:
-        counts = on.empty((4,), i32)
-    on.call("gdn_page_tables", B, page, max_pages, cached, _want(new_lens, "new_lens", i32, (B,), dev),
-            _want(free_pages, "free_pages", i32, (free_pages.numel(),), dev), free_pages.numel(),
-            _want(block_table, "block_table", i32, (B, max_pages), dev), _want(seq_lens, "seq_lens", i32, (B,), dev),
-            _want(cu_new, "cu_new", i32, (B + 1,), dev), _want(slots, "slots", torch.int64, (n_slots,), dev),
-            _want(positions, "positions", i32, (n_slots,), dev), n_slots, _want(counts, "counts", i32, (4,), dev))
+    if slots is None and positions is None and seq_lens is None and cu_new is None and counts is None:
+        # all five from one allocation: the call's own time is a few microseconds, an allocation's one or two
+        n = n_slots
+        whole = _empty((n + (n + 2 * B + 6) // 2,), torch.int64, dev, other)
+        half = whole.view(i32)
+        slots, positions = whole.as_strided((n,), (1,)), half.as_strided((n,), (1,), 2 * n)
+        counts, seq_lens = half.as_strided((4,), (1,), 3 * n), half.as_strided((B,), (1,), 3 * n + 4)
+        cu_new = half.as_strided((B + 1,), (1,), 3 * n + 4 + B)
+        base = whole.data_ptr()
+        out = (base + 12 * n + 16, base + 12 * n + 16 + 4 * B, base, base + 8 * n, n, base + 12 * n)
+    else:
+        slots = _empty((n_slots,), torch.int64, dev, other) if slots is None else slots
+        positions = _empty((n_slots,), i32, dev, other) if positions is None else positions
+        seq_lens = _empty((B,), i32, dev, other) if seq_lens is None else seq_lens
+        cu_new = _empty((B + 1,), i32, dev, other) if cu_new is None else cu_new
+        counts = _empty((4,), i32, dev, other) if counts is None else counts
+        out = (_want(seq_lens, "seq_lens", i32, (B,), dev), _want(cu_new, "cu_new", i32, (B + 1,), dev),
+               _want(slots, "slots", torch.int64, (n_slots,), dev), _want(positions, "positions", i32, (n_slots,), dev), n_slots,
+               _want(counts, "counts", i32, (4,), dev))
+    n_free = free_pages.numel()
+    _call("gdn_page_tables", dev, B, page, max_pages, cached, _want(new_lens, "new_lens", i32, (B,), dev),
+          _want(free_pages, "free_pages", i32, (n_free,), dev), n_free,
+          _want(block_table, "block_table", i32, (B, max_pages), dev), *out, handle)
     return slots, positions, seq_lens, cu_new, counts
 
 
@@ -155,7 +163,7 @@ def gdn_page_tables_status(counts, stream=None) -> int:
     """Status of a gdn_page_tables call from its counts (synchronises the stream): 0, or
     9 (GDN_ERR_CAPACITY) if the free list, the table or the slot map was too short."""
     dev = _cuda(counts, "counts")
-    return int(load().gdn_page_tables_status(_want(counts, "counts", torch.int32, (4,), dev), _On(dev, stream).handle))
+    return int(load().gdn_page_tables_status(_want(counts, "counts", torch.int32, (4,), dev), _handle(dev, stream)[0]))
 
 
 def gdn_kv_append(k, v, slots, k_cache, v_cache, *, k_scale=None, v_scale=None, stream=None):
@@ -174,8 +182,8 @@ def gdn_kv_append(k, v, slots, k_cache, v_cache, *, k_scale=None, v_scale=None, 
     ks, vs = k.stride(), v.stride()
     if ks[2] != 1 or vs[2] != 1:
         raise ValueError("the last dimension of k and v must be contiguous")
-    _On(dev, stream).call("gdn_kv_append", c, n, code, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
-                          _want(slots, "slots", torch.int64, (n,), dev))
+    _call("gdn_kv_append", dev, c, n, code, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+          _want(slots, "slots", torch.int64, (n,), dev), _handle(dev, stream)[0])
 
 
 def gdn_paged_decode(q, k_cache, v_cache, block_table, seq_lens, *, k_scale=None, v_scale=None, scale=None, window=0,
@@ -203,20 +211,30 @@ def gdn_paged_decode(q, k_cache, v_cache, block_table, seq_lens, *, k_scale=None
     rows, max_pages = block_table.shape
     if rows != B or (ts[1] != 1 and max_pages > 1):
         raise ValueError(f"block_table must be [{B}, max_pages] with contiguous rows, got {tuple(block_table.shape)}")
-    on = _On(dev, stream)
+    handle, other = _handle(dev, stream)
     if o is None:
-        o = on.empty((B, heads, d), q.dtype)
+        o = _empty((B, heads, d), q.dtype, dev, other)
+        o_at = o.data_ptr()
+    else:
+        o_at = _want(o, "o", q.dtype, (B, heads, d), dev)
     if lse is None:
-        lse = on.empty((B, heads), torch.float32)
-    ws, ws_bytes = on.workspace(workspace, load().gdn_paged_decode_workspace_bytes(c, heads))
-    on.call("gdn_paged_decode", c, B, heads, code, q.data_ptr(), qs[0], qs[1], block_table.data_ptr(), ts[0], max_pages,
-            _want(seq_lens, "seq_lens", torch.int32, (B,), dev), window, d ** -0.5 if scale is None else scale,
-            _want(o, "o", q.dtype, (B, heads, d), dev), _want(lse, "lse", torch.float32, (B, heads), dev), ws, ws_bytes)
+        lse = _empty((B, heads), torch.float32, dev, other)
+        lse_at = lse.data_ptr()
+    else:
+        lse_at = _want(lse, "lse", torch.float32, (B, heads), dev)
+    key = (c.dtype, d, heads, c.Hkv)
+    nbytes = _ws_bytes.get(key)
+    if nbytes is None:
+        nbytes = _ws_bytes[key] = load().gdn_paged_decode_workspace_bytes(c, heads)
+    ws, ws_bytes = _workspace(workspace, nbytes, dev, handle, other)
+    _call("gdn_paged_decode", dev, c, B, heads, code, q.data_ptr(), qs[0], qs[1], block_table.data_ptr(), ts[0], max_pages,
+          _want(seq_lens, "seq_lens", torch.int32, (B,), dev), window, d ** -0.5 if scale is None else scale, o_at, lse_at,
+          ws, ws_bytes, handle)
     return o, lse
 
 
 def gdn_sample(logits, noise, *, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, logprobs=None,
-               workspace=None, stream=None):
+               stream=None):
     """The next token of every row of logits [B, V] (bfloat16 or float32), from uniform random numbers
     noise [B, V] (fp32).  temperature, top_p, min_p [B] fp32 and top_k [B] int32: include/gdn.h has the
     order of the filters; None leaves one out.  Returns (tokens int32 [B], logprobs fp32 [B])."""
@@ -230,15 +248,13 @@ def gdn_sample(logits, noise, *, temperature=None, top_k=None, top_p=None, min_p
     ls, ns = logits.stride(), noise.stride()
     if V > 1 and (ls[1] != 1 or ns[1] != 1):
         raise ValueError("the rows of logits and noise must be contiguous")
-    on = _On(dev, stream)
+    handle, other = _handle(dev, stream)
     opt = [None if t is None else _want(t, n, torch.int32 if n == "top_k" else torch.float32, (B,), dev)
            for t, n in ((temperature, "temperature"), (top_k, "top_k"), (top_p, "top_p"), (min_p, "min_p"))]
     if tokens is None:
-        tokens = on.empty((B,), torch.int32)
+        tokens = _empty((B,), torch.int32, dev, other)
     if logprobs is None:
-        logprobs = on.empty((B,), torch.float32)
-    ws, ws_bytes = on.workspace(workspace, load().gdn_sample_workspace_bytes(B, V))
-    on.call("gdn_sample", B, V, code, logits.data_ptr(), ls[0], noise.data_ptr(), ns[0], *opt,
-            _want(tokens, "tokens", torch.int32, (B,), dev), _want(logprobs, "logprobs", torch.float32, (B,), dev),
-            ws, ws_bytes)
+        logprobs = _empty((B,), torch.float32, dev, other)
+    _call("gdn_sample", dev, B, V, code, logits.data_ptr(), ls[0], noise.data_ptr(), ns[0], *opt,
+          _want(tokens, "tokens", torch.int32, (B,), dev), _want(logprobs, "logprobs", torch.float32, (B,), dev), handle)
     return tokens, logprobs

@@ -411,13 +411,11 @@ GDN_API gdn_status gdn_paged_decode(const gdn_kv_cache *cache, int32_t B, int32_
  * never chosen, +inf counts as the largest finite number; a row with neither a
  * finite logit nor +inf gets token -1 and logprob -inf.  Masses are held as 64-bit
  * whole numbers in units of 2^-40 of the largest weight, so the result does not
- * depend on the order of any sum.  Workspace: gdn_sample_workspace_bytes(B, V),
- * 256-byte aligned, no set-up. */
-GDN_API size_t gdn_sample_workspace_bytes(int32_t B, int32_t V);
+ * depend on the order of any sum.  No workspace. */
 GDN_API gdn_status gdn_sample(int32_t B, int32_t V, gdn_dtype dtype, const void *logits, int64_t logits_stride,
                               const float *noise, int64_t noise_stride, const float *temperature,
                               const int32_t *top_k, const float *top_p, const float *min_p, int32_t *tokens,
-                              float *logprobs, void *workspace, size_t workspace_bytes, void *stream);
+                              float *logprobs, void *stream);
 
 /* Prefill with HOST inputs and outputs: the same computation as
  * gdn_prefill_sparse (mask != NULL) or gdn_prefill_dense (mask == NULL), with

@@ -48,8 +48,8 @@ def decode(lib, c=None, B=2, Hq=16, dtype=0, q=FAKE, qs=(2048, 128), table=FAKE,
     return lib.gdn_paged_decode(c or cache(), B, Hq, dtype, q, *qs, table, ts, pages, lens, window, 0.1, o, lse, ws, nbytes, None)
 
 
-def sample(lib, B=2, V=100, dtype=1, x=FAKE, xs=100, u=FAKE, us=100, t=None, k=None, p=None, m=None, tok=FAKE, lp=FAKE, ws=FAKE, nbytes=1 << 40):
-    return lib.gdn_sample(B, V, dtype, x, xs, u, us, t, k, p, m, tok, lp, ws, nbytes, None)
+def sample(lib, B=2, V=100, dtype=1, x=FAKE, xs=100, u=FAKE, us=100, t=None, k=None, p=None, m=None, tok=FAKE, lp=FAKE):
+    return lib.gdn_sample(B, V, dtype, x, xs, u, us, t, k, p, m, tok, lp, None)
 
 
 def tables(lib, B=2, page=16, wide=10, cached=None, new=FAKE, free=FAKE, n_free=5, table=FAKE, lens=FAKE, cu=FAKE, slots=FAKE, pos=FAKE, n=4,
@@ -102,18 +102,15 @@ def test_decode_refusals(lib):
 
 def test_sample_refusals(lib):
     assert sample(lib) == DEVICE and sample(lib, lp=None) == DEVICE
-    assert sample(lib, B=0, x=None, u=None, tok=None, ws=None) == OK
+    assert sample(lib, B=0, x=None, u=None, tok=None) == OK
     assert sample(lib, V=0) == SHAPE and sample(lib, B=-1) == SHAPE and sample(lib, xs=-1) == SHAPE
     assert sample(lib, V=(1 << 22) + 1) == UNSUPPORTED
     assert sample(lib, dtype=2) == DTYPE
-    for name in ("x", "u", "tok", "ws"):
+    for name in ("x", "u", "tok"):
         assert sample(lib, **{name: None}) == NULL, name
-    for kw in (dict(x=FAKE + 2), dict(u=FAKE + 2), dict(t=FAKE + 1), dict(k=FAKE + 2), dict(tok=FAKE + 2), dict(ws=FAKE + 16)):
+    for kw in (dict(x=FAKE + 2), dict(u=FAKE + 2), dict(t=FAKE + 1), dict(k=FAKE + 2), dict(tok=FAKE + 2)):
         assert sample(lib, **kw) == ALIGN, kw
     assert sample(lib, dtype=0, x=FAKE + 2) == DEVICE  # bf16 rows need no more than their own alignment
-    need = lib.gdn_sample_workspace_bytes(2, 100)
-    assert need > 0 and sample(lib, nbytes=need - 1) == WORKSPACE
-    assert lib.gdn_sample_workspace_bytes(2, 0) == 0
 
 
 def test_tables_refusals(lib):
