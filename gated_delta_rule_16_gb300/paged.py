@@ -133,29 +133,17 @@ def gdn_page_tables(new_lens, free_pages, block_table, *, page, cached_lens=None
     i32 = torch.int32
     handle, other = _handle(dev, stream)
     cached = None if cached_lens is None else _want(cached_lens, "cached_lens", i32, (B,), dev)
-    if slots is None and positions is None and seq_lens is None and cu_new is None and counts is None:
-        # all five from one allocation: the call's own time is a few microseconds, an allocation's one or two
-        n = n_slots
-        whole = _empty((n + (n + 2 * B + 6) // 2,), torch.int64, dev, other)
-        half = whole.view(i32)
-        slots, positions = whole.as_strided((n,), (1,)), half.as_strided((n,), (1,), 2 * n)
-        counts, seq_lens = half.as_strided((4,), (1,), 3 * n), half.as_strided((B,), (1,), 3 * n + 4)
-        cu_new = half.as_strided((B + 1,), (1,), 3 * n + 4 + B)
-        base = whole.data_ptr()
-        out = (base + 12 * n + 16, base + 12 * n + 16 + 4 * B, base, base + 8 * n, n, base + 12 * n)
-    else:
-        slots = _empty((n_slots,), torch.int64, dev, other) if slots is None else slots
-        positions = _empty((n_slots,), i32, dev, other) if positions is None else positions
-        seq_lens = _empty((B,), i32, dev, other) if seq_lens is None else seq_lens
-        cu_new = _empty((B + 1,), i32, dev, other) if cu_new is None else cu_new
-        counts = _empty((4,), i32, dev, other) if counts is None else counts
-        out = (_want(seq_lens, "seq_lens", i32, (B,), dev), _want(cu_new, "cu_new", i32, (B + 1,), dev),
-               _want(slots, "slots", torch.int64, (n_slots,), dev), _want(positions, "positions", i32, (n_slots,), dev), n_slots,
-               _want(counts, "counts", i32, (4,), dev))
+    slots = _empty((n_slots,), torch.int64, dev, other) if slots is None else slots
+    positions = _empty((n_slots,), i32, dev, other) if positions is None else positions
+    seq_lens = _empty((B,), i32, dev, other) if seq_lens is None else seq_lens
+    cu_new = _empty((B + 1,), i32, dev, other) if cu_new is None else cu_new
+    counts = _empty((4,), i32, dev, other) if counts is None else counts
     n_free = free_pages.numel()
     _call("gdn_page_tables", dev, B, page, max_pages, cached, _want(new_lens, "new_lens", i32, (B,), dev),
           _want(free_pages, "free_pages", i32, (n_free,), dev), n_free,
-          _want(block_table, "block_table", i32, (B, max_pages), dev), *out, handle)
+          _want(block_table, "block_table", i32, (B, max_pages), dev), _want(seq_lens, "seq_lens", i32, (B,), dev),
+          _want(cu_new, "cu_new", i32, (B + 1,), dev), _want(slots, "slots", torch.int64, (n_slots,), dev),
+          _want(positions, "positions", i32, (n_slots,), dev), n_slots, _want(counts, "counts", i32, (4,), dev), handle)
     return slots, positions, seq_lens, cu_new, counts
 
 
