@@ -3,7 +3,8 @@
 // A pure copy (every value read once, written once; an 8-bit cache divides by the
 // head's scale on the way), bound by memory.  A thread keeps one 16-byte piece of a
 // cached row, (head, piece), through the tokens it takes, so its addresses, its scale
-// and the scale's reciprocal are made once; four tokens' loads are in flight together.
+// and the scale's reciprocal are made once.  Copies have four tokens' loads in flight; a conversion has registers for one
+// (two measured 38 us against 35, four 51, at the prompt below).
 #include "paged.cuh"
 
 namespace gdn {
@@ -13,57 +14,59 @@ constexpr int kThreads = 256;
 
 // 8-bit storage: x / scale in fp32 (one rounding), then to nearest even in e4m3, saturated: a cached value is off by
 // half an e4m3 step of its own size at most.  The quotient is corrected once from the rounded reciprocal (Markstein, IBM
-// J. Res. Dev. 34, 1990: with r = RN(1/s), q = RN(x r), RN(q + r RN(x - q s)) is RN(x/s) while nothing over- or underflows),
-// three operations in place of a division's ten.  A scale whose reciprocal leaves the normal range is divided by.
+// J. Res. Dev. 34, 1990: with r = RN(1/s), q = RN(x r), RN(q + r RN(x - q s)) is RN(x/s) while nothing over- or underflows;
+// an underflow here rounds to 0 all the same), three operations in place of a division's ten.  Where the reciprocal
+// or a quotient of the piece leaves the range (infinities among them) the piece is divided.  With a division each a prompt
+// of 32805 tokens, 8 heads of 128, took 39 us.
 struct Scale {
-    float s, r;  // r = 0: divide
-    __device__ explicit Scale(float x) : s(x), r(fabsf(x) > 1e-30f && fabsf(x) < 1e30f ? 1.f / x : 0.f) {}
-    __device__ __forceinline__ float under(float x) const {
-        if (r == 0.f) return x / s;
-        const float q = x * r, rest = __fmaf_rn(-q, s, x);
-        return fabsf(q) < 1e30f ? __fmaf_rn(rest, r, q) : q;  // past it (infinities): saturated all the same
+    float s, r, most;  // |x| < most: corrected quotients
+    __device__ explicit Scale(float x) : s(x), r(1.f / x), most(fabsf(x) > 1e-30f && fabsf(x) < 1e30f ? 1e6f * fabsf(x) : 0.f) {}
+    __device__ __forceinline__ float quotient(float x) const {
+        const float q = x * r;
+        return __fmaf_rn(__fmaf_rn(-q, s, x), r, q);
     }
 };
-__device__ __forceinline__ uint32_t e4m3x4(float x0, float x1, float x2, float x3, const Scale &s) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(s.under(x0), s.under(x1)), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(s.under(x2), s.under(x3)), __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ uint32_t e4m3x4(float x0, float x1, float x2, float x3) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x2, x3), __NV_SATFINITE, __NV_E4M3);
     return lo | hi << 16;
 }
-
-template <typename T> struct Piece;  // 16 cached 8-bit values from 16 values of type T
-template <> struct Piece<__nv_bfloat16> {
-    static __device__ __forceinline__ uint4 pack(const uint4 *src, const Scale &scale) {
-        uint4 out;
-        uint32_t *w = &out.x;
+// 16 cached 8-bit values from 16 values of type T.
+template <typename T>
+__device__ __forceinline__ uint4 quantised(const uint4 *src, const Scale &s) {
+    float x[16], top = 0.f;
+    const uint32_t *w = &src[0].x;
+    if constexpr (sizeof(T) == 2) {
+        __nv_bfloat162 m = __habs2(*(const __nv_bfloat162 *)w);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint4 x = src[i];
-            // a bf16 is the upper half of its fp32
-            w[2 * i] = e4m3x4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u),
-                              __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u), scale);
-            w[2 * i + 1] = e4m3x4(__uint_as_float(x.z << 16), __uint_as_float(x.z & 0xffff0000u),
-                                  __uint_as_float(x.w << 16), __uint_as_float(x.w & 0xffff0000u), scale);
+        for (int i = 0; i < 8; ++i) {
+            m = __hmax2(m, __habs2(*(const __nv_bfloat162 *)(w + i)));
+            x[2 * i] = __uint_as_float(w[i] << 16);  // a bf16 is the upper half of its fp32
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
-        return out;
-    }
-};
-template <> struct Piece<float> {
-    static __device__ __forceinline__ uint4 pack(const uint4 *src, const Scale &scale) {
-        uint4 out;
-        uint32_t *w = &out.x;
+        top = fmaxf(__low2float(m), __high2float(m));
+    } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint4 x = src[i];
-            w[i] = e4m3x4(__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w), scale);
+        for (int i = 0; i < 16; ++i) {
+            x[i] = __uint_as_float(w[i]);
+            top = fmaxf(top, fabsf(x[i]));
         }
-        return out;
     }
-};
+    if (top < s.most) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = s.quotient(x[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = x[i] / s.s;
+    }
+    return make_uint4(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]), e4m3x4(x[8], x[9], x[10], x[11]),
+                      e4m3x4(x[12], x[13], x[14], x[15]));
+}
 
 template <typename T, bool QUANT>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a, int per_token, int tokens) {
     constexpr int kElem = QUANT ? 1 : sizeof(T), kPer = 16 / kElem;  // cached values per piece
-    constexpr int kLoads = QUANT ? sizeof(T) : 1, kAhead = QUANT ? 2 : 4;  // 16-byte loads per piece; tokens in flight
+    constexpr int kLoads = QUANT ? sizeof(T) : 1, kAhead = QUANT ? 1 : 4;  // 16-byte loads per piece; tokens in flight
     // `tokens` tokens of `per_token` pieces side by side in a CTA, a token's pieces over several CTAs in y if they are more
     const int lane = threadIdx.x / per_token, piece = blockIdx.y * kThreads + threadIdx.x % per_token;
     const int pieces = a.c.d / kPer, h = piece / pieces, e = piece % pieces * kPer;
@@ -102,8 +105,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a, int p
             const int64_t at = (page * a.c.stride_page + (slot[u] - page * a.c.page) * a.c.stride_token) * kElem;
             uint4 x, y;
             if constexpr (QUANT) {
-                x = Piece<T>::pack(kx[u], ks);
-                y = Piece<T>::pack(vx[u], vs);
+                x = quantised<T>(kx[u], ks);
+                y = quantised<T>(vx[u], vs);
             } else {
                 x = kx[u][0];
                 y = vx[u][0];
@@ -119,9 +122,10 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a, int p
 cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream) {
     const int per = a.c.dtype == GDN_E4M3 ? 16 : (a.c.dtype == GDN_BF16 ? 8 : 4);
     const int pieces = a.c.Hkv * (a.c.d / per), per_token = min(pieces, kThreads), tokens = kThreads / per_token;
-    // up to eight CTAs per SM, each taking tokens in turn; small calls one token per thread
+    // one wave of CTAs that take tokens in turn, eight per SM for copies, four for conversions (31.4 us against 32.3 with
+    // eight, 38.5 without turns); small calls one token per thread
     const int64_t want = ((int64_t)a.n + tokens - 1) / tokens;
-    const dim3 grid((unsigned)min(want, (int64_t)152 * 8), (pieces + kThreads - 1) / kThreads);
+    const dim3 grid((unsigned)min(want, (int64_t)152 * (a.c.dtype == GDN_E4M3 ? 4 : 8)), (pieces + kThreads - 1) / kThreads);
     auto go = [&](auto kern) { kern<<<grid, kThreads, 0, stream>>>(a, per_token, tokens); };
     if (a.c.dtype == GDN_E4M3) {
         if (a.dtype == GDN_BF16) go(kv_append_kernel<__nv_bfloat16, true>);

@@ -481,39 +481,34 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) enter(v[e], i[e], r[e]);
         };
-        constexpr int kAhead = 4;
-        for (int i0 = from + (tid & ~31); i0 < to; i0 += kAhead * kThreads) {
-            float v[kAhead];
-            uint32_t mask[kAhead];
+        // N tokens from `at` on per lane, -inf where there is none
+        auto take = [&](auto count, const float *w, int at) {
+            constexpr int N = decltype(count)::value;
+            float v[N];
+            uint32_t mask[N];
             int some = 0;
 #pragma unroll
-            for (int e = 0; e < kAhead; ++e) {
-                const int i = i0 + e * kThreads + lane;
-                v[e] = i < to ? io<T>::ld(x + i) : -INFINITY;
-            }
-#pragma unroll
-            for (int e = 0; e < kAhead; ++e) {
-                const int i = i0 + e * kThreads + lane;
-                v[e] = clean(v[e]);
-                const bool in = v[e] >= floor && !(v[e] == cut_v && i > cut_i);
-                v[e] = in ? v[e] : -INFINITY;
+            for (int e = 0; e < N; ++e) {
+                const float y = clean(w[e]);
+                const bool in = y >= floor && !(y == cut_v && at + e > cut_i);
+                v[e] = in ? y : -INFINITY;
                 mask[e] = __ballot_sync(0xffffffffu, in);
                 some += __popc(mask[e]);
             }
-            if (some >= 32 * kAhead / 2) {
-                float r[kAhead];
+            if (some >= 16 * N) {
+                float r[N];
 #pragma unroll
-                for (int e = 0; e < kAhead; ++e) r[e] = v[e] > -INFINITY ? u[i0 + e * kThreads + lane] : 0.5f;
+                for (int e = 0; e < N; ++e) r[e] = v[e] > -INFINITY ? u[at + e] : 0.5f;
 #pragma unroll
-                for (int e = 0; e < kAhead; ++e) enter(v[e], i0 + e * kThreads + lane, r[e]);
-                continue;
+                for (int e = 0; e < N; ++e) enter(v[e], at + e, r[e]);
+                return;
             }
-            if (some == 0) continue;
+            if (some == 0) return;
 #pragma unroll
-            for (int e = 0; e < kAhead; ++e) {
+            for (int e = 0; e < N; ++e) {
                 if (mask[e] == 0) continue;
                 if (v[e] > -INFINITY)
-                    queue[waiting + __popc(mask[e] & ((1u << lane) - 1))] = (u64)__float_as_uint(v[e]) << 32 | (uint32_t)(i0 + e * kThreads + lane);
+                    queue[waiting + __popc(mask[e] & ((1u << lane) - 1))] = (u64)__float_as_uint(v[e]) << 32 | (uint32_t)(at + e);
                 waiting += __popc(mask[e]);
                 __syncwarp();
                 if (waiting >= kBatch) {
@@ -525,6 +520,37 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
                     __syncwarp();
                 }
             }
+        };
+        // as each_piece, but every lane of a warp takes part in every step
+        const T *row = x + from;
+        const int head = min(to - from, (int)((16 - ((uintptr_t)row & 15)) & 15) / (int)sizeof(T)), pieces = (to - from - head) / kPer;
+        const uint4 *p4 = (const uint4 *)(row + head);
+        for (int i0 = warp * 32; i0 < pieces; i0 += 4 * kThreads) {
+            uint4 w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int i = i0 + q * kThreads + lane;
+                // all ones: NaN in either type, never kept
+                w[q] = i < pieces ? p4[i] : make_uint4(~0u, ~0u, ~0u, ~0u);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (i0 + q * kThreads >= pieces) break;
+                const uint32_t b[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+                float v[kPer];
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) {
+                    if constexpr (sizeof(T) == 2) v[e] = __uint_as_float(e & 1 ? b[e / 2] & 0xffff0000u : b[e / 2] << 16);
+                    else v[e] = __uint_as_float(b[e]);
+                }
+                take(Count<kPer>(), v, from + head + (i0 + q * kThreads + lane) * kPer);
+            }
+        }
+        if (warp == 0) {  // the single tokens before and after
+            const int tail = head + pieces * kPer, i = lane < 16 ? lane : tail + lane - 16;
+            const bool have = lane < 16 ? lane < head : i < to - from;
+            const float v = have ? io<T>::ld(row + i) : -INFINITY;
+            take(Count<1>(), &v, have ? from + i : 0);
         }
         run_batch(waiting);
     };

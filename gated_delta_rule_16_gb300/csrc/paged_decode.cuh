@@ -229,25 +229,52 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
     const WsView ws = ws_view(a.ws, NT * 8);
     pdl_trigger();
 
-    // ---- this CTA's run of tiles
+    // ---- this CTA's run of tiles [t0, t0 + n): requests lie one after the other, `rows` rows of the same tiles each
     __shared__ int64_t scan[W];
     __shared__ int4 found;
     Cursor cur;
-    int64_t sum = 0;
-    for (int b = tid; b < a.B; b += C::kThreads) {
-        cur.b = b;
+    int64_t total, t0, n;
+    int ctas;
+    const int cta = blockIdx.x;
+    auto settle = [&](int64_t per_row) {  // false: no tiles for this CTA
+        total = per_row * rows;
+        ctas = (int)min((int64_t)gridDim.x, total);
+        if (cta >= ctas) {
+            if (tid == 0 && !by_row) ws.joins[cta - 1] = make_int4(0, 0, 0, 0);
+            return false;
+        }
+        t0 = split_at(total, ctas, cta);
+        n = split_at(total, ctas, cta + 1) - t0;
+        return true;
+    };
+    if (a.B <= 32) {
+        // a lane per request, every warp for itself
+        cur.b = lane;
         cur.load<TILE>(a);
-        sum += cur.tiles;
-    }
-    const int64_t per_row = block_sum<C::kThreads>(sum, scan), total = per_row * rows;
-    const int ctas = (int)min((int64_t)gridDim.x, total), cta = blockIdx.x;
-    if (cta >= ctas) {
-        if (tid == 0 && !by_row) ws.joins[cta - 1] = make_int4(0, 0, 0, 0);
-        return;
-    }
-    const int64_t t0 = split_at(total, ctas, cta), n = split_at(total, ctas, cta + 1) - t0;
-    {
-        // the request whose tiles hold t0: requests lie one after the other, `rows` rows each
+        const int mine = lane < a.B ? cur.tiles : 0;
+        int64_t incl = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += x;
+        }
+        if (!settle(__shfl_sync(0xffffffffu, incl, 31))) return;
+        const int64_t want = t0 / rows;
+        const int at = __popc(__ballot_sync(0xffffffffu, incl <= want));  // requests that end before
+        const int64_t off = t0 - __shfl_sync(0xffffffffu, incl - mine, at) * rows;
+        const int tiles = __shfl_sync(0xffffffffu, mine, at);
+        cur.b = at;
+        cur.load<TILE>(a);
+        cur.row = (int)(off / tiles);
+        cur.tile = (int)(off % tiles);
+    } else {
+        int64_t sum = 0;
+        for (int b = tid; b < a.B; b += C::kThreads) {
+            cur.b = b;
+            cur.load<TILE>(a);
+            sum += cur.tiles;
+        }
+        if (!settle(block_sum<C::kThreads>(sum, scan))) return;
         const int64_t want = t0 / rows;
         int64_t before = 0;
         for (int b0 = 0; b0 < a.B; b0 += C::kThreads) {
