@@ -15,19 +15,20 @@
 //   2. a threshold that no kept token is below.  For top_k: among the threads' maxima, the ceil(k / CTAs)-th largest of
 //      every CTA, and the least of those (k tokens at least are as large).  For top_p: tokens below (1 - p) M / V hold
 //      (1 - p) M together at most, so the prefix of mass p M ends above it.  What passes the threshold, a few hundred
-//      tokens as a rule, is gathered, sorted and cut in the first CTA's shared memory;
-//   3. if it is more than fits (flat rows, large k), a histogram of 2048 bins over y, of counts for top_k and of the
-//      weights relative to their bin's upper edge for top_p (32-bit atomics), finds the bins where the cut falls: one,
-//      or a few where sums of mass leave it open.  Only their tokens are gathered, with the exact mass above them;
-//   4. if even those are more than fit (thousands of equal logits), the first CTA finds the cut digit by digit of the
-//      sorting key, a pass over the row each;
-//   5. the race.  The largest token is always kept and its Gumbel is above -3.2, no Gumbel is above 16.7:
-//      tokens with y < -20 cannot win, and their noise is not read.  The others race on approximate scores, and
-//      only those within 10^-3 of a thread's best are decided on exact ones.
+//      tokens as a rule, is gathered and cut in the first CTA's shared memory;
+//   3. if it is more than fits (flat rows, large k), the k-th largest logit is bracketed by a histogram of every 8th load
+//      (of every one if that fails, or k is too large for it), the bracket gathered, with the number and mass
+//      of the tokens above it from the same pass; thousands of equal logits leave the first CTA to descend the
+//      sorting key digit by digit, a pass over the row each.  The end of top_p's prefix is not looked for: the race is run
+//      over all of K, and its winner's mass above says whether it was kept.  If not, nothing below it is either, and the race
+//      is run again above it: 1 + log(1 / top_p) times as a rule, or until what is left can be gathered;
+//   4. the race.  The largest token is always kept, so its score bounds the winner's from the start: no Gumbel is above
+//      16.64, and a token whose logit cannot make up for it has its noise not read; of the others one comparison of
+//      1 - u with a multiple of w leaves a few per warp whose score is worked out.
 //
-// Masses are whole numbers in units of 2^-40 of the largest weight, of a token or of the up to 8 tokens of one load,
-// summed in 64 bits: the sums do not depend on the order the atomics come in.  The weights in masses are 2^x approximations
-// (2^-21); w >= min_p and the race are decided in IEEE fp32 with accurate exp and log.
+// Masses are summed as whole numbers in units of 2^-40 of the largest weight, of a token or of what one thread met of a
+// row, so that no sum depends on the order of atomics.  The weights in masses are 2^x approximations (2^-21); w >= min_p
+// and the race are decided in IEEE fp32 with accurate exp and log.
 #include <cooperative_groups.h>
 
 #include "paged.cuh"
@@ -35,7 +36,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCtas = 8;   // per row: the largest cluster every GPU of this kind can place
 constexpr int kList = 2048;   // gathered tokens
 constexpr int kBins = 2048;
@@ -56,16 +57,14 @@ __device__ __forceinline__ float value_of(uint32_t k) {
 }
 // The sorting key of a token: its logit's ordered bits, then the complement of its index.
 __device__ __forceinline__ u64 full_key(float v, int i) { return (u64)key_of(v) << 32 | (uint32_t)~i; }
-__device__ __forceinline__ float lg2(float x) {
-    float r;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+
+// The weight of a logit in units of 2^-40.
+__device__ __forceinline__ u64 mass_of(float v, float top, float rate) { return (u64)(ex2((v - top) * rate) * kUnit + 0.5f); }
 
 struct Best { float v; int i; };
 __device__ __forceinline__ Best better(Best a, Best b) {
@@ -74,21 +73,25 @@ __device__ __forceinline__ Best better(Best a, Best b) {
 
 struct Shared {
     u64 list[kList];
-    u64 mass[kBins];       // of the whole row's bins; before that, the warps' queues of the race
-    uint32_t count[kBins], part[kBins];  // of this CTA's tokens
+    uint32_t count[kBins];  // of this CTA's tokens; the first CTA has the row's in list
+    u64 digit_sum[256];
+    uint32_t digit_count[256];
     u64 sums[kWarps];
     Best bests[kWarps];
     float parts[2][kWarps];
-    int n, found;          // tokens gathered; bin or rank found
-    u64 before, digit;
+    int n, found;           // tokens gathered; bin or rank found
+    u64 before;
+    bool whole;
     // read by the row's other CTAs, each written once between two barriers of the cluster
     struct {
         Best top, won;
         float low, sum, least;
         int gathered;      // tokens gathered, or more than kList
-        u64 mass;          // of the tokens above the gathered bins
-        int lo, hi;        // the first CTA's: bins to gather next; lo < 0: none, race
-        u64 cut;           // the first CTA's: the smallest key that top_k and top_p keep
+        int above;         // tokens above those, or above a race's winner, and their mass
+        u64 mass;
+        int lo, hi;        // the first CTA's: bins to gather
+        bool settled;      // the first CTA's: whether cut is the key of the k-th token (0: K is all that matters), and mass_k
+        u64 cut, mass_k;   // the mass of K
     } x;
 };
 
@@ -194,58 +197,83 @@ __device__ __forceinline__ bool gather(Shared &s, u64 key) {
     return at < kList;
 }
 
-// Sorts the s.n gathered keys in descending order (bitonic).  Key i lies with thread i % kThreads: keys kThreads and more
-// apart meet in a thread, less than 32 apart by shuffles, and only the distances between go through shared memory.
-__device__ void sort_list(Shared &s) {
+// Of the n gathered keys that are `floor` or more: a key that divides off the shortest descending prefix whose measure
+// (tokens, or mass) reaches goal; 0 if all of it does not.  By 8 bits of the key at a time, from the first that differ.
+__device__ __noinline__ u64 select(Shared &s, int n, u64 goal, bool of_mass, u64 floor, float top, float rate) {
     constexpr int kEach = kList / kThreads;
-    const int tid = threadIdx.x, n = s.n;
-    int size = 32;
-    while (size < n) size <<= 1;
-    u64 r[kEach];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    u64 key[kEach], measure[kEach];
+    uint32_t most = 0, least = ~0u;
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
         const int i = e * kThreads + tid;
-        r[e] = i < n ? s.list[i] : 0;
+        key[e] = i < n ? s.list[i] : 0;
+        if (key[e] < floor) key[e] = 0;
+        measure[e] = of_mass ? mass_of(value_of((uint32_t)(key[e] >> 32)), top, rate) : 1;
+        if (key[e]) {
+            most = max(most, (uint32_t)(key[e] >> 32));
+            least = min(least, (uint32_t)(key[e] >> 32));
+        }
     }
-    auto keep = [](u64 mine, u64 other, bool larger) { return (mine < other) == larger ? other : mine; };
-    for (int run = 2; run <= size; run <<= 1)
-        for (int gap = run >> 1; gap; gap >>= 1) {
-            if (gap >= kThreads) {
+    most = __reduce_max_sync(0xffffffffu, most);
+    least = __reduce_min_sync(0xffffffffu, least);
+    __syncthreads();
+    if (lane == 0) s.sums[warp] = (u64)most << 32 | least;
+    __syncthreads();
 #pragma unroll
-                for (int e = 0; e < kEach; ++e) {
-                    const int f = e ^ (gap / kThreads);
-                    if (f > e && f < kEach) {
-                        const bool down = ((e * kThreads + tid) & run) == 0;
-                        const u64 x = r[e], y = r[f];
-                        r[e] = keep(x, y, down);
-                        r[f] = keep(y, x, !down);
-                    }
-                }
-            } else if (gap >= 32) {
-                __syncthreads();
+    for (int w = 0; w < kWarps; ++w) {
+        most = max(most, (uint32_t)(s.sums[w] >> 32));
+        least = min(least, (uint32_t)s.sums[w]);
+    }
+    if (most == 0) return 0;
+    int above = most == least ? 32 : 64 - __clz(most ^ least);  // bits below `above` may differ
+    u64 prefix = above == 64 ? 0 : ((u64)most << 32) >> above, before = 0;
+    for (;;) {
+        const int shift = max(above - 8, 0), bits = above - shift;
+        __syncthreads();
+        if (tid < 256) s.digit_sum[tid] = 0, s.digit_count[tid] = 0;
+        __syncthreads();
 #pragma unroll
-                for (int e = 0; e < kEach; ++e)
-                    if (e * kThreads < size) s.list[e * kThreads + tid] = r[e];
-                __syncthreads();
+        for (int e = 0; e < kEach; ++e)
+            if (key[e] && (above == 64 || key[e] >> above == prefix)) {
+                const int d = (int)(key[e] >> shift) & ((1 << bits) - 1);
+                atomicAdd(&s.digit_count[d], 1u);
+                if (of_mass) atomicAdd(&s.digit_sum[d], measure[e]);
+            }
+        __syncthreads();
+        if (warp == 0) {
+            // lane l has the digits 255 - 8 l down to 248 - 8 l
+            u64 m[8], own = 0;
 #pragma unroll
-                for (int e = 0; e < kEach; ++e) {
-                    const int i = e * kThreads + tid;
-                    if (e * kThreads < size) r[e] = keep(r[e], s.list[i ^ gap], ((i & run) == 0) == ((i & gap) == 0));
-                }
-            } else {
+            for (int j = 0; j < 8; ++j) {
+                const int d = 255 - 8 * lane - j;
+                m[j] = of_mass ? s.digit_sum[d] : s.digit_count[d];
+                own += m[j];
+            }
+            u64 incl = own;
 #pragma unroll
-                for (int e = 0; e < kEach; ++e) {
-                    const int i = e * kThreads + tid;
-                    if (e * kThreads < size)
-                        r[e] = keep(r[e], __shfl_xor_sync(0xffffffffu, r[e], gap), ((i & run) == 0) == ((i & gap) == 0));
-                }
+            for (int off = 1; off < 32; off <<= 1) {
+                const u64 y = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += y;
+            }
+            u64 at = before + incl - own;
+            if (lane == 31 && before + incl < goal) s.found = -1;
+            if (at < goal && at + own >= goal) {
+                int j = 0;
+                for (; at + m[j] < goal; ++j) at += m[j];
+                s.found = 255 - 8 * lane - j;
+                s.before = at;
+                // the prefix ends with this digit if it takes all of it, or its only token
+                s.whole = at + m[j] == goal || s.digit_count[s.found] == 1;
             }
         }
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < kEach; ++e)
-        if (e * kThreads < size) s.list[e * kThreads + tid] = r[e];
-    __syncthreads();
+        __syncthreads();
+        if (s.found < 0) return 0;
+        prefix = prefix << bits | (u64)s.found;
+        before = s.before;
+        above = shift;
+        if (s.whole || above == 0) return prefix << above;
+    }
 }
 
 // Exact score of a token, {-inf, -1} if min_p or a weight of 0 rules it out.  A call: few tokens need it, and inlined in
@@ -257,8 +285,151 @@ __device__ __noinline__ Best exact_score(float v, int i, float top, float t, flo
     return {y - logf(-logf(r)), i};
 }
 
+// ---- passes over a slice [from, to) of a row.  Calls, so that each has the registers to itself.
+
+// 16-byte pieces of a row for whole warps: f(how many, logits as stored or NaN, index of the first) for kAhead pieces at a time,
+// with every lane in every step; every stride-th piece only.  Single tokens before and after the pieces come one to a lane.
+template <int kAhead, typename T, typename F>
+__device__ __forceinline__ void each_together(const T *x, int from, int to, int stride, F f) {
+    constexpr int kPer = 16 / sizeof(T);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const T *row = x + from;
+    const int head = min(to - from, (int)((16 - ((uintptr_t)row & 15)) & 15) / (int)sizeof(T)), pieces = (to - from - head) / kPer;
+    const uint4 *p4 = (const uint4 *)(row + head);
+    for (int i0 = warp * 32; i0 * stride < pieces; i0 += kAhead * kThreads) {
+        uint4 w[kAhead];
+        float v[kAhead][kPer];
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+            const int i = (i0 + q * kThreads + lane) * stride;
+            w[q] = i < pieces ? p4[i] : make_uint4(~0u, ~0u, ~0u, ~0u);  // NaN in either type
+        }
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+            const uint32_t y[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                if constexpr (sizeof(T) == 2) v[q][e] = __uint_as_float(e & 1 ? y[e / 2] & 0xffff0000u : y[e / 2] << 16);
+                else v[q][e] = __uint_as_float(y[e]);
+            }
+        }
+        f(Count<kAhead>(), Count<kPer>(), &v[0][0], from + head + (i0 + lane) * stride * kPer, stride * kThreads * kPer);
+    }
+    if (warp == 0) {
+        const int tail = head + pieces * kPer, i = lane < 16 ? lane : tail + lane - 16;
+        const bool have = lane < 16 ? lane < head : i < to - from;
+        const float v = have ? io<T>::ld(row + i) : __uint_as_float(~0u);
+        f(Count<1>(), Count<1>(), &v, have ? from + i : 0, 0);
+    }
+}
+
+// Gathers the tokens from `least` up and above the key `under`.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
+__device__ __noinline__ void gather_pass(const T *x, int from, int to, float least, u64 under, Shared &s) {
+    each(x, from, to, least, [&](float v, int i) {
+        const u64 key = full_key(v, i);
+        return key > under ? gather(s, key) : true;
+    });
+}
+
+__device__ __forceinline__ int bin_of(float v, float top, float scale) { return (int)fminf((top - v) * scale, (float)(kBins - 1)); }
+
+// Counts by bin of every stride-th load.
+template <typename T>
+__device__ __noinline__ void count_pass(const T *x, int from, int to, int stride, float top, float scale, Shared &s) {
+    each_together<2>(x, from, to, stride, [&](auto q, auto n, const float *w, int, int) {
+#pragma unroll
+        for (int e = 0; e < decltype(q)::value * decltype(n)::value; ++e)
+            if (w[e] > -INFINITY) atomicAdd(&s.count[bin_of(clean(w[e]), top, scale)], 1u);
+    });
+}
+
+// Gathers the tokens of the bins [lo, hi]; number and mass (in weights) of those above.
+struct Above { int n; float mass; };
+template <typename T>
+__device__ __noinline__ Above bracket_pass(const T *x, int from, int to, int lo, int hi, float top, float scale, float rate, Shared &s) {
+    Above a = {0, 0.f};
+    each_together<2>(x, from, to, 1, [&](auto q, auto n, const float *w, int at, int step) {
+        constexpr int N = decltype(n)::value;
+        uint32_t mine = 0;
+#pragma unroll
+        for (int e = 0; e < decltype(q)::value * N; ++e) {
+            const float v = clean(w[e]);
+            const int bin = bin_of(v, top, scale);  // of -inf: the last
+            if (bin < lo) {
+                a.mass += ex2((v - top) * rate);
+                ++a.n;
+            }
+            mine |= (uint32_t)(bin >= lo && bin <= hi && v > -INFINITY) << e;
+        }
+        while (mine) {  // few: read again
+            const int e = __ffs(mine) - 1, i = at + e / N * step + e % N;
+            mine &= mine - 1;
+            gather(s, full_key(clean(io<T>::ld(x + i)), i));
+        }
+    });
+    return a;
+}
+
+// Mass (in weights) of the tokens before token i, of logit `mark`, in descending order.
+template <typename T>
+__device__ __noinline__ float mass_pass(const T *x, int from, int to, float mark, int i, float top, float rate) {
+    float sum = 0.f;
+    each_piece(x, from, to, [&](const float *w, auto n, int at) {
+        constexpr int N = decltype(n)::value;
+        if (!(largest<N>(w) >= mark)) return true;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const float v = clean(w[e]);
+            if (v > mark || (v == mark && at + e < i)) sum += ex2((v - top) * rate);
+        }
+        return true;
+    });
+    return sum;
+}
+
+// The race.  A token beats the score `best` only if -log u <= w exp(-best), and 1 - u <= -log u: one comparison, with room
+// for its rounding, leaves a handful of tokens per warp for exact scores once the best is shared in the warp.
+struct Track {
+    const float *u;
+    float top, t, rate, min_p;
+    float floor, reach;  // logits below cannot be kept or cannot win; exp(-best)
+    u64 cut;             // keys below are not kept
+};
+template <typename T>
+__device__ __noinline__ Best race_pass(const T *x, int from, int to, const Track &track, Best won) {
+    const float *u = track.u;
+    const float top = track.top, rate = track.rate, floor = track.floor;
+    float reach = track.reach;
+    each_together<sizeof(T)>(x, from, to, 1, [&](auto q, auto n, const float *w, int at, int step) {
+        constexpr int N = decltype(n)::value, Q = decltype(q)::value;
+        if (!__any_sync(0xffffffffu, largest<Q * N>(w) >= floor)) return;
+        float r[Q * N];
+        uint32_t hit = 0;
+#pragma unroll
+        for (int e = 0; e < Q * N; ++e) r[e] = w[e] >= floor ? u[at + e / N * step + e % N] : -1.f;
+#pragma unroll
+        for (int e = 0; e < Q * N; ++e) {
+            const float weight = ex2((fminf(w[e], 3.402823466e38f) - top) * rate);  // of NaN: where r = -1
+            hit |= (uint32_t)(1.f - fminf(r[e], 0.999999940395355f) < weight * reach && r[e] >= 0.f) << e;
+        }
+        if (!__any_sync(0xffffffffu, hit != 0)) return;
+        while (hit) {
+            const int e = __ffs(hit) - 1, i = at + e / N * step + e % N;
+            hit &= hit - 1;
+            const float v = clean(io<T>::ld(x + i));
+            if (full_key(v, i) >= track.cut) won = better(won, exact_score(v, i, top, track.t, track.min_p, u));
+        }
+        float best = won.v;
+#pragma unroll
+        for (int off = 16; off; off >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, off));
+        reach = fminf(reach, 1.01f * ex2(best * -1.4426950408889634f));
+    });
+    return won;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
     extern __shared__ __align__(16) uint8_t raw[];
     Shared &s = *(Shared *)raw;
     constexpr int kPer = 16 / sizeof(T);
@@ -376,19 +547,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
         a.tokens[b] = won.i;
         if (a.logprobs) a.logprobs[b] = won.i < 0 ? -INFINITY : greedy ? 0.f : (clean(io<T>::ld(x + won.i)) - top.v) / t - logf(total);
     };
-    if (top.i < 0 || greedy) {
+    if (top.i < 0 || greedy || min_p > 1.f) {
         if (rank == 0 && tid == 0) finish({-INFINITY, -1});
         cluster.sync();  // no CTA leaves while another may read its shared memory
         return;
     }
 
-    auto mass = [&](float v) { return (u64)(ex2((v - top.v) * rate) * kUnit + 0.5f); };
-    // a logit below (side -1) or above (side 1) which w < f (w >= f), with room for every rounding on the way
-    auto logit_of = [&](float f, float side) {
+    // a logit below which w < f, with room for every rounding on the way
+    auto logit_of = [&](float f) {
         const float d = t * logf(f);
-        return top.v + d + side * (1e-5f * (fabsf(top.v) + fabsf(d)) + 1e-3f * t);
+        return top.v + d - (1e-5f * (fabsf(top.v) + fabsf(d)) + 1e-3f * t);
     };
-    const float min_logit = min_p > 0.f ? logit_of(fminf(min_p, 1.f), -1.f) : -INFINITY;
+    const float min_logit = min_p > 0.f ? logit_of(min_p) : -INFINITY;
     auto goal_of = [&](double m) {  // p of mass m, at least one unit: the largest token always stays
         const double g = ceil((double)fmaxf(p, 0.f) * m);
         return g < 1.0 ? 1ull : (u64)g;
@@ -405,394 +575,232 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
             for (int i = lane + 32 * (warp / (kWarps / 2)); i < m; i += 64) s.list[at + i] = peer(r).list[i];
         }
         __syncthreads();
-        if (tid == 0) s.n = n;
-        __syncthreads();
-        sort_list(s);
         return true;
     };
-    // Over the first `limit` tokens of the sorted list, with the mass `start` before them: s.found = the first rank whose
-    // running mass reaches goal (kList: none).  Returns the mass at the end.
-    auto in_list = [&](int limit, u64 start, u64 goal) {
-        constexpr int kEach = kList / kThreads;
-        u64 own = 0, all, m[kEach];
-        for (int e = 0; e < kEach; ++e) {
-            const int r = tid * kEach + e;
-            m[e] = r < limit ? mass(value_of((uint32_t)(s.list[r] >> 32))) : 0;
-            own += m[e];
-        }
-        u64 at = start + block_before(own, all, s);
-        if (tid == 0) s.found = kList;
-        __syncthreads();
-        for (int e = 0; e < kEach; ++e) {
-            if (at < goal && at + m[e] >= goal) s.found = tid * kEach + e;
-            at += m[e];
-        }
-        __syncthreads();
-        return start + all;
+    auto mass_from = [&](int n, u64 key) {  // of the list's keys
+        u64 own = 0, all;
+        for (int i = tid; i < n; i += kThreads) own += s.list[i] >= key ? mass_of(value_of((uint32_t)(s.list[i] >> 32)), top.v, rate) : 0;
+        block_before(own, all, s);
+        return all;
     };
 
-    // 5. the race.  Tokens that may win wait in a queue per warp until four per lane are there: all lanes work, on loads that
-    // overlap.  Where most tokens may win they are taken as they come.
-    Best lead = {-INFINITY, -1}, won = {-INFINITY, -1};
-    float cut_v = -INFINITY, floor = 0.f;  // set by race_from: what is below cannot be kept, or cannot win
-    int cut_i = -1;
-    const float sure = min_p > 1.f ? INFINITY : min_p > 0.f ? logit_of(min_p, 1.f) : -INFINITY;  // w >= min_p from here on
-    auto race_from = [&](u64 key) {
-        cut_v = key ? value_of((uint32_t)(key >> 32)) : -INFINITY;
-        cut_i = (int)~(uint32_t)key;
-        floor = fmaxf(fmaxf(fmaxf(min_logit, top.v - 20.f * t - 1e-5f * fabsf(top.v)), cut_v), -3.402823466e38f);
-        lead = won = {-INFINITY, -1};
-    };
-    auto enter = [&](float v, int i, float r) {  // v = -inf: no token
-        const float c = fminf(fmaxf(r, 2.3283064365386963e-10f), 0.999999940395355f), d = 1.f - c;
-        // -log u: by its series near 1, where the approximate logarithm has no digits left
-        const float clock = c > 0.99f ? d + 0.5f * d * d : lg2(c) * -0.6931471805599453f;
-        const float rough = ((v - top.v) * rate - lg2(clock)) * 0.6931471805599453f;  // good to 10^-4
-        const bool clear = rough > lead.v + 1e-3f && v >= sure;
-        if (!clear && rough >= lead.v - 1e-3f && v > -INFINITY) {  // too near to tell, or min_p in doubt
-            const Best exact = score(v, i);
-            if (exact.i >= 0) {
-                won = better(won, exact);
-                if (rough > lead.v) {
-                    if (lead.i >= 0) won = better(won, score(clean(io<T>::ld(x + lead.i)), lead.i));
-                    lead = {rough, i};
-                }
-            }
-        }
-        lead.v = clear ? rough : lead.v;
-        lead.i = clear ? i : lead.i;
-    };
-    constexpr int kBatch = 128, kRoom = kBatch + 32;
-    static_assert(kWarps * kRoom <= kList + kBins, "the queues lie over list and mass");
-    auto race_tokens = [&]() {
-        u64 *queue = s.list + warp * kRoom;
-        int waiting = 0;
-        auto run_batch = [&](int n) {
-            float v[4], r[4];
-            int i[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const bool have = lane + 32 * e < n;
-                const u64 q = have ? queue[lane + 32 * e] : 0;
-                v[e] = have ? __uint_as_float((uint32_t)(q >> 32)) : -INFINITY;
-                i[e] = (int)(uint32_t)q;
-                r[e] = u[i[e]];
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) enter(v[e], i[e], r[e]);
-        };
-        // N tokens from `at` on per lane, -inf where there is none
-        auto take = [&](auto count, const float *w, int at) {
-            constexpr int N = decltype(count)::value;
-            float v[N];
-            uint32_t mask[N];
-            int some = 0;
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const float y = clean(w[e]);
-                const bool in = y >= floor && !(y == cut_v && at + e > cut_i);
-                v[e] = in ? y : -INFINITY;
-                mask[e] = __ballot_sync(0xffffffffu, in);
-                some += __popc(mask[e]);
-            }
-            if (some >= 16 * N) {
-                float r[N];
-#pragma unroll
-                for (int e = 0; e < N; ++e) r[e] = v[e] > -INFINITY ? u[at + e] : 0.5f;
-#pragma unroll
-                for (int e = 0; e < N; ++e) enter(v[e], at + e, r[e]);
-                return;
-            }
-            if (some == 0) return;
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                if (mask[e] == 0) continue;
-                if (v[e] > -INFINITY)
-                    queue[waiting + __popc(mask[e] & ((1u << lane) - 1))] = (u64)__float_as_uint(v[e]) << 32 | (uint32_t)(at + e);
-                waiting += __popc(mask[e]);
-                __syncwarp();
-                if (waiting >= kBatch) {
-                    run_batch(kBatch);
-                    waiting -= kBatch;
-                    const u64 rest = lane < waiting ? queue[kBatch + lane] : 0;
-                    __syncwarp();
-                    if (lane < waiting) queue[lane] = rest;
-                    __syncwarp();
-                }
-            }
-        };
-        // as each_piece, but every lane of a warp takes part in every step
-        const T *row = x + from;
-        const int head = min(to - from, (int)((16 - ((uintptr_t)row & 15)) & 15) / (int)sizeof(T)), pieces = (to - from - head) / kPer;
-        const uint4 *p4 = (const uint4 *)(row + head);
-        for (int i0 = warp * 32; i0 < pieces; i0 += 4 * kThreads) {
-            uint4 w[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int i = i0 + q * kThreads + lane;
-                // all ones: NaN in either type, never kept
-                w[q] = i < pieces ? p4[i] : make_uint4(~0u, ~0u, ~0u, ~0u);
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (i0 + q * kThreads >= pieces) break;
-                const uint32_t b[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
-                float v[kPer];
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) {
-                    if constexpr (sizeof(T) == 2) v[e] = __uint_as_float(e & 1 ? b[e / 2] & 0xffff0000u : b[e / 2] << 16);
-                    else v[e] = __uint_as_float(b[e]);
-                }
-                take(Count<kPer>(), v, from + head + (i0 + q * kThreads + lane) * kPer);
-            }
-        }
-        if (warp == 0) {  // the single tokens before and after
-            const int tail = head + pieces * kPer, i = lane < 16 ? lane : tail + lane - 16;
-            const bool have = lane < 16 ? lane < head : i < to - from;
-            const float v = have ? io<T>::ld(row + i) : -INFINITY;
-            take(Count<1>(), &v, have ? from + i : 0);
-        }
-        run_batch(waiting);
-    };
-
-    bool raced = false;
-    u64 cut = 0;  // the smallest key that top_k and top_p keep
-    if (by_k || by_p) {
-        // 2. gather what passes the threshold
-        if (!(by_k && by_p)) least = fmaxf(least, min_logit);  // with both, all of K counts in its mass
-        if (by_p && !by_k) least = fmaxf(least, logit_of((1.f - fmaxf(p, 0.f)) * total / (float)a.V, -1.f));
+    Best won = {-INFINITY, -1};
+    // Gathers the tokens from `least` up (and above the key `under`); if they fit, the first CTA cuts the list at rank k and at
+    // mass `goal` (0: at top_p of the list's first k), races what is left and writes the result.
+    auto settle_in_list = [&](float least, u64 under, u64 goal) {
         if (tid == 0) s.n = 0;
         __syncthreads();
-        each(x, from, to, least, [&](float v, int i) { return gather(s, full_key(v, i)); });
+        gather_pass(x, from, to, least, under, s);
         __syncthreads();
         if (tid == 0) s.x.gathered = min(s.n, kList + 1);
         cluster.sync();
         const int n = sum_of(from_peer.x.gathered);
-        if (n <= kList) {
-            if (rank == 0) {
-                collect();
-                const int limit = by_k ? min(n, k) : n;
-                int keep = limit;
+        if (n > kList) return false;
+        if (rank == 0) {
+            collect();
+            if (n <= 256) {
+                // every key against every other: rank and mass before it, by the kThreads / 2^m threads of a key together
+                int per = kThreads / 32;
+                while (kThreads / per < n) per /= 2;
+                if (tid < n) s.digit_sum[tid] = mass_of(value_of((uint32_t)(s.list[tid] >> 32)), top.v, rate);
+                __syncthreads();
+                const int i = tid / per;
+                const u64 key = i < n ? s.list[i] : 0;
+                int ahead = 0;
+                u64 before = 0, all;
+                for (int j = tid % per; j < n; j += per)
+                    if (s.list[j] > key) ++ahead, before += s.digit_sum[j];
+                for (int off = per / 2; off; off >>= 1) {
+                    ahead += __shfl_xor_sync(0xffffffffu, ahead, off);
+                    before += __shfl_xor_sync(0xffffffffu, before, off);
+                }
+                bool keep = tid % per == 0 && i < n && !(by_k && ahead >= k);
                 if (by_p) {
-                    const double m = by_k ? (double)in_list(limit, 0, ~0ull) : (double)total * (double)kUnit;
-                    in_list(limit, 0, goal_of(m));
-                    keep = min(limit, s.found + 1);
+                    if (goal == 0) {
+                        block_before(keep ? s.digit_sum[i] : 0, all, s);
+                        goal = goal_of((double)all);
+                    }
+                    keep = keep && before < goal;
                 }
-                for (int r = tid; r < keep; r += kThreads) {
-                    const u64 key = s.list[r];
-                    won = better(won, score(value_of((uint32_t)(key >> 32)), (int)~(uint32_t)key));
+                if (keep) won = score(value_of((uint32_t)(key >> 32)), (int)~(uint32_t)key);
+            } else {
+                u64 from_key = by_k && n > k ? select(s, n, (u64)k, false, 0, top.v, rate) : 0;
+                if (by_p) {
+                    if (goal == 0) goal = goal_of((double)mass_from(n, from_key));
+                    from_key = max(from_key, select(s, n, goal, true, from_key, top.v, rate));
                 }
-                won = block_best(won, s);
-                if (tid == 0) finish(won);
+                for (int i = tid; i < n; i += kThreads) {
+                    const u64 key = s.list[i];
+                    if (key >= from_key) won = better(won, score(value_of((uint32_t)(key >> 32)), (int)~(uint32_t)key));
+                }
             }
-            cluster.sync();
-            return;
+            won = block_best(won, s);
+            if (tid == 0) finish(won);
         }
-        // 3. histogram over y, from the largest logit down to where no cut can be below
-        const float bottom = fmaxf(fmaxf(top.v - kReach * t, low), by_p && !by_k ? least : -INFINITY);
+        cluster.sync();
+        return true;
+    };
+
+    u64 cut = 0;  // the key of the k-th token
+    u64 goal = by_p && !by_k ? goal_of((double)total * (double)kUnit) : 0;
+    if (by_k || by_p) {
+        // 2. what passes the threshold
+        if (!(by_k && by_p)) least = fmaxf(least, min_logit);  // with both, all of K counts in its mass
+        if (by_p && !by_k) least = fmaxf(least, logit_of((1.f - fmaxf(p, 0.f)) * total / (float)a.V));
+        if (settle_in_list(least, 0, goal)) return;
+    }
+    if (by_k) {
+        // 3. the k-th token, from a histogram over the logits
+        const float bottom = fmaxf(top.v - kReach * t, low);
         const bool deep = bottom == top.v - kReach * t;  // the last bin's tokens have no mass and cannot win
         const float scale = bounded((float)kBins / (top.v - bottom));
-        const float width = (top.v - bottom) / (t * kBins);  // of a bin, in y
-        auto bin_of = [&](float v) { return (int)fminf((top.v - v) * scale, (float)(kBins - 1)); };
-        // sums of weights relative to their bin's upper edge, in units that the CTA's tokens cannot overflow together
-        const float unit = (float)(1u << min(20, 31 - (32 - __clz(share))));
-        for (int i = tid; i < kBins; i += kThreads) s.count[i] = s.part[i] = 0;
-        __syncthreads();
-        each(x, from, to, by_k ? -INFINITY : least, [&](float v, int) {
-            const float d = fminf((top.v - v) * scale, (float)(kBins - 1));
-            const int bin = (int)d;
-            const float f = (d - (float)bin) * width;
-            if (by_k) atomicAdd(&s.count[bin], 1u);
-            if (by_p) atomicAdd(&s.part[bin], (uint32_t)((1.f - f + 0.5f * f * f) * unit + 0.5f));  // exp(-f)
-            return true;
-        });
-        cluster.sync();
-        {
-            // each CTA joins a range of bins for the first one: counts into its list, masses into its mass
-            const int step = kBins / ctas;
-            uint32_t *counts = (uint32_t *)cluster.map_shared_rank(s.list, 0);
-            u64 *masses = cluster.map_shared_rank(s.mass, 0);
-            for (int i = rank * step + tid; i < (rank + 1) * step; i += kThreads) {
-                uint32_t c = 0;
-                u64 m = 0;
+        // of every `stride`-th load, as long as 3 standard deviations either way stay well below the list's room
+        int stride = 8;
+        while (stride > 1 && (int64_t)stride * k > 54000) stride /= 2;
+        for (;; stride = 1) {
+            for (int i = tid; i < kBins; i += kThreads) s.count[i] = 0;
+            __syncthreads();
+            count_pass(x, from, to, stride, top.v, scale, s);
+            cluster.sync();
+            {
+                // each CTA adds up a range of bins for the first one
+                const int step = kBins / ctas;
+                uint32_t *counts = (uint32_t *)cluster.map_shared_rank(s.list, 0);
+                for (int i = rank * step + tid; i < (rank + 1) * step; i += kThreads) {
+                    uint32_t c = 0;
 #pragma unroll
-                for (int r = 0; r < kMaxCtas; ++r)
-                    if (r < ctas) c += peer(r).count[i], m += peer(r).part[i];
-                counts[i] = c;
-                masses[i] = (u64)(ex2(-(float)i * width * 1.4426950408889634f) * (kUnit / unit) * (float)m);
-            }
-        }
-        cluster.sync();
-        // the first bin whose running sum reaches `goal` (s.found, with the sum before it in s.before), or kBins
-        auto find_bin = [&](u64 goal, bool of_mass) {
-            constexpr int kEach = kBins / kThreads;
-            u64 own = 0, all;
-            const uint32_t *counts = (const uint32_t *)s.list;
-            for (int e = 0; e < kEach; ++e) own += of_mass ? s.mass[tid * kEach + e] : counts[tid * kEach + e];
-            u64 at = block_before(own, all, s);
-            if (tid == 0 && all < goal) s.found = kBins;
-            if (at < goal && at + own >= goal) {
-                int e = 0;
-                for (;; ++e) {
-                    const u64 y = of_mass ? s.mass[tid * kEach + e] : counts[tid * kEach + e];
-                    if (at + y >= goal) break;
-                    at += y;
+                    for (int r = 0; r < kMaxCtas; ++r)
+                        if (r < ctas) c += peer(r).count[i];
+                    counts[i] = c;
                 }
-                s.found = tid * kEach + e;
-                s.before = at;
             }
-            __syncthreads();
-        };
-        // the first CTA's decisions
-        int bin_k = kBins, rank_k = 0;
-        bool want_p = false, slow = false;
-        u64 goal = 0;
-        auto set_plan = [&](int lo, int hi) {
-            if (tid == 0) s.x.lo = lo, s.x.hi = hi, s.x.cut = cut;
-        };
-        auto plan_p = [&](int limit) {  // the bins that may hold the end of the mass `goal`: sums are good to 2^-16
-            find_bin(max((u64)((double)goal * (1.0 - 1.0 / 32768)), 1ull), true);
-            const int lo = s.found;
-            __syncthreads();
-            find_bin((u64)((double)goal * (1.0 + 1.0 / 32768)) + 1, true);
-            const int hi = min(min(s.found, kBins - 1), limit);
-            __syncthreads();
-            want_p = true;
-            if (lo > hi) set_plan(-1, 0);  // less mass than that in all: everything stays
-            else set_plan(lo, hi);
-        };
-        if (rank == 0) {
-            if (by_k) {
-                find_bin((u64)k, false);
-                bin_k = s.found;
-                rank_k = k - (int)s.before;
-                if (deep && bin_k == kBins - 1) bin_k = kBins;  // all that matters is in K
-                __syncthreads();
+            cluster.sync();
+            if (rank == 0) {
+                // the first bin whose running count reaches `nth`, or the last
+                auto find_bin = [&](u64 nth) {
+                    constexpr int kEach = kBins / kThreads;
+                    const uint32_t *counts = (const uint32_t *)s.list;
+                    u64 own = 0, all;
+                    for (int e = 0; e < kEach; ++e) own += counts[tid * kEach + e];
+                    u64 at = block_before(own, all, s);
+                    if (tid == 0) s.found = kBins - 1;
+                    __syncthreads();
+                    if (at < nth && at + own >= nth) {
+                        int e = 0;
+                        while ((at += counts[tid * kEach + e]) < nth) ++e;
+                        s.found = tid * kEach + e;
+                    }
+                    __syncthreads();
+                    const int bin = s.found;
+                    __syncthreads();
+                    return bin;
+                };
+                const float mid = (float)k / (float)stride, off = stride > 1 ? 3.2f * sqrtf(mid) + 2.f : 0.f;
+                const int lo = find_bin((u64)fmaxf(stride > 1 ? mid - off : (float)k, 1.f)), hi = stride > 1 ? find_bin((u64)(mid + off)) : lo;
+                if (tid == 0) s.x.lo = lo, s.x.hi = hi;
             }
-            if (bin_k < kBins) set_plan(bin_k, bin_k);
-            else if (by_p) goal = goal_of((double)total * (double)kUnit), plan_p(kBins - 1 - deep);
-            else set_plan(-1, 0);  // K is every token that can win
-        }
-        for (;;) {
             cluster.sync();
             const int lo = peer(0).x.lo, hi = peer(0).x.hi;
-            cut = peer(0).x.cut;
-            if (lo < 0) break;
-            u64 above = 0;
             if (tid == 0) s.n = 0;
             __syncthreads();
-            each_piece(x, from, to, [&](const float *w, auto n, int at) {
-                constexpr int N = decltype(n)::value;
-                float y = 0.f;
-#pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    const float v = clean(w[e]);
-                    const int bin = bin_of(v);  // of -inf: the last
-                    if (bin < lo) y += ex2((v - top.v) * rate);
-                    else if (bin <= hi && v > -INFINITY) gather(s, full_key(v, at + e));
-                }
-                if (by_p) above += (u64)(y * kUnit + 0.5f);
-                return true;
-            });
-            u64 all = 0;
-            block_before(above, all, s);
-            if (tid == 0) s.x.gathered = min(s.n, kList + 1), s.x.mass = all;
+            const Above above = bracket_pass(x, from, to, lo, hi, top.v, scale, rate, s);
+            u64 all_mass, all_above;
+            block_before((u64)(above.mass * kUnit + 0.5f), all_mass, s);
+            block_before((u64)above.n, all_above, s);
+            if (tid == 0) s.x.gathered = min(s.n, kList + 1), s.x.mass = all_mass, s.x.above = (int)all_above;
             cluster.sync();
-            if (rank != 0) continue;
-            above = sum_of(from_peer.x.mass);
-            if (!collect()) {
-                slow = true;
-            } else if (!want_p) {
-                cut = s.list[rank_k - 1];
-                if (!by_p) {
-                    set_plan(-1, 0);
+            if (rank == 0) {
+                const int before = sum_of(from_peer.x.above), n = sum_of(from_peer.x.gathered);
+                const u64 mass_before = sum_of(from_peer.x.mass);
+                bool settled = true;
+                u64 mass_k = (u64)((double)total * (double)kUnit);
+                if (before < k && hi == kBins - 1 && (n <= kList ? before + n < k : deep && lo == hi)) {
+                    // K is every finite logit, or ends among those of no mass: all that matters is in it
+                } else if (before < k && n <= kList && before + n >= k) {
+                    collect();
+                    cut = select(s, n, (u64)(k - before), false, 0, top.v, rate);
+                    mass_k = mass_before + mass_from(n, cut);
+                } else if (stride > 1) {
+                    settled = false;  // outside the bracket, or too many in it
                 } else {
-                    goal = goal_of((double)in_list(rank_k, above, ~0ull));
-                    if (goal > above) {
-                        in_list(rank_k, above, goal);
-                        cut = s.list[min(s.found, rank_k - 1)];
-                        set_plan(-1, 0);
-                    } else {
-                        plan_p(bin_k - 1);
-                    }
-                }
-            } else {
-                const u64 end = in_list(s.n, above, goal);
-                // outside what the bins' sums allow for (a bin of over 2^21 tokens, say): settle it exactly
-                if (above >= goal || s.n == 0 || (end < goal && hi < min(kBins - deep, bin_k) - 1)) slow = true;
-                else cut = s.list[min(s.found, s.n - 1)];
-                set_plan(-1, 0);
-            }
-            if (slow) {
-                // 4. digit by digit: the key of the last token of the shortest descending prefix, among keys >= floor, whose
-                // measure (tokens, or mass) reaches goal
-                auto descend = [&](u64 goal, bool of_mass, u64 floor) {
-                    u64 prefix = 0, before = 0;
+                    // digit by digit: the key of the k-th token
+                    u64 prefix = 0;
+                    int rank_left = k;
                     for (int shift = 56; shift >= 0; shift -= 8) {
                         __syncthreads();
-                        if (tid < 256) s.mass[tid] = 0;
+                        if (tid < 256) s.digit_count[tid] = 0;
                         __syncthreads();
                         each(x, 0, a.V, -INFINITY, [&](float v, int i) {
                             const u64 key = full_key(v, i);
-                            if (key >= floor && (shift == 56 || (key >> (shift + 8)) == prefix))
-                                atomicAdd(&s.mass[(key >> shift) & 255], of_mass ? mass(v) : 1ull);
+                            if (shift == 56 || (key >> (shift + 8)) == prefix) atomicAdd(&s.digit_count[(key >> shift) & 255], 1u);
                             return true;
                         });
                         __syncthreads();
                         if (tid == 0) {
-                            u64 at = before;
-                            int d = 255;
-                            for (; d > 0 && at + s.mass[d] < goal; --d) at += s.mass[d];
-                            s.digit = d;
-                            s.before = at;
+                            int left = rank_left, d = 255;
+                            for (; d > 0 && (int)s.digit_count[d] < left; --d) left -= (int)s.digit_count[d];
+                            s.before = d;
+                            s.found = left;
                         }
                         __syncthreads();
-                        prefix = prefix << 8 | s.digit;
-                        before = s.before;
+                        prefix = prefix << 8 | s.before;
+                        rank_left = s.found;
                     }
-                    return prefix;
-                };
-                cut = bin_k < kBins ? descend((u64)k, false, 0) : 0;
-                if (by_p) {
+                    cut = prefix;
                     u64 own = 0;
                     each(x, 0, a.V, -INFINITY, [&](float v, int i) {
-                        if (full_key(v, i) >= cut) own += mass(v);
+                        if (full_key(v, i) >= cut) own += mass_of(v, top.v, rate);
                         return true;
                     });
-                    block_before(own, all, s);
-                    const u64 c = descend(min(goal_of((double)all), all), true, cut);
-                    cut = c > cut ? c : cut;
+                    block_before(own, mass_k, s);
                 }
-                set_plan(-1, 0);
+                if (tid == 0) s.x.settled = settled, s.x.cut = cut, s.x.mass_k = mass_k;
             }
+            cluster.sync();
+            if (!peer(0).x.settled) continue;
+            cut = peer(0).x.cut;
+            if (by_p) goal = goal_of((double)peer(0).x.mass_k);
+            break;
         }
     }
-
-    // 5. the race over the row
-    if (!raced) {
-        race_from(cut);
-        __syncthreads();  // list and mass are free
-        race_tokens();
-    }
-    if (lead.i >= 0) won = better(won, score(clean(io<T>::ld(x + lead.i)), lead.i));
-    won = block_best(won, s);
-    if (tid == 0) s.x.won = won;
-    cluster.sync();
-    if (rank == 0 && warp == 0) {
+    // 4. the race over K, until its winner is in top_p's prefix
+    // from the largest token, which is always kept, on
+    const uint32_t same = __ballot_sync(0xffffffffu, lane < kPer && top.i + lane < a.V && clean(io<T>::ld(x + top.i + lane)) == top.v);
+    const Best first = score(top.v, top.i + __ffs(same) - 1);
+    for (;;) {
+        // no Gumbel is above 16.64
+        const float floor = fmaxf(fmaxf(min_logit, top.v + t * (first.v - 16.7f) - 1e-5f * fabsf(top.v)), cut ? value_of((uint32_t)(cut >> 32)) : -INFINITY);
+        const Track track = {u, top.v, t, rate, min_p, fmaxf(floor, -3.402823466e38f), 1.01f * ex2(first.v * -1.4426950408889634f), cut};
+        won = race_pass(x, from, to, track, first);
+        won = block_best(won, s);
+        if (tid == 0) s.x.won = won;
+        cluster.sync();
         won = best_of(from_peer.x.won);
-        if (tid == 0) finish(won);
+        if (!by_p || won.i < 0) break;
+        const float won_v = clean(io<T>::ld(x + won.i));
+        const u64 won_key = full_key(won_v, won.i);
+        u64 all;
+        block_before((u64)(mass_pass(x, from, to, won_v, won.i, top.v, rate) * kUnit + 0.5f), all, s);
+        if (tid == 0) s.x.mass = all;
+        cluster.sync();
+        if (sum_of(from_peer.x.mass) < goal) break;  // kept
+        cut = won_key + 1;  // the next key up: the winner and what is below it are not kept
+        won = {-INFINITY, -1};
+        if (settle_in_list(won_v, won_key, goal)) return;
     }
+    if (rank == 0 && tid == 0) finish(won);
     cluster.sync();
 }
 
 }  // namespace
 
 cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream) {
-    // CTAs per row: double while all rows' CTAs fit the GPU at once (152 SMs, two CTAs each) and a CTA has 4096 tokens
-    // left.  Past one wave it costs: 256 rows of 100003 with top_k 50 and top_p 0.9 take 43 us on one CTA each, 59 on
-    // two; 32 rows of 131072 take 24 us on eight.
+    // CTAs per row: double while all rows' CTAs make two waves at most (152 SMs, four CTAs each) and a CTA has 4096 tokens
+    // left.  At 256 rows of 100003, on one, two, four and eight CTAs each: rows alike, with top_k 50 and top_p 0.9, take 53, 39,
+    // 47 and 77 us, rows of mixed settings 317, 202, 134 and 121 us, where the few flat rows' CTAs run on alone.  Four of 256
+    // threads to an SM against two of 512: 32 rows of 131072 take 17.8 us against 20.1.
     int ctas = 1;
-    while (ctas < kMaxCtas && (int64_t)a.B * ctas * 2 <= 304 && a.V / (2 * ctas) >= 4096) ctas *= 2;
+    while (ctas < kMaxCtas && (int64_t)a.B * ctas * 2 <= 1216 && a.V / (2 * ctas) >= 4096) ctas *= 2;
     auto go = [&](auto kern) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
         if (e != cudaSuccess) return e;
