@@ -77,13 +77,15 @@ struct Cfg {
     static constexpr int kTok = 16 * kSub;            // tokens of a warp's slice
     static constexpr int kTile = kTok * kWarps;       // tokens of a tile
     static constexpr int kHalf = kTok * kRow;          // bytes of one warp's K (or V) slice
-    // CTAs per SM and ring slots of half a slice (K or V) per warp.  Warps hide each other's waits, so as many CTAs as
-    // shared memory holds with three slots and the registers allow (8 more heads or 256 dims of output per warp take
-    // twice the registers); what is left deepens the ring.
-    static constexpr int kOcc = kHalf > 8192 && NT == 2 ? 1 : NT == 2 || D == 256 || kHalf > 4096 ? 2 : kHalf > 2048 ? 3 : 4;
-    static constexpr int kSlots = kOcc == 1 ? 6 : kHalf > 4096 ? 3 : kOcc == 2 ? (kHalf > 2048 ? 6 : 8) : kOcc == 3 ? 4 : kHalf > 1024 ? 5 : 8;
+    // CTAs per SM and ring slots of half a slice (K or V) per warp.  Warps hide each other's waits, so as many CTAs as the
+    // registers allow (16 heads, or 256 dims, of output per warp take twice the registers of 8 heads of 128) with three
+    // slots or more; what shared memory is left deepens the ring.  Measured against one CTA less per SM: 32 x 8192 bf16 tokens of
+    // 64 dims 56 -> 53 us, 64 x 8192 of 128 dims 175 -> 170, of 64 dims for 16 heads 66 -> 60, 16 x 8192 fp32 138 -> 99.
+    static constexpr int kOcc = kHalf > 8192 && NT == 2 ? 1 : kHalf > 4096 || D == 256 ? 2
+                                : NT == 2 ? (D == 64 && KIND != GDN_F32 ? 3 : 2) : kHalf > 2048 ? (KIND == GDN_BF16 && D == 64 ? 4 : 3) : 4;
+    static constexpr int kSlots = kOcc == 1 ? 6 : kHalf > 4096 ? 3 : kOcc == 2 ? (kHalf > 2048 ? 6 : 8) : kOcc == 3 ? 4 : kHalf > 2048 ? 3 : kHalf > 1024 ? 5 : 8;
     static constexpr int kRing = kSlots * kHalf;      // per warp
-    static constexpr int kMergeDims = KIND == GDN_F32 && NT == 2 ? 32 : 64;  // output dims joined per round at a row's end
+    static constexpr int kMergeDims = (KIND == GDN_F32 && NT == 2) || (kOcc == 4 && kHalf > 2048) ? 32 : 64;  // output dims joined per round at a row's end
     static constexpr int kMerge = kWarps * 8 * (kMergeDims + 4) * 4;
     static constexpr int kQ = KIND == GDN_F32 ? NT * (D / 8) * 32 * 8 : 0;
     static constexpr int kSmem = kWarps * kRing + kMerge + kWarps * NT * 8 * 8 + kQ + kWarps * kSlots * 4;
