@@ -40,6 +40,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCtas = 8;   // per row: the largest cluster every GPU of this kind can place
 constexpr int kList = 2048;   // gathered tokens
 constexpr int kBins = 2048;
+constexpr int kRounds = 9;    // races before the end of top_p's prefix is looked for
 constexpr float kUnit = 1099511627776.f;  // 2^40
 constexpr float kReach = 28.f;            // in y: 40 ln 2, below which a mass rounds to 0
 using u64 = unsigned long long;
@@ -371,9 +372,9 @@ __device__ __noinline__ Above bracket_pass(const T *x, int from, int to, int lo,
     return a;
 }
 
-// Mass (in weights) of the tokens before token i, of logit `mark`, in descending order.
+// Mass (in weights) of the tokens before one of logit `mark` and index i, in descending order.
 template <typename T>
-__device__ __noinline__ float mass_pass(const T *x, int from, int to, float mark, int i, float top, float rate) {
+__device__ __noinline__ float mass_pass(const T *x, int from, int to, float mark, uint32_t i, float top, float rate) {
     float sum = 0.f;
     each_piece(x, from, to, [&](const float *w, auto n, int at) {
         constexpr int N = decltype(n)::value;
@@ -381,11 +382,39 @@ __device__ __noinline__ float mass_pass(const T *x, int from, int to, float mark
 #pragma unroll
         for (int e = 0; e < N; ++e) {
             const float v = clean(w[e]);
-            if (v > mark || (v == mark && at + e < i)) sum += ex2((v - top) * rate);
+            if (v > mark || (v == mark && (uint32_t)(at + e) < i)) sum += ex2((v - top) * rate);
         }
         return true;
     });
     return sum;
+}
+
+// By one CTA over a whole row, digit by digit: the key of the k-th token.
+template <typename T>
+__device__ __noinline__ u64 kth_key(const T *x, int V, int k, Shared &s) {
+    u64 prefix = 0, before = 0;
+    for (int shift = 56; shift >= 0; shift -= 8) {
+        __syncthreads();
+        for (int d = threadIdx.x; d < 256; d += kThreads) s.digit_count[d] = 0;
+        __syncthreads();
+        each(x, 0, V, -INFINITY, [&](float v, int i) {
+            const u64 key = full_key(v, i);
+            if (shift == 56 || (key >> (shift + 8)) == prefix) atomicAdd(&s.digit_count[(key >> shift) & 255], 1u);
+            return true;
+        });
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            int d = 255;
+            u64 at = before;
+            for (; d > 0 && at + s.digit_count[d] < (u64)k; --d) at += s.digit_count[d];
+            s.found = d;
+            s.before = at;
+        }
+        __syncthreads();
+        prefix = prefix << 8 | (u64)s.found;
+        before = s.before;
+    }
+    return prefix;
 }
 
 // The race.  A token beats the score `best` only if -log u <= w exp(-best), and 1 - u <= -log u: one comparison, with room
@@ -542,7 +571,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
     auto finish = [&](Best won) {  // thread 0 of the first CTA
         if (won.i < 0 && top.i >= 0) {  // greedy, or min_p above 1 leaves nothing: the largest
             won = top;
-            while (clean(io<T>::ld(x + won.i)) != top.v) ++won.i;  // within its load
+            for (int e = kPer - 1; e >= 0; --e)  // within its load
+                if (top.i + e < a.V && clean(io<T>::ld(x + top.i + e)) == top.v) won.i = top.i + e;
         }
         a.tokens[b] = won.i;
         if (a.logprobs) a.logprobs[b] = won.i < 0 ? -INFINITY : greedy ? 0.f : (clean(io<T>::ld(x + won.i)) - top.v) / t - logf(total);
@@ -723,30 +753,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
                 } else if (stride > 1) {
                     settled = false;  // outside the bracket, or too many in it
                 } else {
-                    // digit by digit: the key of the k-th token
-                    u64 prefix = 0;
-                    int rank_left = k;
-                    for (int shift = 56; shift >= 0; shift -= 8) {
-                        __syncthreads();
-                        if (tid < 256) s.digit_count[tid] = 0;
-                        __syncthreads();
-                        each(x, 0, a.V, -INFINITY, [&](float v, int i) {
-                            const u64 key = full_key(v, i);
-                            if (shift == 56 || (key >> (shift + 8)) == prefix) atomicAdd(&s.digit_count[(key >> shift) & 255], 1u);
-                            return true;
-                        });
-                        __syncthreads();
-                        if (tid == 0) {
-                            int left = rank_left, d = 255;
-                            for (; d > 0 && (int)s.digit_count[d] < left; --d) left -= (int)s.digit_count[d];
-                            s.before = d;
-                            s.found = left;
-                        }
-                        __syncthreads();
-                        prefix = prefix << 8 | s.before;
-                        rank_left = s.found;
-                    }
-                    cut = prefix;
+                    cut = kth_key(x, a.V, k, s);
                     u64 own = 0;
                     each(x, 0, a.V, -INFINITY, [&](float v, int i) {
                         if (full_key(v, i) >= cut) own += mass_of(v, top.v, rate);
@@ -767,26 +774,42 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
     // from the largest token, which is always kept, on
     const uint32_t same = __ballot_sync(0xffffffffu, lane < kPer && top.i + lane < a.V && clean(io<T>::ld(x + top.i + lane)) == top.v);
     const Best first = score(top.v, top.i + __ffs(same) - 1);
-    for (;;) {
-        // no Gumbel is above 16.64
-        const float floor = fmaxf(fmaxf(min_logit, top.v + t * (first.v - 16.7f) - 1e-5f * fabsf(top.v)), cut ? value_of((uint32_t)(cut >> 32)) : -INFINITY);
-        const Track track = {u, top.v, t, rate, min_p, fmaxf(floor, -3.402823466e38f), 1.01f * ex2(first.v * -1.4426950408889634f), cut};
-        won = race_pass(x, from, to, track, first);
-        won = block_best(won, s);
-        if (tid == 0) s.x.won = won;
-        cluster.sync();
-        won = best_of(from_peer.x.won);
-        if (!by_p || won.i < 0) break;
-        const float won_v = clean(io<T>::ld(x + won.i));
-        const u64 won_key = full_key(won_v, won.i);
+    // Noise that goes with the logits' order could have winner after winner rejected: from the ninth on the keys between the last
+    // and the largest are halved instead, 64 times at most, and the race is run once more from the end of the prefix.
+    bool verify = by_p;
+    u64 kept = full_key(top.v, 0);  // keys from here on are kept
+    for (int round = 0;; ++round) {
+        const bool racing = round < kRounds || !verify;
+        u64 probe = cut + (kept - cut) / 2;
+        if (racing) {
+            // no Gumbel is above 16.64
+            const float floor = fmaxf(fmaxf(min_logit, top.v + t * (first.v - 16.7f) - 1e-5f * fabsf(top.v)), cut ? value_of((uint32_t)(cut >> 32)) : -INFINITY);
+            const Track track = {u, top.v, t, rate, min_p, fmaxf(floor, -3.402823466e38f), 1.01f * ex2(first.v * -1.4426950408889634f), cut};
+            won = race_pass(x, from, to, track, first);
+            won = block_best(won, s);
+            if (tid == 0) s.x.won = won;
+            cluster.sync();
+            won = best_of(from_peer.x.won);
+            if (!verify || won.i < 0) break;
+            probe = full_key(clean(io<T>::ld(x + won.i)), won.i);
+        }
         u64 all;
-        block_before((u64)(mass_pass(x, from, to, won_v, won.i, top.v, rate) * kUnit + 0.5f), all, s);
+        block_before((u64)(mass_pass(x, from, to, value_of((uint32_t)(probe >> 32)), ~(uint32_t)probe, top.v, rate) * kUnit + 0.5f), all, s);
         if (tid == 0) s.x.mass = all;
         cluster.sync();
-        if (sum_of(from_peer.x.mass) < goal) break;  // kept
-        cut = won_key + 1;  // the next key up: the winner and what is below it are not kept
-        won = {-INFINITY, -1};
-        if (settle_in_list(won_v, won_key, goal)) return;
+        if (sum_of(from_peer.x.mass) < goal) {
+            if (racing) break;
+            kept = probe;
+        } else {
+            cut = probe + 1;  // the probe and what is below it are not kept
+        }
+        if (racing) {
+            won = {-INFINITY, -1};
+            if (settle_in_list(value_of((uint32_t)(probe >> 32)), probe, goal)) return;
+        } else if (cut >= kept) {
+            cut = kept;
+            verify = false;
+        }
     }
     if (rank == 0 && tid == 0) finish(won);
     cluster.sync();

@@ -8,7 +8,8 @@ passed as its ``transpose(1, 2)`` view.  An 8-bit cache is a pair of
 These calls run once per layer and token, so the marshalling is kept short:
 each check reads a tensor's attributes once, and the default workspace belongs
 to one device and stream.  Every call is enqueued on `stream` (default: the
-current stream of the tensors' device) and returns without waiting.
+current stream of the tensors' device) and returns without waiting.  For a call
+inside a CUDA graph pass the outputs and a workspace that outlive the graph.
 """
 from __future__ import annotations
 
@@ -73,6 +74,8 @@ def _workspace(ws, nbytes, dev, handle, other):
         return buf.data_ptr(), buf.numel()
     if isinstance(ws, Workspace):
         ws = ws.get(nbytes, dev)
+        if other is not None:
+            ws.record_stream(other)
     if ws.device != dev:
         raise ValueError(f"workspace must be on {dev}, is on {ws.device}")
     return ws.data_ptr(), ws.numel() * ws.element_size()

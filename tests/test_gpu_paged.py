@@ -603,3 +603,29 @@ def test_refusals():
         gdn.gdn_kv_append(k, k, torch.zeros(3, dtype=torch.int64, device=dev()), s["k_cache"], s["v_cache"])
     with pytest.raises(ValueError):
         gdn.gdn_kv_append(k[:2], k[:2], torch.zeros(3, dtype=torch.int64, device=dev()), s["k_cache"], s["v_cache"])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_sample_noise_in_the_logits_order(kind):
+    # the race's best are outside the kept prefix again and again, in rows too flat for their prefix to be gathered
+    V = 60000
+    x = torch.linspace(0.0, -2.0, V, device=dev()).to(TYPES[kind]).repeat(4, 1)
+    u = torch.linspace(0.0, 1.0, V, device=dev()).repeat(4, 1)
+    check_sample(x, u, t=[1.0, 1.0, 0.5, 2.0], p=[0.5, 0.9, 0.3, 0.01])
+    check_sample(x, u, k=[30000, 0, 50000, 5000], p=[0.5, 0.2, 0.7, 0.9])
+    check_sample(x.flip(1).contiguous(), u, k=[30000, 0, 50000, 5000], p=[0.5, 0.2, 0.7, 0.9])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("spread", [0.05, 1.0, 8.0])
+def test_sample_flat_and_sharp_rows_with_large_k(kind, spread):
+    g = torch.Generator(device=dev()).manual_seed(int(spread * 100))
+    B, V = 12, 70001
+    x = (spread * torch.randn((B, V), device=dev(), generator=g)).to(TYPES[kind])
+    x[3, 1000:] = -math.inf
+    x[4, ::3] = float(x[4].float().max())            # a third of the row in one tie
+    u = torch.rand((B, V), device=dev(), generator=g)
+    for k in ([600, 5000, 20000, 900, 30000, 69000, 2048, 2049, 4096, 513, 257, 70000],):
+        check_sample(x, u, k=k)
+        check_sample(x, u, k=k, p=[0.9, 0.5, 0.99, 0.7, 0.3, 0.05, 0.8, 0.9, 0.95, 0.6, 0.4, 0.2])
+        check_sample(x, u, t=[1.5] * B, k=k, p=[0.7] * B, m=[0.0, 0.01, 0.1] * 4)
