@@ -22,68 +22,65 @@ from ._binding import GDN_BF16, GDN_E4M3, GDN_F32, GdnKvCache, Workspace, _check
 
 _CODES = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
 _CACHE_CODES = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32, torch.float8_e4m3fn: GDN_E4M3}
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 _ws = {}        # the default workspaces, by device and stream
 _ws_bytes = {}  # answers of gdn_paged_decode_workspace_bytes
 _current_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
+_empty = torch.empty
 
 
-def _want(t, name, dtype, shape, device):
-    """A contiguous tensor of this type, shape and device; returns its address."""
+def _want(t, name, dtype, shape, dev):
+    """A contiguous tensor of this type, shape and CUDA device number; returns its address."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, is on {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, is on {t.device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _cuda(t, name):
-    dev = t.device
-    if dev.type != "cuda":
+    """The number of a tensor's CUDA device."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
     return dev
 
 
-def _handle(dev, stream):
-    """The call's stream as an address, and that stream if it is not the device's current one: memory that torch
-    hands out for the current stream is then recorded on it, so that it is not reused while the call still runs."""
-    current = _current_stream(dev.index)
+def _handle(dev, stream, *outputs):
+    """The call's stream as an address.  Outputs that torch has handed out for the current stream are recorded on
+    another one, so that their memory is not reused while the call still runs."""
+    current = _current_stream(dev)
     if stream is None or stream.cuda_stream == current:
-        return current, None
-    return stream.cuda_stream, stream
+        return current
+    for t in outputs:
+        t.record_stream(stream)
+    return stream.cuda_stream
 
 
-def _empty(shape, dtype, dev, other):
-    t = torch.empty(shape, dtype=dtype, device=dev)
-    if other is not None:
-        t.record_stream(other)
-    return t
-
-
-def _workspace(ws, nbytes, dev, handle, other):
+def _workspace(ws, nbytes, dev, handle, stream):
     """(address, bytes) of the caller's workspace, or of this device and stream's own."""
     if ws is None:
-        key = (dev.index, handle)
-        buf = _ws.get(key)
+        buf = _ws.get((dev, handle))
         if buf is None or buf.numel() < nbytes:
-            buf = _ws[key] = _empty((nbytes,), torch.uint8, dev, other)
+            buf = _ws[dev, handle] = _empty((nbytes,), dtype=torch.uint8, device=torch.device("cuda", dev))
+            _handle(dev, stream, buf)
         return buf.data_ptr(), buf.numel()
     if isinstance(ws, Workspace):
-        ws = ws.get(nbytes, dev)
-        if other is not None:
-            ws.record_stream(other)
-    if ws.device != dev:
-        raise ValueError(f"workspace must be on {dev}, is on {ws.device}")
+        ws = ws.get(nbytes, torch.device("cuda", dev))
+        _handle(dev, stream, ws)
+    if ws.get_device() != dev:
+        raise ValueError(f"workspace must be on cuda:{dev}, is on {ws.device}")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def _call(name, dev, *args):
     fn = getattr(_binding._lib or load(), name)
-    if _current_device() == dev.index:
+    if _current_device() == dev:
         rc = fn(*args)
     else:
         with torch.cuda.device(dev):
@@ -94,16 +91,16 @@ def _call(name, dev, *args):
 
 def _cache(k, v, k_scale, v_scale, dev):
     """The C description of a cache, checked."""
-    if k.dim() != 4:
-        raise ValueError(f"k_cache must have 4 dimensions [pages, page, kv_heads, dim], got {k.dim()}")
-    shape, stride = k.shape, k.stride()
-    code = _CACHE_CODES.get(k.dtype)
+    shape, stride, kind = k.shape, k.stride(), k.dtype
+    if len(shape) != 4:
+        raise ValueError(f"k_cache must have 4 dimensions [pages, page, kv_heads, dim], got {len(shape)}")
+    code = _CACHE_CODES.get(kind)
     if code is None:
-        raise TypeError(f"k_cache must be bfloat16, float32 or float8_e4m3fn, got {k.dtype}")
-    if v.dtype is not k.dtype or v.shape != shape or v.stride() != stride:
+        raise TypeError(f"k_cache must be bfloat16, float32 or float8_e4m3fn, got {kind}")
+    if v.dtype is not kind or v.shape != shape or v.stride() != stride:
         raise ValueError("v_cache must have k_cache's dtype, shape and strides")
-    if k.device != dev or v.device != dev:
-        raise ValueError(f"the cache must be on {dev}")
+    if k.get_device() != dev or v.get_device() != dev:
+        raise ValueError(f"the cache must be on cuda:{dev}")
     pages, page, heads, d = shape
     if stride[3] != 1:
         raise ValueError("the cache's last dimension must be contiguous")
@@ -111,7 +108,7 @@ def _cache(k, v, k_scale, v_scale, dev):
     if code == GDN_E4M3:
         if k_scale is None or v_scale is None:
             raise ValueError("an 8-bit cache needs k_scale and v_scale")
-        ks, vs = (_want(t, n, torch.float32, (heads,), dev) for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")))
+        ks, vs = _want(k_scale, "k_scale", _F32, (heads,), dev), _want(v_scale, "v_scale", _F32, (heads,), dev)
     elif k_scale is not None or v_scale is not None:
         raise ValueError("k_scale and v_scale belong to an 8-bit cache")
     return GdnKvCache(k.data_ptr(), v.data_ptr(), stride[0], stride[1], stride[2], ks, vs, pages, page, heads, d, code)
@@ -133,20 +130,24 @@ def gdn_page_tables(new_lens, free_pages, block_table, *, page, cached_lens=None
         if slots is None:
             raise ValueError("gdn_page_tables needs n_slots or slots")
         n_slots = slots.numel()
-    i32 = torch.int32
-    handle, other = _handle(dev, stream)
-    cached = None if cached_lens is None else _want(cached_lens, "cached_lens", i32, (B,), dev)
-    slots = _empty((n_slots,), torch.int64, dev, other) if slots is None else slots
-    positions = _empty((n_slots,), i32, dev, other) if positions is None else positions
-    seq_lens = _empty((B,), i32, dev, other) if seq_lens is None else seq_lens
-    cu_new = _empty((B + 1,), i32, dev, other) if cu_new is None else cu_new
-    counts = _empty((4,), i32, dev, other) if counts is None else counts
+    device = block_table.device
+    if slots is None:
+        slots = _empty((n_slots,), dtype=_I64, device=device)
+    if positions is None:
+        positions = _empty((n_slots,), dtype=_I32, device=device)
+    if seq_lens is None:
+        seq_lens = _empty((B,), dtype=_I32, device=device)
+    if cu_new is None:
+        cu_new = _empty((B + 1,), dtype=_I32, device=device)
+    if counts is None:
+        counts = _empty((4,), dtype=_I32, device=device)
     n_free = free_pages.numel()
-    _call("gdn_page_tables", dev, B, page, max_pages, cached, _want(new_lens, "new_lens", i32, (B,), dev),
-          _want(free_pages, "free_pages", i32, (n_free,), dev), n_free,
-          _want(block_table, "block_table", i32, (B, max_pages), dev), _want(seq_lens, "seq_lens", i32, (B,), dev),
-          _want(cu_new, "cu_new", i32, (B + 1,), dev), _want(slots, "slots", torch.int64, (n_slots,), dev),
-          _want(positions, "positions", i32, (n_slots,), dev), n_slots, _want(counts, "counts", i32, (4,), dev), handle)
+    _call("gdn_page_tables", dev, B, page, max_pages, None if cached_lens is None else _want(cached_lens, "cached_lens", _I32, (B,), dev),
+          _want(new_lens, "new_lens", _I32, (B,), dev), _want(free_pages, "free_pages", _I32, (n_free,), dev), n_free,
+          _want(block_table, "block_table", _I32, (B, max_pages), dev), _want(seq_lens, "seq_lens", _I32, (B,), dev),
+          _want(cu_new, "cu_new", _I32, (B + 1,), dev), _want(slots, "slots", _I64, (n_slots,), dev),
+          _want(positions, "positions", _I32, (n_slots,), dev), n_slots, _want(counts, "counts", _I32, (4,), dev),
+          _handle(dev, stream, slots, positions, seq_lens, cu_new, counts))
     return slots, positions, seq_lens, cu_new, counts
 
 
@@ -154,7 +155,7 @@ def gdn_page_tables_status(counts, stream=None) -> int:
     """Status of a gdn_page_tables call from its counts (synchronises the stream): 0, or
     9 (GDN_ERR_CAPACITY) if the free list, the table or the slot map was too short."""
     dev = _cuda(counts, "counts")
-    return int(load().gdn_page_tables_status(_want(counts, "counts", torch.int32, (4,), dev), _handle(dev, stream)[0]))
+    return int(load().gdn_page_tables_status(_want(counts, "counts", _I32, (4,), dev), _handle(dev, stream)))
 
 
 def gdn_kv_append(k, v, slots, k_cache, v_cache, *, k_scale=None, v_scale=None, stream=None):
@@ -168,13 +169,13 @@ def gdn_kv_append(k, v, slots, k_cache, v_cache, *, k_scale=None, v_scale=None, 
     n = slots.numel()
     if k.shape != (n, c.Hkv, c.d) or v.shape != k.shape:
         raise ValueError(f"k and v must be [{n}, {c.Hkv}, {c.d}], got {tuple(k.shape)} and {tuple(v.shape)}")
-    if k.device != dev or v.device != dev:
-        raise ValueError(f"k and v must be on {dev}")
+    if k.get_device() != dev or v.get_device() != dev:
+        raise ValueError(f"k and v must be on cuda:{dev}")
     ks, vs = k.stride(), v.stride()
     if ks[2] != 1 or vs[2] != 1:
         raise ValueError("the last dimension of k and v must be contiguous")
     _call("gdn_kv_append", dev, c, n, code, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
-          _want(slots, "slots", torch.int64, (n,), dev), _handle(dev, stream)[0])
+          _want(slots, "slots", _I64, (n,), dev), _handle(dev, stream))
 
 
 def gdn_paged_decode(q, k_cache, v_cache, block_table, seq_lens, *, k_scale=None, v_scale=None, scale=None, window=0,
@@ -195,31 +196,31 @@ def gdn_paged_decode(q, k_cache, v_cache, block_table, seq_lens, *, k_scale=None
     qs, ts = q.stride(), block_table.stride()
     if qs[2] != 1:
         raise ValueError("the last dimension of q must be contiguous")
-    if block_table.dtype is not torch.int32:
+    if block_table.dtype is not _I32:
         raise TypeError(f"block_table must be int32, got {block_table.dtype}")
-    if block_table.device != dev:
-        raise ValueError(f"block_table must be on {dev}, is on {block_table.device}")
+    if block_table.get_device() != dev:
+        raise ValueError(f"block_table must be on cuda:{dev}, is on {block_table.device}")
     rows, max_pages = block_table.shape
     if rows != B or (ts[1] != 1 and max_pages > 1):
         raise ValueError(f"block_table must be [{B}, max_pages] with contiguous rows, got {tuple(block_table.shape)}")
-    handle, other = _handle(dev, stream)
     if o is None:
-        o = _empty((B, heads, d), q.dtype, dev, other)
+        o = _empty((B, heads, d), dtype=q.dtype, device=q.device)
         o_at = o.data_ptr()
     else:
         o_at = _want(o, "o", q.dtype, (B, heads, d), dev)
     if lse is None:
-        lse = _empty((B, heads), torch.float32, dev, other)
+        lse = _empty((B, heads), dtype=_F32, device=q.device)
         lse_at = lse.data_ptr()
     else:
-        lse_at = _want(lse, "lse", torch.float32, (B, heads), dev)
+        lse_at = _want(lse, "lse", _F32, (B, heads), dev)
+    handle = _handle(dev, stream, o, lse)
     key = (c.dtype, d, heads, c.Hkv)
     nbytes = _ws_bytes.get(key)
     if nbytes is None:
         nbytes = _ws_bytes[key] = load().gdn_paged_decode_workspace_bytes(c, heads)
-    ws, ws_bytes = _workspace(workspace, nbytes, dev, handle, other)
+    ws, ws_bytes = _workspace(workspace, nbytes, dev, handle, stream)
     _call("gdn_paged_decode", dev, c, B, heads, code, q.data_ptr(), qs[0], qs[1], block_table.data_ptr(), ts[0], max_pages,
-          _want(seq_lens, "seq_lens", torch.int32, (B,), dev), window, d ** -0.5 if scale is None else scale, o_at, lse_at,
+          _want(seq_lens, "seq_lens", _I32, (B,), dev), window, d ** -0.5 if scale is None else scale, o_at, lse_at,
           ws, ws_bytes, handle)
     return o, lse
 
@@ -234,18 +235,21 @@ def gdn_sample(logits, noise, *, temperature=None, top_k=None, top_p=None, min_p
     if code is None:
         raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
     B, V = logits.shape
-    if noise.dtype is not torch.float32 or noise.shape != logits.shape or noise.device != dev:
-        raise ValueError(f"noise must be float32 {tuple(logits.shape)} on {dev}")
+    if noise.dtype is not _F32 or noise.shape != logits.shape or noise.get_device() != dev:
+        raise ValueError(f"noise must be float32 {tuple(logits.shape)} on cuda:{dev}")
     ls, ns = logits.stride(), noise.stride()
     if V > 1 and (ls[1] != 1 or ns[1] != 1):
         raise ValueError("the rows of logits and noise must be contiguous")
-    handle, other = _handle(dev, stream)
-    opt = [None if t is None else _want(t, n, torch.int32 if n == "top_k" else torch.float32, (B,), dev)
-           for t, n in ((temperature, "temperature"), (top_k, "top_k"), (top_p, "top_p"), (min_p, "min_p"))]
+    rows = (B,)
     if tokens is None:
-        tokens = _empty((B,), torch.int32, dev, other)
+        tokens = _empty(rows, dtype=_I32, device=logits.device)
     if logprobs is None:
-        logprobs = _empty((B,), torch.float32, dev, other)
-    _call("gdn_sample", dev, B, V, code, logits.data_ptr(), ls[0], noise.data_ptr(), ns[0], *opt,
-          _want(tokens, "tokens", torch.int32, (B,), dev), _want(logprobs, "logprobs", torch.float32, (B,), dev), handle)
+        logprobs = _empty(rows, dtype=_F32, device=logits.device)
+    _call("gdn_sample", dev, B, V, code, logits.data_ptr(), ls[0], noise.data_ptr(), ns[0],
+          None if temperature is None else _want(temperature, "temperature", _F32, rows, dev),
+          None if top_k is None else _want(top_k, "top_k", _I32, rows, dev),
+          None if top_p is None else _want(top_p, "top_p", _F32, rows, dev),
+          None if min_p is None else _want(min_p, "min_p", _F32, rows, dev),
+          _want(tokens, "tokens", _I32, rows, dev), _want(logprobs, "logprobs", _F32, rows, dev),
+          _handle(dev, stream, tokens, logprobs))
     return tokens, logprobs
