@@ -578,8 +578,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
         if (a.logprobs) a.logprobs[b] = won.i < 0 ? -INFINITY : greedy ? 0.f : (clean(io<T>::ld(x + won.i)) - top.v) / t - logf(total);
     };
     if (top.i < 0 || greedy || min_p > 1.f) {
-        if (rank == 0 && tid == 0) finish({-INFINITY, -1});
         cluster.sync();  // no CTA leaves while another may read its shared memory
+        if (rank == 0 && tid == 0) finish({-INFINITY, -1});
         return;
     }
 
@@ -626,8 +626,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
         cluster.sync();
         const int n = sum_of(from_peer.x.gathered);
         if (n > kList) return false;
+        if (rank == 0) collect();
+        cluster.sync();  // the others are done
         if (rank == 0) {
-            collect();
             if (n <= 256) {
                 // every key against every other: rank and mass before it, by the kThreads / 2^m threads of a key together
                 int per = kThreads / 32;
@@ -667,7 +668,6 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
             won = block_best(won, s);
             if (tid == 0) finish(won);
         }
-        cluster.sync();
         return true;
     };
 
@@ -811,8 +811,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
             verify = false;
         }
     }
-    if (rank == 0 && tid == 0) finish(won);
     cluster.sync();
+    if (rank == 0 && tid == 0) finish(won);
 }
 
 }  // namespace
