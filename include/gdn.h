@@ -1,6 +1,8 @@
 /*
  * gdn.h -- C ABI of libgdn: the chunkwise (64-token) Gated Delta Network
- * prefill core on NVIDIA GB300 (sm_103a), dense and event-sparse forms.
+ * prefill core on NVIDIA GB300 (sm_103a), dense and event-sparse forms, and the
+ * decode step of softmax-attention layers beside it (paged cache, one-token
+ * attention, sampling; "Decode step" below).
  *
  * Source of the operator: "SparseGDN: Chunk Sparse in Linear Attention"
  * (arXiv 2610.41420v1), as paraphrased by its Chinese reading notes:
