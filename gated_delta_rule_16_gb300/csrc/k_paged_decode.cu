@@ -5,7 +5,9 @@
 // CTA per (cut row, query head), in the order of the tokens, so the result does not depend on which part was done
 // first.  Latency is all there is to it: the parts lie in L2, so a thread has its first four loads of outputs in
 // flight beside those of maxima and sums.  With 8 CTAs or more to a row (few long rows, up to 608 parts each) there is an
-// entry per row and 512 threads to each; else one per CTA edge, of a few parts, and 128 threads.
+// entry per row and 512 threads to every 64 dims; else one per CTA edge, of a few parts, and 128 threads.  After 1 x 131072
+// tokens (4 rows of 114 parts) it adds 4 us to the call, after 64 requests up to 8192 (455 edges) 4 us, most of them the wait for
+// the kernel before and three loads that depend on one another.
 #include "paged_decode.cuh"
 
 namespace gdn {
@@ -14,7 +16,8 @@ namespace {
 
 template <typename T, int D, int THREADS>
 __global__ void __launch_bounds__(THREADS) join_kernel(AttendArgs a, int heads) {
-    constexpr int kLanes = D / 4, kGroups = THREADS / kLanes, kFirst = 4;
+    constexpr int kDims = THREADS == 512 ? 64 : D;  // of this CTA
+    constexpr int kLanes = kDims / 4, kGroups = THREADS / kLanes, kFirst = 4;
     __shared__ float2 ml[kMaxCtas];
     __shared__ float2 red[THREADS / 32];
     __shared__ float4 acc[THREADS];
@@ -29,7 +32,7 @@ __global__ void __launch_bounds__(THREADS) join_kernel(AttendArgs a, int heads) 
     if (hh >= group) return;
     // the row's last in its first CTA (or that CTA's only one), then the first of each CTA up to the row's end
     auto part = [&](int k) { return (int64_t)(k == 0 ? at.z : 2 * ((at.z >> 1) + k)) * heads + blockIdx.y; };
-    const int own = tid / kLanes, d4 = tid % kLanes * 4;
+    const int own = tid / kLanes, d4 = blockIdx.z * kDims + tid % kLanes * 4;
     float4 y[kFirst];
 #pragma unroll
     for (int e = 0; e < kFirst; ++e)
@@ -80,7 +83,7 @@ __global__ void __launch_bounds__(THREADS) join_kernel(AttendArgs a, int heads) 
         *(float4 *)((float *)a.o + out * D + d4) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
     else
         *(uint2 *)((__nv_bfloat16 *)a.o + out * D + d4) = make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
-    if (tid == 0 && a.lse) a.lse[out] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+    if (d4 == 0 && a.lse) a.lse[out] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
 }
 
 template <typename T, int D>
@@ -88,7 +91,7 @@ cudaError_t join(const AttendArgs &a, int grid, int heads, cudaStream_t stream) 
     const int group = a.Hq / a.c.Hkv;
     const int64_t rows = (int64_t)a.B * a.c.Hkv * ((group + heads - 1) / heads);
     if (join_by_row(rows, grid))
-        return launch_kernel(true, join_kernel<T, D, 512>, dim3((unsigned)rows, min(heads, group)), 512, 0, stream, a, heads);
+        return launch_kernel(true, join_kernel<T, D, 512>, dim3((unsigned)rows, min(heads, group), D / 64), 512, 0, stream, a, heads);
     return launch_kernel(true, join_kernel<T, D, 128>, dim3(grid - 1, min(heads, group)), 128, 0, stream, a, heads);
 }
 template <typename T>

@@ -11,7 +11,7 @@
 // What bounds it: the row is read once from HBM; everything after works on few tokens, or on the
 // row in L2, where instructions per token count (about 10 to 20 in each pass below).  A
 // cluster of CTAs shares a row, as many as fill the GPU, each with a slice:
-//   1. one pass for the maximum, the minimum, the sum of weights and every thread's own maximum;
+//   1. one pass for the maximum, the sum of weights and every thread's own maximum;
 //   2. a threshold that no kept token is below.  For top_k: among the threads' maxima, the ceil(k / CTAs)-th largest of
 //      every CTA, and the least of those (k tokens at least are as large).  For top_p: tokens below (1 - p) M / V hold
 //      (1 - p) M together at most, so the prefix of mass p M ends above it.  What passes the threshold, a few hundred
@@ -821,7 +821,8 @@ cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream) {
     // CTAs per row: double while all rows' CTAs make two waves at most (152 SMs, four CTAs each) and a CTA has 4096 tokens
     // left.  At 256 rows of 100003, on one, two, four and eight CTAs each: rows alike, with top_k 50 and top_p 0.9, take 53, 39,
     // 47 and 77 us, rows of mixed settings 317, 202, 134 and 121 us, where the few flat rows' CTAs run on alone.  Four of 256
-    // threads to an SM against two of 512: 32 rows of 131072 take 17.8 us against 20.1.
+    // threads to an SM against two of 512: 32 rows of 131072 take 17.8 us against 20.1.  (One wave, with the rows that step 2 does
+    // not settle left to a second launch of eight CTAs each, took 156 us for the mixed rows: the worst row's own time remains.)
     int ctas = 1;
     while (ctas < kMaxCtas && (int64_t)a.B * ctas * 2 <= 1216 && a.V / (2 * ctas) >= 4096) ctas *= 2;
     auto go = [&](auto kern) {
