@@ -40,7 +40,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCtas = 8;   // per row: the largest cluster every GPU of this kind can place
 constexpr int kList = 2048;   // gathered tokens
 constexpr int kBins = 2048;
-constexpr int kRounds = 9;    // races before the end of top_p's prefix is looked for
+constexpr int kRounds = 24;   // races and probes before the end of top_p's prefix is looked for
 constexpr float kUnit = 1099511627776.f;  // 2^40
 constexpr float kReach = 28.f;            // in y: 40 ln 2, below which a mass rounds to 0
 using u64 = unsigned long long;
@@ -372,21 +372,24 @@ __device__ __noinline__ Above bracket_pass(const T *x, int from, int to, int lo,
     return a;
 }
 
-// Mass (in weights) of the tokens before one of logit `mark` and index i, in descending order.
+// Number and mass (in weights) of the tokens before one of logit `mark` and index i, in descending order.
 template <typename T>
-__device__ __noinline__ float mass_pass(const T *x, int from, int to, float mark, uint32_t i, float top, float rate) {
-    float sum = 0.f;
+__device__ __noinline__ Above mass_pass(const T *x, int from, int to, float mark, uint32_t i, float top, float rate) {
+    Above a = {0, 0.f};
     each_piece(x, from, to, [&](const float *w, auto n, int at) {
         constexpr int N = decltype(n)::value;
         if (!(largest<N>(w) >= mark)) return true;
 #pragma unroll
         for (int e = 0; e < N; ++e) {
             const float v = clean(w[e]);
-            if (v > mark || (v == mark && (uint32_t)(at + e) < i)) sum += ex2((v - top) * rate);
+            if (v > mark || (v == mark && (uint32_t)(at + e) < i)) {
+                a.mass += ex2((v - top) * rate);
+                ++a.n;
+            }
         }
         return true;
     });
-    return sum;
+    return a;
 }
 
 // By one CTA over a whole row, digit by digit: the key of the k-th token.
@@ -733,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
             const int lo = peer(0).x.lo, hi = peer(0).x.hi;
             if (tid == 0) s.n = 0;
             __syncthreads();
-            const Above above = bracket_pass(x, from, to, lo, hi, top.v, scale, rate, s);
+            const Above above = bracket_pass(x, from, to, lo, deep ? min(hi, kBins - 2) : hi, top.v, scale, rate, s);
             u64 all_mass, all_above;
             block_before((u64)(above.mass * kUnit + 0.5f), all_mass, s);
             block_before((u64)above.n, all_above, s);
@@ -744,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
                 const u64 mass_before = sum_of(from_peer.x.mass);
                 bool settled = true;
                 u64 mass_k = (u64)((double)total * (double)kUnit);
-                if (before < k && hi == kBins - 1 && (n <= kList ? before + n < k : deep && lo == hi)) {
+                if (before < k && hi == kBins - 1 && n <= kList && before + n < k) {
                     // K is every finite logit, or ends among those of no mass: all that matters is in it
                 } else if (before < k && n <= kList && before + n >= k) {
                     collect();
@@ -774,13 +777,20 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
     // from the largest token, which is always kept, on
     const uint32_t same = __ballot_sync(0xffffffffu, lane < kPer && top.i + lane < a.V && clean(io<T>::ld(x + top.i + lane)) == top.v);
     const Best first = score(top.v, top.i + __ffs(same) - 1);
-    // Noise that goes with the logits' order could have winner after winner rejected: from the ninth on the keys between the last
-    // and the largest are halved instead, 64 times at most, and the race is run once more from the end of the prefix.
+    // A rejected winner with well over the goal's mass above it leaves another race a poor chance: two probes between it and
+    // the largest, a pass for the mass each, come first.  Noise that goes with the logits' order could have winner after
+    // winner rejected: from round kRounds on the keys between are halved, 64 times at most, and the race is run once more from
+    // the end of the prefix.
     bool verify = by_p;
+    int probes = 0;
     u64 kept = full_key(top.v, 0);  // keys from here on are kept
     for (int round = 0;; ++round) {
-        const bool racing = round < kRounds || !verify;
+        const bool racing = probes == 0 && (round < kRounds || !verify);
         u64 probe = cut + (kept - cut) / 2;
+        if (probes > 0) {
+            const u64 middle = (u64)key_of(0.5f * (value_of((uint32_t)(cut >> 32)) + value_of((uint32_t)(kept >> 32)))) << 32;
+            if (middle > cut && middle < kept) probe = middle;
+        }
         if (racing) {
             // no Gumbel is above 16.64
             const float floor = fmaxf(fmaxf(min_logit, top.v + t * (first.v - 16.7f) - 1e-5f * fabsf(top.v)), cut ? value_of((uint32_t)(cut >> 32)) : -INFINITY);
@@ -793,22 +803,29 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
             if (!verify || won.i < 0) break;
             probe = full_key(clean(io<T>::ld(x + won.i)), won.i);
         }
-        u64 all;
-        block_before((u64)(mass_pass(x, from, to, value_of((uint32_t)(probe >> 32)), ~(uint32_t)probe, top.v, rate) * kUnit + 0.5f), all, s);
-        if (tid == 0) s.x.mass = all;
+        const Above above = mass_pass(x, from, to, value_of((uint32_t)(probe >> 32)), ~(uint32_t)probe, top.v, rate);
+        u64 all_mass, all_above;
+        block_before((u64)(above.mass * kUnit + 0.5f), all_mass, s);
+        block_before((u64)above.n, all_above, s);
+        if (tid == 0) s.x.mass = all_mass, s.x.above = (int)all_above;
         cluster.sync();
-        if (sum_of(from_peer.x.mass) < goal) {
+        const u64 mass = sum_of(from_peer.x.mass);
+        const int before = sum_of(from_peer.x.above);
+        if (probes > 0) --probes;
+        if (mass < goal) {
             if (racing) break;
             kept = probe;
         } else {
             cut = probe + 1;  // the probe and what is below it are not kept
-        }
-        if (racing) {
             won = {-INFINITY, -1};
-            if (settle_in_list(value_of((uint32_t)(probe >> 32)), probe, goal)) return;
-        } else if (cut >= kept) {
+            if (before <= kList && settle_in_list(value_of((uint32_t)(probe >> 32)), probe, goal)) return;
+            if (mass < goal + goal / 4) probes = 0;
+            else if (racing) probes = 2;
+        }
+        if (!racing && cut >= kept) {
             cut = kept;
             verify = false;
+            probes = 0;
         }
     }
     cluster.sync();
