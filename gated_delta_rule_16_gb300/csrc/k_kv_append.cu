@@ -4,7 +4,8 @@
 // head's scale on the way), bound by memory.  A thread keeps one 16-byte piece of a
 // cached row, (head, piece), through the tokens it takes, so its addresses, its scale
 // and the scale's reciprocal are made once.  Copies have four tokens' loads in flight; a conversion has registers for one
-// (two measured 38 us against 35, four 51, at the prompt below).
+// (two measured 38 us against 35, four 51, at the prompt below).  That prompt takes 31.3 us, 6.05 TB/s or 89 % of a copy; 64 tokens of
+// a decode step 2.0 us, a launch.
 #include "paged.cuh"
 
 namespace gdn {

