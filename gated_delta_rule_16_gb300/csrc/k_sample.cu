@@ -8,22 +8,25 @@
 // needs no running sum over the kept tokens, so its result does not hang on the
 // rounding of one.
 //
-// What bounds it: the row is read once from HBM; everything after works on few tokens, or on the
-// row in L2, where instructions per token count (about 10 to 20 in each pass below).  Greedy rows, one
-// pass, take 21 us at 256 rows of 100003 fp32 logits (4.9 TB/s), with top_k 50 and top_p 0.9 47 us, unfiltered ones 71 us with
-// their noise read; one row of 131072 in bf16 4.8, 14.4 and 11.3 us.  A cluster of CTAs shares a row, as many as fill the
-// GPU, each with a slice:
+// What bounds it: the row is read once from HBM; everything after works on few tokens, or on the row in L2, where
+// instructions per token (about 10 in each pass below) and barriers of the cluster count.  A pass handles 16 tokens per
+// thread at a time without a branch between them, as few warps are there to hide their latency: one branch per token made the
+// passes for masses twice as long.  Greedy rows, one pass, take 22 us at 256 rows of 100003 fp32 logits (4.7 TB/s), with
+// top_k 50 and top_p 0.9 47 us, unfiltered ones 67 us with their noise read; one row of 131072 in bf16 5.0, 14.5 and 10.4 us.
+// A cluster of CTAs shares a row, as many as fill the GPU, each with a slice:
 //   1. one pass for the maximum, the sum of weights and every thread's own maximum;
 //   2. a threshold that no kept token is below.  For top_k: among the threads' maxima, the ceil(k / CTAs)-th largest of
 //      every CTA, and the least of those (k tokens at least are as large).  For top_p: tokens below (1 - p) M / V hold
 //      (1 - p) M together at most, so the prefix of mass p M ends above it.  What passes the threshold, a few hundred
-//      tokens as a rule, is gathered and cut in the first CTA's shared memory;
+//      tokens as a rule, is gathered and cut in the first CTA's shared memory.  (If the largest token alone holds p M, it is
+//      taken at once.)
 //   3. if it is more than fits (flat rows, large k), the k-th largest logit is bracketed by a histogram of every 8th load
 //      (of every one if that fails, or k is too large for it), the bracket gathered, with the number and mass
-//      of the tokens above it from the same pass; thousands of equal logits leave the first CTA to descend the
-//      sorting key digit by digit, a pass over the row each.  The end of top_p's prefix is not looked for: the race is run
-//      over all of K, and its winner's mass above says whether it was kept.  If not, nothing below it is either, and the race
-//      is run again above it: 1 + log(1 / top_p) times as a rule, or until what is left can be gathered;
+//      of the tokens above it from the same pass; every CTA finds the k-th in it for itself, which costs less than to wait
+//      for one that does.  Thousands of equal logits leave them to descend the sorting key digit by digit, a pass over the
+//      row each.  The end of top_p's prefix is not looked for: the race is run over all of K, and its winner's mass above
+//      says whether it was kept.  If not, nothing below it is either, and the race is run again above it:
+//      1 + log(1 / top_p) times as a rule, or until what is left is few enough to be ranked;
 //   4. the race.  The largest token is always kept, so its score bounds the winner's from the start: no Gumbel is above
 //      16.64, and a token whose logit cannot make up for it has its noise not read; of the others one comparison of
 //      1 - u with a multiple of w leaves a few per warp whose score is worked out.
@@ -41,8 +44,9 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCtas = 8;   // per row: the largest cluster every GPU of this kind can place
 constexpr int kList = 2048;   // gathered tokens
+constexpr int kRanked = 256;  // of them ranked by comparing all with all
 constexpr int kBins = 2048;
-constexpr int kRounds = 24;   // races and probes before the end of top_p's prefix is looked for
+constexpr int kRounds = 24;   // races before the end of top_p's prefix is looked for
 constexpr float kUnit = 1099511627776.f;  // 2^40
 constexpr float kReach = 28.f;            // in y: 40 ln 2, below which a mass rounds to 0
 using u64 = unsigned long long;
@@ -76,13 +80,15 @@ __device__ __forceinline__ Best better(Best a, Best b) {
 
 struct Shared {
     u64 list[kList];
-    uint32_t count[kBins];  // of this CTA's tokens; the first CTA has the row's in list
+    uint32_t count[kBins];  // of this CTA's tokens
     u64 digit_sum[256];
     uint32_t digit_count[256];
     u64 sums[kWarps];
     Best bests[kWarps];
     float parts[2][kWarps];
-    int n, found;           // tokens gathered; bin or rank found
+    uint32_t leasts[kWarps];
+    int n, found;           // tokens gathered; digit found
+    int lo, hi;             // bins found
     u64 before;
     bool whole;
     // read by the row's other CTAs, each written once between two barriers of the cluster
@@ -92,9 +98,6 @@ struct Shared {
         int gathered;      // tokens gathered, or more than kList
         int above[2];      // tokens above those, or above a race's winner, and their mass: by turns, so that a round's are
         u64 mass[2];       // written while others may still read the last's
-        int lo, hi;        // the first CTA's: bins to gather
-        bool settled;      // the first CTA's: whether cut is the key of the k-th token (0: K is all that matters), and mass_k
-        u64 cut, mass_k;   // the mass of K
     } x;
 };
 
@@ -189,17 +192,6 @@ __device__ __forceinline__ void each(const T *row, int from, int to, float least
     });
 }
 
-// Appends to the list (or only counts, past its room); false once it has overflowed.
-__device__ __forceinline__ bool gather(Shared &s, u64 key) {
-    const unsigned peers = __activemask();
-    const int lane = threadIdx.x & 31, first = __ffs(peers) - 1;
-    int at = 0;
-    if (lane == first) at = atomicAdd(&s.n, __popc(peers));
-    at = __shfl_sync(peers, at, first) + __popc(peers & ((1u << lane) - 1));
-    if (at < kList) s.list[at] = key;
-    return at < kList;
-}
-
 // Of the n gathered keys that are `floor` or more: a key that divides off the shortest descending prefix whose measure
 // (tokens, or mass) reaches goal; 0 if all of it does not.  By 8 bits of the key at a time, from the first that differ.
 __device__ __noinline__ u64 select(Shared &s, int n, u64 goal, bool of_mass, u64 floor, float top, float rate) {
@@ -281,10 +273,10 @@ __device__ __noinline__ u64 select(Shared &s, int n, u64 goal, bool of_mass, u64
 
 // Exact score of a token, {-inf, -1} if min_p or a weight of 0 rules it out.  A call: few tokens need it, and inlined in
 // several loops it crowds the instruction cache.
-__device__ __noinline__ Best exact_score(float v, int i, float top, float t, float min_p, const float *u) {
+__device__ __noinline__ Best exact_score(float v, int i, float top, float t, float min_p, float u) {
     const float y = (v - top) / t, w = expf(y);
     if (!(w > 0.f) || w < min_p) return {-INFINITY, -1};
-    const float r = fminf(fmaxf(u[i], 2.3283064365386963e-10f), 0.999999940395355f);
+    const float r = fminf(fmaxf(u, 2.3283064365386963e-10f), 0.999999940395355f);
     return {y - logf(-logf(r)), i};
 }
 
@@ -292,6 +284,7 @@ __device__ __noinline__ Best exact_score(float v, int i, float top, float t, flo
 
 // 16-byte pieces of a row for whole warps: f(how many, logits as stored or NaN, index of the first) for kAhead pieces at a time,
 // with every lane in every step; every stride-th piece only.  Single tokens before and after the pieces come one to a lane.
+// f returns false, in the whole warp, to end the warp's pass.
 template <int kAhead, typename T, typename F>
 __device__ __forceinline__ void each_together(const T *x, int from, int to, int stride, F f) {
     constexpr int kPer = 16 / sizeof(T);
@@ -316,7 +309,7 @@ __device__ __forceinline__ void each_together(const T *x, int from, int to, int 
                 else v[q][e] = __uint_as_float(y[e]);
             }
         }
-        f(Count<kAhead>(), Count<kPer>(), &v[0][0], from + head + (i0 + lane) * stride * kPer, stride * kThreads * kPer);
+        if (!f(Count<kAhead>(), Count<kPer>(), &v[0][0], from + head + (i0 + lane) * stride * kPer, stride * kThreads * kPer)) return;
     }
     if (warp == 0) {
         const int tail = head + pieces * kPer, i = lane < 16 ? lane : tail + lane - 16;
@@ -326,13 +319,45 @@ __device__ __forceinline__ void each_together(const T *x, int from, int to, int 
     }
 }
 
-// Gathers the tokens from `least` up and above the key `under`.
-template <typename T>
-__device__ __noinline__ void gather_pass(const T *x, int from, int to, float least, u64 under, Shared &s) {
-    each(x, from, to, least, [&](float v, int i) {
-        const u64 key = full_key(v, i);
-        return key > under ? gather(s, key) : true;
+struct Above { int n; float mass; };
+
+// Gathers the tokens with logits in [least, upto), of logit `least` only those up to index `last`; the warp ends its pass
+// once they are too many.  Number and mass (in weights) of the tokens from upto up.
+template <bool kAbove, typename T>
+__device__ __noinline__ Above gather_pass(const T *x, int from, int to, float least, uint32_t last, float upto, float top, float rate, Shared &s) {
+    const int lane = threadIdx.x & 31;
+    Above a = {0, 0.f};
+    least = fmaxf(least, -3.402823466e38f);
+    each_together<sizeof(T)>(x, from, to, 1, [&](auto q, auto n, const float *w, int at, int step) {
+        constexpr int N = decltype(n)::value, Q = decltype(q)::value;
+        if (!__any_sync(0xffffffffu, largest<Q * N>(w) >= least)) return true;
+        uint32_t mine = 0;
+#pragma unroll
+        for (int e = 0; e < Q * N; ++e) {  // no branches: the tokens' latencies overlap
+            const float v = fminf(w[e], 3.402823466e38f);
+            const bool in = w[e] >= least, above = kAbove && in && v >= upto;  // NaN is not
+            if constexpr (kAbove) {
+                a.mass += ex2(((above ? v : -INFINITY) - top) * rate);
+                a.n += above;
+            }
+            mine |= (uint32_t)(in && !above && (v > least || (uint32_t)(at + e / N * step + e % N) <= last)) << e;
+        }
+        int end = 0;
+        for (unsigned peers; (peers = __ballot_sync(0xffffffffu, mine != 0)) != 0;) {
+            int place = 0;
+            if (lane == 0) place = atomicAdd(&s.n, __popc(peers));
+            place = __shfl_sync(0xffffffffu, place, 0);
+            end = place + __popc(peers);
+            place += __popc(peers & ((1u << lane) - 1));
+            if (mine) {
+                const int e = __ffs(mine) - 1, i = at + e / N * step + e % N;
+                mine &= mine - 1;
+                if (place < kList) s.list[place] = full_key(clean(io<T>::ld(x + i)), i);
+            }
+        }
+        return end <= kList;
     });
+    return a;
 }
 
 __device__ __forceinline__ int bin_of(float v, float top, float scale) { return (int)fminf((top - v) * scale, (float)(kBins - 1)); }
@@ -344,57 +369,44 @@ __device__ __noinline__ void count_pass(const T *x, int from, int to, int stride
 #pragma unroll
         for (int e = 0; e < decltype(q)::value * decltype(n)::value; ++e)
             if (w[e] > -INFINITY) atomicAdd(&s.count[bin_of(clean(w[e]), top, scale)], 1u);
+        return true;
     });
 }
 
-// Gathers the tokens of the bins [lo, hi]; number and mass (in weights) of those above.
-struct Above { int n; float mass; };
-template <typename T>
-__device__ __noinline__ Above bracket_pass(const T *x, int from, int to, int lo, int hi, float top, float scale, float rate, Shared &s) {
-    Above a = {0, 0.f};
-    each_together<2>(x, from, to, 1, [&](auto q, auto n, const float *w, int at, int step) {
-        constexpr int N = decltype(n)::value;
-        uint32_t mine = 0;
-#pragma unroll
-        for (int e = 0; e < decltype(q)::value * N; ++e) {
-            const float v = clean(w[e]);
-            const int bin = bin_of(v, top, scale);  // of -inf: the last
-            if (bin < lo) {
-                a.mass += ex2((v - top) * rate);
-                ++a.n;
-            }
-            mine |= (uint32_t)(bin >= lo && bin <= hi && v > -INFINITY) << e;
-        }
-        while (mine) {  // few: read again
-            const int e = __ffs(mine) - 1, i = at + e / N * step + e % N;
-            mine &= mine - 1;
-            gather(s, full_key(clean(io<T>::ld(x + i)), i));
-        }
-    });
-    return a;
+// The smallest logit whose bin is `bin` or before it; by a whole warp.
+__device__ float edge_of(int bin, float top, float scale) {
+    const uint32_t lane = threadIdx.x & 31;
+    uint32_t lo = key_of(-3.402823466e38f), hi = key_of(top);
+    while (lo < hi) {
+        const uint32_t step = (hi - lo) / 32 + 1;
+        const unsigned in = __ballot_sync(0xffffffffu, bin_of(value_of(min(lo + lane * step, hi)), top, scale) <= bin);
+        const uint32_t first = in ? __ffs(in) - 1 : 32;
+        if (first < 32) hi = min(lo + first * step, hi);
+        if (first > 0) lo = min(lo + (first - 1) * step + 1, hi);
+    }
+    return value_of(hi);
 }
 
 // Number and mass (in weights) of the tokens before one of logit `mark` and index i, in descending order.
 template <typename T>
 __device__ __noinline__ Above mass_pass(const T *x, int from, int to, float mark, uint32_t i, float top, float rate) {
     Above a = {0, 0.f};
-    each_piece(x, from, to, [&](const float *w, auto n, int at) {
-        constexpr int N = decltype(n)::value;
-        if (!(largest<N>(w) >= mark)) return true;
+    each_together<sizeof(T)>(x, from, to, 1, [&](auto q, auto n, const float *w, int at, int step) {
+        constexpr int N = decltype(n)::value, Q = decltype(q)::value;
+        if (!__any_sync(0xffffffffu, largest<Q * N>(w) >= mark)) return true;
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const float v = clean(w[e]);
-            if (v > mark || (v == mark && (uint32_t)(at + e) < i)) {
-                a.mass += ex2((v - top) * rate);
-                ++a.n;
-            }
+        for (int e = 0; e < Q * N; ++e) {
+            const float v = fminf(w[e], 3.402823466e38f);
+            const bool in = w[e] >= mark && (v > mark || (uint32_t)(at + e / N * step + e % N) < i);  // NaN is not
+            a.mass += ex2(((in ? v : -INFINITY) - top) * rate);
+            a.n += in;
         }
         return true;
     });
     return a;
 }
 
-// By one CTA over a whole row, digit by digit: the key of the k-th token.
+// Over a whole row, digit by digit: the key of the k-th token.
 template <typename T>
 __device__ __noinline__ u64 kth_key(const T *x, int V, int k, Shared &s) {
     u64 prefix = 0, before = 0;
@@ -427,9 +439,10 @@ __device__ __noinline__ u64 kth_key(const T *x, int V, int k, Shared &s) {
 struct Track {
     const float *u;
     float top, t, rate, min_p;
-    float floor, reach;  // logits below cannot be kept or cannot win; exp(-best)
+    float floor, reach;  // logits below cannot be kept or cannot win; log2 exp(-best), with room
     u64 cut;             // keys below are not kept
 };
+__device__ __forceinline__ float reach_of(float best) { return fmaf(best, -1.4426950408889634f, 0.015f); }
 template <typename T>
 __device__ __noinline__ Best race_pass(const T *x, int from, int to, const Track &track, Best won) {
     const float *u = track.u;
@@ -437,27 +450,37 @@ __device__ __noinline__ Best race_pass(const T *x, int from, int to, const Track
     float reach = track.reach;
     each_together<sizeof(T)>(x, from, to, 1, [&](auto q, auto n, const float *w, int at, int step) {
         constexpr int N = decltype(n)::value, Q = decltype(q)::value;
-        if (!__any_sync(0xffffffffu, largest<Q * N>(w) >= floor)) return;
+        if (!__any_sync(0xffffffffu, largest<Q * N>(w) >= floor)) return true;
         float r[Q * N];
+        if (N >= 4 && ((uintptr_t)(u + at) & 15) == 0) {  // the same for all pieces
+#pragma unroll
+            for (int e = 0; e < Q * N; e += N < 4 ? 1 : 4) {
+                constexpr int M = N < 4 ? 1 : 4;
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (largest<M>(w + e) >= floor) y = *(const float4 *)(u + at + e / N * step + e % N);
+                const float z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int j = 0; j < M; ++j) r[e + j] = z[j];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < Q * N; ++e) r[e] = w[e] >= floor ? u[at + e / N * step + e % N] : 0.f;
+        }
         uint32_t hit = 0;
 #pragma unroll
-        for (int e = 0; e < Q * N; ++e) r[e] = w[e] >= floor ? u[at + e / N * step + e % N] : -1.f;
-#pragma unroll
-        for (int e = 0; e < Q * N; ++e) {
-            const float weight = ex2((fminf(w[e], 3.402823466e38f) - top) * rate);  // of NaN: where r = -1
-            hit |= (uint32_t)(1.f - fminf(r[e], 0.999999940395355f) < weight * reach && r[e] >= 0.f) << e;
-        }
-        if (!__any_sync(0xffffffffu, hit != 0)) return;
+        for (int e = 0; e < Q * N; ++e) hit |= (uint32_t)(w[e] >= floor && !(1.f - r[e] >= ex2(fmaf(w[e] - top, rate, reach)))) << e;
+        if (!__any_sync(0xffffffffu, hit != 0)) return true;
         while (hit) {
             const int e = __ffs(hit) - 1, i = at + e / N * step + e % N;
             hit &= hit - 1;
             const float v = clean(io<T>::ld(x + i));
-            if (full_key(v, i) >= track.cut) won = better(won, exact_score(v, i, top, track.t, track.min_p, u));
+            if (full_key(v, i) >= track.cut) won = better(won, exact_score(v, i, top, track.t, track.min_p, u[i]));
         }
         float best = won.v;
 #pragma unroll
         for (int off = 16; off; off >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, off));
-        reach = fminf(reach, 1.01f * ex2(best * -1.4426950408889634f));
+        reach = fminf(reach, reach_of(best));
+        return true;
     });
     return won;
 }
@@ -520,7 +543,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
         sum = mine > -INFINITY ? sum * ex2((mine - top.v) * rate) : 0.f;
 #pragma unroll
         for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        if ((tid & 31) == 0) s.bests[tid >> 5] = top, s.parts[0][tid >> 5] = sum, s.parts[1][tid >> 5] = low;
+        const uint32_t own = mine > -INFINITY ? key_of(mine) : 0u, least_own = __reduce_min_sync(0xffffffffu, own);
+        if ((tid & 31) == 0) s.leasts[tid >> 5] = least_own, s.bests[tid >> 5] = top, s.parts[0][tid >> 5] = sum, s.parts[1][tid >> 5] = low;
         __syncthreads();
         for (int w = 0; w < kWarps; ++w) top = better(top, s.bests[w]), low = fminf(low, s.parts[1][w]);
         sum = 0.f;
@@ -532,13 +556,16 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
         const int need = (k + ctas - 1) / ctas;
         if (need <= kThreads) {
             const uint32_t own = mine > -INFINITY ? key_of(mine) : 0u;
-            uint32_t key = 0;
+            // between the least and the largest of them, to 1 / 256 of what is between: a little low, a few tokens more
+            uint32_t lo = s.leasts[0], hi = key_of(top.v);
+            for (int w = 1; w < kWarps; ++w) lo = min(lo, s.leasts[w]);
 #pragma unroll 1
-            for (int bit = 31; bit >= 16; --bit) {  // the leading bits will do: a little lower, a few tokens more
-                const uint32_t next = key | 1u << bit;
-                if (__syncthreads_count(own >= next) >= need) key = next;
+            for (int bit = 0; bit < 8; ++bit) {
+                const uint32_t mid = lo + (hi - lo) / 2 + 1;
+                if (__syncthreads_count(own >= mid) >= need) lo = mid;
+                else hi = mid - 1;
             }
-            if (key) least = value_of(key);
+            if (lo) least = value_of(lo);
         }
     }
     if (tid == 0) s.x.top = top, s.x.sum = sum, s.x.low = low, s.x.least = least;
@@ -573,16 +600,20 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
     least = least_of(its_least);
     const float total = sum_of(its_top.i >= 0 ? its_sum * ex2((its_top.v - top.v) * rate) : 0.f);
 
+    auto write = [&](int i, float v) {
+        a.tokens[b] = i;
+        if (a.logprobs) a.logprobs[b] = i < 0 ? -INFINITY : greedy ? 0.f : (v - top.v) / t - logf(total);
+    };
     auto finish = [&](Best won) {  // thread 0 of the first CTA
-        if (won.i < 0 && top.i >= 0) {  // greedy, or min_p above 1 leaves nothing: the largest
+        if (won.i < 0 && top.i >= 0) {  // the largest
             won = top;
             for (int e = kPer - 1; e >= 0; --e)  // within its load
                 if (top.i + e < a.V && clean(io<T>::ld(x + top.i + e)) == top.v) won.i = top.i + e;
         }
-        a.tokens[b] = won.i;
-        if (a.logprobs) a.logprobs[b] = won.i < 0 ? -INFINITY : greedy ? 0.f : (clean(io<T>::ld(x + won.i)) - top.v) / t - logf(total);
+        write(won.i, won.i < 0 ? -INFINITY : clean(io<T>::ld(x + won.i)));
     };
-    if (top.i < 0 || greedy || min_p > 1.f) {
+    // whatever the noise: also if the largest token alone holds top_p of the mass
+    if (top.i < 0 || greedy || min_p > 1.f || (by_p && (double)fmaxf(p, 0.f) * (double)total <= 1.0)) {
         cluster.sync();  // no CTA leaves while another may read its shared memory
         if (rank == 0 && tid == 0) finish({-INFINITY, -1});
         return;
@@ -598,19 +629,16 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
         const double g = ceil((double)fmaxf(p, 0.f) * m);
         return g < 1.0 ? 1ull : (u64)g;
     };
-    auto score = [&](float v, int i) { return exact_score(v, i, top.v, t, min_p, u); };
-    // the first CTA takes over the tokens that the others have gathered; false if they are too many
-    auto collect = [&]() {
-        const int its_n = from_peer.x.gathered, n = sum_of(its_n);
-        if (n > kList) return false;
-        for (int r = 1 + warp % (kWarps / 2); r < ctas; r += kWarps / 2) {  // two warps to a CTA
-            int at = 0;
-            for (int q = 0; q < r; ++q) at += __shfl_sync(0xffffffffu, its_n, q);
-            const int m = __shfl_sync(0xffffffffu, its_n, r);
+    auto score = [&](float v, int i, float r) { return exact_score(v, i, top.v, t, min_p, r); };
+    // takes over the tokens that the row's other CTAs have gathered
+    auto collect = [&](int its_n) {  // the lanes' counts of the CTAs that they read
+        for (int q = 1 + warp % (kWarps / 2); q < ctas; q += kWarps / 2) {  // two warps to a CTA
+            int at = 0;  // behind this CTA's own, which others may be reading
+            for (int j = 0; j < q; ++j) at += __shfl_sync(0xffffffffu, its_n, (rank + j) % ctas);
+            const int r = (rank + q) % ctas, m = __shfl_sync(0xffffffffu, its_n, r);
             for (int i = lane + 32 * (warp / (kWarps / 2)); i < m; i += 64) s.list[at + i] = peer(r).list[i];
         }
         __syncthreads();
-        return true;
     };
     auto mass_from = [&](int n, u64 key) {  // of the list's keys
         u64 own = 0, all;
@@ -620,21 +648,27 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
     };
 
     Best won = {-INFINITY, -1};
-    // Gathers the tokens from `least` up (and above the key `under`); if they fit, the first CTA cuts the list at rank k and at
-    // mass `goal` (0: at top_p of the list's first k), races what is left and writes the result.
-    auto settle_in_list = [&](float least, u64 under, u64 goal) {
+    // Gathers the tokens from `least` up (of that logit: up to index `last`); if they fit, the first CTA cuts the list at
+    // rank k and at mass `goal` (0: at top_p of the list's first k), races what is left and writes the result.
+    auto settle_in_list = [&](float least, uint32_t last, u64 goal, bool few) {
         if (tid == 0) s.n = 0;
-        __syncthreads();
-        gather_pass(x, from, to, least, under, s);
+        // unless they are known to be few: if every thread has some in a long slice, they are too many
+        const int passing = __syncthreads_count(mine >= least);
+        if (!few && passing == kThreads && to - from > 2 * kList) {
+            if (tid == 0) s.n = kList + 1;
+        } else {
+            gather_pass<false>(x, from, to, least, last, INFINITY, top.v, rate, s);
+        }
         __syncthreads();
         if (tid == 0) s.x.gathered = min(s.n, kList + 1);
         cluster.sync();
-        const int n = sum_of(from_peer.x.gathered);
+        const int its_n = from_peer.x.gathered, n = sum_of(its_n);
         if (n > kList) return false;
-        if (rank == 0) collect();
-        cluster.sync();  // the others are done
+        if (rank == 0) collect(its_n);
+        cluster.sync();
         if (rank == 0) {
-            if (n <= 256) {
+            float won_at = 0.f;
+            if (n <= kRanked) {
                 // every key against every other: rank and mass before it, by the kThreads / 2^m threads of a key together
                 int per = kThreads / 32;
                 while (kThreads / per < n) per /= 2;
@@ -642,6 +676,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
                 __syncthreads();
                 const int i = tid / per;
                 const u64 key = i < n ? s.list[i] : 0;
+                const float r = i < n ? u[~(uint32_t)key] : 0.f;  // on its way while the keys are ranked
                 int ahead = 0;
                 u64 before = 0, all;
                 for (int j = tid % per; j < n; j += per)
@@ -658,7 +693,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
                     }
                     keep = keep && before < goal;
                 }
-                if (keep) won = score(value_of((uint32_t)(key >> 32)), (int)~(uint32_t)key);
+                won_at = value_of((uint32_t)(key >> 32));
+                if (keep) won = score(won_at, (int)~(uint32_t)key, r);
             } else {
                 u64 from_key = by_k && n > k ? select(s, n, (u64)k, false, 0, top.v, rate) : 0;
                 if (by_p) {
@@ -667,11 +703,15 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
                 }
                 for (int i = tid; i < n; i += kThreads) {
                     const u64 key = s.list[i];
-                    if (key >= from_key) won = better(won, score(value_of((uint32_t)(key >> 32)), (int)~(uint32_t)key));
+                    if (key < from_key) continue;
+                    const Best now = better(won, score(value_of((uint32_t)(key >> 32)), (int)~(uint32_t)key, u[~(uint32_t)key]));
+                    if (now.i != won.i) won_at = value_of((uint32_t)(key >> 32));
+                    won = now;
                 }
             }
-            won = block_best(won, s);
-            if (tid == 0) finish(won);
+            const Best all = block_best(won, s);
+            if (won.i >= 0 && won.i == all.i) write(won.i, won_at);
+            if (all.i < 0 && tid == 0) finish(all);
         }
         return true;
     };
@@ -682,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
         // 2. what passes the threshold
         if (!(by_k && by_p)) least = fmaxf(least, min_logit);  // with both, all of K counts in its mass
         if (by_p && !by_k) least = fmaxf(least, logit_of((1.f - fmaxf(p, 0.f)) * total / (float)a.V));
-        if (settle_in_list(least, 0, goal)) return;
+        if ((least > -INFINITY || a.V <= kList) && settle_in_list(least, ~0u, goal, false)) return;
     }
     if (by_k) {
         // 3. the k-th token, from a histogram over the logits
@@ -697,106 +737,92 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
             __syncthreads();
             count_pass(x, from, to, stride, top.v, scale, s);
             cluster.sync();
-            {
-                // each CTA adds up a range of bins for the first one
-                const int step = kBins / ctas;
-                uint32_t *counts = (uint32_t *)cluster.map_shared_rank(s.list, 0);
-                for (int i = rank * step + tid; i < (rank + 1) * step; i += kThreads) {
-                    uint32_t c = 0;
+            // the row's counts: each thread has 8 bins of all CTAs
+            constexpr int kEach = kBins / kThreads;
+            uint32_t counts[kEach] = {};
+#pragma unroll 1
+            for (int r = 0; r < ctas; ++r) {
+                const uint4 *c = (const uint4 *)(peer(r).count + tid * kEach);
 #pragma unroll
-                    for (int r = 0; r < kMaxCtas; ++r)
-                        if (r < ctas) c += peer(r).count[i];
-                    counts[i] = c;
+                for (int e = 0; e < kEach; e += 4) {
+                    const uint4 y = c[e / 4];
+                    counts[e] += y.x, counts[e + 1] += y.y, counts[e + 2] += y.z, counts[e + 3] += y.w;
                 }
             }
-            cluster.sync();
-            if (rank == 0) {
-                // the first bin whose running count reaches `nth`, or the last
-                auto find_bin = [&](u64 nth) {
-                    constexpr int kEach = kBins / kThreads;
-                    const uint32_t *counts = (const uint32_t *)s.list;
-                    u64 own = 0, all;
-                    for (int e = 0; e < kEach; ++e) own += counts[tid * kEach + e];
-                    u64 at = block_before(own, all, s);
-                    if (tid == 0) s.found = kBins - 1;
-                    __syncthreads();
-                    if (at < nth && at + own >= nth) {
-                        int e = 0;
-                        while ((at += counts[tid * kEach + e]) < nth) ++e;
-                        s.found = tid * kEach + e;
-                    }
-                    __syncthreads();
-                    const int bin = s.found;
-                    __syncthreads();
-                    return bin;
-                };
-                const float mid = (float)k / (float)stride, off = stride > 1 ? 3.2f * sqrtf(mid) + 2.f : 0.f;
-                const int lo = find_bin((u64)fmaxf(stride > 1 ? mid - off : (float)k, 1.f)), hi = stride > 1 ? find_bin((u64)(mid + off)) : lo;
-                if (tid == 0) s.x.lo = lo, s.x.hi = hi;
-            }
-            cluster.sync();
-            const int lo = peer(0).x.lo, hi = peer(0).x.hi;
+            u64 own = 0, all;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) own += counts[e];
+            const u64 at = block_before(own, all, s);
+            // the first bin whose running count reaches `nth`, or the last
+            auto find_bin = [&](u64 nth, int &bin) {
+                if (at < nth && at + own >= nth) {
+                    u64 running = at;
+                    int e = 0;
+#pragma unroll
+                    for (; e < kEach - 1 && (running += counts[e]) < nth; ++e) {}
+                    bin = tid * kEach + e;
+                }
+            };
+            const float mid = (float)k / (float)stride, off = stride > 1 ? 3.2f * sqrtf(mid) + 2.f : 0.f;
+            if (tid == 0) s.lo = s.hi = kBins - 1;
+            __syncthreads();
+            find_bin((u64)fmaxf(stride > 1 ? mid - off : (float)k, 1.f), s.lo);
+            find_bin((u64)fmaxf(stride > 1 ? mid + off : (float)k, 1.f), s.hi);
+            __syncthreads();
+            const int lo = s.lo, hi = s.hi;
+            const float gather_from = edge_of(deep ? min(hi, kBins - 2) : hi, top.v, scale), gather_upto = lo > 0 ? edge_of(lo - 1, top.v, scale) : INFINITY;
             if (tid == 0) s.n = 0;
             __syncthreads();
-            const Above above = bracket_pass(x, from, to, lo, deep ? min(hi, kBins - 2) : hi, top.v, scale, rate, s);
+            const Above above = gather_pass<true>(x, from, to, gather_from, ~0u, gather_upto, top.v, rate, s);
             u64 all_mass, all_above;
             block_before((u64)(above.mass * kUnit + 0.5f), all_mass, s);
             block_before((u64)above.n, all_above, s);
             if (tid == 0) s.x.gathered = min(s.n, kList + 1), s.x.mass[0] = all_mass, s.x.above[0] = (int)all_above;
             cluster.sync();
-            if (rank == 0) {
-                const int before = sum_of(from_peer.x.above[0]), n = sum_of(from_peer.x.gathered);
-                const u64 mass_before = sum_of(from_peer.x.mass[0]);
-                bool settled = true;
-                u64 mass_k = (u64)((double)total * (double)kUnit);
-                if (before < k && hi == kBins - 1 && n <= kList && before + n < k) {
-                    // K is every finite logit, or ends among those of no mass: all that matters is in it
-                } else if (before < k && n <= kList && before + n >= k) {
-                    collect();
-                    cut = select(s, n, (u64)(k - before), false, 0, top.v, rate);
-                    mass_k = mass_before + mass_from(n, cut);
-                } else if (stride > 1) {
-                    settled = false;  // outside the bracket, or too many in it
-                } else {
-                    cut = kth_key(x, a.V, k, s);
-                    u64 own = 0;
-                    each(x, 0, a.V, -INFINITY, [&](float v, int i) {
-                        if (full_key(v, i) >= cut) own += mass_of(v, top.v, rate);
-                        return true;
-                    });
-                    block_before(own, mass_k, s);
-                }
-                if (tid == 0) s.x.settled = settled, s.x.cut = cut, s.x.mass_k = mass_k;
+            const int its_n = from_peer.x.gathered, its_above = from_peer.x.above[0];
+            const u64 its_mass = from_peer.x.mass[0], mass_before = sum_of(its_mass);
+            const int before = sum_of(its_above), n = sum_of(its_n);
+            // every CTA settles it for itself
+            u64 mass_k = (u64)((double)total * (double)kUnit);
+            if (before < k && hi == kBins - 1 && n <= kList && before + n < k) {
+                // K is every finite logit, or ends among those of no mass: all that matters is in it
+            } else if (before < k && n <= kList && before + n >= k) {
+                collect(its_n);
+                cut = select(s, n, (u64)(k - before), false, 0, top.v, rate);
+                mass_k = mass_before + mass_from(n, cut);
+            } else if (stride > 1) {
+                cluster.sync();  // others may still read what the next turn writes
+                continue;        // outside the bracket, or too many in it
+            } else {
+                cut = kth_key(x, a.V, k, s);
+                u64 own_mass = 0;
+                each(x, 0, a.V, -INFINITY, [&](float v, int i) {
+                    if (full_key(v, i) >= cut) own_mass += mass_of(v, top.v, rate);
+                    return true;
+                });
+                block_before(own_mass, mass_k, s);
             }
-            cluster.sync();
-            if (!peer(0).x.settled) continue;
-            cut = peer(0).x.cut;
-            if (by_p) goal = goal_of((double)peer(0).x.mass_k);
+            if (by_p) goal = goal_of((double)mass_k);
             break;
         }
     }
     // 4. the race over K, until its winner is in top_p's prefix
     // from the largest token, which is always kept, on
     const uint32_t same = __ballot_sync(0xffffffffu, lane < kPer && top.i + lane < a.V && clean(io<T>::ld(x + top.i + lane)) == top.v);
-    const Best first = score(top.v, top.i + __ffs(same) - 1);
-    // A rejected winner with well over the goal's mass above it leaves another race a poor chance: two probes between it and
-    // the largest, a pass for the mass each, come first.  Noise that goes with the logits' order could have winner after
-    // winner rejected: from round kRounds on the keys between are halved, 64 times at most, and the race is run once more from
-    // the end of the prefix.
+    const int first_i = top.i + __ffs(same) - 1;
+    const Best first = score(top.v, first_i, u[first_i]);
+    // Noise that goes with the logits' order could have winner after winner rejected: from round kRounds on the keys between
+    // the last one and the lowest known to be kept are halved, 64 times at most, and the race is run once more from the end of
+    // the prefix.
     bool verify = by_p;
-    int probes = 0;
     u64 kept = full_key(top.v, 0);  // keys from here on are kept
     for (int round = 0;; ++round) {
-        const bool racing = probes == 0 && (round < kRounds || !verify);
+        const bool racing = round < kRounds || !verify;
         u64 probe = cut + (kept - cut) / 2;
-        if (probes > 0) {
-            const u64 middle = (u64)key_of(0.5f * (value_of((uint32_t)(cut >> 32)) + value_of((uint32_t)(kept >> 32)))) << 32;
-            if (middle > cut && middle < kept) probe = middle;
-        }
         if (racing) {
             // no Gumbel is above 16.64
             const float floor = fmaxf(fmaxf(min_logit, top.v + t * (first.v - 16.7f) - 1e-5f * fabsf(top.v)), cut ? value_of((uint32_t)(cut >> 32)) : -INFINITY);
-            const Track track = {u, top.v, t, rate, min_p, fmaxf(floor, -3.402823466e38f), 1.01f * ex2(first.v * -1.4426950408889634f), cut};
+            const Track track = {u, top.v, t, rate, min_p, fmaxf(floor, -3.402823466e38f), reach_of(first.v), cut};
             won = race_pass(x, from, to, track, first);
             won = block_best(won, s);
             if (tid == 0) s.x.won = won;
@@ -809,25 +835,22 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
         u64 all_mass, all_above;
         block_before((u64)(above.mass * kUnit + 0.5f), all_mass, s);
         block_before((u64)above.n, all_above, s);
-        if (tid == 0) s.x.mass[round & 1] = all_mass, s.x.above[round & 1] = (int)all_above;
+        const int slot = round & 1;
+        if (tid == 0) s.x.mass[slot] = all_mass, s.x.above[slot] = (int)all_above;
         cluster.sync();
-        const u64 mass = sum_of(from_peer.x.mass[round & 1]);
-        const int before = sum_of(from_peer.x.above[round & 1]);
-        if (probes > 0) --probes;
+        const u64 mass = sum_of(from_peer.x.mass[slot]);
+        const int before = sum_of(from_peer.x.above[slot]);
         if (mass < goal) {
             if (racing) break;
             kept = probe;
         } else {
             cut = probe + 1;  // the probe and what is below it are not kept
             won = {-INFINITY, -1};
-            if (before <= kList && settle_in_list(value_of((uint32_t)(probe >> 32)), probe, goal)) return;
-            if (mass < goal + goal / 4) probes = 0;
-            else if (racing) probes = 2;
+            if (before <= kRanked && settle_in_list(value_of((uint32_t)(cut >> 32)), ~(uint32_t)cut, goal, true)) return;
         }
         if (!racing && cut >= kept) {
             cut = kept;
             verify = false;
-            probes = 0;
         }
     }
     cluster.sync();
@@ -838,10 +861,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
 
 cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream) {
     // CTAs per row: double while all rows' CTAs make two waves at most (152 SMs, four CTAs each) and a CTA has 4096 tokens
-    // left.  At 256 rows of 100003, on one, two, four and eight CTAs each: rows alike, with top_k 50 and top_p 0.9, take 53, 39,
-    // 47 and 77 us, rows of mixed settings 317, 202, 134 and 121 us, where the few flat rows' CTAs run on alone.  Four of 256
-    // threads to an SM against two of 512: 32 rows of 131072 take 17.8 us against 20.1.  (One wave, with the rows that step 2 does
-    // not settle left to a second launch of eight CTAs each, took 156 us for the mixed rows: the worst row's own time remains.)
+    // left.  At 256 rows of 100003, on one, two, four and eight CTAs each: rows alike, with top_k 50 and top_p 0.9, take 53, 40,
+    // 47 and 70 us, rows of mixed settings 204, 133, 92 and 104 us, where the few flat rows' CTAs run on alone.  Four of 256
+    // threads to an SM against three: greedy rows 22 us and 25, rows with top_k 50 and top_p 0.9 47 and 56, mixed ones 92 and 90.
     int ctas = 1;
     while (ctas < kMaxCtas && (int64_t)a.B * ctas * 2 <= 1216 && a.V / (2 * ctas) >= 4096) ctas *= 2;
     auto go = [&](auto kern) {

@@ -629,3 +629,20 @@ def test_sample_flat_and_sharp_rows_with_large_k(kind, spread):
         check_sample(x, u, k=k)
         check_sample(x, u, k=k, p=[0.9, 0.5, 0.99, 0.7, 0.3, 0.05, 0.8, 0.9, 0.95, 0.6, 0.4, 0.2])
         check_sample(x, u, t=[1.5] * B, k=k, p=[0.7] * B, m=[0.0, 0.01, 0.1] * 4)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [900, 70001])
+def test_sample_prefix_of_the_largest_token_alone(kind, V):
+    # top_p below, at and above the share of the largest token; of equal largest ones the first is the prefix
+    g = torch.Generator(device=dev()).manual_seed(V)
+    x = (0.5 * torch.randn((8, V), device=dev(), generator=g)).to(TYPES[kind])
+    x[0, V // 3] = 16.0                               # nearly all of the mass
+    x[1, V // 2] = 9.0
+    x[2, [V // 5, V // 2]] = 14.0                     # half of it each
+    x[3, [V // 5, V // 2]] = 14.0
+    x[4:6] = 0.0                                      # as many shares as tokens
+    u = torch.rand((8, V), device=dev(), generator=g)
+    for k in (None, [3, 0, 1, 2, 0, 700, 0, 5]):
+        tok, _ = check_sample(x, u, k=k, p=[0.9, 0.1, 0.4, 0.6, 0.5 / V, 0.0, 0.0, 1e-7], m=[0.0, 0.0, 0.5, 0.0, 0.0, 0.0, 0.9, 0.0])
+        assert tok[2] == V // 5 and tok[4] == 0 and tok[5] == 0
