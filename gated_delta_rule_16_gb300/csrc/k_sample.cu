@@ -26,7 +26,8 @@
 //      for one that does.  Thousands of equal logits leave them to descend the sorting key digit by digit, a pass over the
 //      row each.  The end of top_p's prefix is not looked for: the race is run over all of K, and its winner's mass above
 //      says whether it was kept.  If not, nothing below it is either, and the race is run again above it:
-//      1 + log(1 / top_p) times as a rule, or until what is left is few enough to be ranked;
+//      1 + log(1 / top_p) times as a rule.  As soon as each CTA's part of K, or of what lies above a rejected winner, is
+//      short enough, it is held in shared memory, and races and masses take it from there;
 //   4. the race.  The largest token is always kept, so its score bounds the winner's from the start: no Gumbel is above
 //      16.64, and a token whose logit cannot make up for it has its noise not read; of the others one comparison of
 //      1 - u with a multiple of w leaves a few per warp whose score is worked out.
@@ -46,6 +47,9 @@ constexpr int kMaxCtas = 8;   // per row: the largest cluster every GPU of this 
 constexpr int kList = 2048;   // gathered tokens
 constexpr int kRanked = 256;  // of them ranked by comparing all with all
 constexpr int kBins = 2048;
+// Tokens that a CTA holds for races.  With twice as many, four CTAs' shared memory leaves an SM 28 KB of L1, and greedy rows take
+// 27 us instead of 22 (256 x 100003); with none held, rows with top_k 5000 and top_p 0.5 take 197 us instead of 165.
+constexpr int kHeld = 1472;
 constexpr int kRounds = 24;   // races before the end of top_p's prefix is looked for
 constexpr float kUnit = 1099511627776.f;  // 2^40
 constexpr float kReach = 28.f;            // in y: 40 ln 2, below which a mass rounds to 0
@@ -80,6 +84,7 @@ __device__ __forceinline__ Best better(Best a, Best b) {
 
 struct Shared {
     u64 list[kList];
+    u64 held[kHeld];        // this CTA's tokens that may yet win
     uint32_t count[kBins];  // of this CTA's tokens
     u64 digit_sum[256];
     uint32_t digit_count[256];
@@ -87,7 +92,7 @@ struct Shared {
     Best bests[kWarps];
     float parts[2][kWarps];
     uint32_t leasts[kWarps];
-    int n, found;           // tokens gathered; digit found
+    int n, held_n, found;   // tokens gathered, held; digit found
     int lo, hi;             // bins found
     u64 before;
     bool whole;
@@ -319,45 +324,85 @@ __device__ __forceinline__ void each_together(const T *x, int from, int to, int 
     }
 }
 
-struct Above { int n; float mass; };
-
-// Gathers the tokens with logits in [least, upto), of logit `least` only those up to index `last`; the warp ends its pass
-// once they are too many.  Number and mass (in weights) of the tokens from upto up.
-template <bool kAbove, typename T>
-__device__ __noinline__ Above gather_pass(const T *x, int from, int to, float least, uint32_t last, float upto, float top, float rate, Shared &s) {
+// Gathers the tokens with logits from `least` up, of logit `least` only those up to index `last`, in list[0, room) and their
+// number in n; a warp ends its pass once they are too many.
+template <typename T>
+__device__ __noinline__ void gather_pass(const T *x, int from, int to, float least, uint32_t last, u64 *list, int room, int *n) {
     const int lane = threadIdx.x & 31;
-    Above a = {0, 0.f};
     least = fmaxf(least, -3.402823466e38f);
-    each_together<sizeof(T)>(x, from, to, 1, [&](auto q, auto n, const float *w, int at, int step) {
-        constexpr int N = decltype(n)::value, Q = decltype(q)::value;
+    each_together<sizeof(T)>(x, from, to, 1, [&](auto q, auto per, const float *w, int at, int step) {
+        constexpr int N = decltype(per)::value, Q = decltype(q)::value;
         if (!__any_sync(0xffffffffu, largest<Q * N>(w) >= least)) return true;
         uint32_t mine = 0;
 #pragma unroll
-        for (int e = 0; e < Q * N; ++e) {  // no branches: the tokens' latencies overlap
-            const float v = fminf(w[e], 3.402823466e38f);
-            const bool in = w[e] >= least, above = kAbove && in && v >= upto;  // NaN is not
-            if constexpr (kAbove) {
-                a.mass += ex2(((above ? v : -INFINITY) - top) * rate);
-                a.n += above;
-            }
-            mine |= (uint32_t)(in && !above && (v > least || (uint32_t)(at + e / N * step + e % N) <= last)) << e;
-        }
+        for (int e = 0; e < Q * N; ++e)  // NaN is not in
+            mine |= (uint32_t)(w[e] >= least && (fminf(w[e], 3.402823466e38f) > least || (uint32_t)(at + e / N * step + e % N) <= last)) << e;
         int end = 0;
         for (unsigned peers; (peers = __ballot_sync(0xffffffffu, mine != 0)) != 0;) {
             int place = 0;
-            if (lane == 0) place = atomicAdd(&s.n, __popc(peers));
+            if (lane == 0) place = atomicAdd(n, __popc(peers));
             place = __shfl_sync(0xffffffffu, place, 0);
             end = place + __popc(peers);
             place += __popc(peers & ((1u << lane) - 1));
             if (mine) {
                 const int e = __ffs(mine) - 1, i = at + e / N * step + e % N;
                 mine &= mine - 1;
-                if (place < kList) s.list[place] = full_key(clean(io<T>::ld(x + i)), i);
+                if (place < room) list[place] = full_key(clean(io<T>::ld(x + i)), i);
+            }
+        }
+        return end <= room;
+    });
+}
+
+// Gathers the tokens with logits in [least, upto); a warp ends its pass once they are too many.  Those from upto up are held, as
+// far as there is room, and counted; their mass (in weights).
+template <typename T>
+__device__ __noinline__ float bracket_pass(const T *x, int from, int to, float least, float upto, float top, float rate, Shared &s) {
+    const int lane = threadIdx.x & 31;
+    float mass = 0.f;
+    least = fmaxf(least, -3.402823466e38f);
+    each_together<sizeof(T)>(x, from, to, 1, [&](auto q, auto per, const float *w, int at, int step) {
+        constexpr int N = decltype(per)::value, Q = decltype(q)::value;
+        if (!__any_sync(0xffffffffu, largest<Q * N>(w) >= least)) return true;
+        uint32_t in = 0, above = 0;
+#pragma unroll
+        for (int e = 0; e < Q * N; ++e) {  // no branches: the tokens' latencies overlap
+            const float v = fminf(w[e], 3.402823466e38f);
+            const bool over = w[e] >= least && v >= upto;  // NaN is not
+            mass += ex2(((over ? v : -INFINITY) - top) * rate);
+            above |= (uint32_t)over << e;
+            in |= (uint32_t)(w[e] >= least && !over) << e;
+        }
+        // places of both kinds from one sum over the warp
+        const uint32_t own = __popc(in) | __popc(above) << 16;
+        uint32_t upto_here = own;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, upto_here, off);
+            if (lane >= off) upto_here += y;
+        }
+        int place = 0, held = 0;
+        if (lane == 31) {
+            place = atomicAdd(&s.n, (int)(upto_here & 0xffff));
+            held = atomicAdd(&s.held_n, (int)(upto_here >> 16));
+        }
+        const int end = __shfl_sync(0xffffffffu, place + (int)(upto_here & 0xffff), 31);
+        place = __shfl_sync(0xffffffffu, place, 31) + (int)(upto_here - own & 0xffff);
+        held = __shfl_sync(0xffffffffu, held, 31) + (int)(upto_here - own >> 16);
+        for (uint32_t left = in | above; left; left &= left - 1) {
+            const int e = __ffs(left) - 1, i = at + e / N * step + e % N;
+            const u64 key = full_key(clean(io<T>::ld(x + i)), i);
+            if (above >> e & 1) {
+                if (held < kHeld) s.held[held] = key;
+                ++held;
+            } else {
+                if (place < kList) s.list[place] = key;
+                ++place;
             }
         }
         return end <= kList;
     });
-    return a;
+    return mass;
 }
 
 __device__ __forceinline__ int bin_of(float v, float top, float scale) { return (int)fminf((top - v) * scale, (float)(kBins - 1)); }
@@ -387,6 +432,7 @@ __device__ float edge_of(int bin, float top, float scale) {
     return value_of(hi);
 }
 
+struct Above { int n; float mass; };
 // Number and mass (in weights) of the tokens before one of logit `mark` and index i, in descending order.
 template <typename T>
 __device__ __noinline__ Above mass_pass(const T *x, int from, int to, float mark, uint32_t i, float top, float rate) {
@@ -482,6 +528,29 @@ __device__ __noinline__ Best race_pass(const T *x, int from, int to, const Track
         reach = fminf(reach, reach_of(best));
         return true;
     });
+    return won;
+}
+
+// The same among the tokens held.
+__device__ __noinline__ Best race_held(const Track &track, Best won, Shared &s) {
+    constexpr int kStep = 4;
+    const int n = s.held_n;
+    float reach = track.reach;
+    for (int i0 = threadIdx.x; i0 < n; i0 += kStep * kThreads) {
+        u64 key[kStep];
+        float r[kStep];
+#pragma unroll
+        for (int j = 0; j < kStep; ++j) key[j] = i0 + j * kThreads < n ? s.held[i0 + j * kThreads] : 0;
+#pragma unroll
+        for (int j = 0; j < kStep; ++j) r[j] = key[j] >= track.cut && key[j] ? track.u[~(uint32_t)key[j]] : 0.f;
+#pragma unroll
+        for (int j = 0; j < kStep; ++j) {
+            const float v = value_of((uint32_t)(key[j] >> 32));
+            if (key[j] < track.cut || !key[j] || 1.f - r[j] >= ex2(fmaf(v - track.top, track.rate, reach))) continue;
+            won = better(won, exact_score(v, (int)~(uint32_t)key[j], track.top, track.t, track.min_p, r[j]));
+            reach = fminf(reach, reach_of(won.v));
+        }
+    }
     return won;
 }
 
@@ -648,16 +717,15 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
     };
 
     Best won = {-INFINITY, -1};
-    // Gathers the tokens from `least` up (of that logit: up to index `last`); if they fit, the first CTA cuts the list at
-    // rank k and at mass `goal` (0: at top_p of the list's first k), races what is left and writes the result.
-    auto settle_in_list = [&](float least, uint32_t last, u64 goal, bool few) {
+    // Gathers the tokens from `least` up; if they fit, the first CTA cuts the list at rank k and at mass `goal` (0: at top_p of the list's first k), races what is left and writes the result.
+    auto settle_in_list = [&](float least, u64 goal) {
         if (tid == 0) s.n = 0;
-        // unless they are known to be few: if every thread has some in a long slice, they are too many
+        // if every thread has some in a long slice, they are too many
         const int passing = __syncthreads_count(mine >= least);
-        if (!few && passing == kThreads && to - from > 2 * kList) {
+        if (passing == kThreads && to - from > 2 * kList) {
             if (tid == 0) s.n = kList + 1;
         } else {
-            gather_pass<false>(x, from, to, least, last, INFINITY, top.v, rate, s);
+            gather_pass(x, from, to, least, ~0u, s.list, kList, &s.n);
         }
         __syncthreads();
         if (tid == 0) s.x.gathered = min(s.n, kList + 1);
@@ -717,12 +785,15 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
     };
 
     u64 cut = 0;  // the key of the k-th token
+    bool held = false;  // whether what may yet win is held by the CTAs
+    // whether all CTAs of the row have room for what they count
+    auto fits = [&](int its_n) { return (int)__reduce_max_sync(0xffffffffu, reads ? its_n : 0) <= kHeld; };
     u64 goal = by_p && !by_k ? goal_of((double)total * (double)kUnit) : 0;
     if (by_k || by_p) {
         // 2. what passes the threshold
         if (!(by_k && by_p)) least = fmaxf(least, min_logit);  // with both, all of K counts in its mass
         if (by_p && !by_k) least = fmaxf(least, logit_of((1.f - fmaxf(p, 0.f)) * total / (float)a.V));
-        if ((least > -INFINITY || a.V <= kList) && settle_in_list(least, ~0u, goal, false)) return;
+        if ((least > -INFINITY || a.V <= kList) && settle_in_list(least, goal)) return;
     }
     if (by_k) {
         // 3. the k-th token, from a histogram over the logits
@@ -771,13 +842,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
             __syncthreads();
             const int lo = s.lo, hi = s.hi;
             const float gather_from = edge_of(deep ? min(hi, kBins - 2) : hi, top.v, scale), gather_upto = lo > 0 ? edge_of(lo - 1, top.v, scale) : INFINITY;
-            if (tid == 0) s.n = 0;
+            if (tid == 0) s.n = s.held_n = 0;
             __syncthreads();
-            const Above above = gather_pass<true>(x, from, to, gather_from, ~0u, gather_upto, top.v, rate, s);
-            u64 all_mass, all_above;
-            block_before((u64)(above.mass * kUnit + 0.5f), all_mass, s);
-            block_before((u64)above.n, all_above, s);
-            if (tid == 0) s.x.gathered = min(s.n, kList + 1), s.x.mass[0] = all_mass, s.x.above[0] = (int)all_above;
+            const float mass_above = bracket_pass(x, from, to, gather_from, gather_upto, top.v, rate, s);
+            u64 all_mass;
+            block_before((u64)(mass_above * kUnit + 0.5f), all_mass, s);
+            if (tid == 0) s.x.gathered = min(s.n, kList + 1), s.x.mass[0] = all_mass, s.x.above[0] = s.held_n;
             cluster.sync();
             const int its_n = from_peer.x.gathered, its_above = from_peer.x.above[0];
             const u64 its_mass = from_peer.x.mass[0], mass_before = sum_of(its_mass);
@@ -790,6 +860,13 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
                 collect(its_n);
                 cut = select(s, n, (u64)(k - before), false, 0, top.v, rate);
                 mass_k = mass_before + mass_from(n, cut);
+                held = fits(its_above + its_n);
+                if (held) {
+                    const int own_n = s.n;
+                    for (int i = tid; i < own_n; i += kThreads)
+                        if (s.list[i] >= cut) s.held[atomicAdd(&s.held_n, 1)] = s.list[i];
+                    __syncthreads();
+                }
             } else if (stride > 1) {
                 cluster.sync();  // others may still read what the next turn writes
                 continue;        // outside the bracket, or too many in it
@@ -823,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
             // no Gumbel is above 16.64
             const float floor = fmaxf(fmaxf(min_logit, top.v + t * (first.v - 16.7f) - 1e-5f * fabsf(top.v)), cut ? value_of((uint32_t)(cut >> 32)) : -INFINITY);
             const Track track = {u, top.v, t, rate, min_p, fmaxf(floor, -3.402823466e38f), reach_of(first.v), cut};
-            won = race_pass(x, from, to, track, first);
+            won = held ? race_held(track, first, s) : race_pass(x, from, to, track, first);
             won = block_best(won, s);
             if (tid == 0) s.x.won = won;
             cluster.sync();
@@ -831,22 +908,36 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
             if (!verify || won.i < 0) break;
             probe = full_key(clean(io<T>::ld(x + won.i)), won.i);
         }
-        const Above above = mass_pass(x, from, to, value_of((uint32_t)(probe >> 32)), ~(uint32_t)probe, top.v, rate);
-        u64 all_mass, all_above;
-        block_before((u64)(above.mass * kUnit + 0.5f), all_mass, s);
-        block_before((u64)above.n, all_above, s);
+        u64 own_mass = 0, own_above = 0, all_mass, all_above;
+        if (held) {
+            const int n = s.held_n;
+            for (int i = tid; i < n; i += kThreads)
+                if (s.held[i] > probe) own_mass += mass_of(value_of((uint32_t)(s.held[i] >> 32)), top.v, rate);
+        } else {
+            const Above above = mass_pass(x, from, to, value_of((uint32_t)(probe >> 32)), ~(uint32_t)probe, top.v, rate);
+            own_mass = (u64)(above.mass * kUnit + 0.5f);
+            own_above = (u64)above.n;
+        }
+        block_before(own_mass, all_mass, s);
+        block_before(own_above, all_above, s);
         const int slot = round & 1;
         if (tid == 0) s.x.mass[slot] = all_mass, s.x.above[slot] = (int)all_above;
         cluster.sync();
         const u64 mass = sum_of(from_peer.x.mass[slot]);
-        const int before = sum_of(from_peer.x.above[slot]);
+        const int its_above = from_peer.x.above[slot];
         if (mass < goal) {
             if (racing) break;
             kept = probe;
         } else {
             cut = probe + 1;  // the probe and what is below it are not kept
             won = {-INFINITY, -1};
-            if (before <= kRanked && settle_in_list(value_of((uint32_t)(cut >> 32)), ~(uint32_t)cut, goal, true)) return;
+            if (!held && fits(its_above)) {  // what is left: those above the probe
+                held = true;
+                if (tid == 0) s.held_n = 0;
+                __syncthreads();
+                gather_pass(x, from, to, value_of((uint32_t)(cut >> 32)), ~(uint32_t)cut, s.held, kHeld, &s.held_n);
+                __syncthreads();
+            }
         }
         if (!racing && cut >= kept) {
             cut = kept;
