@@ -7,7 +7,7 @@
 // What bounds it: every cached byte is read once and used for 2 G operations (G query heads per KV head; at most
 // 16 to a pass), so HBM, as long as tensor and issue slots keep up.  Measured: 64 requests of up to 8192 bf16 tokens
 // (8 KV heads of 128, G = 4) 170 us, 6.2 TB/s or 92 % of a copy; one of 131072 tokens 48 us; 32 e4m3 requests of up to 32768
-// (G = 8) 92 us, 5.6 TB/s; 256 dims 5.5 TB/s; fp32 4.8 TB/s; 16 heads to a pass 5.2 (bf16), 3.1 (e4m3).  The design
+// (G = 8) 92 us, 5.6 TB/s; 256 dims 5.5 TB/s; fp32 5.0 TB/s; 16 heads to a pass 5.2 (bf16), 3.1 (e4m3).  The design
 // follows from the bound:
 //   - Work is cut by cached tokens, not by requests.  All (request, KV head) rows are laid end to end in tiles of
 //     16 tokens per warp and the CTAs of one wave get equal runs of tiles.  A row inside one CTA is written out
@@ -83,7 +83,7 @@ struct Cfg {
     // CTAs per SM and ring slots of half a slice (K or V) per warp.  Warps hide each other's waits, so as many CTAs as the
     // registers allow (16 heads, or 256 dims, of output per warp take twice the registers of 8 heads of 128) with three
     // slots or more; what shared memory is left deepens the ring.  Measured against one CTA less per SM: 32 x 8192 bf16 tokens of
-    // 64 dims 56 -> 53 us, 64 x 8192 of 128 dims 175 -> 170, of 64 dims for 16 heads 66 -> 60, 16 x 8192 fp32 138 -> 99.
+    // 64 dims 56 -> 53 us, 64 x 8192 of 128 dims 175 -> 170, of 64 dims for 16 heads 66 -> 60, 16 x 8192 fp32 138 -> 99 (96 since).
     static constexpr int kOcc = kHalf > 8192 && NT == 2 ? 1 : kHalf > 4096 || D == 256 ? 2
                                 : NT == 2 ? (D == 64 && KIND != GDN_F32 ? 3 : 2) : kHalf > 2048 ? (KIND == GDN_BF16 && D == 64 ? 4 : 3) : 4;
     static constexpr int kSlots = kOcc == 1 ? 6 : kHalf > 4096 ? 3 : kOcc == 2 ? (kHalf > 2048 ? 6 : 8) : kOcc == 3 ? 4 : kHalf > 2048 ? 3 : kHalf > 1024 ? 5 : 8;
@@ -150,7 +150,7 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // x = hi + lo to 2^-24 of x, each rounded to tf32's 11 bits.  In integer arithmetic at the full rate, as the conversion
-// instruction has a quarter of it (16 x 8192 tokens: 98.8 us with it against 96.8).  lo cut instead of rounded saves another
+// instruction has a quarter of it (16 x 8192 tokens: 99 us with it against 96).  lo cut instead of rounded saves another
 // microsecond, but scores in the thousands then lose the bits that order their softmax.
 __device__ __forceinline__ uint32_t round_tf32(uint32_t x) { return (x + 0x1000u) & 0xffffe000u; }
 __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t &hi, uint32_t &lo) {
