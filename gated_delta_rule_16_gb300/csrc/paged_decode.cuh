@@ -6,8 +6,8 @@
 //
 // What bounds it: every cached byte is read once and used for 2 G operations (G query heads per KV head; at most
 // 16 to a pass), so HBM, as long as tensor and issue slots keep up.  Measured: 64 requests of up to 8192 bf16 tokens
-// (8 KV heads of 128, G = 4) 170 us, 6.2 TB/s or 92 % of a copy; one of 131072 tokens 48 us; 32 e4m3 requests of up to 32768
-// (G = 8) 92 us, 5.6 TB/s; 256 dims 5.5 TB/s; fp32 5.0 TB/s; 16 heads to a pass 5.2 (bf16), 3.1 (e4m3).  The design
+// (8 KV heads of 128, G = 4) 168 us, 6.3 TB/s or 93 % of a copy; one of 131072 tokens 48 us; 32 e4m3 requests of up to 32768
+// (G = 8) 86 us, 6.0 TB/s; 256 dims 5.6 TB/s; fp32 5.7 TB/s; 16 heads to a pass 5.4 (bf16), 3.4 (e4m3).  The design
 // follows from the bound:
 //   - Work is cut by cached tokens, not by requests.  All (request, KV head) rows are laid end to end in tiles of
 //     16 tokens per warp and the CTAs of one wave get equal runs of tiles.  A row inside one CTA is written out
@@ -38,6 +38,7 @@ namespace paged {
 
 constexpr int kSMs = 152;
 constexpr int kMaxCtas = 4 * kSMs;   // one wave
+constexpr int kPadded = 8;           // tiles per CTA from which on a row counts one tile more
 
 // Workspace.  A row cut between CTAs is described by one entry {request, row in request, first part, parts}: entry r of row
 // r = request * rows + row if rows are few (join_by_row; parts 0: not cut), else entry i - 1 of the
@@ -83,7 +84,7 @@ struct Cfg {
     // CTAs per SM and ring slots of half a slice (K or V) per warp.  Warps hide each other's waits, so as many CTAs as the
     // registers allow (16 heads, or 256 dims, of output per warp take twice the registers of 8 heads of 128) with three
     // slots or more; what shared memory is left deepens the ring.  Measured against one CTA less per SM: 32 x 8192 bf16 tokens of
-    // 64 dims 56 -> 53 us, 64 x 8192 of 128 dims 175 -> 170, of 64 dims for 16 heads 66 -> 60, 16 x 8192 fp32 138 -> 99 (96 since).
+    // 64 dims 56 -> 53 us, 64 x 8192 of 128 dims 175 -> 170, of 64 dims for 16 heads 66 -> 60, 16 x 8192 fp32 138 -> 99.
     static constexpr int kOcc = kHalf > 8192 && NT == 2 ? 1 : kHalf > 4096 || D == 256 ? 2
                                 : NT == 2 ? (D == 64 && KIND != GDN_F32 ? 3 : 2) : kHalf > 2048 ? (KIND == GDN_BF16 && D == 64 ? 4 : 3) : 4;
     static constexpr int kSlots = kOcc == 1 ? 6 : kHalf > 4096 ? 3 : kOcc == 2 ? (kHalf > 2048 ? 6 : 8) : kOcc == 3 ? 4 : kHalf > 2048 ? 3 : kHalf > 1024 ? 5 : 8;
@@ -237,15 +238,20 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
     const WsView ws = ws_view(a.ws, NT * 8);
     pdl_trigger();
 
-    // ---- this CTA's run of tiles [t0, t0 + n): requests lie one after the other, `rows` rows of the same tiles each
+    // ---- this CTA's run of tiles [t0, t0 + n): requests lie one after the other, `rows` rows of the same tiles each.  To begin
+    // and end a row takes a CTA about as long as a tile, so where runs are long enough to divide so finely a row counts one
+    // tile more (pad), which nobody has to do.  Without it CTAs with many short rows are the last: 32 e4m3 requests up to 32768
+    // tokens 92 us against 86, 256 bf16 requests up to 300 43 against 36, 16 fp32 up to 8192 95 against 82.  (Two or three tiles
+    // more: within 2 % of one, and 36 -> 38 us for the 256.)
     __shared__ int64_t scan[W];
     __shared__ int4 found;
     Cursor cur;
     int64_t total, t0, n;
-    int ctas;
+    int ctas, pad;
     const int cta = blockIdx.x;
     auto settle = [&](int64_t per_row) {  // false: no tiles for this CTA
-        total = per_row * rows;
+        pad = per_row * rows >= (int64_t)kPadded * gridDim.x;
+        total = (per_row + pad * a.B) * rows;
         ctas = (int)min((int64_t)gridDim.x, total);
         if (cta >= ctas) {
             if (tid == 0 && !by_row) ws.joins[cta - 1] = make_int4(0, 0, 0, 0);
@@ -268,9 +274,9 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
         }
         if (!settle(__shfl_sync(0xffffffffu, incl, 31))) return;
         const int64_t want = t0 / rows;
-        const int at = __popc(__ballot_sync(0xffffffffu, incl <= want));  // requests that end before
-        const int64_t off = t0 - __shfl_sync(0xffffffffu, incl - mine, at) * rows;
-        const int tiles = __shfl_sync(0xffffffffu, mine, at);
+        const int at = __popc(__ballot_sync(0xffffffffu, lane < a.B && incl + pad * (lane + 1) <= want));  // requests that end before
+        const int64_t off = t0 - (__shfl_sync(0xffffffffu, incl - mine, at) + pad * at) * rows;
+        const int tiles = __shfl_sync(0xffffffffu, mine, at) + pad;
         cur.b = at;
         cur.load<TILE>(a);
         cur.row = (int)(off / tiles);
@@ -288,7 +294,7 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
         for (int b0 = 0; b0 < a.B; b0 += C::kThreads) {
             cur.b = b0 + tid;
             cur.load<TILE>(a);
-            const int64_t mine = cur.b < a.B ? cur.tiles : 0;
+            const int64_t mine = cur.b < a.B ? cur.tiles + pad : 0;
             int64_t incl = mine;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -724,18 +730,27 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
         }
     };
 
+    int64_t done = 0;  // of the run, behind `cur`
+    if (cur.tile >= cur.tiles) {
+        done = cur.tiles + pad - cur.tile;
+        cur.tile = cur.tiles - 1;
+        cur.next<TILE>(a, rows);
+    }
     Cursor ahead = cur;  // the tile whose loads go out next
-    int64_t issued = 0;  // halves
-    Next next = find(ahead);
+    int64_t left = n - done;  // of the run from there on
+    bool second = false;      // V's half
+    Next next;
+    if (left > 0) next = find(ahead);
     int feed_slot = 0;
     auto feed = [&]() {
-        if (issued < 2 * n) {
-            const bool second = issued & 1;
+        if (left > 0) {
             issue(feed_slot, next, second ? a.c.v : a.c.k);
-            if (++issued < 2 * n && second) {
+            if (second) {
+                left -= ahead.tile == ahead.tiles - 1 ? 1 + pad : 1;
                 ahead.next<TILE>(a, rows);
-                next = find(ahead);
+                if (left > 0) next = find(ahead);
             }
+            second = !second;
         }
         feed_slot = feed_slot == C::kSlots - 1 ? 0 : feed_slot + 1;
         cp_commit();
@@ -749,11 +764,11 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
     };
     if (tid == 32 && !by_row && cta > 0) {  // beside the first loads
         const int64_t row0 = t0 - cur.tile, before = split_at(total, ctas, cta - 1);
-        const bool second = cur.tile > 0 && before <= row0;
-        ws.joins[cta - 1] = make_int4(cur.b, cur.row, 2 * (cta - 1) + (before < row0), second ? spread(cta - 1, row0 + cur.tiles) : 0);
+        const bool cut = cur.tile > 0 && before <= row0;
+        ws.joins[cta - 1] = make_int4(cur.b, cur.row, 2 * (cta - 1) + (before < row0), cut ? spread(cta - 1, row0 + cur.tiles) : 0);
     }
     bool open = false, began_here = false;
-    int segment = 0, slot = 0;
+    int part = 2 * cta, slot = 0;
     auto arrive = [&]() -> uint32_t {  // at the next half
         cp_wait<C::kSlots - 2>();
         __syncwarp();  // every lane's copies into this slot have landed, and the slot before is read
@@ -762,14 +777,15 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
         slot = slot == C::kSlots - 1 ? 0 : slot + 1;
         return at;
     };
-    for (int64_t it = 0; it < n; ++it) {
+    while (done < n) {
         if (!open) {
             begin_row(cur);
             open = true;
             began_here = cur.tile == 0;
+            part = 2 * cta + (done > 0);
             if (by_row && began_here && tid == 32) {
-                const int parts = n - it < cur.tiles ? spread(cta, t0 + it + cur.tiles) : 0;
-                ws.joins[cur.b * rows + cur.row] = make_int4(cur.b, cur.row, 2 * cta + (segment > 0), parts);
+                const int parts = n - done < cur.tiles ? spread(cta, t0 + done + cur.tiles) : 0;
+                ws.joins[cur.b * rows + cur.row] = make_int4(cur.b, cur.row, part, parts);
             }
         }
         const int k_slot = slot;
@@ -778,10 +794,10 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
         const uint32_t vb = arrive();
         if (mask) values(vb);
         const bool row_ends = cur.tile == cur.tiles - 1;
-        if (row_ends || it == n - 1) {
-            end_row(cur, began_here && row_ends, 2 * cta + (segment > 0));
+        done += row_ends ? 1 + pad : 1;
+        if (row_ends || done == n) {
+            end_row(cur, began_here && row_ends, part);
             open = false;
-            ++segment;
         }
         cur.next<TILE>(a, rows);
     }

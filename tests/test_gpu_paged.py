@@ -646,3 +646,16 @@ def test_sample_prefix_of_the_largest_token_alone(kind, V):
     for k in (None, [3, 0, 1, 2, 0, 700, 0, 5]):
         tok, _ = check_sample(x, u, k=k, p=[0.9, 0.1, 0.4, 0.6, 0.5 / V, 0.0, 0.0, 1e-7], m=[0.0, 0.0, 0.5, 0.0, 0.0, 0.0, 0.9, 0.0])
         assert tok[2] == V // 5 and tok[4] == 0 and tok[5] == 0
+
+
+@pytest.mark.parametrize("kind,d", [("bf16", 128), ("e4m3", 128), ("f32", 64), ("bf16", 256)])
+@pytest.mark.parametrize("lens", [
+    [9000, 1, 0, 17, 12000, 128, 64, 129, 1, 1, 9001, 15000, 3, 63, 65, 14000, 0, 5000],
+    [1] * 60 + [20000] + [64, 128, 0, 1] * 12 + [700] * 30 + [19999] + [2] * 40 + [4096, 3],
+])
+def test_attend_long_and_short_rows_together(kind, d, lens):
+    # enough tokens that a row's ends count in the shares of the CTAs, which may then begin or end between two rows
+    s = make(kind, lens, 8, 4, d, 16, seed=len(lens) + d)
+    poison(s)
+    check_attend(kind, s)
+    check_attend(kind, s, window=8000)
