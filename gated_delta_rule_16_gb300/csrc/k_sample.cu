@@ -634,7 +634,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
                 if (__syncthreads_count(own >= mid) >= need) lo = mid;
                 else hi = mid - 1;
             }
-            if (lo) least = value_of(lo);
+            // lo starts at 0 where a thread met no finite token, and keys below the lowest finite number's are no numbers: no threshold
+            if (lo >= key_of(-3.402823466e38f)) least = value_of(lo);
         }
     }
     if (tid == 0) s.x.top = top, s.x.sum = sum, s.x.low = low, s.x.least = least;

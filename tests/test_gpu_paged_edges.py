@@ -1,0 +1,71 @@
+"""The decode step over a paged cache at the edges of its inputs: masked rows of logits.
+
+References and tolerances are those of test_gpu_paged.py.
+"""
+import math
+
+import pytest
+import torch
+
+import gated_delta_rule_16_gb300 as gdn
+from test_gpu_paged import TYPES, check_sample, dev
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from gated_delta_rule_16_gb300 import build
+    build.build()
+    gdn.load()
+
+
+# ---- sampling: rows masked with the type's lowest value --------------------------------------------------
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [40, 512, 1000, 2000, 100003])
+def test_sample_top_k_of_rows_masked_with_the_lowest_value(kind, V):
+    # log-probabilities of a few allowed tokens; the others finfo.min, -inf, or both: fewer allowed tokens than top_k asks for,
+    # slices of the row without one, and threads that meet none that is finite
+    lowest = float(torch.finfo(TYPES[kind]).min)
+    g = torch.Generator(device=dev()).manual_seed(V)
+    allowed = torch.tensor([-0.5, -0.75, -1.0, -1.5, -2.0], device=dev())
+    x = torch.full((8, V), lowest, device=dev())
+    at = torch.randperm(V, device=dev(), generator=g)
+    x[1, ::2] = -math.inf
+    x[2] = -math.inf
+    x[3, V // 2:] = -math.inf
+    x[4, : V // 3] = -math.inf
+    x[5, torch.arange(V, device=dev()) % 1024 >= 28] = -math.inf   # whole threads without a finite token
+    for r in range(6):
+        x[r, at[:5]] = allowed
+    x[5, :20] = -1.25
+    x[6, 1::2] = -math.inf                           # nothing but the lowest value
+    x[7, at[: V // 2]] = -3e38                       # a large negative level above the lowest
+    x = x.to(TYPES[kind])
+    drawn = set()
+    for seed in range(6):
+        u = torch.rand((8, V), device=dev(), generator=g)
+        for k in (4, 10, 50, 600):
+            tok, _ = check_sample(x, u, k=[k] * 8)
+            drawn.add(int(tok[0]))
+            check_sample(x, u, t=[0.7] * 8, k=[k] * 8, p=[0.8] * 8)
+            check_sample(x, u, k=[k] * 8, m=[0.3] * 8)
+    assert len(drawn) > 1                            # drawn, not the largest each time
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_sample_top_k_where_one_slice_of_the_row_has_few_tokens(kind):
+    # 100003 tokens are shared by several CTAs; the k-th token lies in the slice with fewer than its share of the k
+    V, k = 100003, 50
+    x = torch.full((1, V), float(torch.finfo(TYPES[kind]).min), device=dev())
+    x[0, :12000][torch.arange(12000, device=dev()) % 2048 >= 56] = -math.inf
+    for s in range(1, 8):
+        x[0, 12600 * s: 12600 * s + 7 * 300: 300] = -1.0 - 0.0625 * s
+    x[0, 5] = -5.0
+    x = x.to(TYPES[kind])
+    u = torch.full((1, V), 0.25, device=dev())
+    u[0, 5] = 1.0
+    tok, _ = check_sample(x, u, k=[k])
+    assert int(tok[0]) == 5
