@@ -153,10 +153,11 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
 // x = hi + lo to 2^-24 of x, each rounded to tf32's 11 bits.  In integer arithmetic at the full rate, as the conversion
 // instruction has a quarter of it (16 x 8192 tokens: 99 us with it against 96).  lo cut instead of rounded saves another
 // microsecond, but scores in the thousands then lose the bits that order their softmax.
-__device__ __forceinline__ uint32_t round_tf32(uint32_t x) { return (x + 0x1000u) & 0xffffe000u; }
+// hi's rounding may carry a NaN's bits over into a zero's, so lo has to keep the NaN: it has 12 bits at most, for which a product
+// with 1 + 2^-11 that is cut rounds the same as an addition of half a unit would, and a NaN stays one.
 __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t &hi, uint32_t &lo) {
-    hi = round_tf32(x);
-    lo = round_tf32(__float_as_uint(__uint_as_float(x) - __uint_as_float(hi)));
+    hi = (x + 0x1000u) & 0xffffe000u;
+    lo = __float_as_uint((__uint_as_float(x) - __uint_as_float(hi)) * 1.00048828125f) & 0xffffe000u;
 }
 // both 8-bit values of x's low (high) half as f16: exact
 __device__ __forceinline__ uint32_t f16_lo(uint32_t x) {

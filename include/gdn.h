@@ -379,7 +379,8 @@ GDN_API gdn_status gdn_kv_append(const gdn_kv_cache *cache, int32_t n, gdn_dtype
  * Query head h reads KV head h / (Hq / Hkv).  A request left without a token
  * gets o = 0 and lse = -inf.  What the cache holds outside those tokens is
  * never used, whatever its bits; a non-finite value inside them reaches only the
- * rows and elements that read it (as infinity or NaN).
+ * rows and elements that read it (as infinity or NaN).  In fp32 storage
+ * magnitudes from 2^128 - 2^115 up count as infinite.
  * q [B][Hq][d] at b * q_stride_request + h * q_stride_head elements (multiples of
  * 16 bytes); o [B][Hq][d] contiguous; lse [B][Hq] fp32; q and o have the cache's
  * dtype, or GDN_BF16 with a GDN_E4M3 cache.  Row b of the block table starts at

@@ -1,4 +1,4 @@
-"""The decode step over a paged cache at the edges of its inputs: masked rows of logits.
+"""The decode step over a paged cache at the edges of its inputs: masked rows of logits, bit patterns of NaN.
 
 References and tolerances are those of test_gpu_paged.py.
 """
@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import gated_delta_rule_16_gb300 as gdn
-from test_gpu_paged import TYPES, check_sample, dev
+from test_gpu_paged import TYPES, check_sample, dev, make
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +69,43 @@ def test_sample_top_k_where_one_slice_of_the_row_has_few_tokens(kind):
     u[0, 5] = 1.0
     tok, _ = check_sample(x, u, k=[k])
     assert int(tok[0]) == 5
+
+
+# ---- attention: NaN whatever its bits ---------------------------------------------------------------------
+NAN_BITS = {"f32": [0x7FC00000, 0x7FFFFFFF, 0xFFFFFFFF, 0xFFC00000, 0x7F800001, 0xFFFFF000],
+            "bf16": [0x7FC0, 0x7FFF, 0xFFFF, 0x7F81], "e4m3": [0x7F, 0xFF]}
+WORDS = {1: torch.uint8, 2: torch.int16, 4: torch.int32}
+
+
+def put(t, where, bits):
+    size = t.element_size()
+    bits -= 1 << 8 * size if size > 1 and bits >> (8 * size - 1) else 0
+    t.view(WORDS[size])[where] = bits
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "f32"])
+@pytest.mark.parametrize("d,group", [(64, 4), (128, 9), (256, 1)])
+def test_attend_nan_of_any_bits_reaches_its_row_alone(kind, d, group):
+    lens, page, heads = [40, 90, 2000, 17], 16, 2
+    for bits in NAN_BITS[kind]:
+        for token, b in ((0, 0), (89, 1), (1111, 2)):
+            cell = lambda s: (int(s["block_table"][b, token // page]), token % page, 1, d - 3)
+            mine = slice(group, 2 * group)
+            for where in ("q", "k_cache", "v_cache"):
+                s = make(kind, lens, heads, group, d, page, seed=d + group)
+                if where == "q":
+                    wide = bits if s["q"].element_size() == s["k_cache"].element_size() else 0x7FFF
+                    put(s["q"], (b, group, 5), wide)
+                else:
+                    put(s[where], cell(s), bits)
+                o, lse = gdn.gdn_paged_decode(**s)
+                bad_o, bad_lse = torch.isnan(o), torch.isnan(lse)
+                want_o, want_lse = torch.zeros_like(bad_o), torch.zeros_like(bad_lse)
+                if where == "q":
+                    want_o[b, group], want_lse[b, group] = True, True
+                elif where == "k_cache":
+                    want_o[b, mine], want_lse[b, mine] = True, True
+                else:
+                    want_o[b, mine, d - 3] = True
+                assert torch.equal(bad_o, want_o) and torch.equal(bad_lse, want_lse), (hex(bits), token, where)
+                assert torch.isfinite(o[~want_o]).all() and torch.isfinite(lse[~want_lse]).all()
