@@ -7,13 +7,15 @@ passed as its ``transpose(1, 2)`` view.  An 8-bit cache is a pair of
 
 These calls run once per layer and token, so the marshalling is kept short:
 each check reads a tensor's attributes once, and the default workspace belongs
-to one device and stream.  Every call is enqueued on `stream` (default: the
+to one host thread, device and stream.  A workspace of the caller's is for one
+call at a time: calls of several threads need one each.  Every call is enqueued on `stream` (default: the
 current stream of the tensors' device) and returns without waiting.  For a call
 inside a CUDA graph pass the outputs and a workspace that outlive the graph.
 """
 from __future__ import annotations
 
 import ctypes
+import threading
 
 import torch
 
@@ -23,7 +25,17 @@ from ._binding import GDN_BF16, GDN_E4M3, GDN_F32, GdnKvCache, Workspace, _check
 _CODES = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
 _CACHE_CODES = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32, torch.float8_e4m3fn: GDN_E4M3}
 _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
-_ws = {}        # the default workspaces, by device and stream
+
+
+class _Local(threading.local):
+    """A thread's default workspaces, by device and stream.  Attention is two launches, between which another thread's
+    calls on the same stream may come."""
+
+    def __init__(self):
+        self.ws = {}
+
+
+_local = _Local()
 _ws_bytes = {}  # answers of gdn_paged_decode_workspace_bytes
 _current_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
@@ -63,11 +75,12 @@ def _handle(dev, stream, *outputs):
 
 
 def _workspace(ws, nbytes, dev, handle, stream):
-    """(address, bytes) of the caller's workspace, or of this device and stream's own."""
+    """(address, bytes) of the caller's workspace, or of this thread, device and stream's own."""
     if ws is None:
-        buf = _ws.get((dev, handle))
+        own = _local.ws
+        buf = own.get((dev, handle))
         if buf is None or buf.numel() < nbytes:
-            buf = _ws[dev, handle] = _empty((nbytes,), dtype=torch.uint8, device=torch.device("cuda", dev))
+            buf = own[dev, handle] = _empty((nbytes,), dtype=torch.uint8, device=torch.device("cuda", dev))
             _handle(dev, stream, buf)
         return buf.data_ptr(), buf.numel()
     if isinstance(ws, Workspace):

@@ -390,7 +390,9 @@ GDN_API gdn_status gdn_kv_append(const gdn_kv_cache *cache, int32_t n, gdn_dtype
  * the lengths of all requests of the call, never on timing: the same call gives
  * the same bits.
  * Workspace: gdn_paged_decode_workspace_bytes(cache, Hq), 256-byte aligned; its
- * contents need no set-up and do not outlive the call. */
+ * contents need no set-up and do not outlive the call.  The call is two launches:
+ * host threads that share a stream need a workspace each, as the launches of one
+ * may come between those of the other. */
 GDN_API size_t gdn_paged_decode_workspace_bytes(const gdn_kv_cache *cache, int32_t Hq);
 GDN_API gdn_status gdn_paged_decode(const gdn_kv_cache *cache, int32_t B, int32_t Hq, gdn_dtype dtype, const void *q,
                                     int64_t q_stride_request, int64_t q_stride_head, const int32_t *block_table,

@@ -1,8 +1,9 @@
-"""The decode step over a paged cache at the edges of its inputs: masked rows of logits, bit patterns of NaN.
+"""The decode step over a paged cache at the edges of its inputs: masked rows of logits, bit patterns of NaN, several host threads.
 
 References and tolerances are those of test_gpu_paged.py.
 """
 import math
+import threading
 
 import pytest
 import torch
@@ -109,3 +110,31 @@ def test_attend_nan_of_any_bits_reaches_its_row_alone(kind, d, group):
                     want_o[b, mine, d - 3] = True
                 assert torch.equal(bad_o, want_o) and torch.equal(bad_lse, want_lse), (hex(bits), token, where)
                 assert torch.isfinite(o[~want_o]).all() and torch.isfinite(lse[~want_lse]).all()
+
+
+# ---- several host threads -----------------------------------------------------------------------------------
+def test_attend_from_two_threads_on_one_stream():
+    # rows cut between CTAs, joined by a second launch: another thread's calls come in between
+    cases = [make("bf16", [9000, 300, 4000], 2, 4, 128, 16, seed=21), make("e4m3", [20000, 1, 77, 5000, 12000], 4, 9, 128, 64, seed=22)]
+    want = [gdn.gdn_paged_decode(**s) for s in cases]
+    torch.cuda.synchronize()
+    got, errors = [[], []], []
+    meet = threading.Barrier(2)
+
+    def run(i):
+        try:
+            meet.wait(30)
+            for _ in range(200):
+                got[i].append(gdn.gdn_paged_decode(**cases[i]))
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for i in (0, 1):
+        assert len(got[i]) == 200 and all(torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1]) for o, lse in got[i])

@@ -1,0 +1,75 @@
+"""The binding of the decode-step entry points: what it passes on to the library.  No GPU: host tensors that say they are on
+device 0, and a library that only takes down its arguments."""
+import threading
+
+import pytest
+import torch
+
+import gated_delta_rule_16_gb300 as gdn
+from gated_delta_rule_16_gb300 import _binding, paged
+
+
+class OnDevice(torch.Tensor):
+    def get_device(self):
+        return 0
+
+
+def empty(shape, dtype=torch.float32, device=None):
+    return torch.empty(shape, dtype=dtype).as_subclass(OnDevice)
+
+
+class Library:
+    """Workspaces of 1000 bytes per query head; calls wait at `meet`, then are noted."""
+
+    def __init__(self, meet=None):
+        self.meet, self.calls = meet, []
+
+    def gdn_paged_decode_workspace_bytes(self, cache, heads):
+        return 1000 * heads
+
+    def gdn_paged_decode(self, *args):
+        if self.meet:
+            self.meet.wait(10)
+        self.calls.append(args)
+        return 0
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    def use(lib, stream=7):
+        monkeypatch.setattr(_binding, "_lib", lib)
+        monkeypatch.setattr(paged, "_current_device", lambda: 0)
+        monkeypatch.setattr(paged, "_current_stream", lambda dev: stream)
+        monkeypatch.setattr(paged, "_empty", empty)
+        monkeypatch.setattr(paged, "_ws_bytes", {})
+        return lib
+    return use
+
+
+def decode(heads=4, **kw):
+    cache = empty((3, 16, 2, 64), torch.bfloat16)
+    return gdn.gdn_paged_decode(empty((2, heads, 64), torch.bfloat16), cache, cache, empty((2, 3), torch.int32), empty((2,), torch.int32), **kw)
+
+
+def test_threads_on_one_stream_have_workspaces_of_their_own(fake):
+    # a call is two launches, between which another thread's may come: both calls are in the library at once here
+    lib = fake(Library(threading.Barrier(2)))
+    errors = []
+
+    def run(heads):
+        try:
+            for _ in range(3):
+                decode(heads)
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(h,)) for h in (4, 8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    by_heads = {h: {a[-3] for a in lib.calls if a[2] == h} for h in (4, 8)}
+    assert len(lib.calls) == 6 and all(a[-2] >= 1000 * a[2] for a in lib.calls)
+    assert len(by_heads[4]) == len(by_heads[8]) == 1      # a thread keeps its own from call to call
+    assert by_heads[4] != by_heads[8]
