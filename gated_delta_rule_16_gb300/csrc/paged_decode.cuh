@@ -22,8 +22,10 @@
 //     both operands in shared memory; at 2 G flops a byte the warp form has the rate needed, and P stays in registers.
 //     P^T comes from the S^T fragment by transposing 8x8 tiles between registers (movmatrix).
 //   - Rounding: scores, maxima, sums and outputs are fp32.  P enters the second product as two bf16 terms (16 bits
-//     together) for a bf16 cache, as f16 (11 bits) for an 8-bit cache, where K and V are converted exactly to f16 and
-//     q, scaled by a power of two to below 2, loses nothing unless it is 2^14 times smaller than the row's largest.  A
+//     together) for a bf16 cache; for an 8-bit cache as f16 of 2^15 P (11 bits down to 2^-29 of a warp's largest weight, an
+//     absolute 2^-40 of it below, so that a long tail of small weights keeps its mass; a second f16 term would bring the outputs
+//     five times as near to those of fp32 weights, below bf16's own rounding, and take 5 % more time), where K and V are
+//     converted exactly to f16 and q, scaled by a power of two to below 2, loses nothing unless it is 2^14 times smaller than the row's largest.  A
 //     32-bit cache splits every operand into two tf32 terms, drops the product of the low ones (2^-22) and adds each
 //     8-wide product to its sum outside the tensor core, whose own accumulation cuts instead of rounding: that
 //     drift alone put scores of thousands past 1e-5.
@@ -89,6 +91,7 @@ struct Cfg {
                                 : NT == 2 ? (D == 64 && KIND != GDN_F32 ? 3 : 2) : kHalf > 2048 ? (KIND == GDN_BF16 && D == 64 ? 4 : 3) : 4;
     static constexpr int kSlots = kOcc == 1 ? 6 : kHalf > 4096 ? 3 : kOcc == 2 ? (kHalf > 2048 ? 6 : 8) : kOcc == 3 ? 4 : kHalf > 2048 ? 3 : kHalf > 1024 ? 5 : 8;
     static constexpr int kRing = kSlots * kHalf;      // per warp
+    static constexpr float kUnit = KIND == GDN_E4M3 ? 32768.f : 1.f;  // of weights and of outputs until a row's end
     static constexpr int kMergeDims = (KIND == GDN_F32 && NT == 2) || (kOcc == 4 && kHalf > 2048) ? 32 : 64;  // output dims joined per round at a row's end
     static constexpr int kMerge = kWarps * 8 * (kMergeDims + 4) * 4;
     static constexpr int kQ = KIND == GDN_F32 ? NT * (D / 8) * 32 * 8 : 0;
@@ -597,7 +600,8 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) b[u][nt][i] = transpose8x8(pack_f16(p[u][nt][2 * i], p[u][nt][2 * i + 1]));
+                    for (int i = 0; i < 2; ++i)
+                        b[u][nt][i] = transpose8x8(pack_f16(p[u][nt][2 * i] * C::kUnit, p[u][nt][2 * i + 1] * C::kUnit));
             // a lane's 4 bytes of a token are dims 4 g .. 4 g + 3 of a block of 32; bytes of neighbouring tokens are
             // paired into the A fragments of two 16-row tiles whose rows g, g + 8 are dims 4 g, 4 g + 1 and 4 g + 2, 4 g + 3
 #pragma unroll
@@ -679,7 +683,7 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
                 float top = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < W; ++w) top = fmaxf(top, ml[w * NT * 8 + nt * 8 + 2 * q4 + j].x);
-                f[j] = exp2_fast(m[nt][j] - (top == -INFINITY ? 0.f : top));
+                f[j] = exp2_fast(m[nt][j] - (top == -INFINITY ? 0.f : top)) * (1.f / C::kUnit);
             }
 #pragma unroll
             for (int r = 0; r < D / kMergeDims; ++r) {

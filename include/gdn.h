@@ -386,7 +386,10 @@ GDN_API gdn_status gdn_kv_append(const gdn_kv_cache *cache, int32_t n, gdn_dtype
  * dtype, or GDN_BF16 with a GDN_E4M3 cache.  Row b of the block table starts at
  * b * table_stride (0: all requests share one row, as the rows of a prompt chunk
  * do with seq_lens c+1, c+2, ...).
- * Sums are held in fp32; a row's tokens are summed in an order that depends on
+ * Scores, maxima, sums and outputs are held in fp32.  Weights exp(z - max z) enter
+ * the product with V in fewer bits, those of o's type at least: 16 with a GDN_BF16
+ * cache; 11 with a GDN_E4M3 one, or 2^-40 of the largest where that is coarser; 22
+ * with a GDN_F32 one.  A row's tokens are summed in an order that depends on
  * the lengths of all requests of the call, never on timing: the same call gives
  * the same bits.
  * Workspace: gdn_paged_decode_workspace_bytes(cache, Hq), 256-byte aligned; its

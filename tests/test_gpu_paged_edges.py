@@ -1,4 +1,5 @@
-"""The decode step over a paged cache at the edges of its inputs: masked rows of logits, bit patterns of NaN, several host threads.
+"""The decode step over a paged cache at the edges of its inputs: masked rows of logits, bit patterns of NaN, weights far
+below the largest, several host threads.
 
 References and tolerances are those of test_gpu_paged.py.
 """
@@ -9,7 +10,7 @@ import pytest
 import torch
 
 import gated_delta_rule_16_gb300 as gdn
-from test_gpu_paged import TYPES, check_sample, dev, make
+from test_gpu_paged import ROW_TOL, TYPES, check_sample, dev, i32, make, ref_attend
 
 pytestmark = pytest.mark.gpu
 
@@ -138,3 +139,35 @@ def test_attend_from_two_threads_on_one_stream():
     assert not errors
     for i in (0, 1):
         assert len(got[i]) == 200 and all(torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1]) for o, lse in got[i])
+
+
+# ---- attention: weights far below the largest ---------------------------------------------------------------
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "f32"])
+@pytest.mark.parametrize("octaves", [10.0, 14.5, 20.3, 24.5, 25.0, 26.0, 30.0])
+@pytest.mark.parametrize("tokens,rows", [(300, 1), (1 << 17, 1), (1 << 17, 700)])
+def test_attend_a_long_tail_below_one_token(kind, octaves, tokens, rows):
+    # One token's weight is 1, every other's 2^-octaves: what the tail holds together must not be lost.  With many rows each is
+    # one CTA's, and a quarter of its tail one warp's.
+    d, page, group = 64, 64, 4
+    g = torch.Generator(device=dev()).manual_seed(3)
+    q = torch.zeros((rows, group, d), device=dev())
+    q[..., 0] = 1.0
+    k, v = (torch.zeros((2, page, 1, d), device=dev()) for _ in range(2))
+    k[0, 5, 0, 0] = 64.0                             # exact in every type
+    v[0] = 0.25 * torch.randn((page, 1, d), device=dev(), generator=g)
+    v[0, 5] = 0.5
+    v[1] = 300.0
+    table = torch.ones((1, tokens // page + 1), dtype=torch.int32, device=dev())
+    table[0, 0] = 0                                  # the token's page once, the other one again and again
+    scales = dict(zip(("k_scale", "v_scale"), torch.ones((2, 1), device=dev()) if kind == "e4m3" else (None, None)))
+    scale = octaves * math.log(2.0) / 64.0
+    # a warp adds tokens / 64 slices one after the other in fp32
+    steps = tokens / 64 * 2.0 ** -23
+    for order, n in ((table, tokens), (table.flip(1), table.shape[1] * page)):   # the token first, or in the row's last page
+        s = dict(q=q.to(torch.float32 if kind == "f32" else torch.bfloat16), k_cache=k.to(TYPES[kind]), v_cache=v.to(TYPES[kind]),
+                 block_table=order.contiguous().expand(rows, -1), seq_lens=i32([n] * rows), **scales)
+        o, lse = gdn.gdn_paged_decode(**s, scale=scale)
+        want_o, want_lse, off = ref_attend({**s, "q": s["q"][:1], "block_table": s["block_table"][:1], "seq_lens": s["seq_lens"][:1]}, scale=scale)
+        err = (o.double() - want_o).norm(dim=-1) / want_o.norm(dim=-1)
+        assert (err <= ROW_TOL[kind] + steps).all(), err.max().item()
+        assert ((lse.double() - want_lse).abs() <= off + steps + 2.0 ** -20 * (1 + want_lse.abs())).all()
