@@ -574,10 +574,11 @@ __global__ void __launch_bounds__(Cfg<KIND, D, NT>::kThreads, Cfg<KIND, D, NT>::
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const float p0 = p[u][nt][2 * i], p1 = p[u][nt][2 * i + 1];
-                        // cut, not rounded, so that both terms of a weight are positive: an infinite value stays infinite
+                        // cut, not rounded, so that both terms of a weight are positive: an infinite value stays infinite.  The low
+                        // one is at least 2^-24 of the weight: a fixed least would let values of 1e38 in that have no weight
                         const uint32_t h = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
-                        const uint32_t r = pack_bf16(fmaxf(p0 - __uint_as_float(h << 16), 1.17549435e-38f),
-                                                     fmaxf(p1 - __uint_as_float(h & 0xffff0000u), 1.17549435e-38f));
+                        const uint32_t r = pack_bf16(fmaxf(p0 - __uint_as_float(h << 16), p0 * 5.9604645e-8f),
+                                                     fmaxf(p1 - __uint_as_float(h & 0xffff0000u), p1 * 5.9604645e-8f));
                         hi[u][nt][i] = transpose8x8(h);
                         lo[u][nt][i] = transpose8x8(r);
                     }

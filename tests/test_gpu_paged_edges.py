@@ -1,5 +1,5 @@
 """The decode step over a paged cache at the edges of its inputs: masked rows of logits, bit patterns of NaN, weights far
-below the largest, several host threads.
+below the largest, values near the type's largest, several host threads.
 
 References and tolerances are those of test_gpu_paged.py.
 """
@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import gated_delta_rule_16_gb300 as gdn
-from test_gpu_paged import ROW_TOL, TYPES, check_sample, dev, i32, make, ref_attend
+from test_gpu_paged import ROW_TOL, TYPES, check_attend, check_sample, dev, i32, make, ref_attend
 
 pytestmark = pytest.mark.gpu
 
@@ -171,3 +171,18 @@ def test_attend_a_long_tail_below_one_token(kind, octaves, tokens, rows):
         err = (o.double() - want_o).norm(dim=-1) / want_o.norm(dim=-1)
         assert (err <= ROW_TOL[kind] + steps).all(), err.max().item()
         assert ((lse.double() - want_lse).abs() <= off + steps + 2.0 ** -20 * (1 + want_lse.abs())).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_attend_huge_values_of_tokens_without_weight(kind):
+    # 3e38 at a weight of 2^-400 (0 in fp32) adds nothing
+    s = make(kind, [100, 5000], 2, 4, 128, 16, seed=12)
+    s["q"][...] = 0
+    s["q"][..., 0] = 8.0
+    s["k_cache"][..., 0] = 8.0
+    huge = torch.finfo(TYPES[kind]).min / 2
+    for b, token in ((0, 0), (0, 33), (0, 99), (1, 4000), (1, 3)):
+        page, cell = int(s["block_table"][b, token // 16]), token % 16
+        s["k_cache"][page, cell, :, 0] = -28.0
+        s["v_cache"][page, cell, :, ::3] = huge
+    check_attend(kind, s, scale=1.0)
