@@ -8,8 +8,9 @@ passed as its ``transpose(1, 2)`` view.  An 8-bit cache is a pair of
 These calls run once per layer and token, so the marshalling is kept short:
 each check reads a tensor's attributes once, and the default workspace belongs
 to one host thread, device and stream.  A workspace of the caller's is for one
-call at a time: calls of several threads need one each.  Every call is enqueued on `stream` (default: the
-current stream of the tensors' device) and returns without waiting.  For a call
+call at a time: calls of several threads need one each.  Every call is enqueued
+on `stream` (default: the current stream of the tensors' device) and returns
+without waiting; what it allocates is free in that stream's order.  For a call
 inside a CUDA graph pass the outputs and a workspace that outlive the graph.
 """
 from __future__ import annotations
@@ -63,29 +64,45 @@ def _cuda(t, name):
     return dev
 
 
-def _handle(dev, stream, *outputs):
-    """The call's stream as an address.  Outputs that torch has handed out for the current stream are recorded on
-    another one, so that their memory is not reused while the call still runs."""
-    current = _current_stream(dev)
-    if stream is None or stream.cuda_stream == current:
-        return current
-    for t in outputs:
-        t.record_stream(stream)
-    return stream.cuda_stream
+def _handle(dev, stream):
+    """The call's stream as an address."""
+    return _current_stream(dev) if stream is None else stream.cuda_stream
 
 
-def _workspace(ws, nbytes, dev, handle, stream):
+def _elsewhere(dev, stream):
+    """Whether the call's stream is not the current one."""
+    return stream.cuda_stream != _current_stream(dev)
+
+
+def _on(stream, dev, fn, given, *args, **kw):
+    """fn on another stream than the current one.  It becomes the current one for the call, so that the memory of outputs
+    and workspaces which the call makes is free in that stream's order; memory that work of the stream outside may still
+    use is not handed out.  Tensors of either stream are recorded on the other: they are not reused while one of both uses them."""
+    if stream.device_index != dev:
+        raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors are on cuda:{dev}")
+    outside = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        got = fn(*args, **kw)
+    for t in given:
+        if isinstance(t, Workspace):
+            t = t.buf
+        if t is not None:
+            t.record_stream(stream)
+    for t in got:
+        t.record_stream(outside)
+    return got
+
+
+def _workspace(ws, nbytes, dev, handle):
     """(address, bytes) of the caller's workspace, or of this thread, device and stream's own."""
     if ws is None:
         own = _local.ws
         buf = own.get((dev, handle))
         if buf is None or buf.numel() < nbytes:
             buf = own[dev, handle] = _empty((nbytes,), dtype=torch.uint8, device=torch.device("cuda", dev))
-            _handle(dev, stream, buf)
         return buf.data_ptr(), buf.numel()
     if isinstance(ws, Workspace):
         ws = ws.get(nbytes, torch.device("cuda", dev))
-        _handle(dev, stream, ws)
     if ws.get_device() != dev:
         raise ValueError(f"workspace must be on cuda:{dev}, is on {ws.device}")
     return ws.data_ptr(), ws.numel() * ws.element_size()
@@ -138,6 +155,10 @@ def gdn_page_tables(new_lens, free_pages, block_table, *, page, cached_lens=None
     Returns (slots int64, positions int32, seq_lens int32 [B], cu_new int32 [B+1], counts int32 [4] =
     {tokens, pages taken, status bits, longest sequence}); gdn_page_tables_status reads the status."""
     dev = _cuda(block_table, "block_table")
+    if stream is not None and _elsewhere(dev, stream):
+        return _on(stream, dev, gdn_page_tables, (slots, positions, seq_lens, cu_new, counts), new_lens, free_pages, block_table,
+                   page=page, cached_lens=cached_lens, n_slots=n_slots, slots=slots, positions=positions, seq_lens=seq_lens,
+                   cu_new=cu_new, counts=counts)
     B, max_pages = block_table.shape
     if n_slots is None:
         if slots is None:
@@ -160,7 +181,7 @@ def gdn_page_tables(new_lens, free_pages, block_table, *, page, cached_lens=None
           _want(block_table, "block_table", _I32, (B, max_pages), dev), _want(seq_lens, "seq_lens", _I32, (B,), dev),
           _want(cu_new, "cu_new", _I32, (B + 1,), dev), _want(slots, "slots", _I64, (n_slots,), dev),
           _want(positions, "positions", _I32, (n_slots,), dev), n_slots, _want(counts, "counts", _I32, (4,), dev),
-          _handle(dev, stream, slots, positions, seq_lens, cu_new, counts))
+          _current_stream(dev))
     return slots, positions, seq_lens, cu_new, counts
 
 
@@ -199,6 +220,9 @@ def gdn_paged_decode(q, k_cache, v_cache, block_table, seq_lens, *, k_scale=None
     [B] int32, the new token included; window: only the last `window` tokens (0: all); scale:
     default dim ** -0.5.  Returns (o [B, heads, dim] in q's dtype, lse [B, heads] fp32)."""
     dev = _cuda(q, "q")
+    if stream is not None and _elsewhere(dev, stream):
+        return _on(stream, dev, gdn_paged_decode, (o, lse, workspace), q, k_cache, v_cache, block_table, seq_lens, k_scale=k_scale,
+                   v_scale=v_scale, scale=scale, window=window, o=o, lse=lse, workspace=workspace)
     c = _cache(k_cache, v_cache, k_scale, v_scale, dev)
     code = _CODES.get(q.dtype)
     if code is None or (c.dtype != GDN_E4M3 and c.dtype != code):
@@ -226,12 +250,12 @@ def gdn_paged_decode(q, k_cache, v_cache, block_table, seq_lens, *, k_scale=None
         lse_at = lse.data_ptr()
     else:
         lse_at = _want(lse, "lse", _F32, (B, heads), dev)
-    handle = _handle(dev, stream, o, lse)
+    handle = _current_stream(dev)
     key = (c.dtype, d, heads, c.Hkv)
     nbytes = _ws_bytes.get(key)
     if nbytes is None:
         nbytes = _ws_bytes[key] = load().gdn_paged_decode_workspace_bytes(c, heads)
-    ws, ws_bytes = _workspace(workspace, nbytes, dev, handle, stream)
+    ws, ws_bytes = _workspace(workspace, nbytes, dev, handle)
     _call("gdn_paged_decode", dev, c, B, heads, code, q.data_ptr(), qs[0], qs[1], block_table.data_ptr(), ts[0], max_pages,
           _want(seq_lens, "seq_lens", _I32, (B,), dev), window, d ** -0.5 if scale is None else scale, o_at, lse_at,
           ws, ws_bytes, handle)
@@ -244,6 +268,9 @@ def gdn_sample(logits, noise, *, temperature=None, top_k=None, top_p=None, min_p
     noise [B, V] (fp32).  temperature, top_p, min_p [B] fp32 and top_k [B] int32: include/gdn.h has the
     order of the filters; None leaves one out.  Returns (tokens int32 [B], logprobs fp32 [B])."""
     dev = _cuda(logits, "logits")
+    if stream is not None and _elsewhere(dev, stream):
+        return _on(stream, dev, gdn_sample, (tokens, logprobs), logits, noise, temperature=temperature, top_k=top_k, top_p=top_p,
+                   min_p=min_p, tokens=tokens, logprobs=logprobs)
     code = _CODES.get(logits.dtype)
     if code is None:
         raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
@@ -264,5 +291,5 @@ def gdn_sample(logits, noise, *, temperature=None, top_k=None, top_p=None, min_p
           None if top_p is None else _want(top_p, "top_p", _F32, rows, dev),
           None if min_p is None else _want(min_p, "min_p", _F32, rows, dev),
           _want(tokens, "tokens", _I32, rows, dev), _want(logprobs, "logprobs", _F32, rows, dev),
-          _handle(dev, stream, tokens, logprobs))
+          _current_stream(dev))
     return tokens, logprobs

@@ -1,5 +1,5 @@
 """The decode step over a paged cache at the edges of its inputs: masked rows of logits, bit patterns of NaN, weights far
-below the largest, values near the type's largest, several host threads.
+below the largest, values near the type's largest, several host threads and streams.
 
 References and tolerances are those of test_gpu_paged.py.
 """
@@ -186,3 +186,27 @@ def test_attend_huge_values_of_tokens_without_weight(kind):
         s["k_cache"][page, cell, :, 0] = -28.0
         s["v_cache"][page, cell, :, ::3] = huge
     check_attend(kind, s, scale=1.0)
+
+
+def test_outputs_on_another_stream_are_not_what_pending_work_still_writes():
+    s = make("bf16", [9000, 300, 4000], 2, 4, 128, 16, seed=23)
+    x, u = (torch.rand((4, 50000), device=dev(), generator=torch.Generator(device=dev()).manual_seed(24)) for _ in range(2))
+    top_k, new, free, table = i32([40] * 4), i32([5, 40]), i32(list(range(9))), torch.full((2, 4), -1, dtype=torch.int32, device=dev())
+    calls = [lambda **kw: gdn.gdn_paged_decode(**s, **kw), lambda **kw: gdn.gdn_sample(x, u, top_k=top_k, **kw),
+             lambda **kw: gdn.gdn_page_tables(new, free, table, page=16, n_slots=50, **kw)]
+    side = torch.cuda.Stream()
+    for call in calls:
+        want = call()
+        torch.cuda.synchronize()
+        side.wait_stream(torch.cuda.current_stream())
+        # memory of every output's and the workspace's size that the current stream still writes after its owner is gone
+        old = [torch.empty_like(t) for t in want for _ in range(3)] + [torch.empty(1 << 25, dtype=torch.uint8, device=dev())]
+        torch.cuda._sleep(200_000_000)
+        for t in old:
+            t.fill_(3)
+        del old, t
+        got = call(stream=side)
+        side.synchronize()
+        first = [t.cpu() for t in got]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b.cpu()) and torch.equal(a, w.cpu()) for a, b, w in zip(first, got, want))

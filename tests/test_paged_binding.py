@@ -73,3 +73,65 @@ def test_threads_on_one_stream_have_workspaces_of_their_own(fake):
     assert len(lib.calls) == 6 and all(a[-2] >= 1000 * a[2] for a in lib.calls)
     assert len(by_heads[4]) == len(by_heads[8]) == 1      # a thread keeps its own from call to call
     assert by_heads[4] != by_heads[8]
+
+
+class Stream:
+    def __init__(self, handle, device_index=0):
+        self.cuda_stream, self.device_index = handle, device_index
+
+
+@pytest.mark.parametrize("op", ["tables", "decode", "sample"])
+def test_outputs_and_workspace_are_made_on_the_calls_stream(fake, monkeypatch, op):
+    # memory that is free in the current stream's order may still be in use when the call runs on another one
+    now, made, recorded = [7], [], []
+
+    class Within:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.stream.cuda_stream
+
+        def __exit__(self, *_):
+            now[0] = self.before
+
+    class Noted(Library):
+        def gdn_page_tables(self, *args):
+            self.calls.append(args)
+            return 0
+
+        gdn_sample = gdn_page_tables
+
+    def tracked(shape, dtype=torch.float32, device=None):
+        t = empty(shape, dtype)
+        made.append((now[0], t.data_ptr()))
+        return t
+
+    lib = fake(Noted())
+    monkeypatch.setattr(paged, "_current_stream", lambda dev: now[0])
+    monkeypatch.setattr(paged, "_empty", tracked)
+    monkeypatch.setattr(torch.cuda, "stream", Within)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: Stream(now[0]))
+    monkeypatch.setattr(OnDevice, "record_stream", lambda t, s: recorded.append((t.data_ptr(), s.cuda_stream)), raising=False)
+    i32 = lambda *shape: empty(shape, torch.int32)
+    # one output given, which torch has made for the current stream
+    if op == "tables":
+        given = i32(4)
+        call = lambda s: gdn.gdn_page_tables(i32(2), i32(5), i32(2, 3), page=16, n_slots=4, counts=given, stream=s)
+    elif op == "decode":
+        given = empty((2, 4))
+        call = lambda s: decode(lse=given, stream=s)
+    else:
+        given = empty((2,))
+        call = lambda s: gdn.gdn_sample(empty((2, 9)), empty((2, 9)), logprobs=given, stream=s)
+    got = call(Stream(9))
+    assert lib.calls[-1][-1] == 9 and now[0] == 7
+    assert made and all(stream == 9 for stream, _ in made)
+    assert (given.data_ptr(), 9) in recorded
+    assert all((t.data_ptr(), 7) in recorded for t in got if t is not given)
+    with pytest.raises(ValueError):
+        call(Stream(9, device_index=1))
+    # the current stream, given or not: nothing to record
+    made.clear(), recorded.clear()
+    call(None), call(Stream(7))
+    assert all(stream == 7 for stream, _ in made) and not recorded and [a[-1] for a in lib.calls[-2:]] == [7, 7]
