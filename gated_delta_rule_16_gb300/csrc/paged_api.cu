@@ -60,6 +60,15 @@ gdn_status gdn_page_tables(int32_t B, int32_t page, int32_t max_pages, const int
         if ((uintptr_t)p & 3u) return GDN_ERR_ALIGN;
     if ((uintptr_t)slots & 7u) return GDN_ERR_ALIGN;
     if (!device_ok()) return GDN_ERR_DEVICE;
+    // Every CTA reads all lengths, and one of them writes the results: in place a CTA would read what another has written.
+    struct Range { const void *p; int64_t bytes; };
+    const Range in[] = {{cached_lens, 4ll * B}, {new_lens, 4ll * B}, {free_pages, 4ll * n_free}};
+    const Range out[] = {{block_table, 4ll * B * max_pages}, {seq_lens, 4ll * B}, {cu_new, 4ll * (B + 1ll)}, {slots, 8ll * n_slots},
+                         {positions, 4ll * n_slots}, {counts, 16}};
+    for (const Range &x : in)
+        for (const Range &y : out)
+            if (x.p && x.bytes > 0 && y.bytes > 0 && (uintptr_t)x.p < (uintptr_t)y.p + y.bytes && (uintptr_t)y.p < (uintptr_t)x.p + x.bytes)
+                return GDN_ERR_UNSUPPORTED;
     const TablesArgs a = {B, page, max_pages, n_free, n_slots, cached_lens, new_lens, free_pages,
                           block_table, seq_lens, cu_new, positions, counts, slots};
     return launch_page_tables(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;

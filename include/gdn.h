@@ -350,7 +350,9 @@ typedef struct {
  *   counts [4] {new tokens, pages taken, status bits, longest sequence}.
  * Status bits: 1 the free list was too short, 2 a sequence needs more than
  * max_pages pages, 4 more new tokens than n_slots.  Calling again with the same
- * lengths and free list writes the same values. */
+ * lengths and free list writes the same values.  No output may overlap an input
+ * (GDN_ERR_UNSUPPORTED): seq_lens becomes the next step's cached_lens, but not in
+ * place. */
 GDN_API gdn_status gdn_page_tables(int32_t B, int32_t page, int32_t max_pages, const int32_t *cached_lens,
                                    const int32_t *new_lens, const int32_t *free_pages, int32_t n_free,
                                    int32_t *block_table, int32_t *seq_lens, int32_t *cu_new, int64_t *slots,

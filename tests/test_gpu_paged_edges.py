@@ -1,5 +1,6 @@
 """The decode step over a paged cache at the edges of its inputs: masked rows of logits, bit patterns of NaN, weights far
-below the largest, values near the type's largest, several host threads and streams.
+below the largest, values near the type's largest, several host threads and streams,
+outputs that overlap inputs.
 
 References and tolerances are those of test_gpu_paged.py.
 """
@@ -210,3 +211,20 @@ def test_outputs_on_another_stream_are_not_what_pending_work_still_writes():
         first = [t.cpu() for t in got]
         torch.cuda.synchronize()
         assert all(torch.equal(a, b.cpu()) and torch.equal(a, w.cpu()) for a, b, w in zip(first, got, want))
+
+
+# ---- block tables -------------------------------------------------------------------------------------------
+def test_tables_refuse_outputs_over_inputs():
+    # all CTAs read the lengths and one writes the results: in place one would read what another has written
+    lens, new, free = i32([5, 40, 3, 17]), i32([1, 1, 1, 1]), i32(list(range(12)))
+    table = torch.full((4, 4), -1, dtype=torch.int32, device=dev())
+    both = torch.zeros(9, dtype=torch.int32, device=dev())
+    call = lambda **kw: gdn.gdn_page_tables(**{**dict(new_lens=new, free_pages=free, block_table=table, page=16, cached_lens=lens, n_slots=4), **kw})
+    for kw in (dict(seq_lens=lens), dict(seq_lens=new), dict(cached_lens=both[:4], cu_new=both[3:8]), dict(positions=free[8:]),
+               dict(counts=lens), dict(free_pages=table.view(-1))):
+        with pytest.raises(gdn.GdnError):
+            call(**kw)
+    torch.cuda.synchronize()
+    assert lens.tolist() == [5, 40, 3, 17] and (table == -1).all()
+    got = call(cached_lens=both[:4], cu_new=both[4:])         # side by side
+    assert got[0].tolist() == [0, 16, 32, 48] and both[4:].tolist() == [0, 1, 2, 3, 4]
