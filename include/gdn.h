@@ -367,8 +367,9 @@ GDN_API gdn_status gdn_page_tables_status(const int32_t *counts, void *stream);
  * 16 bytes; v alike) goes to slot slots[t]; slots outside [0, pages * page) are
  * skipped.  Rows of dtype (GDN_BF16 or GDN_F32) are copied into a cache of the
  * same dtype, or stored in a GDN_E4M3 cache as x / scale[head], rounded to
- * nearest even and saturated at +-448 (NaN stays NaN).  Two rows with the same
- * slot: either is kept. */
+ * nearest even and saturated at +-448 (NaN stays NaN).  What a slot holds
+ * after two rows were written to it is undefined: each 16 bytes are those of
+ * either row. */
 GDN_API gdn_status gdn_kv_append(const gdn_kv_cache *cache, int32_t n, gdn_dtype dtype, const void *k,
                                  int64_t k_stride_token, int64_t k_stride_head, const void *v,
                                  int64_t v_stride_token, int64_t v_stride_head, const int64_t *slots, void *stream);
