@@ -33,7 +33,8 @@
 //      1 - u with a multiple of w leaves a few per warp whose score is worked out.
 //
 // Masses are summed as whole numbers in units of 2^-40 of the largest weight, of a token or of what one thread met of a
-// row, so that no sum depends on the order of atomics.  The weights in masses are 2^x approximations (2^-21); w >= min_p
+// row (in fp32, in the order of its tokens), and the sum of all weights in fp32 by thread, warp and CTA in turn: no sum depends on
+// the order of atomics, but its last bits do on how many CTAs share the row.  The weights in masses are 2^x approximations (2^-21); w >= min_p
 // and the race are decided in IEEE fp32 with accurate exp and log.
 #include <cooperative_groups.h>
 

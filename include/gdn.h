@@ -420,9 +420,13 @@ GDN_API gdn_status gdn_paged_decode(const gdn_kv_cache *cache, int32_t B, int32_
  * row.  T <= 0: the largest logit (ties: lowest index), logprob 0.  A NULL array
  * stands for T = 1, top_k = 0, top_p = 1, min_p = 0.  Logits of -inf and NaN are
  * never chosen, +inf counts as the largest finite number; a row with neither a
- * finite logit nor +inf gets token -1 and logprob -inf.  Masses are held as 64-bit
- * whole numbers in units of 2^-40 of the largest weight, so the result does not
- * depend on the order of any sum.  No workspace. */
+ * finite logit nor +inf gets token -1 and logprob -inf.  The same call gives the
+ * same bits: parts of a row are summed in fp32 in a fixed order and joined as
+ * 64-bit whole numbers in units of 2^-40 of the largest weight, so that no order of
+ * events matters.  The parts depend on B, V and the row's alignment: in another
+ * batch a row's logprob may differ in its last bits, and a token at top_p's very
+ * edge (within the fp32 rounding of the masses) may fall on its other side.  w_i >= min_p and
+ * the scores are fp32 and do not depend on the batch.  No workspace. */
 GDN_API gdn_status gdn_sample(int32_t B, int32_t V, gdn_dtype dtype, const void *logits, int64_t logits_stride,
                               const float *noise, int64_t noise_stride, const float *temperature,
                               const int32_t *top_k, const float *top_p, const float *min_p, int32_t *tokens,

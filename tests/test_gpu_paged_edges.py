@@ -1,6 +1,6 @@
 """The decode step over a paged cache at the edges of its inputs: masked rows of logits, bit patterns of NaN, weights far
 below the largest, values near the type's largest, several host threads and streams,
-outputs that overlap inputs.
+outputs that overlap inputs, calls made again.
 
 References and tolerances are those of test_gpu_paged.py.
 """
@@ -228,3 +228,22 @@ def test_tables_refuse_outputs_over_inputs():
     assert lens.tolist() == [5, 40, 3, 17] and (table == -1).all()
     got = call(cached_lens=both[:4], cu_new=both[4:])         # side by side
     assert got[0].tolist() == [0, 16, 32, 48] and both[4:].tolist() == [0, 1, 2, 3, 4]
+
+
+# ---- sampling: what repeats ---------------------------------------------------------------------------------
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_sample_repeats_bit_for_bit_and_across_batches_to_rounding(kind):
+    g = torch.Generator(device=dev()).manual_seed(31)
+    B, V = 40, 50001
+    x = (torch.linspace(0.2, 6.0, B, device=dev())[:, None] * torch.randn((B, V), device=dev(), generator=g)).to(TYPES[kind])
+    u = torch.rand((B, V), device=dev(), generator=g)
+    f = lambda *v: torch.tensor([v[b % len(v)] for b in range(B)], device=dev())
+    kw = dict(temperature=f(0.7, 1.0, 1.3), top_k=i32([[0, 40, 3000, 700][b % 4] for b in range(B)]), top_p=f(1.0, 0.5, 0.9, 0.95, 0.3),
+              min_p=f(0.0, 0.02))
+    want = gdn.gdn_sample(x, u, **kw)
+    for _ in range(20):
+        got = gdn.gdn_sample(x, u, **kw)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    big = gdn.gdn_sample(x.repeat(20, 1), u.repeat(20, 1), **{n: t.repeat(20) for n, t in kw.items()})   # fewer CTAs to a row
+    assert torch.equal(big[0], want[0].repeat(20))       # no token of these rows is at an edge
+    assert ((big[1] - want[1].repeat(20)).abs() <= 2.0 ** -20 * (1 + want[1].repeat(20).abs())).all()
