@@ -38,8 +38,9 @@ class _Local(threading.local):
 
 _local = _Local()
 _ws_bytes = {}  # answers of gdn_paged_decode_workspace_bytes
-_current_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# not in a torch built without CUDA, in which no call gets as far as these
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 _empty = torch.empty
 
 

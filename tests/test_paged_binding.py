@@ -1,5 +1,8 @@
 """The binding of the decode-step entry points: what it passes on to the library.  No GPU: host tensors that say they are on
 device 0, and a library that only takes down its arguments."""
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -135,3 +138,16 @@ def test_outputs_and_workspace_are_made_on_the_calls_stream(fake, monkeypatch, o
     made.clear(), recorded.clear()
     call(None), call(Stream(7))
     assert all(stream == 7 for stream, _ in made) and not recorded and [a[-1] for a in lib.calls[-2:]] == [7, 7]
+
+
+def test_import_with_a_torch_without_cuda():
+    # what such a torch lacks; the calls refuse host tensors before they would need it
+    code = ("import torch\n"
+            "for n in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n"
+            "    if hasattr(torch._C, n): delattr(torch._C, n)\n"
+            "import gated_delta_rule_16_gb300 as gdn\n"
+            "try: gdn.gdn_sample(torch.zeros(2, 8), torch.zeros(2, 8))\n"
+            "except ValueError as e: print('refused:', e)\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0 and "refused: logits must be a CUDA tensor" in r.stdout, r.stderr
