@@ -109,13 +109,17 @@ def _workspace(ws, nbytes, dev, handle):
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def _call(name, dev, *args):
+def _status(name, dev, *args):
+    """The library's answer, with the tensors' device as the current one."""
     fn = getattr(_binding._lib or load(), name)
     if _current_device() == dev:
-        rc = fn(*args)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args)
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
+def _call(name, dev, *args):
+    rc = _status(name, dev, *args)
     if rc:
         _check(name, rc)
 
@@ -190,7 +194,7 @@ def gdn_page_tables_status(counts, stream=None) -> int:
     """Status of a gdn_page_tables call from its counts (synchronises the stream): 0, or
     9 (GDN_ERR_CAPACITY) if the free list, the table or the slot map was too short."""
     dev = _cuda(counts, "counts")
-    return int(load().gdn_page_tables_status(_want(counts, "counts", _I32, (4,), dev), _handle(dev, stream)))
+    return int(_status("gdn_page_tables_status", dev, _want(counts, "counts", _I32, (4,), dev), _handle(dev, stream)))
 
 
 def gdn_kv_append(k, v, slots, k_cache, v_cache, *, k_scale=None, v_scale=None, stream=None):

@@ -151,3 +151,32 @@ def test_import_with_a_torch_without_cuda():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
     assert r.returncode == 0 and "refused: logits must be a CUDA tensor" in r.stdout, r.stderr
+
+
+def test_status_is_asked_on_the_counts_device(fake, monkeypatch):
+    # stream 0 is the current device's: another device's would not wait for the call that writes the counts
+    now = [1]
+
+    class Device:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.dev
+
+        def __exit__(self, *_):
+            now[0] = self.before
+
+    class Asked(Library):
+        def gdn_page_tables_status(self, counts, stream):
+            self.calls.append((now[0], stream))
+            return 9
+
+    lib = fake(Asked(), stream=0)
+    monkeypatch.setattr(paged, "_current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    counts = empty((4,), torch.int32)
+    assert gdn.gdn_page_tables_status(counts) == 9
+    now[0] = 0
+    assert gdn.gdn_page_tables_status(counts) == 9
+    assert lib.calls == [(0, 0), (0, 0)] and now[0] == 0
