@@ -7,7 +7,9 @@
 // flight beside those of maxima and sums.  With 8 CTAs or more to a row (few long rows, up to 608 parts each) there is an
 // entry per row and 512 threads to every 64 dims; else one per CTA edge, of a few parts, and 128 threads.  After 1 x 131072
 // tokens (4 rows of 114 parts) it adds 4 us to the call, after 64 requests up to 8192 (455 edges) 4 us, most of them the wait for
-// the kernel before and three loads that depend on one another.
+// the kernel before and three loads that depend on one another.  The choice looks at the number of rows only: where one of many is as
+// long as all others together, 128 threads join its hundreds of parts (one request of 100000 tokens among 60 of 50, one KV head:
+// 13 us of 31; with 4 KV heads and 18 others 6 of 43).
 #include "paged_decode.cuh"
 
 namespace gdn {

@@ -11,8 +11,8 @@
 // What bounds it: the row is read once from HBM; everything after works on few tokens, or on the row in L2, where
 // instructions per token (about 10 in each pass below) and barriers of the cluster count.  A pass handles 16 tokens per
 // thread at a time without a branch between them, as few warps are there to hide their latency: one branch per token made the
-// passes for masses twice as long.  Greedy rows, one pass, take 22 us at 256 rows of 100003 fp32 logits (4.7 TB/s), with
-// top_k 50 and top_p 0.9 47 us, unfiltered ones 67 us with their noise read; one row of 131072 in bf16 5.0, 14.5 and 10.4 us.
+// passes for masses twice as long.  Greedy rows, one pass, take 26 us at 256 rows of 100003 fp32 logits (3.9 TB/s), with
+// top_k 50 and top_p 0.9 50 us, unfiltered ones 66 us with their noise read; one row of 131072 in bf16 5.5, 14.3 and 11 us.
 // A cluster of CTAs shares a row, as many as fill the GPU, each with a slice:
 //   1. one pass for the maximum, the sum of weights and every thread's own maximum;
 //   2. a threshold that no kept token is below.  For top_k: among the threads' maxima, the ceil(k / CTAs)-th largest of
@@ -49,7 +49,7 @@ constexpr int kList = 2048;   // gathered tokens
 constexpr int kRanked = 256;  // of them ranked by comparing all with all
 constexpr int kBins = 2048;
 // Tokens that a CTA holds for races.  With twice as many, four CTAs' shared memory leaves an SM 28 KB of L1, and greedy rows take
-// 27 us instead of 22 (256 x 100003); with none held, rows with top_k 5000 and top_p 0.5 take 197 us instead of 165.
+// 33 us instead of 26 (256 x 100003); with none held, rows with top_k 5000 and top_p 0.5 take 188 us instead of 157.
 constexpr int kHeld = 1472;
 constexpr int kRounds = 24;   // races before the end of top_p's prefix is looked for
 constexpr float kUnit = 1099511627776.f;  // 2^40
@@ -954,9 +954,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
 
 cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream) {
     // CTAs per row: double while all rows' CTAs make two waves at most (152 SMs, four CTAs each) and a CTA has 4096 tokens
-    // left.  At 256 rows of 100003, on one, two, four and eight CTAs each: rows alike, with top_k 50 and top_p 0.9, take 53, 40,
-    // 47 and 70 us, rows of mixed settings 204, 133, 92 and 104 us, where the few flat rows' CTAs run on alone.  Four of 256
-    // threads to an SM against three: greedy rows 22 us and 25, rows with top_k 50 and top_p 0.9 47 and 56, mixed ones 92 and 90.
+    // left.  At 256 rows of 100003, on one, two, four and eight CTAs each: rows alike, with top_k 50 and top_p 0.9, take 58, 45,
+    // 50 and 72 us, greedy ones 27, 22, 26 and 37, rows of mixed settings (six draws of them) 160 to 197, 108 to 117, 80 to 93 and 95
+    // to 107 us, where the few flat rows' CTAs run on alone.  Four of 256 threads to an SM against three: greedy rows 26 us and 32,
+    // rows with top_k 50 and top_p 0.9 50 and 60, mixed ones 80 to 93 and 84 to 95.
     int ctas = 1;
     while (ctas < kMaxCtas && (int64_t)a.B * ctas * 2 <= 1216 && a.V / (2 * ctas) >= 4096) ctas *= 2;
     auto go = [&](auto kern) {

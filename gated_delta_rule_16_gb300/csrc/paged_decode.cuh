@@ -6,8 +6,8 @@
 //
 // What bounds it: every cached byte is read once and used for 2 G operations (G query heads per KV head; at most
 // 16 to a pass), so HBM, as long as tensor and issue slots keep up.  Measured: 64 requests of up to 8192 bf16 tokens
-// (8 KV heads of 128, G = 4) 168 us, 6.3 TB/s or 93 % of a copy; one of 131072 tokens 48 us; 32 e4m3 requests of up to 32768
-// (G = 8) 86 us, 6.0 TB/s; 256 dims 5.6 TB/s; fp32 5.7 TB/s; 16 heads to a pass 5.4 (bf16), 3.4 (e4m3).  The design
+// (8 KV heads of 128, G = 4) 170 us, 6.2 TB/s or 92 % of a copy; one of 131072 tokens 48 us; 32 e4m3 requests of up to 32768
+// (G = 8) 87 us, 6.0 TB/s; 256 dims 5.6 TB/s; fp32 5.7 TB/s; 16 heads to a pass 5.4 (bf16), 3.4 (e4m3).  The design
 // follows from the bound:
 //   - Work is cut by cached tokens, not by requests.  All (request, KV head) rows are laid end to end in tiles of
 //     16 tokens per warp and the CTAs of one wave get equal runs of tiles.  A row inside one CTA is written out
@@ -154,8 +154,8 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // x = hi + lo to 2^-24 of x, each rounded to tf32's 11 bits.  In integer arithmetic at the full rate, as the conversion
-// instruction has a quarter of it (16 x 8192 tokens: 99 us with it against 96).  lo cut instead of rounded saves another
-// microsecond, but scores in the thousands then lose the bits that order their softmax.
+// instruction has a quarter of it (16 requests up to 8192 tokens, 8 KV heads of 128: 91 us with it against 84; of 256 dims 213
+// against 181).  lo cut instead of rounded takes 0 to 6 % less, but scores in the thousands then lose the bits that order their softmax.
 // hi's rounding may carry a NaN's bits over into a zero's, so lo has to keep the NaN: it has 12 bits at most, for which a product
 // with 1 + 2^-11 that is cut rounds the same as an addition of half a unit would, and a NaN stays one.
 __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t &hi, uint32_t &lo) {

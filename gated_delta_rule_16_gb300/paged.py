@@ -10,7 +10,9 @@ each check reads a tensor's attributes once, and the default workspace belongs
 to one host thread, device and stream.  A workspace of the caller's is for one
 call at a time: calls of several threads need one each.  Every call is enqueued
 on `stream` (default: the current stream of the tensors' device) and returns
-without waiting; what it allocates is free in that stream's order.  For a call
+without waiting; what it allocates is free in that stream's order.  Inputs have to
+be ready in it, and to live (or to be recorded on it) until the call has run, as for
+any torch operation.  For a call
 inside a CUDA graph pass the outputs and a workspace that outlive the graph.
 """
 from __future__ import annotations
