@@ -10,10 +10,10 @@ each check reads a tensor's attributes once, and the default workspace belongs
 to one host thread, device and stream.  A workspace of the caller's is for one
 call at a time: calls of several threads need one each.  Every call is enqueued
 on `stream` (default: the current stream of the tensors' device) and returns
-without waiting; what it allocates is free in that stream's order.  Inputs have to
-be ready in it, and to live (or to be recorded on it) until the call has run, as for
-any torch operation.  For a call
-inside a CUDA graph pass the outputs and a workspace that outlive the graph.
+without waiting; what it allocates is free in that stream's order.  Inputs have
+to be ready in it and to live (or be recorded on it) until the call has run, as
+for any torch operation.  For a call inside a CUDA graph pass the outputs and a
+workspace that outlive the graph.
 """
 from __future__ import annotations
 
@@ -111,17 +111,13 @@ def _workspace(ws, nbytes, dev, handle):
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def _status(name, dev, *args):
-    """The library's answer, with the tensors' device as the current one."""
+def _call(name, dev, *args):
     fn = getattr(_binding._lib or load(), name)
     if _current_device() == dev:
-        return fn(*args)
-    with torch.cuda.device(dev):
-        return fn(*args)
-
-
-def _call(name, dev, *args):
-    rc = _status(name, dev, *args)
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args)
     if rc:
         _check(name, rc)
 
@@ -196,7 +192,8 @@ def gdn_page_tables_status(counts, stream=None) -> int:
     """Status of a gdn_page_tables call from its counts (synchronises the stream): 0, or
     9 (GDN_ERR_CAPACITY) if the free list, the table or the slot map was too short."""
     dev = _cuda(counts, "counts")
-    return int(_status("gdn_page_tables_status", dev, _want(counts, "counts", _I32, (4,), dev), _handle(dev, stream)))
+    with torch.cuda.device(dev):
+        return int(load().gdn_page_tables_status(_want(counts, "counts", _I32, (4,), dev), _handle(dev, stream)))
 
 
 def gdn_kv_append(k, v, slots, k_cache, v_cache, *, k_scale=None, v_scale=None, stream=None):
