@@ -1,5 +1,6 @@
-"""GB300-native chunkwise Gated Delta Network prefill core (dense and event-sparse), and the decode
-step of the softmax-attention layers beside it (paged cache, one-token attention, sampling).
+"""GB300-native chunkwise Gated Delta Network prefill core (dense and event-sparse), and the softmax-attention
+layers beside it: their decode step (paged cache, one-token attention, sampling) and their prompt chunks (rotary
+positions, attention of new tokens, log probabilities).
 
 The compute path is libgdn.so (hand-written CUDA for sm_103a behind the C ABI
 in include/gdn.h); this package is its thin ctypes binding.
@@ -40,4 +41,10 @@ from .paged import (  # noqa: F401
     gdn_page_tables_status,
     gdn_paged_decode,
     gdn_sample,
+)
+from .prompt import (  # noqa: F401
+    gdn_logprobs,
+    gdn_paged_prefill,
+    gdn_paged_prefill_status,
+    gdn_qk_rope,
 )

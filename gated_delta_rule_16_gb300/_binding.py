@@ -28,7 +28,8 @@ EXPORTS = ("gdn_workspace_bytes", "gdn_select_events", "gdn_events_status", "gdn
            "gdn_prefill_host", "gdn_prefill_host_workspace_bytes", "gdn_decode_step", "gdn_prefill_ex",
            "gdn_workspace_bytes_ex", "gdn_events_bytes", "gdn_events_carve", "gdn_noalloc_status",
            "gdn_select_events_gamma", "gdn_page_tables", "gdn_page_tables_status", "gdn_kv_append",
-           "gdn_paged_decode", "gdn_paged_decode_workspace_bytes", "gdn_sample")
+           "gdn_paged_decode", "gdn_paged_decode_workspace_bytes", "gdn_sample", "gdn_qk_rope", "gdn_paged_prefill",
+           "gdn_paged_prefill_workspace_bytes", "gdn_paged_prefill_status", "gdn_logprobs")
 STAGES = ("select", "prefix", "intra", "wbuild", "scan_runs", "scan_chain", "scan", "output", "selector")
 
 
@@ -139,6 +140,19 @@ def load(path: str | None = None):
             lib.gdn_paged_decode.restype = i32
             lib.gdn_sample.argtypes = [i32, i32, i32, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp]
             lib.gdn_sample.restype = i32
+            f32 = ctypes.c_float
+            lib.gdn_qk_rope.argtypes = [i32, i32, i32, i32, i32, vp, i64, i64, vp, i64, i64, vp, vp, i32, i32, f32, vp, vp, f32,
+                                        vp, i64, i64, vp, i64, i64, vp]
+            lib.gdn_qk_rope.restype = i32
+            lib.gdn_paged_prefill_workspace_bytes.argtypes = [kvp, i32, i32, i32]
+            lib.gdn_paged_prefill_workspace_bytes.restype = sz
+            lib.gdn_paged_prefill.argtypes = [kvp, i32, i32, i32, i32, vp, i64, i64, vp, i64, i32, vp, vp, i32, f32, vp, vp, vp, sz,
+                                              vp]
+            lib.gdn_paged_prefill.restype = i32
+            lib.gdn_paged_prefill_status.argtypes = [vp, vp]
+            lib.gdn_paged_prefill_status.restype = i32
+            lib.gdn_logprobs.argtypes = [i32, i32, i32, vp, i64, vp, i32, vp, vp, vp, vp, vp]
+            lib.gdn_logprobs.restype = i32
             lib.gdn_version.argtypes = []
             lib.gdn_version.restype = ctypes.c_int32
             lib.gdn_profile_enable.argtypes = [i32]

@@ -1,6 +1,6 @@
 // paged.cuh -- shared declarations of the decode-step operators over a paged
-// key-value cache (block tables, cache writes, one-token attention) and of the
-// sampling step (not part of the ABI).
+// key-value cache (block tables, cache writes, one-token attention), of the
+// sampling step, and of the prompt chunks' operators (not part of the ABI).
 #pragma once
 
 #include <cuda_fp8.h>
@@ -53,10 +53,54 @@ struct SampleArgs {
     float *logprobs;  // may be NULL
 };
 
+struct RopeArgs {
+    int n, Hq, Hkv, d;
+    gdn_dtype dtype;
+    const void *q, *k;
+    void *q_out, *k_out;
+    int64_t q_tok, q_head, k_tok, k_head, qo_tok, qo_head, ko_tok, ko_head;  // strides in elements
+    const int32_t *positions;
+    const double *freqs;
+    int pairs, interleaved;
+    float mscale, eps;
+    const float *q_weight, *k_weight;  // each may be NULL
+    int heads_per_cta;                 // set by the launch
+};
+
+struct PrefillArgs {
+    gdn_kv_cache c;
+    int B, n, Hq;
+    const void *q;
+    int64_t q_tok, q_head;  // strides in elements
+    const int32_t *table;
+    int64_t table_stride;
+    int max_pages, window;
+    const int32_t *lens, *cu;
+    float scale;
+    void *o;
+    float *lse;  // may be NULL
+    void *ws;
+};
+
+struct LogprobArgs {
+    int B, V, top;
+    gdn_dtype dtype;
+    const void *logits;
+    int64_t stride;
+    const int32_t *tokens;
+    float *logprobs, *entropy;  // entropy may be NULL
+    int32_t *top_tokens;        // NULL where top is 0
+    float *top_logprobs;
+};
+
 cudaError_t launch_page_tables(const TablesArgs &a, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream);
 size_t paged_decode_workspace_bytes(const gdn_kv_cache &c, int Hq);
 cudaError_t launch_paged_decode(const AttendArgs &a, cudaStream_t stream);
 cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream);
+cudaError_t launch_qk_rope(const RopeArgs &a, cudaStream_t stream);
+size_t paged_prefill_workspace_bytes(const gdn_kv_cache &c, int B, int n, int Hq);
+cudaError_t launch_paged_prefill(const PrefillArgs &a, cudaStream_t stream);
+cudaError_t launch_logprobs(const LogprobArgs &a, cudaStream_t stream);
 
 }  // namespace gdn

@@ -1,4 +1,4 @@
-// paged_api.cu -- the extern "C" entry points of the decode-step operators (declared in
+// paged_api.cu -- the extern "C" entry points of the decode-step and prompt-chunk operators (declared in
 // include/gdn.h): argument validation and launches.  No allocation, no synchronisation
 // except in the status query.
 #include "paged.cuh"
@@ -152,6 +152,98 @@ gdn_status gdn_sample(int32_t B, int32_t V, gdn_dtype dtype, const void *logits,
     const SampleArgs a = {B, V, dtype, logits, logits_stride, noise, noise_stride, temperature, top_p, min_p, top_k,
                           tokens, logprobs};
     return launch_sample(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_qk_rope(int32_t n, int32_t Hq, int32_t Hkv, int32_t d, gdn_dtype dtype, const void *q, int64_t q_stride_token,
+                       int64_t q_stride_head, const void *k, int64_t k_stride_token, int64_t k_stride_head,
+                       const int32_t *positions, const double *freqs, int32_t pairs, int32_t interleaved, float mscale,
+                       const float *q_weight, const float *k_weight, float eps, void *q_out, int64_t q_out_stride_token,
+                       int64_t q_out_stride_head, void *k_out, int64_t k_out_stride_token, int64_t k_out_stride_head,
+                       void *stream) {
+    if (dtype != GDN_BF16 && dtype != GDN_F32) return GDN_ERR_DTYPE;
+    if (n < 0 || Hq < 0 || Hkv < 0 || (int64_t)Hq + Hkv > 65535 || pairs < 0) return GDN_ERR_SHAPE;
+    if (d != 64 && d != 128 && d != 256) return GDN_ERR_UNSUPPORTED;
+    if (2ll * pairs > d) return GDN_ERR_SHAPE;
+    if (n == 0 || Hq + Hkv == 0) return GDN_OK;
+    if (!positions || (pairs > 0 && !freqs)) return GDN_ERR_NULL;
+    if (((uintptr_t)positions & 3u) || ((uintptr_t)freqs & 7u)) return GDN_ERR_ALIGN;
+    struct Side { int heads; const void *in; int64_t tok, head; const void *out; int64_t out_tok, out_head; const float *w; };
+    const Side sides[] = {{Hq, q, q_stride_token, q_stride_head, q_out, q_out_stride_token, q_out_stride_head, q_weight},
+                          {Hkv, k, k_stride_token, k_stride_head, k_out, k_out_stride_token, k_out_stride_head, k_weight}};
+    for (const Side &x : sides) {
+        if (x.heads == 0) continue;
+        if (!x.in || !x.out) return GDN_ERR_NULL;
+        if (!aligned16(x.in) || !aligned16(x.out) || !stride_ok(x.tok, dtype) || !stride_ok(x.head, dtype) ||
+            !stride_ok(x.out_tok, dtype) || !stride_ok(x.out_head, dtype) || ((uintptr_t)x.w & 3u))
+            return GDN_ERR_ALIGN;
+        // a row is read before it is written: in place only the same row
+        if (x.in == x.out && ((n > 1 && x.tok != x.out_tok) || (x.heads > 1 && x.head != x.out_head))) return GDN_ERR_UNSUPPORTED;
+    }
+    if (!device_ok()) return GDN_ERR_DEVICE;
+    const RopeArgs a = {n, Hq, Hkv, d, dtype, q, k, q_out, k_out, q_stride_token, q_stride_head, k_stride_token, k_stride_head,
+                        q_out_stride_token, q_out_stride_head, k_out_stride_token, k_out_stride_head, positions, freqs,
+                        pairs, interleaved, mscale, eps, q_weight, k_weight, 0};
+    return launch_qk_rope(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+size_t gdn_paged_prefill_workspace_bytes(const gdn_kv_cache *cache, int32_t B, int32_t n, int32_t Hq) {
+    if (check_cache_sizes(cache) != GDN_OK || Hq <= 0 || Hq % cache->Hkv || B < 0 || n < 0 || (int64_t)n * Hq > INT32_MAX) return 0;
+    return paged_prefill_workspace_bytes(*cache, B, n, Hq) + kWsAlign;
+}
+
+gdn_status gdn_paged_prefill(const gdn_kv_cache *cache, int32_t B, int32_t n, int32_t Hq, gdn_dtype dtype, const void *q,
+                             int64_t q_stride_token, int64_t q_stride_head, const int32_t *block_table, int64_t table_stride,
+                             int32_t max_pages, const int32_t *seq_lens, const int32_t *cu_new, int32_t window, float scale,
+                             void *o, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+    gdn_status st = check_cache_sizes(cache);
+    if (st != GDN_OK) return st;
+    if (B < 0 || n < 0 || Hq <= 0 || Hq % cache->Hkv || max_pages < 0 || window < 0 || table_stride < 0) return GDN_ERR_SHAPE;
+    if (dtype != (cache->dtype == GDN_E4M3 ? GDN_BF16 : cache->dtype)) return GDN_ERR_DTYPE;
+    if ((int64_t)n * Hq > INT32_MAX) return GDN_ERR_SHAPE;
+    if ((int64_t)max_pages * cache->page > INT32_MAX - 127) return GDN_ERR_UNSUPPORTED;  // token positions are int32
+    if (B == 0 || n == 0) return GDN_OK;
+    // with no page in the pool or no column in the table every row is empty, but o and lse are still written
+    if (cache->pages > 0 && max_pages > 0) {
+        if ((st = check_cache(cache)) != GDN_OK) return st;
+        if (!block_table) return GDN_ERR_NULL;
+    }
+    if (!q || !seq_lens || !cu_new || !o || !workspace) return GDN_ERR_NULL;
+    if (!aligned16(q) || !aligned16(o) || !stride_ok(q_stride_token, dtype) || !stride_ok(q_stride_head, dtype) ||
+        (((uintptr_t)block_table | (uintptr_t)seq_lens | (uintptr_t)cu_new | (uintptr_t)lse) & 3u) ||
+        (uintptr_t)workspace % kWsAlign)
+        return GDN_ERR_ALIGN;
+    if (workspace_bytes < gdn_paged_prefill_workspace_bytes(cache, B, n, Hq)) return GDN_ERR_WORKSPACE;
+    if (!device_ok()) return GDN_ERR_DEVICE;
+    PrefillArgs a = {*cache, B, n, Hq, q, q_stride_token, q_stride_head, block_table, table_stride,
+                     cache->pages > 0 ? max_pages : 0, window, seq_lens, cu_new, scale, o, lse, workspace};
+    if (a.max_pages == 0) a.c.k_scale = a.c.v_scale = nullptr;
+    return launch_paged_prefill(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_paged_prefill_status(const void *workspace, void *stream) {
+    if (!workspace) return GDN_ERR_NULL;
+    if ((uintptr_t)workspace % kWsAlign) return GDN_ERR_ALIGN;
+    int32_t status = 0;
+    if (cudaMemcpyAsync(&status, workspace, sizeof(status), cudaMemcpyDeviceToHost, (cudaStream_t)stream) != cudaSuccess ||
+        cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess)
+        return GDN_ERR_CUDA;
+    return status ? GDN_ERR_TIMEOUT : GDN_OK;
+}
+
+gdn_status gdn_logprobs(int32_t B, int32_t V, gdn_dtype dtype, const void *logits, int64_t logits_stride,
+                        const int32_t *tokens, int32_t top, float *logprobs, float *entropy, int32_t *top_tokens,
+                        float *top_logprobs, void *stream) {
+    if (dtype != GDN_BF16 && dtype != GDN_F32) return GDN_ERR_DTYPE;
+    if (B < 0 || V <= 0 || logits_stride < 0 || top < 0 || top > V) return GDN_ERR_SHAPE;
+    if (top > 32 || V > (1 << 30) || B > (1 << 27)) return GDN_ERR_UNSUPPORTED;
+    if (B == 0) return GDN_OK;
+    if (!logits || !tokens || !logprobs || (top > 0 && (!top_tokens || !top_logprobs))) return GDN_ERR_NULL;
+    if ((uintptr_t)logits % (unsigned)bytes_of(dtype) ||
+        (((uintptr_t)tokens | (uintptr_t)logprobs | (uintptr_t)entropy | (uintptr_t)top_tokens | (uintptr_t)top_logprobs) & 3u))
+        return GDN_ERR_ALIGN;
+    if (!device_ok()) return GDN_ERR_DEVICE;
+    const LogprobArgs a = {B, V, top, dtype, logits, logits_stride, tokens, logprobs, entropy, top_tokens, top_logprobs};
+    return launch_logprobs(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -2,7 +2,8 @@
  * gdn.h -- C ABI of libgdn: the chunkwise (64-token) Gated Delta Network
  * prefill core on NVIDIA GB300 (sm_103a), dense and event-sparse forms, and the
  * decode step of softmax-attention layers beside it (paged cache, one-token
- * attention, sampling; "Decode step" below).
+ * attention, sampling; "Decode step" below) with their prompt chunks (rotary
+ * positions, attention of new tokens, log probabilities; "Prompt chunks" below).
  *
  * Source of the operator: "SparseGDN: Chunk Sparse in Linear Attention"
  * (arXiv 2610.41420v1), as paraphrased by its Chinese reading notes:
@@ -431,6 +432,75 @@ GDN_API gdn_status gdn_sample(int32_t B, int32_t V, gdn_dtype dtype, const void 
                               const float *noise, int64_t noise_stride, const float *temperature,
                               const int32_t *top_k, const float *top_p, const float *min_p, int32_t *tokens,
                               float *logprobs, void *stream);
+
+/* ---- Prompt chunks through softmax-attention layers -------------------------
+ * What a layer does with the new tokens of a step before and after the cache:
+ * gdn_qk_rope, then gdn_kv_append of the keys, then gdn_paged_prefill; and
+ * gdn_logprobs where a prompt is scored. */
+
+/* Per-head norm and rotary positions of new tokens' queries and keys, in one
+ * pass.  Row t, head h of q ([n][Hq][d] at t * q_stride_token + h * q_stride_head
+ * elements; k alike with Hkv heads; outputs with strides of their own; all strides
+ * multiples of 16 bytes), in fp32 and rounded once:
+ *   y = x w / sqrt(mean(x^2) + eps)   with weights [d] fp32 (NULL: y = x);
+ *   the first 2 * pairs dims turn by angles positions[t] * freqs[i], i < pairs:
+ *   (a, b) -> mscale (a cos - b sin, a sin + b cos) on the pairs (y_i, y_(i+pairs)),
+ *   or (y_2i, y_(2i+1)) where `interleaved` is not 0; the other dims stay y.
+ * freqs [pairs] fp64 in radians per token (finite); positions any int32.  Angles are
+ * products of whole numbers modulo a turn: they lose nothing at far positions beyond
+ * what freqs itself, in 53 bits, leaves open.  q_out may be q, and k_out k, with
+ * the same strides (other strides there are GDN_ERR_UNSUPPORTED); apart from that
+ * outputs do not overlap inputs.  d is 64, 128 or 256; Hq or Hkv may be 0, whose
+ * pointers are not looked at. */
+GDN_API gdn_status gdn_qk_rope(int32_t n, int32_t Hq, int32_t Hkv, int32_t d, gdn_dtype dtype, const void *q,
+                               int64_t q_stride_token, int64_t q_stride_head, const void *k, int64_t k_stride_token,
+                               int64_t k_stride_head, const int32_t *positions, const double *freqs, int32_t pairs,
+                               int32_t interleaved, float mscale, const float *q_weight, const float *k_weight,
+                               float eps, void *q_out, int64_t q_out_stride_token, int64_t q_out_stride_head,
+                               void *k_out, int64_t k_out_stride_token, int64_t k_out_stride_head, void *stream);
+
+/* Softmax attention of new tokens over the paged cache, which holds them already.
+ * Request b's new tokens are the rows cu_new[b] <= t < cu_new[b+1] of q [n][Hq][d]
+ * (cut to [0, n]); row t has position p = seq_lens[b] - cu_new[b+1] + t and attends to
+ * the tokens j with max(0, p - window + 1) <= j <= p (window 0: from 0 on) and
+ * j < max_pages * page, whose table entry lies in [0, pages):
+ *   o[t,h] = sum_j p_j v_j,  p = softmax_j(scale * <q[t,h], k_j>),
+ *   lse[t,h] = log sum_j exp(scale * <q[t,h], k_j>)           (lse may be NULL).
+ * A row left without a token gets o = 0 and lse = -inf.  Rows of no request are not
+ * written (a captured step's rows behind cu_new[B]); rows of two requests hold either's.
+ * Everything else is as in gdn_paged_decode: heads, strides, types, what is never
+ * used, where non-finite values reach (a later token's do not reach the rows before it).
+ * Weights exp(z - max z) enter the product with V in the bits of o's type or more:
+ * 8 with a GDN_BF16 cache, 11 with a GDN_E4M3 one, 22 with a GDN_F32 one.
+ * Workspace: gdn_paged_prefill_workspace_bytes(cache, B, n, Hq), 256-byte aligned;
+ * its contents need no set-up.  The call is several launches: host threads that
+ * share a stream need a workspace each, and so do two captured graphs that may run
+ * at the same time.  gdn_paged_prefill_status synchronises `stream` and reports
+ * the call that used the workspace last (GDN_ERR_TIMEOUT: a wait inside a kernel ran
+ * out and o and lse are not valid). */
+GDN_API size_t gdn_paged_prefill_workspace_bytes(const gdn_kv_cache *cache, int32_t B, int32_t n, int32_t Hq);
+GDN_API gdn_status gdn_paged_prefill(const gdn_kv_cache *cache, int32_t B, int32_t n, int32_t Hq, gdn_dtype dtype,
+                                     const void *q, int64_t q_stride_token, int64_t q_stride_head,
+                                     const int32_t *block_table, int64_t table_stride, int32_t max_pages,
+                                     const int32_t *seq_lens, const int32_t *cu_new, int32_t window, float scale,
+                                     void *o, float *lse, void *workspace, size_t workspace_bytes, void *stream);
+GDN_API gdn_status gdn_paged_prefill_status(const void *workspace, void *stream);
+
+/* Log probabilities of given tokens, of every row of logits [B][V] (row b at
+ * b * logits_stride elements; GDN_BF16 or GDN_F32; V <= 2^30).  With m the row's largest
+ * logit and Z = sum_i exp(x_i - m):
+ *   logprobs[b] = x_token - m - log Z, token = tokens[b]; 0 for a token outside [0, V);
+ *   entropy[b] = log Z - sum_i exp(x_i - m) (x_i - m) / Z          (may be NULL);
+ *   top_tokens, top_logprobs [B][top]: the `top` largest logits, descending (ties:
+ *   lowest index first), and their log probabilities (top <= 32 and <= V).
+ * Logits of -inf have no mass and log probability -inf; among the top they come
+ * last.  A row with a NaN or +inf has NaN for every result but top_tokens, where
+ * +inf comes first and NaN last; a row of -inf alone has log probabilities of -inf and
+ * entropy 0.  Sums are fp32 in a fixed order that depends on B, V and the row's
+ * alignment: the same call gives the same bits.  No workspace. */
+GDN_API gdn_status gdn_logprobs(int32_t B, int32_t V, gdn_dtype dtype, const void *logits, int64_t logits_stride,
+                                const int32_t *tokens, int32_t top, float *logprobs, float *entropy,
+                                int32_t *top_tokens, float *top_logprobs, void *stream);
 
 /* Prefill with HOST inputs and outputs: the same computation as
  * gdn_prefill_sparse (mask != NULL) or gdn_prefill_dense (mask == NULL), with
