@@ -1,85 +1,210 @@
-// k_paged_prefill.cu -- softmax attention of new tokens over the paged cache: the simple form.
-//
-// One CTA per (token, query head) goes over the row's keys 128 at a time with a running maximum and sum in fp32.
-#include "paged.cuh"
+// k_paged_prefill.cu -- softmax attention of new tokens over the paged cache: the plan before the attention
+// kernels, and the join of rows that were cut between CTAs after them (paged_prefill.cuh has the scheme).
+#include "paged_prefill.cuh"
 
 namespace gdn {
+namespace prefill {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kPlanThreads = 1024, kHeldUnits = 2048;
 
-template <typename T> __device__ __forceinline__ float value(const T *p) { return io<T>::ld(p); }
-template <> __device__ __forceinline__ float value(const __nv_fp8_e4m3 *p) { return (float)*p; }
-
-// Maximum (of numbers: NaN is left out) or sum over the CTA.
-template <bool MAX> __device__ float reduce(float x, float *buf) {
-    for (int off = 16; off; off >>= 1) {
-        const float y = __shfl_xor_sync(0xffffffffu, x, off);
-        x = MAX ? fmaxf(x, y) : x + y;
+// Running sum over the CTA, inclusive; `all` gets the total.
+__device__ int64_t scan(int64_t x, int64_t *buf, int64_t &all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
     }
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
+    if (lane == 31) buf[warp] = x;
     __syncthreads();
-    x = buf[0];
-    for (int w = 1; w < kThreads / 32; ++w) x = MAX ? fmaxf(x, buf[w]) : x + buf[w];
+    if (warp == 0) {
+        int64_t y = buf[lane];
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t z = __shfl_up_sync(0xffffffffu, y, off);
+            if (lane >= off) y += z;
+        }
+        buf[lane] = y;
+    }
+    __syncthreads();
+    if (warp) x += buf[warp - 1];
+    all = buf[31];
     __syncthreads();
     return x;
 }
 
-template <typename C, typename T>
-__global__ void __launch_bounds__(kThreads) prefill_simple(PrefillArgs a) {
-    __shared__ float q[256], p[kThreads], buf[kThreads / 32];
-    __shared__ int64_t at[kThreads];
-    const int tid = threadIdx.x, t = blockIdx.x, h = blockIdx.y, d = a.c.d, kv = h / (a.Hq / a.c.Hkv);
-    int lo = 0, hi = a.B;  // the last request that begins at or before t
-    while (lo + 1 < hi) {
-        const int mid = (lo + hi) / 2;
-        if (a.cu[mid] <= t) lo = mid;
-        else hi = mid;
+// One CTA: a thread per request counts its units, a thread per unit finds its request, rows and keys, a thread per CTA its run.
+// A unit costs its tiles and one more, for its beginning and end.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(PrefillArgs a, int tile, int keys, int grid) {
+    __shared__ int64_t buf[32];
+    __shared__ int64_t held[kHeldUnits];
+    View v;
+    layout(a.ws, a.B, a.n, a.Hq, a.c.Hkv, a.c.d, tile, &v);
+    const int tid = threadIdx.x, group = a.Hq / a.c.Hkv, room = a.max_pages * a.c.page;
+    pdl_trigger();
+    auto rows_of = [&](int b, int &first) {
+        first = min(max(a.cu[b], 0), a.n);
+        return max(min(a.cu[b + 1], a.n) - first, 0) * group;
+    };
+    int64_t units = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+        int first;
+        const int b = b0 + tid, mine = b < a.B ? (rows_of(b, first) + tile - 1) / tile : 0;
+        int64_t all;
+        const int64_t incl = scan(mine, buf, all);
+        if (b < a.B) v.first[b] = (int)min(units + incl - mine, (int64_t)INT32_MAX);
+        units += all;
     }
-    if (t < a.cu[lo] || t >= a.cu[lo + 1]) return;
-    const int64_t pos = (int64_t)a.lens[lo] - a.cu[lo + 1] + t, room = (int64_t)a.max_pages * a.c.page;
-    const int64_t first = a.window > 0 ? max((int64_t)0, pos - a.window + 1) : 0, last = min(pos + 1, room);
-    const float ks = a.c.k_scale ? a.c.k_scale[kv] : 1.f, vs = a.c.v_scale ? a.c.v_scale[kv] : 1.f;
-    for (int i = tid; i < d; i += kThreads) q[i] = value((const T *)a.q + t * a.q_tok + h * a.q_head + i);
-    float m = -INFINITY, l = 0.f, o[2] = {0.f, 0.f};
+    // cu_new that goes back and forth names rows more often than there is room for: the last units are left out
+    units = min(units, unit_capacity(a.B, (int64_t)a.n * group, tile));
     __syncthreads();
-    for (int64_t j0 = first; j0 < last; j0 += kThreads) {
-        const int64_t j = j0 + tid;
-        const int page = j < last ? a.table[lo * a.table_stride + j / a.c.page] : -1;
-        const bool real = page >= 0 && page < a.c.pages;
-        at[tid] = real ? page * a.c.stride_page + j % a.c.page * a.c.stride_token + kv * a.c.stride_head : -1;
-        float z = -INFINITY;
-        if (real) {
-            z = 0.f;
-            for (int i = 0; i < d; ++i) z += q[i] * value((const C *)a.c.k + at[tid] + i);
-            z *= ks * a.scale;
+    int64_t cost = 0;
+    for (int64_t i0 = 0; i0 < units; i0 += kPlanThreads) {
+        const int64_t i = i0 + tid;
+        int mine = 0;
+        if (i < units) {
+            int lo = 0, hi = a.B;  // the last request whose first unit is at or before i: requests without units are skipped
+            while (lo + 1 < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (v.first[mid] <= i) lo = mid;
+                else hi = mid;
+            }
+            Unit u;
+            u.b = lo;
+            const int rows = rows_of(lo, u.first);
+            u.row = (int)(i - v.first[lo]) * tile;
+            u.rows = min(tile, rows - u.row);
+            const int64_t shift = (int64_t)a.lens[lo] - a.cu[lo + 1];
+            u.shift = (int)max(min(shift, (int64_t)INT32_MAX), (int64_t)INT32_MIN);
+            const Reach r0 = reach_of((int64_t)u.first + u.row / group + u.shift, a.window, room);
+            const Reach r1 = reach_of((int64_t)u.first + (u.row + u.rows - 1) / group + u.shift, a.window, room);
+            u.key = r0.lo / keys * keys;
+            u.tiles = r1.hi >= r0.lo ? (r1.hi - u.key) / keys + 1 : 0;
+            u.pad = 0;
+            v.unit[i] = u;
+            mine = u.tiles + 1;
         }
-        const float top = fmaxf(m, reduce<true>(z, buf)), ref = top == -INFINITY ? 0.f : top, f = expf(m - ref);
-        p[tid] = expf(z - ref);
-        l = l * f + reduce<false>(p[tid], buf);
-        o[0] *= f, o[1] *= f;
-        m = top;
-        for (int k = 0; k < kThreads; ++k)
-            if (at[k] >= 0)
-                for (int e = 0; e < 2; ++e)
-                    if (tid + e * kThreads < d) o[e] += p[k] * value((const C *)a.c.v + at[k] + tid + e * kThreads);
-        __syncthreads();
+        int64_t all;
+        const int64_t incl = cost + scan(mine, buf, all);
+        if (i < units) {
+            v.ends[i] = incl;
+            if (i < kHeldUnits) held[i] = incl;
+        }
+        cost += all;
     }
-    const int64_t row = (int64_t)t * a.Hq + h;
-    for (int e = 0; e < 2; ++e)
-        if (tid + e * kThreads < d) io<T>::st((T *)a.o + row * d + tid + e * kThreads, l == 0.f ? 0.f : o[e] * vs / l);
-    if (tid == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : m + logf(l);
+    __syncthreads();
+    const int64_t *ends = units <= kHeldUnits ? held : v.ends;
+    const int64_t total = cost * a.c.Hkv;
+    const int ctas = (int)max((int64_t)1, min((int64_t)grid, total / kMinRun));
+    for (int i = tid; i <= grid; i += kPlanThreads) {
+        int4 run = make_int4(-1, 0, 0, 0);
+        if (i == ctas || total == 0) run = i <= ctas ? make_int4(a.c.Hkv, 0, 0, 0) : run;
+        else if (i < ctas) {
+            const int64_t x = split_at(total, ctas, i), head = x / cost, rest = x % cost;
+            int lo = 0, hi = (int)units - 1;  // the first unit that ends behind it
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (ends[mid] > rest) hi = mid;
+                else lo = mid + 1;
+            }
+            const int64_t begin = lo ? ends[lo - 1] : 0;
+            run = make_int4((int)head, lo, (int)(rest - begin), (int)(ends[lo] - begin) - 1);
+        }
+        v.runs[i] = run;
+    }
+    if (tid == 0) {
+        *v.status = 0;
+        *v.units = (int)units;
+    }
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A unit cut into parts (m_i, l_i, o_i): o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i, M = max m_i, in the keys' order.
+// Grid: an entry per edge between two CTAs, which is idle unless it is the first inside its unit; times the tile's blocks of rows; times
+// blocks of dims.  A thread has 8 dims of a row.
+constexpr int kJoinRows = 32, kJoinThreads = 256;
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(PrefillArgs a, int tile) {
+    View v;
+    layout(a.ws, a.B, a.n, a.Hq, a.c.Hkv, a.c.d, tile, &v);
+    pdl_wait();
+    const int edge = blockIdx.x + 1;
+    auto inside = [&](const int4 &r) { return r.x >= 0 && r.z > 0 && r.z < r.w; };
+    const int4 r = v.runs[edge];
+    if (!inside(r)) return;
+    const int4 before = v.runs[edge - 1];
+    if (inside(before) && before.x == r.x && before.y == r.y) return;
+    int parts = 2;
+    for (; edge + parts - 1 <= kMaxCtas; ++parts) {
+        const int4 next = v.runs[edge + parts - 1];
+        if (!inside(next) || next.x != r.x || next.y != r.y) break;
+    }
+    const Unit u = v.unit[r.y];
+    const int row = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows;
+    const int d0 = (blockIdx.z * (kJoinThreads / kJoinRows) + threadIdx.x / kJoinRows) * 8;
+    if (row >= u.rows || d0 >= a.c.d) return;
+    // the unit's beginning is the last piece of the CTA before the edge, the rest are first pieces
+    auto slot = [&](int k) { return k == 0 ? 2 * (edge - 1) + 1 : 2 * (edge - 1 + k); };
+    float top = -INFINITY;
+    for (int k = 0; k < parts; ++k) top = fmaxf(top, v.ml[(size_t)slot(k) * tile + row].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float x[8] = {}, sum = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+        const float2 ml = v.ml[(size_t)slot(k) * tile + row];
+        const float4 *o = (const float4 *)v.o + ((size_t)slot(k) * (a.c.d / 4) + d0 / 4) * tile + row;
+        const float4 lo = o[0], hi = o[tile];
+        const float f = exp2_fast(ml.x - ref);
+        sum += f * ml.y;
+        x[0] += f * lo.x, x[1] += f * lo.y, x[2] += f * lo.z, x[3] += f * lo.w;
+        x[4] += f * hi.x, x[5] += f * hi.y, x[6] += f * hi.z, x[7] += f * hi.w;
+    }
+    const int group = a.Hq / a.c.Hkv, rr = u.row + row;
+    float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (a.c.v_scale) inv *= a.c.v_scale[r.x];
+    const int64_t out = ((int64_t)u.first + rr / group) * a.Hq + r.x * group + rr % group;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = sum == 0.f ? 0.f : x[i] * inv;
+    if constexpr (sizeof(T) == 4) {
+        float4 *o = (float4 *)((float *)a.o + out * a.c.d + d0);
+        o[0] = make_float4(x[0], x[1], x[2], x[3]);
+        o[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+        __nv_bfloat162 p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        *(uint4 *)((__nv_bfloat16 *)a.o + out * a.c.d + d0) = *(const uint4 *)p;
+    }
+    if (d0 == 0 && a.lse) a.lse[out] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
 }
 
 }  // namespace
+}  // namespace prefill
 
-size_t paged_prefill_workspace_bytes(const gdn_kv_cache &, int, int, int) { return 256; }
+size_t paged_prefill_workspace_bytes(const gdn_kv_cache &c, int B, int n, int Hq) {
+    return prefill::layout(nullptr, B, n, Hq, c.Hkv, c.d, prefill::row_tile(c.dtype, c.d), nullptr);
+}
 
-cudaError_t launch_paged_prefill(const PrefillArgs &a, cudaStream_t stream) {
-    const dim3 grid((unsigned)a.n, (unsigned)a.Hq);
-    if (a.c.dtype == GDN_BF16) return launch_kernel(false, prefill_simple<__nv_bfloat16, __nv_bfloat16>, grid, kThreads, 0, stream, a);
-    if (a.c.dtype == GDN_E4M3) return launch_kernel(false, prefill_simple<__nv_fp8_e4m3, __nv_bfloat16>, grid, kThreads, 0, stream, a);
-    return launch_kernel(false, prefill_simple<float, float>, grid, kThreads, 0, stream, a);
+cudaError_t launch_paged_prefill(const PrefillArgs &args, cudaStream_t stream) {
+    using namespace prefill;
+    PrefillArgs a = args;
+    if (a.max_pages == 0) a.c.k = a.c.v = (void *)a.q;  // an address for copies of no bytes
+    const int tile = row_tile(a.c.dtype, a.c.d), grid = kMaxCtas;
+    cudaError_t e = launch_kernel(false, plan_kernel, 1, kPlanThreads, 0, stream, a, tile, key_tile(a.c.dtype), grid);
+    if (e != cudaSuccess) return e;
+    e = a.c.dtype == GDN_BF16 ? launch_bf16(a, grid, stream) : a.c.dtype == GDN_E4M3 ? launch_e4m3(a, grid, stream) : launch_f32(a, grid, stream);
+    if (e != cudaSuccess) return e;
+    const int dims = kJoinThreads / kJoinRows * 8;
+    const int64_t rows = (int64_t)a.n * (a.Hq / a.c.Hkv);
+    const dim3 blocks(grid - 1, (unsigned)((min((int64_t)tile, rows) + kJoinRows - 1) / kJoinRows), a.c.d / dims);
+    return a.c.dtype == GDN_F32 ? launch_kernel(true, join_kernel<float>, blocks, kJoinThreads, 0, stream, a, tile)
+                                : launch_kernel(true, join_kernel<__nv_bfloat16>, blocks, kJoinThreads, 0, stream, a, tile);
 }
 
 }  // namespace gdn

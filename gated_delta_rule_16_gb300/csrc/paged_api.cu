@@ -187,7 +187,7 @@ gdn_status gdn_qk_rope(int32_t n, int32_t Hq, int32_t Hkv, int32_t d, gdn_dtype 
 }
 
 size_t gdn_paged_prefill_workspace_bytes(const gdn_kv_cache *cache, int32_t B, int32_t n, int32_t Hq) {
-    if (check_cache_sizes(cache) != GDN_OK || Hq <= 0 || Hq % cache->Hkv || B < 0 || n < 0 || (int64_t)n * Hq > INT32_MAX) return 0;
+    if (check_cache_sizes(cache) != GDN_OK || Hq <= 0 || Hq % cache->Hkv || B < 0 || n < 0 || (int64_t)n * Hq > INT32_MAX - 255) return 0;
     return paged_prefill_workspace_bytes(*cache, B, n, Hq) + kWsAlign;
 }
 
@@ -199,7 +199,7 @@ gdn_status gdn_paged_prefill(const gdn_kv_cache *cache, int32_t B, int32_t n, in
     if (st != GDN_OK) return st;
     if (B < 0 || n < 0 || Hq <= 0 || Hq % cache->Hkv || max_pages < 0 || window < 0 || table_stride < 0) return GDN_ERR_SHAPE;
     if (dtype != (cache->dtype == GDN_E4M3 ? GDN_BF16 : cache->dtype)) return GDN_ERR_DTYPE;
-    if ((int64_t)n * Hq > INT32_MAX) return GDN_ERR_SHAPE;
+    if ((int64_t)n * Hq > INT32_MAX - 255) return GDN_ERR_SHAPE;
     if ((int64_t)max_pages * cache->page > INT32_MAX - 127) return GDN_ERR_UNSUPPORTED;  // token positions are int32
     if (B == 0 || n == 0) return GDN_OK;
     // with no page in the pool or no column in the table every row is empty, but o and lse are still written

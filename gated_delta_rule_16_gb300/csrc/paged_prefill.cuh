@@ -1,0 +1,120 @@
+// paged_prefill.cuh -- softmax attention of new tokens over the paged cache: how the work is cut and where the
+// parts of cut rows lie, shared by the kernels that k_paged_prefill*.cu instantiate.
+//
+// A unit is a tile of rows (new token t, query head of one KV head's group, in this order) of one request with all the keys
+// they attend to, in tiles of 128 keys or less.  The units of all requests are laid end to end, once for each KV head, and the CTAs of one
+// wave get equal runs of key tiles; a unit cut by a CTA's edge leaves unnormalised fp32 parts that a last launch joins in
+// the keys' order.  Lengths are only known on the GPU, so a first launch of one CTA lists the units and finds the runs.  Causal rows
+// make units of 1 to hundreds of tiles, and equal runs need no luck with their order: of 8192 tokens at once every CTA
+// has the same number of tiles, and one row over 131072 is shared by all of them.
+#pragma once
+
+#include "paged.cuh"
+
+namespace gdn {
+namespace prefill {
+
+constexpr int kMaxCtas = 152;  // of a wave: one per SM
+constexpr int kMinRun = 2;     // tiles that a CTA takes at least
+
+struct Unit {       // 32 bytes
+    int b, first;   // request; its first row of q
+    int row, rows;  // of the request's (token, head of the group) rows: the first, and how many
+    int shift;      // position of a token: its row of q + shift
+    int key, tiles; // first key, a multiple of the tile; tiles of keys
+    int pad;
+};
+
+struct View {
+    int32_t *status;  // bits, 0: nothing ran out
+    int4 *runs;       // [kMaxCtas + 1] {KV head, unit, place in the unit, its tiles}; x < 0: no such CTA
+    int32_t *units;   // how many
+    Unit *unit;
+    int64_t *ends;    // running sum of the units' costs
+    int32_t *first;   // of each request: its first unit
+    float2 *ml;       // [2 kMaxCtas][rows of a unit] reference and sum of a part
+    float *o;         // [2 kMaxCtas][d / 4][rows of a unit][4]
+};
+
+inline __host__ __device__ int64_t unit_capacity(int B, int64_t rows, int tile) { return rows / tile + 1 + B; }
+
+// Byte offsets of View's parts; returns the size.
+inline __host__ __device__ size_t layout(void *ws, int B, int n, int Hq, int Hkv, int d, int tile, View *v) {
+    const int64_t units = unit_capacity(B, (int64_t)n * (Hq / Hkv), tile);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += (bytes + 255) & ~(size_t)255;
+        return (uint8_t *)ws + here;
+    };
+    View x;
+    x.status = (int32_t *)take(256);
+    x.units = x.status + 1;
+    x.runs = (int4 *)take((kMaxCtas + 1) * sizeof(int4));
+    x.unit = (Unit *)take(units * sizeof(Unit));
+    x.ends = (int64_t *)take(units * sizeof(int64_t));
+    x.first = (int32_t *)take(((size_t)B + 1) * sizeof(int32_t));
+    x.ml = (float2 *)take((size_t)2 * kMaxCtas * tile * sizeof(float2));
+    x.o = (float *)take((size_t)2 * kMaxCtas * tile * d * sizeof(float));
+    if (v) *v = x;
+    return at;
+}
+
+// Rows and keys of a tile: what the kernels are built for.
+inline __host__ __device__ int row_tile(gdn_dtype kind, int d) { return kind == GDN_F32 || d == 256 ? 128 : 256; }
+inline __host__ __device__ int key_tile(gdn_dtype kind) { return kind == GDN_F32 ? 32 : 128; }
+
+inline __host__ __device__ int64_t split_at(int64_t total, int ctas, int i) { return total / ctas * i + total % ctas * i / ctas; }
+
+// Keys [lo, hi] that a token attends to.
+struct Reach { int lo, hi; };
+__device__ __forceinline__ Reach reach_of(int64_t pos, int window, int room) {
+    const int64_t hi = pos < room ? pos : room - 1;
+    const int64_t lo = window > 0 && pos >= window ? pos - window + 1 : 0;
+    return {(int)(lo < room ? lo : room), (int)(hi < -1 ? -1 : hi)};
+}
+
+// What a CTA does, one piece of a unit after the other.  Every thread that walks it sees the same pieces.
+struct Walk {
+    View v;
+    int4 at, end;
+    int units;
+    Unit u;           // the piece's unit
+    int h;            // its KV head
+    int t0, t1;       // its tiles [t0, t1)
+    int cta;
+
+    __device__ __forceinline__ void start(const View &view, int which) {
+        v = view;
+        cta = which;
+        at = v.runs[which];
+        end = v.runs[which + 1];
+        units = *v.units;
+    }
+    // The next piece that has something to do; false: there is none.
+    __device__ __forceinline__ bool next() {
+        for (;;) {
+            if (at.x < 0 || end.x < 0) return false;
+            const bool last = at.x == end.x && at.y == end.y;
+            if (at.x > end.x || (at.x == end.x && at.y > end.y) || (last && at.z >= end.z)) return false;
+            u = v.unit[at.y];
+            h = at.x;
+            t0 = min(at.z, u.tiles);
+            t1 = last ? min(end.z, u.tiles) : u.tiles;
+            at.z = 0;
+            if (++at.y == units) at.y = 0, ++at.x;
+            if (t0 < t1 || u.tiles == 0) return true;
+        }
+    }
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == u.tiles; }
+    // Where a part lies: a CTA's first piece if its unit began in another CTA, else its last.
+    __device__ __forceinline__ int slot() const { return 2 * cta + (t0 > 0 ? 0 : 1); }
+};
+
+// prefill kernels: a.ws holds the View; launched as programmatic dependents of the plan
+cudaError_t launch_bf16(const PrefillArgs &a, int grid, cudaStream_t stream);
+cudaError_t launch_e4m3(const PrefillArgs &a, int grid, cudaStream_t stream);
+cudaError_t launch_f32(const PrefillArgs &a, int grid, cudaStream_t stream);
+
+}  // namespace prefill
+}  // namespace gdn

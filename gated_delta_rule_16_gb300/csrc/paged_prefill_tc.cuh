@@ -1,0 +1,698 @@
+// paged_prefill_tc.cuh -- softmax attention of new tokens over the paged cache on tcgen05 tensor cores: the
+// kernel template that k_paged_prefill_{bf16,e4m3}.cu instantiate.
+//
+// S = Q K^T, P = 2^(z - ref), O += P V with z = scale log2(e) S, for tiles of 128 rows and 128 keys; S and O are accumulators in
+// tensor memory, P is written over S in 16 bits and read from there as the second product's A operand.  ref follows the running
+// maximum of a row lazily: only when z passes it by kSlack is ref raised and O, in tensor memory, rescaled.
+//
+// One CTA of 16 warps per SM:
+//   warps 0-3, 4-7   softmax of the unit's first and second 128 rows, a thread per row: while one group works on its S the tensor
+//                    core does the other's products.  With 256 dims O fills tensor memory beside two S tiles, and with 128 rows or less there is
+//                    no second tile: then the first group takes all tiles, and S alternates between the two places;
+//   warps 8-11       copy keys and values into a ring of shared memory, in the 128-byte swizzle, 16 bytes at a time by cp.async: any
+//                    page size and any strides cost the same, and what is not attended to is filled with zeros;
+//   warp 12          one thread issues the products.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "paged_prefill.cuh"
+#include "tc.cuh"
+
+namespace gdn {
+namespace prefill {
+
+using namespace tc;
+
+constexpr int kThreads = 512;
+constexpr uint32_t kSlab = 16384;  // [128 rows][128 bytes]
+constexpr int kWords = 16;         // tiles whose masks of real keys are kept
+
+template <gdn_dtype KIND, int D>
+struct Cfg {
+    static constexpr bool kE4M3 = KIND == GDN_E4M3;
+    static constexpr int kDims = D < 128 ? D : 128;    // of a ring stage: 128 keys
+    static constexpr int kParts = D / kDims;           // stages of a tile of keys (and of one of values)
+    static constexpr int kSlabs = kDims / 64;
+    static constexpr uint32_t kStage = kSlabs * kSlab;
+    static constexpr int kTiles = D == 256 ? 1 : 2;    // of 128 rows
+    static constexpr uint32_t kQTile = D / 64 * kSlab;
+    static constexpr int kStages = kE4M3 ? (D == 64 ? 8 : 4) : (D == 64 ? 10 : 5);
+    static constexpr int kRaw = kE4M3 ? (D == 64 ? 4 : 2) : 0;  // stages of 8-bit values on their way
+    static constexpr uint32_t kRawStage = 128 * kDims;
+    static constexpr uint32_t kSmem = kTiles * kQTile + kStages * kStage + kRaw * kRawStage;  // and Bars behind it
+    static constexpr uint32_t kO = 256;                // tensor memory: S at 0 and 128, O from here on
+    // ref is raised when a score passes it by 2^kSlack; weights are 2^kShift times 2^(z - ref).  bf16 has fp32's range; f16 gets
+    // 11 bits for weights down to 2^-25 of the largest, and what sums to less than 2^-36 of it is lost.
+    static constexpr float kSlack = kE4M3 ? 4.f : 8.f, kShift = kE4M3 ? 11.f : 0.f;
+    static constexpr uint32_t kKindBits = kE4M3 ? 0u : (1u << 7) | (1u << 10);  // instruction descriptor: A and B are f16 or bf16
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void lds128(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint32_t f16_of_e4m3(uint32_t x) {  // both values of the low half: exact
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// D[tmem] (+)= A[tmem] * B, issued by a single thread.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        "}\n" ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+template <int N> __device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+// Waits on mbarriers end after kWaitLimitNs, or soon after another thread's did.
+struct Waiter {
+    volatile int *gave_up;
+    __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const {
+        if (mbar_try_wait(bar, parity)) return true;
+        const uint64_t since = globaltimer();
+        for (;;) {
+#pragma unroll 1
+            for (int i = 0; i < 64; ++i)
+                if (mbar_try_wait(bar, parity)) return true;
+            if (*gave_up || globaltimer() - since > kWaitLimitNs) {
+                *gave_up = 1;
+                return false;
+            }
+        }
+    }
+};
+
+struct Bars {
+    static constexpr int kMaxStages = 10;
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t q_full, q_empty;
+    uint64_t s_full[3], p_full[3];  // first group's S at 0; second group's S at 128; first group's S at 128
+    uint64_t pv_done[2];            // of a group
+    uint64_t joint[2], drain;       // joint: a group's votes
+    uint32_t words[kWords][4];      // real keys of a tile
+    float row_scale[2][256];        // e4m3: of q's rows, by turns
+    int vote[2][3];                 // of a group, by turns
+    int skip[3];                    // the group has added this tile's P V itself
+    int gave_up;
+    uint32_t tmem;
+};
+
+static_assert(sizeof(Bars) <= 3 * 1024, "shared memory");
+
+// A warp's waits succeed or fail for all of its lanes.
+__device__ __forceinline__ bool warp_wait(const Waiter &wait, uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait(bar, parity));
+}
+// Whether any thread of a group says x, in `any`; false: a wait ran out.  `turn` counts the group's votes.
+__device__ __forceinline__ bool group_any(const Waiter &wait, Bars &bars, int group, int &turn, bool x, bool &any) {
+    if (x) *(volatile int *)&bars.vote[group][turn % 3] = 1;
+    mbar_arrive(&bars.joint[group]);
+    const bool ok = warp_wait(wait, &bars.joint[group], turn & 1);
+    any = *(volatile int *)&bars.vote[group][turn % 3];
+    // the turn before has been read by all who came here, and nobody gets to the one after next before this thread does
+    if ((threadIdx.x & 127) == 0) *(volatile int *)&bars.vote[group][(turn + 2) % 3] = 0;
+    ++turn;
+    return ok;
+}
+
+// Bits of keys kb .. kb + 127 inside [lo, hi].
+__device__ __forceinline__ uint32_t range_bits(int part, int kb, int lo, int hi) {
+    const int l = lo - kb - 32 * part, h = hi - kb - 32 * part;
+    if (l > 31 || h < 0) return 0;
+    return (l <= 0 ? ~0u : ~0u << l) & (h >= 31 ? ~0u : (2u << h) - 1);
+}
+
+// O += P V of one tile for a group's rows without the tensor core, which multiplies a masked weight of 0 with what it masks: a tile of
+// values with an infinity or NaN that some of the rows do not attend to.  P is in tensor memory, a row's thread reads its own.
+template <gdn_dtype KIND, int D>
+__device__ __noinline__ void add_masked(uint32_t t_p, uint32_t t_o, const uint8_t *ring, int stage0, const uint32_t (&bits)[4], bool first) {
+    using C = Cfg<KIND, D>;
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+        float o[32];
+        tmem_ld32(t_o + 32 * c, o);
+        tmem_ld_wait();
+        if (first)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+        const int d0 = 32 * c;
+        const uint8_t *stage = ring + (uint32_t)((stage0 + d0 / C::kDims) % C::kStages) * C::kStage + d0 % C::kDims / 64 * kSlab;
+#pragma unroll 1
+        for (int part = 0; part < 4; ++part) {
+            float p[16];
+            tmem_ld16(t_p + 16 * part, p);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+                if (!(bits[part] >> k & 1)) continue;
+                const uint32_t w = __float_as_uint(p[k / 2]);
+                float x;
+                if constexpr (C::kE4M3) x = __half2float(__ushort_as_half((unsigned short)(k & 1 ? w >> 16 : w & 0xffff)));
+                else x = __uint_as_float(k & 1 ? w & 0xffff0000u : w << 16);
+                const int key = 32 * part + k;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t v[4];
+                    lds128(v, smem_addr(stage) + sw128_offset(key, d0 % 64 + 8 * e));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float lo, hi;
+                        if constexpr (C::kE4M3) {
+                            lo = __half2float(__ushort_as_half((unsigned short)(v[i] & 0xffff)));
+                            hi = __half2float(__ushort_as_half((unsigned short)(v[i] >> 16)));
+                        } else {
+                            lo = __uint_as_float(v[i] << 16);
+                            hi = __uint_as_float(v[i] & 0xffff0000u);
+                        }
+                        o[8 * e + 2 * i] += x * lo;
+                        o[8 * e + 2 * i + 1] += x * hi;
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        tmem_st32(t_o + 32 * c, o);
+        tmem_st_wait();
+    }
+}
+
+template <gdn_dtype KIND, int D>
+__global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) {
+    using C = Cfg<KIND, D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Bars &bars = *reinterpret_cast<Bars *>(smem + C::kSmem);
+    uint8_t *const q_smem = smem, *const ring = smem + C::kTiles * C::kQTile;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warpgroup = warp >> 2;
+    const int group = a.Hq / a.c.Hkv, room = a.max_pages * a.c.page;
+    const Waiter wait = {&bars.gave_up};
+    View view;
+    layout(a.ws, a.B, a.n, a.Hq, a.c.Hkv, D, 128 * C::kTiles, &view);
+
+    if (tid == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&bars.full[i], 128);
+            mbar_init(&bars.empty[i], 1);
+        }
+        mbar_init(&bars.q_full, 128);
+        mbar_init(&bars.q_empty, 1);
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&bars.s_full[i], 1);
+            mbar_init(&bars.p_full[i], 128);
+            bars.skip[i] = 0;
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.pv_done[i], 1);
+            mbar_init(&bars.joint[i], 128);
+            for (int j = 0; j < 3; ++j) bars.vote[i][j] = 0;
+        }
+        mbar_init(&bars.drain, 1);
+        bars.gave_up = 0;
+        fence_mbar_init();
+    }
+    if (warp == 12) tmem_alloc<512>(&bars.tmem);
+    pdl_wait();  // the plan
+    pdl_trigger();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem;
+    Walk walk;
+    walk.start(view, blockIdx.x);
+    if (smem_addr(smem) & 1023u) walk.at.x = -1, bars.gave_up = 1;  // the swizzle needs aligned tiles, which shared memory without static parts is
+
+    if (warpgroup == 2) {
+        // ---- copies ---------------------------------------------------------------------------------------
+        regs_less<80>();
+        const int pt = tid - 256, pw = pt >> 5;
+        constexpr int kChunks = C::kDims * (C::kE4M3 ? 1 : 2) / 16, kAtOnce = 32 / kChunks, kSteps = 32 / kAtOnce;  // 16-byte pieces of a row; rows per copy
+        const int chunk = lane % kChunks, sub = lane / kChunks;
+        int issued = 0, told = 0, stage_in = 0, stage_out = 0, q_at = -1, units = 0, tiles = 0;  // groups and stages so far
+        bool ok = true;
+        const uint32_t ring_at = smem_addr(ring), raw_at = smem_addr(ring + C::kStages * C::kStage);
+        auto free_stage = [&](int n) { return n < C::kStages || warp_wait(wait, &bars.empty[n % C::kStages], (n / C::kStages - 1) & 1); };
+        // bf16: the oldest group has arrived
+        auto tell = [&] {
+            fence_async_smem();
+            if (told == q_at) mbar_arrive(&bars.q_full);
+            else mbar_arrive(&bars.full[stage_out++ % C::kStages]);
+            ++told;
+        };
+        auto flush = [&] {
+            cp_wait<0>();
+            while (told < issued) tell();
+        };
+        // e4m3: 8-bit values of the oldest stage become f16; a thread reads what it copied itself
+        auto convert = [&] {
+            const int n = stage_out;
+            if (!free_stage(n)) return false;
+            const uint32_t from = raw_at + n % (C::kRaw ? C::kRaw : 1) * C::kRawStage, to = ring_at + n % C::kStages * C::kStage;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int key = 32 * pw + i * kAtOnce + sub;
+                uint32_t x[4];
+                lds128(x, from + key * C::kDims + 16 * chunk);
+                const uint32_t at = to + chunk / 4 * kSlab;
+                sts128(at + sw128_offset(key, chunk % 4 * 16), f16_of_e4m3(x[0]), f16_of_e4m3(x[0] >> 16), f16_of_e4m3(x[1]), f16_of_e4m3(x[1] >> 16));
+                sts128(at + sw128_offset(key, chunk % 4 * 16 + 8), f16_of_e4m3(x[2]), f16_of_e4m3(x[2] >> 16), f16_of_e4m3(x[3]), f16_of_e4m3(x[3] >> 16));
+            }
+            fence_async_smem();
+            mbar_arrive(&bars.full[n % C::kStages]);
+            ++stage_out;
+            return true;
+        };
+        auto copy = [&](const void *base, int part, int64_t row, bool real) {  // one stage; row: this lane's key's offset in elements
+            const uint8_t *src = (const uint8_t *)base + part * C::kDims * (C::kE4M3 ? 1 : 2) + 16 * chunk;
+            if constexpr (!C::kE4M3) {
+                const int n = stage_in;
+                if (n >= C::kStages && !__all_sync(0xffffffffu, mbar_try_wait(&bars.empty[n % C::kStages], (n / C::kStages - 1) & 1))) {
+                    flush();  // what waits for the stage may itself be waited for
+                    if (!free_stage(n)) return false;
+                }
+            }
+            const uint32_t dst = C::kE4M3 ? raw_at + stage_in % (C::kRaw ? C::kRaw : 1) * C::kRawStage : ring_at + stage_in % C::kStages * C::kStage + chunk / 8 * kSlab;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int from = i * kAtOnce + sub, key = 32 * pw + from;
+                const int64_t off = __shfl_sync(0xffffffffu, row, from);
+                const bool there = __shfl_sync(0xffffffffu, (int)real, from);
+                if constexpr (C::kE4M3) cp16(dst + key * C::kDims + 16 * chunk, src + off, there);
+                else cp16(dst + sw128_offset(key, chunk % 8 * 8), src + off * 2, there);
+            }
+            cp_commit();
+            ++issued;
+            ++stage_in;
+            if constexpr (C::kE4M3) {
+                if (stage_in - stage_out >= C::kRaw) {
+                    cp_wait<(C::kRaw > 0 ? C::kRaw - 1 : 0)>();
+                    return convert();
+                }
+            } else if (issued - told > C::kStages - 2) {
+                cp_wait<C::kStages - 2>();
+                tell();
+            }
+            return true;
+        };
+        auto settle = [&] {  // everything issued has been passed on
+            if constexpr (C::kE4M3) {
+                cp_wait<0>();
+                while (stage_out < stage_in)
+                    if (!convert()) return false;
+            } else {
+                flush();
+            }
+            return true;
+        };
+        // the unit's rows of q; rows behind its last are zeros
+        auto load_q = [&](const Unit &u, int h) {
+            if (!settle()) return false;
+            if (units > 0 && !warp_wait(wait, &bars.q_empty, (units - 1) & 1)) return false;
+            constexpr int kLanes = D / 8, kGo = 32 / kLanes;  // 16 bytes to a lane; rows that a warp has at a time
+            const int rows = u.rows <= 128 ? 128 : 128 * C::kTiles;
+            const int piece = lane % kLanes;
+#pragma unroll 4
+            for (int r = pw * kGo + lane / kLanes; r < rows; r += 4 * kGo) {
+                const int rr = u.row + min(r, u.rows - 1);
+                const uint8_t *src = (const uint8_t *)a.q + 2 * (((int64_t)u.first + rr / group) * a.q_tok + (int64_t)(h * group + rr % group) * a.q_head) + 16 * piece;
+                const uint32_t dst = smem_addr(q_smem) + r / 128 * C::kQTile + piece / 8 * kSlab + sw128_offset(r % 128, piece % 8 * 8);
+                if constexpr (!C::kE4M3) {
+                    cp16(dst, src, r < u.rows);
+                } else {
+                    // f16 of q times a power of two that takes the row's largest to 2^14 or so: 8 bits of any value down to 2^-30 of it,
+                    // and what it loses below is lost in the fp32 sum too
+                    uint4 x = r < u.rows ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                    uint32_t most = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) most = max(most, max(w[i] & 0x7fffu, w[i] >> 16 & 0x7fffu));
+#pragma unroll
+                    for (int off = kLanes / 2; off; off >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
+                    const int e = min((int)(most >> 7), 254), lift = min(141 - e, 126);
+                    const float f = __uint_as_float((uint32_t)(127 + lift) << 23);
+                    uint32_t y[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[i] = pack_f16x2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
+                    sts128(dst, y[0], y[1], y[2], y[3]);
+                    if (piece == 0) bars.row_scale[units & 1][r] = __uint_as_float((uint32_t)(127 - lift) << 23);
+                }
+            }
+            if constexpr (C::kE4M3) {
+                fence_async_smem();
+                mbar_arrive(&bars.q_full);
+            } else {
+                cp_commit();
+                q_at = issued++;
+            }
+            ++units;
+            return true;
+        };
+        while (ok && walk.next()) {
+            const Unit u = walk.u;
+            if (walk.t0 == walk.t1) continue;
+            const int first = u.first + u.row / group, last = u.first + (u.row + u.rows - 1) / group;
+            const int lo = reach_of((int64_t)first + u.shift, a.window, room).lo, hi = reach_of((int64_t)last + u.shift, a.window, room).hi;
+            const int32_t *table = a.table + u.b * a.table_stride;
+            auto entry = [&](int key, int &cell) {  // the key's page, -1 where it has none
+                const int page = key / a.c.page;
+                cell = key - page * a.c.page;
+                return key >= lo && key <= hi ? table[page] : -1;
+            };
+            int cell_next, page_next = entry(u.key + 128 * walk.t0 + pt, cell_next);
+            for (int t = walk.t0; ok && t < walk.t1; ++t) {
+                const int page = page_next, cell = cell_next;
+                if (t + 1 < walk.t1) page_next = entry(u.key + 128 * (t + 1) + pt, cell_next);
+                const bool real = page >= 0 && page < a.c.pages;
+                const int64_t row = real ? page * a.c.stride_page + cell * a.c.stride_token + walk.h * a.c.stride_head : 0;
+                const uint32_t word = __ballot_sync(0xffffffffu, real);
+                if (lane == 0) bars.words[tiles % kWords][pw] = word;
+                ++tiles;
+                for (int part = 0; ok && part < C::kParts; ++part) ok = copy(a.c.k, part, row, real);
+                if (ok && t == walk.t0) ok = load_q(u, walk.h);
+                for (int part = 0; ok && part < C::kParts; ++part) ok = copy(a.c.v, part, row, real);
+            }
+        }
+        if (ok) settle();
+        cp_wait<0>();
+    } else if (warpgroup == 3) {
+        // ---- products -------------------------------------------------------------------------------------
+        regs_less<48>();
+        if (warp == 12 && lane == 0) {
+            constexpr uint32_t kBase = (1u << 4) | C::kKindBits | (128u >> 4 << 24);
+            constexpr uint32_t id_qk = kBase | (128u >> 3 << 17), id_pv = kBase | (1u << 16) | ((uint32_t)C::kDims >> 3 << 17);
+            const uint32_t q_at = smem_addr(q_smem), ring_at = smem_addr(ring);
+            int stage = 0, units = 0;          // stages and units before this piece
+            int n_p[3] = {0, 0, 0};            // P tiles so far, by barrier
+            bool ok = true;
+            auto ready = [&](int n) { return wait(&bars.full[n % C::kStages], n / C::kStages & 1); };
+            auto release = [&](int n) { mma_commit(&bars.empty[n % C::kStages]); };
+            auto qk = [&](int tile, int place, int first_stage) {
+#pragma unroll
+                for (int part = 0; part < C::kParts; ++part) {
+                    const uint32_t k_at = ring_at + (uint32_t)((first_stage + part) % C::kStages) * C::kStage;
+#pragma unroll
+                    for (int ks = 0; ks < C::kDims / 16; ++ks)
+                        mma_bf16(tmem + 128 * place, kmajor_desc(q_at + tile * C::kQTile + part * C::kSlabs * kSlab, ks, kSlab), kmajor_desc(k_at, ks, kSlab), id_qk, part + ks > 0);
+                }
+            };
+            auto pv = [&](int which, int place, int out, int first_stage, bool more) {
+                tc_fence_after();
+                if (*(volatile int *)&bars.skip[which]) return;
+#pragma unroll
+                for (int part = 0; part < C::kParts; ++part) {
+                    const uint32_t v_at = ring_at + (uint32_t)((first_stage + part) % C::kStages) * C::kStage;
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_ts(tmem + C::kO + out * D + part * C::kDims, tmem + 128 * place + 8 * ks, mnmajor_desc(v_at, ks, kSlab), id_pv, more || ks > 0);
+                }
+            };
+            auto got_p = [&](int which) { return wait(&bars.p_full[which], n_p[which]++ & 1); };
+            while (ok && walk.next()) {
+                const int n = walk.t1 - walk.t0;
+                if (n == 0) continue;
+                const bool two = walk.u.rows > 128;
+                auto key_stage = [&](int i) { return stage + 2 * C::kParts * i; };
+                auto value_stage = [&](int i) { return stage + 2 * C::kParts * i + C::kParts; };
+                auto values = [&](int i) {
+                    bool there = true;
+                    for (int part = 0; part < C::kParts; ++part) there = there && ready(value_stage(i) + part);
+                    return there;
+                };
+                for (int i = 0; ok && i <= n; ++i) {
+                    if (i < n) {
+                        for (int part = 0; ok && part < C::kParts; ++part) ok = ready(key_stage(i) + part);
+                        if (ok && i == 0) ok = wait(&bars.q_full, units & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    if (two) {
+                        for (int m = 0; m < 2; ++m) {
+                            if (i > 0) {
+                                if (!(ok = (m || values(i - 1)) && got_p(m))) break;
+                                pv(m, m, m, value_stage(i - 1), i > 1);
+                                mma_commit(&bars.pv_done[m]);
+                                if (m)
+                                    for (int part = 0; part < C::kParts; ++part) release(value_stage(i - 1) + part);
+                            }
+                            if (i < n) {
+                                qk(m, m, key_stage(i));
+                                mma_commit(&bars.s_full[m]);
+                            }
+                        }
+                    } else {
+                        if (i < n) {
+                            qk(0, i & 1, key_stage(i));
+                            mma_commit(&bars.s_full[i & 1 ? 2 : 0]);
+                        }
+                    }
+                    if (!ok) break;
+                    if (i < n)
+                        for (int part = 0; part < C::kParts; ++part) release(key_stage(i) + part);
+                    if (i == n - 1) mma_commit(&bars.q_empty);
+                    if (!two && i > 0) {
+                        const int which = (i - 1) & 1 ? 2 : 0;
+                        if (!(ok = values(i - 1) && got_p(which))) break;
+                        pv(which, (i - 1) & 1, 0, value_stage(i - 1), i > 1);
+                        mma_commit(&bars.pv_done[0]);
+                        for (int part = 0; part < C::kParts; ++part) release(value_stage(i - 1) + part);
+                    }
+                }
+                stage += 2 * C::kParts * n;
+                ++units;
+            }
+            mma_commit(&bars.drain);
+            mbar_wait(&bars.drain, 0);
+        }
+        __syncwarp();
+    } else {
+        // ---- softmax --------------------------------------------------------------------------------------
+        regs_more<192>();
+        const int m = warpgroup, r = tid & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // tensor memory lanes of this warp
+        const float log2e = 1.4426950408889634f;
+        int stage = 0, units = 0, tiles = 0, n_s[3] = {0, 0, 0}, n_pv = 0, votes = 0;
+        bool ok = true;
+        while (ok && walk.next()) {
+            const Unit u = walk.u;
+            const int n = walk.t1 - walk.t0;
+            const bool two = u.rows > 128;
+            if (m == 1 && !two) {  // the first group has all of it
+                stage += 2 * C::kParts * n;
+                tiles += n;
+                units += n > 0;
+                continue;
+            }
+            const int rows = min(128, u.rows - 128 * m);
+            const int rr = u.row + 128 * m + min(r, rows - 1);
+            const int token = u.first + rr / group, head = walk.h * group + rr % group;
+            const Reach mine = reach_of((int64_t)token + u.shift, a.window, room);
+            const int first = u.first + (u.row + 128 * m) / group, last = u.first + (u.row + 128 * m + rows - 1) / group;
+            // keys that all rows attend to
+            const int all_lo = reach_of((int64_t)last + u.shift, a.window, room).lo, all_hi = reach_of((int64_t)first + u.shift, a.window, room).hi;
+            const uint32_t t_o = tmem + lanes + C::kO + m * D;
+            float ref = -INFINITY, sum = 0.f, zs = a.scale * log2e;
+            if (a.c.k_scale) zs *= a.c.k_scale[walk.h];
+            for (int i = 0; ok && i < n; ++i) {
+                const int which = two ? m : (i & 1 ? 2 : 0), place = two ? m : i & 1;
+                const uint32_t t_s = tmem + lanes + 128 * place;
+                if (!(ok = warp_wait(wait, &bars.s_full[which], n_s[which]++ & 1))) break;
+                tc_fence_after();
+                if (C::kE4M3 && i == 0) zs *= bars.row_scale[units & 1][128 * m + r];
+                float s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, s[c]);
+                tmem_ld_wait();
+                const int kb = u.key + 128 * (walk.t0 + i);
+                uint32_t bits[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) bits[c] = bars.words[(tiles + i) % kWords][c];
+                const bool edge = kb < all_lo || kb + 127 > all_hi || (bits[0] & bits[1] & bits[2] & bits[3]) != ~0u;
+                float f = zs;
+                if (!(zs > 0.f)) {  // the maximum below is that of s
+                    f = 1.f;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) s[c][j] *= zs;
+                }
+                if (edge) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        bits[c] &= range_bits(c, kb, mine.lo, mine.hi);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (!(bits[c] >> j & 1)) s[c][j] = -INFINITY;
+                    }
+                }
+                float most = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) most = fmaxf(most, fmaxf(s[c][j], s[c][j + 1]));
+                most *= f;
+                const bool raise = most > ref + C::kSlack || (ref == -INFINITY && most > -INFINITY);
+                if (__any_sync(0xffffffffu, raise)) {
+                    float lower = 1.f;
+                    if (raise) {
+                        lower = ex2(ref - most);
+                        ref = most;
+                        sum *= lower;
+                    }
+                    if (i > 0) {
+                        if (!(ok = warp_wait(wait, &bars.pv_done[m], (n_pv + i - 1) & 1))) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D / 16; ++c) {
+                            float o[16];
+                            tmem_ld16(t_o + 16 * c, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) o[j] *= lower;
+                            tmem_st16(t_o + 16 * c, o);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+                const float base = ref == -INFINITY ? 0.f : ref - C::kShift;
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 4; c += 2) {
+                    float p[32];
+#pragma unroll
+                    for (int j = 0; j < 64; j += 2) {
+                        const float x = ex2(s[c + j / 32][j % 32] * f - base), y = ex2(s[c + j / 32][j % 32 + 1] * f - base);
+                        part[j / 2 % 2 * 2] += x;
+                        part[j / 2 % 2 * 2 + 1] += y;
+                        p[j / 2] = __uint_as_float(C::kE4M3 ? pack_f16x2(x, y) : pack_bf16x2(x, y));
+                    }
+                    tmem_st32(t_s + 16 * c, p);
+                }
+                sum += (part[0] + part[1]) + (part[2] + part[3]);
+                tmem_st_wait();
+                if (edge) {
+                    // values that only some rows attend to have to be numbers
+                    const int at = stage + 2 * C::kParts * i + C::kParts;
+                    uint32_t bad = 0;
+                    for (int k = 0; ok && k < C::kParts; ++k) {
+                        ok = warp_wait(wait, &bars.full[(at + k) % C::kStages], (at + k) / C::kStages & 1);
+                        const uint32_t v_at = smem_addr(ring) + (uint32_t)((at + k) % C::kStages) * C::kStage;
+#pragma unroll
+                        for (int e = 0; e < C::kDims / 8; ++e) {
+                            uint32_t x[4];
+                            lds128(x, v_at + e / 8 * kSlab + sw128_offset(r, e % 8 * 8));
+#pragma unroll
+                            for (int w = 0; w < 4; ++w)
+                                bad |= C::kE4M3 ? ((x[w] & 0x7c007c00u) + 0x04000400u) & 0x80008000u : ((x[w] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+                        }
+                    }
+                    bool tainted = false;
+                    if (!(ok = ok && group_any(wait, bars, m, votes, bad != 0, tainted))) break;
+                    if (tainted) {
+                        if (!(ok = i == 0 || warp_wait(wait, &bars.pv_done[m], (n_pv + i - 1) & 1))) break;
+                        tc_fence_after();
+                        add_masked<KIND, D>(t_s, t_o, ring, at, bits, i == 0);
+                    }
+                    if (r == 0) bars.skip[which] = tainted;
+                } else if (r == 0) {
+                    bars.skip[which] = 0;
+                }
+                tc_fence_before();
+                mbar_arrive(&bars.p_full[which]);
+            }
+            if (!ok) break;
+            if (n > 0) {
+                // S of a tile is there after the products two tiles before, with one S after those of the tile before: a wait tells only
+                // the next product's end from the one before
+                if (n > 1 && !(ok = warp_wait(wait, &bars.pv_done[m], (n_pv + n - 2) & 1))) break;
+                if (!(ok = warp_wait(wait, &bars.pv_done[m], (n_pv + n - 1) & 1))) break;
+                tc_fence_after();
+            }
+            stage += 2 * C::kParts * n;
+            tiles += n;
+            units += n > 0;
+            n_pv += n;
+            // ---- the row's end in this CTA
+            const bool there = r < rows;
+            if (walk.whole()) {
+                const bool none = n == 0 || (ref == -INFINITY && sum == 0.f);  // NaN is not nothing
+                float inv = none ? 0.f : 1.f / sum;
+                if (a.c.v_scale) inv *= a.c.v_scale[walk.h];
+                const int64_t out = (int64_t)token * a.Hq + head;
+                uint4 *o_at = (uint4 *)((__nv_bfloat16 *)a.o + out * D);
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    tmem_ld32(t_o + 32 * c, o);
+                    tmem_ld_wait();
+                    uint32_t w[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) w[j] = none ? 0u : pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv);
+                    if (there)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) o_at[4 * c + j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                }
+                if (there && a.lse) a.lse[out] = none ? -INFINITY : (ref - C::kShift + log2f(sum)) * 0.6931471805599453f;
+            } else {
+                const int slot = walk.slot(), tile = 128 * C::kTiles, row = 128 * m + r;
+                float4 *o_at = (float4 *)view.o + (size_t)slot * (D / 4) * tile + row;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    tmem_ld32(t_o + 32 * c, o);
+                    tmem_ld_wait();
+                    if (there)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) o_at[(size_t)(8 * c + j) * tile] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                }
+                if (there) view.ml[(size_t)slot * tile + row] = make_float2(ref == -INFINITY ? -INFINITY : ref - C::kShift, sum);
+            }
+            tc_fence_before();
+        }
+    }
+    __syncthreads();
+    if (bars.gave_up && tid == 0) atomicOr(view.status, 1);
+    if (warp == 12) {
+        tc_fence_after();
+        tmem_dealloc<512>(tmem);
+    }
+}
+
+template <gdn_dtype KIND, int D>
+cudaError_t launch_tc(const PrefillArgs &a, int grid, cudaStream_t stream) {
+    using C = Cfg<KIND, D>;
+    constexpr int kSmem = (int)(C::kSmem + sizeof(Bars));
+    // the warp groups' shares of registers are what a block of 128 to a thread has: with fewer they would wait for ever
+    static const int regs = [] {
+        cudaFuncAttributes attr;
+        return cudaFuncGetAttributes(&attr, prefill_tc_kernel<KIND, D>) == cudaSuccess ? attr.numRegs : 0;
+    }();
+    if (regs != 128) return cudaErrorInvalidConfiguration;
+    const cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<KIND, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    return e != cudaSuccess ? e : launch_kernel(true, prefill_tc_kernel<KIND, D>, grid, kThreads, kSmem, stream, a);
+}
+template <gdn_dtype KIND>
+cudaError_t launch_tc(const PrefillArgs &a, int grid, cudaStream_t stream) {
+    switch (a.c.d) {
+        case 64: return launch_tc<KIND, 64>(a, grid, stream);
+        case 128: return launch_tc<KIND, 128>(a, grid, stream);
+        default: return launch_tc<KIND, 256>(a, grid, stream);
+    }
+}
+
+}  // namespace prefill
+}  // namespace gdn

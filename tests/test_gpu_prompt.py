@@ -390,7 +390,7 @@ def test_attend_non_finite_values_reach_later_rows_only(kind, d, bad, which):
         pytest.skip("the format has no infinity")
     c = Case([(0, 700), (60, 50)], kind=kind, d=d, heads=4, kv_heads=2, page=16)
     t = {"k": c.k, "v": c.v}[which]
-    clean, _ = c.call()
+    want, _, far, _ = c.ref()
     j, dim = 413, 17
     cell = t[int(c.table[0, j // 16]), j % 16, 1]
     if kind == "e4m3":
@@ -400,8 +400,9 @@ def test_attend_non_finite_values_reach_later_rows_only(kind, d, bad, which):
     o, lse = c.call()
     before = torch.ones(750, dtype=torch.bool, device=dev())
     before[413:700] = False
-    same_rows = o == clean
-    assert same_rows[before].all() and same_rows[:, :2].all()
+    # a tile with such a value sums its products in another order, as any order inside the bounds
+    fine = (o.double() - want).abs() <= far
+    assert fine[before].all() and fine[:, :2].all()
     hit = ~o[413:700, 2:].isfinite()
     if which == "v":
         assert hit[..., dim].all() and hit.sum() == hit[..., dim].numel()
@@ -415,7 +416,7 @@ def test_attend_non_finite_values_reach_later_rows_only(kind, d, bad, which):
 @pytest.mark.parametrize("kind", KINDS)
 def test_attend_non_finite_values_in_a_window(kind):
     c = Case([(200, 400)], kind=kind, heads=4, kv_heads=1, window=150, page=16, d=64)
-    clean, _ = c.call()
+    want, _, far, _ = c.ref()
     for j in (50, 255, 256, 400):
         c.v[int(c.table[0, j // 16]), j % 16, 0].view(torch.uint8 if kind == "e4m3" else c.v.dtype)[9] = 0x7F if kind == "e4m3" else NAN
     o, _ = c.call()
@@ -423,9 +424,10 @@ def test_attend_non_finite_values_in_a_window(kind):
     hit = torch.zeros(400, dtype=torch.bool, device=dev())
     for j in (50, 255, 256, 400):
         hit |= (pos >= j) & (pos < j + 150)
-    assert (o[..., 9].isnan().all(1) == hit).all() and (o[~hit] == clean[~hit]).all()
+    assert (o[..., 9].isnan().all(1) == hit).all()
+    fine = (o.double() - want).abs() <= far
     rest = [i for i in range(64) if i != 9]
-    assert o[..., rest].isfinite().all()
+    assert fine[~hit].all() and fine[..., rest].all()
 
 
 @pytest.mark.parametrize("kind", KINDS)
