@@ -37,8 +37,8 @@ struct Cfg {
     static constexpr uint32_t kStage = kSlabs * kSlab;
     static constexpr int kTiles = D == 256 ? 1 : 2;    // of 128 rows
     static constexpr uint32_t kQTile = D / 64 * kSlab;
-    static constexpr int kStages = kE4M3 ? (D == 64 ? 8 : 4) : (D == 64 ? 10 : 5);
-    static constexpr int kRaw = kE4M3 ? (D == 64 ? 4 : 2) : 0;  // stages of 8-bit values on their way
+    static constexpr int kStages = kE4M3 ? (D == 64 ? 6 : D == 128 ? 3 : 4) : (D == 64 ? 10 : 5);
+    static constexpr int kRaw = kE4M3 ? (D == 64 ? 8 : D == 128 ? 4 : 2) : 0;  // stages of 8-bit values on their way
     static constexpr uint32_t kRawStage = 128 * kDims;
     static constexpr uint32_t kSmem = kTiles * kQTile + kStages * kStage + kRaw * kRawStage;  // and Bars behind it
     static constexpr uint32_t kO = 256;                // tensor memory: S at 0 and 128, O from here on
@@ -52,6 +52,10 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool real) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Arrive on `bar` once this thread's copies so far are there.
+__device__ __forceinline__ void cp_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void lds128(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -78,6 +82,16 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
         "}\n" ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "elect.sync _|p, 0xffffffff;\n"
+        "selp.u32 %0, 1, 0, p;\n"
+        "}\n" : "=r"(r));
+    return r != 0;
 }
 template <int N> __device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -207,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
 
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(&bars.full[i], 128);
+            mbar_init(&bars.full[i], C::kE4M3 ? 128 : 128 + 4);
             mbar_init(&bars.empty[i], 1);
         }
         mbar_init(&bars.q_full, 128);
@@ -243,21 +257,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
         const int pt = tid - 256, pw = pt >> 5;
         constexpr int kChunks = C::kDims * (C::kE4M3 ? 1 : 2) / 16, kAtOnce = 32 / kChunks, kSteps = 32 / kAtOnce;  // 16-byte pieces of a row; rows per copy
         const int chunk = lane % kChunks, sub = lane / kChunks;
-        int issued = 0, told = 0, stage_in = 0, stage_out = 0, q_at = -1, units = 0, tiles = 0;  // groups and stages so far
+        int stage_in = 0, stage_out = 0, units = 0, tiles = 0;  // stages issued, stages converted (e4m3)
         bool ok = true;
         const uint32_t ring_at = smem_addr(ring), raw_at = smem_addr(ring + C::kStages * C::kStage);
         auto free_stage = [&](int n) { return n < C::kStages || warp_wait(wait, &bars.empty[n % C::kStages], (n / C::kStages - 1) & 1); };
-        // bf16: the oldest group has arrived
-        auto tell = [&] {
-            fence_async_smem();
-            if (told == q_at) mbar_arrive(&bars.q_full);
-            else mbar_arrive(&bars.full[stage_out++ % C::kStages]);
-            ++told;
-        };
-        auto flush = [&] {
-            cp_wait<0>();
-            while (told < issued) tell();
-        };
         // e4m3: 8-bit values of the oldest stage become f16; a thread reads what it copied itself
         auto convert = [&] {
             const int n = stage_out;
@@ -279,13 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
         };
         auto copy = [&](const void *base, int part, int64_t row, bool real) {  // one stage; row: this lane's key's offset in elements
             const uint8_t *src = (const uint8_t *)base + part * C::kDims * (C::kE4M3 ? 1 : 2) + 16 * chunk;
-            if constexpr (!C::kE4M3) {
-                const int n = stage_in;
-                if (n >= C::kStages && !__all_sync(0xffffffffu, mbar_try_wait(&bars.empty[n % C::kStages], (n / C::kStages - 1) & 1))) {
-                    flush();  // what waits for the stage may itself be waited for
-                    if (!free_stage(n)) return false;
-                }
-            }
+            if (!C::kE4M3 && !free_stage(stage_in)) return false;
             const uint32_t dst = C::kE4M3 ? raw_at + stage_in % (C::kRaw ? C::kRaw : 1) * C::kRawStage : ring_at + stage_in % C::kStages * C::kStage + chunk / 8 * kSlab;
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
@@ -295,27 +292,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
                 if constexpr (C::kE4M3) cp16(dst + key * C::kDims + 16 * chunk, src + off, there);
                 else cp16(dst + sw128_offset(key, chunk % 8 * 8), src + off * 2, there);
             }
-            cp_commit();
-            ++issued;
-            ++stage_in;
             if constexpr (C::kE4M3) {
-                if (stage_in - stage_out >= C::kRaw) {
-                    cp_wait<(C::kRaw > 0 ? C::kRaw - 1 : 0)>();
-                    return convert();
-                }
-            } else if (issued - told > C::kStages - 2) {
-                cp_wait<C::kStages - 2>();
-                tell();
+                cp_commit();
+                if (++stage_in - stage_out < C::kRaw) return true;
+                cp_wait<(C::kRaw > 0 ? C::kRaw - 1 : 0)>();
+                return convert();
+            } else {
+                uint64_t *bar = &bars.full[stage_in++ % C::kStages];
+                cp_arrive(bar);
+                if (lane == 0) mbar_arrive(bar);  // and the mask of real keys
+                return true;
             }
-            return true;
         };
-        auto settle = [&] {  // everything issued has been passed on
+        auto settle = [&] {  // e4m3: everything issued has been converted
             if constexpr (C::kE4M3) {
                 cp_wait<0>();
                 while (stage_out < stage_in)
                     if (!convert()) return false;
-            } else {
-                flush();
             }
             return true;
         };
@@ -356,8 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
                 fence_async_smem();
                 mbar_arrive(&bars.q_full);
             } else {
-                cp_commit();
-                q_at = issued++;
+                cp_arrive(&bars.q_full);
             }
             ++units;
             return true;
@@ -392,22 +384,34 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
     } else if (warpgroup == 3) {
         // ---- products -------------------------------------------------------------------------------------
         regs_less<48>();
-        if (warp == 12 && lane == 0) {
+        if (warp == 12) {
+            // the whole warp goes along, so that descriptors are uniform values, and one lane issues: with one lane in a branch of
+            // its own an MMA took four times as long to issue as to run
+            const bool leader = elect_one();
             constexpr uint32_t kBase = (1u << 4) | C::kKindBits | (128u >> 4 << 24);
             constexpr uint32_t id_qk = kBase | (128u >> 3 << 17), id_pv = kBase | (1u << 16) | ((uint32_t)C::kDims >> 3 << 17);
             const uint32_t q_at = smem_addr(q_smem), ring_at = smem_addr(ring);
             int stage = 0, units = 0;          // stages and units before this piece
             int n_p[3] = {0, 0, 0};            // P tiles so far, by barrier
             bool ok = true;
-            auto ready = [&](int n) { return wait(&bars.full[n % C::kStages], n / C::kStages & 1); };
-            auto release = [&](int n) { mma_commit(&bars.empty[n % C::kStages]); };
+            // copies by cp.async and the tensor core see shared memory through different proxies
+            auto ready = [&](uint64_t *bar, uint32_t parity) {
+                if (!warp_wait(wait, bar, parity)) return false;
+                if constexpr (!C::kE4M3) fence_async_smem();
+                return true;
+            };
+            auto stage_ready = [&](int n) { return ready(&bars.full[n % C::kStages], n / C::kStages & 1); };
+            auto commit = [&](uint64_t *bar) {
+                if (leader) mma_commit(bar);
+            };
+            auto release = [&](int n) { commit(&bars.empty[n % C::kStages]); };
             auto qk = [&](int tile, int place, int first_stage) {
 #pragma unroll
                 for (int part = 0; part < C::kParts; ++part) {
                     const uint32_t k_at = ring_at + (uint32_t)((first_stage + part) % C::kStages) * C::kStage;
 #pragma unroll
                     for (int ks = 0; ks < C::kDims / 16; ++ks)
-                        mma_bf16(tmem + 128 * place, kmajor_desc(q_at + tile * C::kQTile + part * C::kSlabs * kSlab, ks, kSlab), kmajor_desc(k_at, ks, kSlab), id_qk, part + ks > 0);
+                        if (leader) mma_bf16(tmem + 128 * place, kmajor_desc(q_at + tile * C::kQTile + part * C::kSlabs * kSlab, ks, kSlab), kmajor_desc(k_at, ks, kSlab), id_qk, part + ks > 0);
                 }
             };
             auto pv = [&](int which, int place, int out, int first_stage, bool more) {
@@ -418,10 +422,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
                     const uint32_t v_at = ring_at + (uint32_t)((first_stage + part) % C::kStages) * C::kStage;
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
-                        mma_ts(tmem + C::kO + out * D + part * C::kDims, tmem + 128 * place + 8 * ks, mnmajor_desc(v_at, ks, kSlab), id_pv, more || ks > 0);
+                        if (leader) mma_ts(tmem + C::kO + out * D + part * C::kDims, tmem + 128 * place + 8 * ks, mnmajor_desc(v_at, ks, kSlab), id_pv, more || ks > 0);
                 }
             };
-            auto got_p = [&](int which) { return wait(&bars.p_full[which], n_p[which]++ & 1); };
+            auto got_p = [&](int which) { return warp_wait(wait, &bars.p_full[which], n_p[which]++ & 1); };
             while (ok && walk.next()) {
                 const int n = walk.t1 - walk.t0;
                 if (n == 0) continue;
@@ -430,13 +434,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
                 auto value_stage = [&](int i) { return stage + 2 * C::kParts * i + C::kParts; };
                 auto values = [&](int i) {
                     bool there = true;
-                    for (int part = 0; part < C::kParts; ++part) there = there && ready(value_stage(i) + part);
+                    for (int part = 0; part < C::kParts; ++part) there = there && stage_ready(value_stage(i) + part);
                     return there;
                 };
                 for (int i = 0; ok && i <= n; ++i) {
                     if (i < n) {
-                        for (int part = 0; ok && part < C::kParts; ++part) ok = ready(key_stage(i) + part);
-                        if (ok && i == 0) ok = wait(&bars.q_full, units & 1);
+                        for (int part = 0; ok && part < C::kParts; ++part) ok = stage_ready(key_stage(i) + part);
+                        if (ok && i == 0) ok = ready(&bars.q_full, units & 1);
                         if (!ok) break;
                         tc_fence_after();
                     }
@@ -445,37 +449,37 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
                             if (i > 0) {
                                 if (!(ok = (m || values(i - 1)) && got_p(m))) break;
                                 pv(m, m, m, value_stage(i - 1), i > 1);
-                                mma_commit(&bars.pv_done[m]);
+                                commit(&bars.pv_done[m]);
                                 if (m)
                                     for (int part = 0; part < C::kParts; ++part) release(value_stage(i - 1) + part);
                             }
                             if (i < n) {
                                 qk(m, m, key_stage(i));
-                                mma_commit(&bars.s_full[m]);
+                                commit(&bars.s_full[m]);
                             }
                         }
                     } else {
                         if (i < n) {
                             qk(0, i & 1, key_stage(i));
-                            mma_commit(&bars.s_full[i & 1 ? 2 : 0]);
+                            commit(&bars.s_full[i & 1 ? 2 : 0]);
                         }
                     }
                     if (!ok) break;
                     if (i < n)
                         for (int part = 0; part < C::kParts; ++part) release(key_stage(i) + part);
-                    if (i == n - 1) mma_commit(&bars.q_empty);
+                    if (i == n - 1) commit(&bars.q_empty);
                     if (!two && i > 0) {
                         const int which = (i - 1) & 1 ? 2 : 0;
                         if (!(ok = values(i - 1) && got_p(which))) break;
                         pv(which, (i - 1) & 1, 0, value_stage(i - 1), i > 1);
-                        mma_commit(&bars.pv_done[0]);
+                        commit(&bars.pv_done[0]);
                         for (int part = 0; part < C::kParts; ++part) release(value_stage(i - 1) + part);
                     }
                 }
                 stage += 2 * C::kParts * n;
                 ++units;
             }
-            mma_commit(&bars.drain);
+            commit(&bars.drain);
             mbar_wait(&bars.drain, 0);
         }
         __syncwarp();
@@ -539,12 +543,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
                             if (!(bits[c] >> j & 1)) s[c][j] = -INFINITY;
                     }
                 }
-                float most = -INFINITY;
+                float mx[8];
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int j = 0; j < 8; ++j) mx[j] = s[j / 2][j % 2 * 16];
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) most = fmaxf(most, fmaxf(s[c][j], s[c][j + 1]));
-                most *= f;
+                for (int k = 1; k < 16; k += 2)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        mx[j] = k < 15 ? fmaxf(fmaxf(mx[j], s[j / 2][j % 2 * 16 + k]), s[j / 2][j % 2 * 16 + k + 1]) : fmaxf(mx[j], s[j / 2][j % 2 * 16 + k]);
+                const float most = f * fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
                 const bool raise = most > ref + C::kSlack || (ref == -INFINITY && most > -INFINITY);
                 if (__any_sync(0xffffffffu, raise)) {
                     float lower = 1.f;
@@ -611,14 +618,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
                 } else if (r == 0) {
                     bars.skip[which] = 0;
                 }
+                // the product before this one has ended, as S by turns does not say: a wait tells a product's end from the one before only
+                if (i > 0 && !(ok = warp_wait(wait, &bars.pv_done[m], (n_pv + i - 1) & 1))) break;
                 tc_fence_before();
                 mbar_arrive(&bars.p_full[which]);
             }
             if (!ok) break;
             if (n > 0) {
-                // S of a tile is there after the products two tiles before, with one S after those of the tile before: a wait tells only
-                // the next product's end from the one before
-                if (n > 1 && !(ok = warp_wait(wait, &bars.pv_done[m], (n_pv + n - 2) & 1))) break;
                 if (!(ok = warp_wait(wait, &bars.pv_done[m], (n_pv + n - 1) & 1))) break;
                 tc_fence_after();
             }
