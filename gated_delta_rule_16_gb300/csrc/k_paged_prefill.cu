@@ -35,7 +35,6 @@ __device__ int64_t scan(int64_t x, int64_t *buf, int64_t &all) {
 }
 
 // One CTA: a thread per request counts its units, a thread per unit finds its request, rows and keys, a thread per CTA its run.
-// A unit costs its tiles and one more, for its beginning and end.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PrefillArgs a, int tile, int keys, int grid) {
     __shared__ int64_t buf[32];
     __shared__ int64_t held[kHeldUnits];
@@ -83,7 +82,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PrefillArgs a, int t
             u.tiles = r1.hi >= r0.lo ? (r1.hi - u.key) / keys + 1 : 0;
             u.pad = 0;
             v.unit[i] = u;
-            mine = u.tiles + 1;
+            mine = u.tiles + kPad;
         }
         int64_t all;
         const int64_t incl = cost + scan(mine, buf, all);
@@ -109,7 +108,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PrefillArgs a, int t
                 else lo = mid + 1;
             }
             const int64_t begin = lo ? ends[lo - 1] : 0;
-            run = make_int4((int)head, lo, (int)(rest - begin), (int)(ends[lo] - begin) - 1);
+            run = make_int4((int)head, lo, (int)(rest - begin), (int)(ends[lo] - begin) - kPad);
         }
         v.runs[i] = run;
     }

@@ -2,7 +2,7 @@
 // parts of cut rows lie, shared by the kernels that k_paged_prefill*.cu instantiate.
 //
 // A unit is a tile of rows (new token t, query head of one KV head's group, in this order) of one request with all the keys
-// they attend to, in tiles of 128 keys or less.  The units of all requests are laid end to end, once for each KV head, and the CTAs of one
+// they attend to, in tiles of 64 keys (32-bit storage: 32).  The units of all requests are laid end to end, once for each KV head, and the CTAs of one
 // wave get equal runs of key tiles; a unit cut by a CTA's edge leaves unnormalised fp32 parts that a last launch joins in
 // the keys' order.  Lengths are only known on the GPU, so a first launch of one CTA lists the units and finds the runs.  Causal rows
 // make units of 1 to hundreds of tiles, and equal runs need no luck with their order: of 8192 tokens at once every CTA
@@ -15,7 +15,6 @@ namespace gdn {
 namespace prefill {
 
 constexpr int kMaxCtas = 152;  // of a wave: one per SM
-constexpr int kMinRun = 2;     // tiles that a CTA takes at least
 
 struct Unit {       // 32 bytes
     int b, first;   // request; its first row of q
@@ -62,7 +61,9 @@ inline __host__ __device__ size_t layout(void *ws, int B, int n, int Hq, int Hkv
 
 // Rows and keys of a tile: what the kernels are built for.
 inline __host__ __device__ int row_tile(gdn_dtype kind, int d) { return kind == GDN_F32 || d == 256 ? 128 : 256; }
-inline __host__ __device__ int key_tile(gdn_dtype kind) { return kind == GDN_F32 ? 32 : 128; }
+inline __host__ __device__ int key_tile(gdn_dtype kind) { return kind == GDN_F32 ? 32 : 64; }
+// A unit costs its tiles and this many more, for its beginning and end; a CTA takes a run of kMinRun at least.
+constexpr int kPad = 2, kMinRun = 4;
 
 inline __host__ __device__ int64_t split_at(int64_t total, int ctas, int i) { return total / ctas * i + total % ctas * i / ctas; }
 
@@ -99,11 +100,12 @@ struct Walk {
             if (at.x > end.x || (at.x == end.x && at.y > end.y) || (last && at.z >= end.z)) return false;
             u = v.unit[at.y];
             h = at.x;
+            const bool begin = at.z == 0;
             t0 = min(at.z, u.tiles);
             t1 = last ? min(end.z, u.tiles) : u.tiles;
             at.z = 0;
             if (++at.y == units) at.y = 0, ++at.x;
-            if (t0 < t1 || u.tiles == 0) return true;
+            if (t0 < t1 || (u.tiles == 0 && begin)) return true;
         }
     }
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == u.tiles; }

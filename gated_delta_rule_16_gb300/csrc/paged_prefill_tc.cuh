@@ -1,17 +1,20 @@
 // paged_prefill_tc.cuh -- softmax attention of new tokens over the paged cache on tcgen05 tensor cores: the
 // kernel template that k_paged_prefill_{bf16,e4m3}.cu instantiate.
 //
-// S = Q K^T, P = 2^(z - ref), O += P V with z = scale log2(e) S, for tiles of 128 rows and 128 keys; S and O are accumulators in
+// S = Q K^T, P = 2^(z - ref), O += P V with z = scale log2(e) S, for tiles of 128 rows and 64 keys; S and O are accumulators in
 // tensor memory, P is written over S in 16 bits and read from there as the second product's A operand.  ref follows the running
 // maximum of a row lazily: only when z passes it by kSlack is ref raised and O, in tensor memory, rescaled.
 //
 // One CTA of 16 warps per SM:
-//   warps 0-3, 4-7   softmax of the unit's first and second 128 rows, a thread per row: while one group works on its S the tensor
-//                    core does the other's products.  With 256 dims O fills tensor memory beside two S tiles, and with 128 rows or less there is
-//                    no second tile: then the first group takes all tiles, and S alternates between the two places;
+//   warps 0-3, 4-7   softmax of the unit's first and second 128 rows, a thread per row.  Each has two S tiles: the tensor core makes
+//                    one while the other is worked on, so that neither waits for the other's latency (with one S tile of 128 keys a
+//                    tile took 4600 clocks of 2048 in the tensor core);
 //   warps 8-11       copy keys and values into a ring of shared memory, in the 128-byte swizzle, 16 bytes at a time by cp.async: any
 //                    page size and any strides cost the same, and what is not attended to is filled with zeros;
-//   warp 12          one thread issues the products.
+//   warps 12, 13     issue the products of the first and second row tile.  Between two batches of MMAs a warp has some tens of
+//                    instructions to go through, which beside the busy softmax warps take hundreds of clocks, more than the tensor core has queued:
+//                    the other warp's batches fill the gap.
+// With 256 dims O fills the tensor memory of two row tiles, and a unit has one.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -26,12 +29,13 @@ using namespace tc;
 
 constexpr int kThreads = 512;
 constexpr uint32_t kSlab = 16384;  // [128 rows][128 bytes]
-constexpr int kWords = 16;         // tiles whose masks of real keys are kept
+constexpr int kTileKeys = 64;
+constexpr int kWords = 16;         // stages whose masks of real keys are kept
 
 template <gdn_dtype KIND, int D>
 struct Cfg {
     static constexpr bool kE4M3 = KIND == GDN_E4M3;
-    static constexpr int kDims = D < 128 ? D : 128;    // of a ring stage: 128 keys
+    static constexpr int kDims = D < 128 ? D : 128;    // of a ring stage, which has 128 keys: two tiles
     static constexpr int kParts = D / kDims;           // stages of a tile of keys (and of one of values)
     static constexpr int kSlabs = kDims / 64;
     static constexpr uint32_t kStage = kSlabs * kSlab;
@@ -41,7 +45,7 @@ struct Cfg {
     static constexpr int kRaw = kE4M3 ? (D == 64 ? 8 : D == 128 ? 4 : 2) : 0;  // stages of 8-bit values on their way
     static constexpr uint32_t kRawStage = 128 * kDims;
     static constexpr uint32_t kSmem = kTiles * kQTile + kStages * kStage + kRaw * kRawStage;  // and Bars behind it
-    static constexpr uint32_t kO = 256;                // tensor memory: S at 0 and 128, O from here on
+    static constexpr uint32_t kO = 256;                // tensor memory: S at 0, 64 (first row tile), 128, 192 (second), O from here on
     // ref is raised when a score passes it by 2^kSlack; weights are 2^kShift times 2^(z - ref).  bf16 has fp32's range; f16 gets
     // 11 bits for weights down to 2^-25 of the largest, and what sums to less than 2^-36 of it is lost.
     static constexpr float kSlack = kE4M3 ? 4.f : 8.f, kShift = kE4M3 ? 11.f : 0.f;
@@ -50,6 +54,9 @@ struct Cfg {
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool real) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void mma_commit_at(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Arrive on `bar` once this thread's copies so far are there.
@@ -73,14 +80,50 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// D[tmem] (+)= A[tmem] * B, issued by a single thread.
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// Four K steps of D[tmem] (+)= A B, issued by the lane with `issue`: both operands K-major in shared memory, or A in tensor memory and B
+// MN-major.  One block of predicated instructions with their descriptors counted up in it: with a branch and descriptors of its own for
+// each, the MMAs of a tile took longer to issue, beside the other warps of the scheduler, than to run.
+__device__ __forceinline__ void mma4_ss(bool issue, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, bool accumulate) {
     asm volatile(
         "{\n"
-        ".reg .pred p;\n"
+        ".reg .pred p, q, t;\n"
+        ".reg .b64 a, b;\n"
+        "setp.ne.b32 q, %5, 0;\n"
         "setp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
-        "}\n" ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "setp.eq.b32 t, 0, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+        "add.s64 a, %1, 2;\n"
+        "add.s64 b, %2, 2;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+        "add.s64 a, %1, 4;\n"
+        "add.s64 b, %2, 4;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+        "add.s64 a, %1, 6;\n"
+        "add.s64 b, %2, 6;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+        "}\n" ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate), "r"((uint32_t)issue)
+        : "memory");
+}
+__device__ __forceinline__ void mma4_ts(bool issue, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p, q, t;\n"
+        ".reg .b64 b;\n"
+        ".reg .b32 a;\n"
+        "setp.ne.b32 q, %5, 0;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "setp.eq.b32 t, 0, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        "add.s32 a, %1, 8;\n"
+        "add.s64 b, %2, 128;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+        "add.s32 a, %1, 16;\n"
+        "add.s64 b, %2, 256;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+        "add.s32 a, %1, 24;\n"
+        "add.s64 b, %2, 384;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+        "}\n" ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate), "r"((uint32_t)issue)
         : "memory");
 }
 __device__ __forceinline__ bool elect_one() {
@@ -95,35 +138,44 @@ __device__ __forceinline__ bool elect_one() {
 }
 template <int N> __device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-// Waits on mbarriers end after kWaitLimitNs, or soon after another thread's did.
+// Waits on mbarriers end after kWaitLimitNs, or soon after another thread's did.  A try suspends the warp for up to a millisecond, so that
+// those that wait leave the issue slots to the others.
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n"
+        "selp.u32 %0, 1, 0, p;\n"
+        "}\n" : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+    return done != 0;
+}
 struct Waiter {
     volatile int *gave_up;
-    __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const {
-        if (mbar_try_wait(bar, parity)) return true;
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+        if (try_wait(bar, parity)) return true;
         const uint64_t since = globaltimer();
-        for (;;) {
 #pragma unroll 1
-            for (int i = 0; i < 64; ++i)
-                if (mbar_try_wait(bar, parity)) return true;
+        while (!try_wait(bar, parity))
             if (*gave_up || globaltimer() - since > kWaitLimitNs) {
                 *gave_up = 1;
                 return false;
             }
-        }
+        return true;
     }
+    __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const { return (*this)(smem_addr(bar), parity); }
 };
 
 struct Bars {
     static constexpr int kMaxStages = 10;
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t q_full, q_empty;
-    uint64_t s_full[3], p_full[3];  // first group's S at 0; second group's S at 128; first group's S at 128
-    uint64_t pv_done[2];            // of a group
-    uint64_t joint[2], drain;       // joint: a group's votes
-    uint32_t words[kWords][4];      // real keys of a tile
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // of a group's two S tiles
+    uint64_t joint[2], drain[2];    // joint: a group's votes
+    uint32_t words[kWords][4];      // real keys of a stage
     float row_scale[2][256];        // e4m3: of q's rows, by turns
     int vote[2][3];                 // of a group, by turns
-    int skip[3];                    // the group has added this tile's P V itself
+    int skip[2][2];                 // the group has added this tile's P V itself
     int gave_up;
     uint32_t tmem;
 };
@@ -131,7 +183,7 @@ struct Bars {
 static_assert(sizeof(Bars) <= 3 * 1024, "shared memory");
 
 // A warp's waits succeed or fail for all of its lanes.
-__device__ __forceinline__ bool warp_wait(const Waiter &wait, uint64_t *bar, uint32_t parity) {
+template <typename Bar> __device__ __forceinline__ bool warp_wait(const Waiter &wait, Bar bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait(bar, parity));
 }
 // Whether any thread of a group says x, in `any`; false: a wait ran out.  `turn` counts the group's votes.
@@ -146,17 +198,36 @@ __device__ __forceinline__ bool group_any(const Waiter &wait, Bars &bars, int gr
     return ok;
 }
 
-// Bits of keys kb .. kb + 127 inside [lo, hi].
+// Bits of keys kb + 32 part .. inside [lo, hi].
 __device__ __forceinline__ uint32_t range_bits(int part, int kb, int lo, int hi) {
     const int l = lo - kb - 32 * part, h = hi - kb - 32 * part;
     if (l > 31 || h < 0) return 0;
     return (l <= 0 ? ~0u : ~0u << l) & (h >= 31 ? ~0u : (2u << h) - 1);
 }
 
-// O += P V of one tile for a group's rows without the tensor core, which multiplies a masked weight of 0 with what it masks: a tile of
-// values with an infinity or NaN that some of the rows do not attend to.  P is in tensor memory, a row's thread reads its own.
+// Whether half of a key's values in a ring stage are finite: thread r of a group has key r % 64 of a tile's, and its first or second half.
+// Values that only some rows attend to have to be.
 template <gdn_dtype KIND, int D>
-__device__ __noinline__ void add_masked(uint32_t t_p, uint32_t t_o, const uint8_t *ring, int stage0, const uint32_t (&bits)[4], bool first) {
+__device__ __noinline__ bool all_numbers(uint32_t stage, int key0, int r) {
+    using C = Cfg<KIND, D>;
+    uint32_t bad = 0;
+#pragma unroll 4
+    for (int e = 0; e < C::kDims / 16; ++e) {
+        const int piece = (r >> 6) * (C::kDims / 16) + e;
+        uint32_t x[4];
+        lds128(x, stage + piece / 8 * kSlab + sw128_offset(key0 + (r & 63), piece % 8 * 8));
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            bad |= C::kE4M3 ? ((x[w] & 0x7c007c00u) + 0x04000400u) & 0x80008000u : ((x[w] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+    }
+    return bad == 0;
+}
+
+// O += P V of one tile for a group's rows without the tensor core, which multiplies a masked weight of 0 with what it masks: a tile of
+// values with an infinity or NaN that some of the rows do not attend to.  P is in tensor memory, a row's thread reads its own; the
+// values are rows `key0` on of the stages from stage0 on.
+template <gdn_dtype KIND, int D>
+__device__ __noinline__ void add_masked(uint32_t t_p, uint32_t t_o, const uint8_t *ring, int stage0, int key0, uint32_t bits0, uint32_t bits1, bool first) {
     using C = Cfg<KIND, D>;
 #pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
@@ -167,24 +238,25 @@ __device__ __noinline__ void add_masked(uint32_t t_p, uint32_t t_o, const uint8_
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = 0.f;
         const int d0 = 32 * c;
-        const uint8_t *stage = ring + (uint32_t)((stage0 + d0 / C::kDims) % C::kStages) * C::kStage + d0 % C::kDims / 64 * kSlab;
+        const uint32_t stage = smem_addr(ring) + (uint32_t)((stage0 + d0 / C::kDims) % C::kStages) * C::kStage + d0 % C::kDims / 64 * kSlab;
 #pragma unroll 1
-        for (int part = 0; part < 4; ++part) {
+        for (int part = 0; part < 2; ++part) {
+            const uint32_t bits = part ? bits1 : bits0;
             float p[16];
             tmem_ld16(t_p + 16 * part, p);
             tmem_ld_wait();
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
-                if (!(bits[part] >> k & 1)) continue;
+                if (!(bits >> k & 1)) continue;
                 const uint32_t w = __float_as_uint(p[k / 2]);
                 float x;
                 if constexpr (C::kE4M3) x = __half2float(__ushort_as_half((unsigned short)(k & 1 ? w >> 16 : w & 0xffff)));
                 else x = __uint_as_float(k & 1 ? w & 0xffff0000u : w << 16);
-                const int key = 32 * part + k;
+                const int key = key0 + 32 * part + k;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     uint32_t v[4];
-                    lds128(v, smem_addr(stage) + sw128_offset(key, d0 % 64 + 8 * e));
+                    lds128(v, stage + sw128_offset(key, d0 % 64 + 8 * e));
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         float lo, hi;
@@ -200,8 +272,8 @@ __device__ __noinline__ void add_masked(uint32_t t_p, uint32_t t_o, const uint8_
                     }
                 }
             }
+            __syncwarp();
         }
-        __syncwarp();
         tmem_st32(t_o + 32 * c, o);
         tmem_st_wait();
     }
@@ -222,21 +294,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&bars.full[i], C::kE4M3 ? 128 : 128 + 4);
-            mbar_init(&bars.empty[i], 1);
+            mbar_init(&bars.empty[i], C::kTiles);
         }
         mbar_init(&bars.q_full, 128);
-        mbar_init(&bars.q_empty, 1);
-        for (int i = 0; i < 3; ++i) {
-            mbar_init(&bars.s_full[i], 1);
-            mbar_init(&bars.p_full[i], 128);
-            bars.skip[i] = 0;
-        }
+        mbar_init(&bars.q_empty, C::kTiles);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars.pv_done[i], 1);
+            for (int j = 0; j < 2; ++j) {
+                mbar_init(&bars.s_full[i][j], 1);
+                mbar_init(&bars.p_full[i][j], 128);
+                mbar_init(&bars.pv_done[i][j], 1);
+                bars.skip[i][j] = 0;
+            }
             mbar_init(&bars.joint[i], 128);
             for (int j = 0; j < 3; ++j) bars.vote[i][j] = 0;
         }
-        mbar_init(&bars.drain, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&bars.drain[i], 1);
         bars.gave_up = 0;
         fence_mbar_init();
     }
@@ -284,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
             const uint8_t *src = (const uint8_t *)base + part * C::kDims * (C::kE4M3 ? 1 : 2) + 16 * chunk;
             if (!C::kE4M3 && !free_stage(stage_in)) return false;
             const uint32_t dst = C::kE4M3 ? raw_at + stage_in % (C::kRaw ? C::kRaw : 1) * C::kRawStage : ring_at + stage_in % C::kStages * C::kStage + chunk / 8 * kSlab;
-#pragma unroll
+#pragma unroll 4
             for (int i = 0; i < kSteps; ++i) {
                 const int from = i * kAtOnce + sub, key = 32 * pw + from;
                 const int64_t off = __shfl_sync(0xffffffffu, row, from);
@@ -360,23 +432,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
             const int first = u.first + u.row / group, last = u.first + (u.row + u.rows - 1) / group;
             const int lo = reach_of((int64_t)first + u.shift, a.window, room).lo, hi = reach_of((int64_t)last + u.shift, a.window, room).hi;
             const int32_t *table = a.table + u.b * a.table_stride;
+            const int begin = u.key + kTileKeys * walk.t0, end = min(hi, u.key + kTileKeys * walk.t1 - 1), n = (walk.t1 - walk.t0 + 1) / 2;
             auto entry = [&](int key, int &cell) {  // the key's page, -1 where it has none
                 const int page = key / a.c.page;
                 cell = key - page * a.c.page;
-                return key >= lo && key <= hi ? table[page] : -1;
+                return key >= lo && key <= end ? table[page] : -1;
             };
-            int cell_next, page_next = entry(u.key + 128 * walk.t0 + pt, cell_next);
-            for (int t = walk.t0; ok && t < walk.t1; ++t) {
+            int cell_next, page_next = entry(begin + pt, cell_next);
+            for (int t = 0; ok && t < n; ++t) {
                 const int page = page_next, cell = cell_next;
-                if (t + 1 < walk.t1) page_next = entry(u.key + 128 * (t + 1) + pt, cell_next);
+                if (t + 1 < n) page_next = entry(begin + 128 * (t + 1) + pt, cell_next);
                 const bool real = page >= 0 && page < a.c.pages;
                 const int64_t row = real ? page * a.c.stride_page + cell * a.c.stride_token + walk.h * a.c.stride_head : 0;
                 const uint32_t word = __ballot_sync(0xffffffffu, real);
                 if (lane == 0) bars.words[tiles % kWords][pw] = word;
                 ++tiles;
-                for (int part = 0; ok && part < C::kParts; ++part) ok = copy(a.c.k, part, row, real);
-                if (ok && t == walk.t0) ok = load_q(u, walk.h);
-                for (int part = 0; ok && part < C::kParts; ++part) ok = copy(a.c.v, part, row, real);
+#pragma unroll 1
+                for (int part = 0; ok && part < 2 * C::kParts; ++part) {
+                    if (t == 0 && part == C::kParts && !(ok = load_q(u, walk.h))) break;
+                    ok = copy(part < C::kParts ? a.c.k : a.c.v, part % C::kParts, row, real);
+                }
             }
         }
         if (ok) settle();
@@ -384,103 +459,123 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
     } else if (warpgroup == 3) {
         // ---- products -------------------------------------------------------------------------------------
         regs_less<48>();
-        if (warp == 12) {
+        if (warp < 12 + C::kTiles) {
             // the whole warp goes along, so that descriptors are uniform values, and one lane issues: with one lane in a branch of
             // its own an MMA took four times as long to issue as to run
             const bool leader = elect_one();
             constexpr uint32_t kBase = (1u << 4) | C::kKindBits | (128u >> 4 << 24);
-            constexpr uint32_t id_qk = kBase | (128u >> 3 << 17), id_pv = kBase | (1u << 16) | ((uint32_t)C::kDims >> 3 << 17);
-            const uint32_t q_at = smem_addr(q_smem), ring_at = smem_addr(ring);
-            int stage = 0, units = 0;          // stages and units before this piece
-            int n_p[3] = {0, 0, 0};            // P tiles so far, by barrier
+            constexpr uint32_t id_qk = kBase | ((uint32_t)kTileKeys >> 3 << 17), id_pv = kBase | (1u << 16) | ((uint32_t)C::kDims >> 3 << 17);
+            const uint64_t q_desc = kmajor_desc(smem_addr(q_smem), 0, kSlab), k_desc = kmajor_desc(smem_addr(ring), 0, kSlab), v_desc = mnmajor_desc(smem_addr(ring), 0, kSlab);
+            const uint32_t full_at = smem_addr(&bars.full), empty_at = smem_addr(&bars.empty), s_at = smem_addr(&bars.s_full), p_at = smem_addr(&bars.p_full),
+                           pv_at = smem_addr(&bars.pv_done);
+            const int m = warp - 12;
+            int units = 0, done = 0;  // units, and tiles of this group, before this piece; tiles take a group's two places by turns
             bool ok = true;
             // copies by cp.async and the tensor core see shared memory through different proxies
-            auto ready = [&](uint64_t *bar, uint32_t parity) {
+            auto ready = [&](uint32_t bar, uint32_t parity) {
                 if (!warp_wait(wait, bar, parity)) return false;
                 if constexpr (!C::kE4M3) fence_async_smem();
                 return true;
             };
-            auto stage_ready = [&](int n) { return ready(&bars.full[n % C::kStages], n / C::kStages & 1); };
-            auto commit = [&](uint64_t *bar) {
-                if (leader) mma_commit(bar);
+            auto commit = [&](uint32_t bar) {
+                if (leader) mma_commit_at(bar);
             };
-            auto release = [&](int n) { commit(&bars.empty[n % C::kStages]); };
-            auto qk = [&](int tile, int place, int first_stage) {
-#pragma unroll
-                for (int part = 0; part < C::kParts; ++part) {
-                    const uint32_t k_at = ring_at + (uint32_t)((first_stage + part) % C::kStages) * C::kStage;
-#pragma unroll
-                    for (int ks = 0; ks < C::kDims / 16; ++ks)
-                        if (leader) mma_bf16(tmem + 128 * place, kmajor_desc(q_at + tile * C::kQTile + part * C::kSlabs * kSlab, ks, kSlab), kmajor_desc(k_at, ks, kSlab), id_qk, part + ks > 0);
+            // a place in the ring: the first stage of a tile pair's keys or values
+            struct Place {
+                int slot;
+                uint32_t parity;
+                __device__ __forceinline__ void step(int by) {
+                    slot += by;
+                    if (slot >= C::kStages) slot -= C::kStages, parity ^= 1;
                 }
             };
-            auto pv = [&](int which, int place, int out, int first_stage, bool more) {
-                tc_fence_after();
-                if (*(volatile int *)&bars.skip[which]) return;
-#pragma unroll
-                for (int part = 0; part < C::kParts; ++part) {
-                    const uint32_t v_at = ring_at + (uint32_t)((first_stage + part) % C::kStages) * C::kStage;
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        if (leader) mma_ts(tmem + C::kO + out * D + part * C::kDims, tmem + 128 * place + 8 * ks, mnmajor_desc(v_at, ks, kSlab), id_pv, more || ks > 0);
+            auto stages_ready = [&](Place at) {
+                bool there = ready(full_at + 8 * at.slot, at.parity);
+                if constexpr (C::kParts == 2) {
+                    at.step(1);
+                    there = there && ready(full_at + 8 * at.slot, at.parity);
+                }
+                return there;
+            };
+            auto release_stages = [&](Place at) {
+                commit(empty_at + 8 * at.slot);
+                if constexpr (C::kParts == 2) {
+                    at.step(1);
+                    commit(empty_at + 8 * at.slot);
                 }
             };
-            auto got_p = [&](int which) { return warp_wait(wait, &bars.p_full[which], n_p[which]++ & 1); };
+            Place k_place = {0, 0}, v_place = {C::kParts, 0};
             while (ok && walk.next()) {
                 const int n = walk.t1 - walk.t0;
                 if (n == 0) continue;
-                const bool two = walk.u.rows > 128;
-                auto key_stage = [&](int i) { return stage + 2 * C::kParts * i; };
-                auto value_stage = [&](int i) { return stage + 2 * C::kParts * i + C::kParts; };
-                auto values = [&](int i) {
-                    bool there = true;
-                    for (int part = 0; part < C::kParts; ++part) there = there && stage_ready(value_stage(i) + part);
-                    return there;
+                if (m == 1 && walk.u.rows <= 128) {  // nothing to do but to say so, stage by stage
+                    if (!(ok = warp_wait(wait, smem_addr(&bars.q_full), units & 1))) break;
+                    if (leader) mbar_arrive(&bars.q_empty);
+                    for (int i = 0; ok && i < (n + 1) / 2; ++i)
+                        for (Place *at : {&k_place, &v_place}) {
+                            if (!(ok = warp_wait(wait, full_at + 8 * at->slot, at->parity))) break;
+                            if (leader) mbar_arrive(&bars.empty[at->slot]);
+                            at->step(2);
+                        }
+                    ++units;
+                    continue;
+                }
+                // S = Q K^T of a row tile and half of a stage's keys
+                auto qk = [&](int place, int half) {
+                    Place at = k_place;
+#pragma unroll
+                    for (int part = 0; part < C::kParts; ++part) {
+                        const uint64_t k = k_desc + (uint32_t)(at.slot * (int)(C::kStage >> 4) + half * (int)(kSlab >> 5));
+#pragma unroll
+                        for (int slab = 0; slab < C::kSlabs; ++slab)
+                            mma4_ss(leader, tmem + 128 * m + 64 * place, q_desc + ((m * C::kQTile + (part * C::kSlabs + slab) * kSlab) >> 4), k + (slab * kSlab >> 4), id_qk, part + slab > 0);
+                        at.step(1);
+                    }
+                    commit(s_at + 16 * m + 8 * place);
                 };
-                for (int i = 0; ok && i <= n; ++i) {
+                auto pv = [&](int tile, int half, bool more) {
+                    const int place = tile & 1;
+                    if (!warp_wait(wait, p_at + 16 * m + 8 * place, tile >> 1 & 1)) return false;
+                    tc_fence_after();
+                    if (!*(volatile int *)&bars.skip[m][place]) {
+                        Place at = v_place;
+#pragma unroll
+                        for (int part = 0; part < C::kParts; ++part) {
+                            mma4_ts(leader, tmem + C::kO + m * D + part * C::kDims, tmem + 128 * m + 64 * place, v_desc + (uint32_t)(at.slot * (int)(C::kStage >> 4) + half * (int)(kSlab >> 5)), id_pv, more);
+                            at.step(1);
+                        }
+                    }
+                    commit(pv_at + 16 * m + 8 * place);
+                    return true;
+                };
+                // the scores of a tile are asked for before the weights of the one before are waited for
+                for (int i = 0; i <= n; ++i) {
                     if (i < n) {
-                        for (int part = 0; ok && part < C::kParts; ++part) ok = stage_ready(key_stage(i) + part);
-                        if (ok && i == 0) ok = ready(&bars.q_full, units & 1);
-                        if (!ok) break;
+                        if (!(i & 1) && !(ok = stages_ready(k_place))) break;
+                        if (i == 0 && !(ok = ready(smem_addr(&bars.q_full), units & 1))) break;
                         tc_fence_after();
-                    }
-                    if (two) {
-                        for (int m = 0; m < 2; ++m) {
-                            if (i > 0) {
-                                if (!(ok = (m || values(i - 1)) && got_p(m))) break;
-                                pv(m, m, m, value_stage(i - 1), i > 1);
-                                commit(&bars.pv_done[m]);
-                                if (m)
-                                    for (int part = 0; part < C::kParts; ++part) release(value_stage(i - 1) + part);
-                            }
-                            if (i < n) {
-                                qk(m, m, key_stage(i));
-                                commit(&bars.s_full[m]);
-                            }
+                        qk((done + i) & 1, i & 1);
+                        if ((i & 1) || i == n - 1) {
+                            release_stages(k_place);
+                            k_place.step(2 * C::kParts);
                         }
-                    } else {
-                        if (i < n) {
-                            qk(0, i & 1, key_stage(i));
-                            commit(&bars.s_full[i & 1 ? 2 : 0]);
-                        }
+                        if (i == n - 1) commit(smem_addr(&bars.q_empty));
                     }
-                    if (!ok) break;
-                    if (i < n)
-                        for (int part = 0; part < C::kParts; ++part) release(key_stage(i) + part);
-                    if (i == n - 1) commit(&bars.q_empty);
-                    if (!two && i > 0) {
-                        const int which = (i - 1) & 1 ? 2 : 0;
-                        if (!(ok = values(i - 1) && got_p(which))) break;
-                        pv(which, (i - 1) & 1, 0, value_stage(i - 1), i > 1);
-                        commit(&bars.pv_done[0]);
-                        for (int part = 0; part < C::kParts; ++part) release(value_stage(i - 1) + part);
+                    if (i > 0) {
+                        const int j = i - 1;
+                        if (!(j & 1) && !(ok = stages_ready(v_place))) break;
+                        if (!(ok = pv(done + j, j & 1, j > 0))) break;
+                        if ((j & 1) || j == n - 1) {
+                            release_stages(v_place);
+                            v_place.step(2 * C::kParts);
+                        }
                     }
                 }
-                stage += 2 * C::kParts * n;
+                done += n;
                 ++units;
             }
-            commit(&bars.drain);
-            mbar_wait(&bars.drain, 0);
+            commit(smem_addr(&bars.drain[m]));
+            mbar_wait(&bars.drain[m], 0);
         }
         __syncwarp();
     } else {
@@ -489,15 +584,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
         const int m = warpgroup, r = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // tensor memory lanes of this warp
         const float log2e = 1.4426950408889634f;
-        int stage = 0, units = 0, tiles = 0, n_s[3] = {0, 0, 0}, n_pv = 0, votes = 0;
+        int stage = 0, units = 0, loads = 0, done = 0, votes = 0;  // before this piece: ring stages, units, masks of keys, tiles
         bool ok = true;
         while (ok && walk.next()) {
             const Unit u = walk.u;
             const int n = walk.t1 - walk.t0;
             const bool two = u.rows > 128;
             if (m == 1 && !two) {  // the first group has all of it
-                stage += 2 * C::kParts * n;
-                tiles += n;
+                stage += 2 * C::kParts * ((n + 1) / 2);
+                loads += (n + 1) / 2;
                 units += n > 0;
                 continue;
             }
@@ -512,46 +607,47 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
             float ref = -INFINITY, sum = 0.f, zs = a.scale * log2e;
             if (a.c.k_scale) zs *= a.c.k_scale[walk.h];
             for (int i = 0; ok && i < n; ++i) {
-                const int which = two ? m : (i & 1 ? 2 : 0), place = two ? m : i & 1;
-                const uint32_t t_s = tmem + lanes + 128 * place;
-                if (!(ok = warp_wait(wait, &bars.s_full[which], n_s[which]++ & 1))) break;
+                const int place = (done + i) & 1;
+                const uint32_t t_s = tmem + lanes + 128 * m + 64 * place;
+                // the product of tile j has ended; tile i's scores say so for j <= i - 2
+                auto ended = [&](int j) { return warp_wait(wait, &bars.pv_done[m][(done + j) & 1], (done + j) >> 1 & 1); };
+                if (!(ok = warp_wait(wait, &bars.s_full[m][place], (done + i) >> 1 & 1))) break;
                 tc_fence_after();
                 if (C::kE4M3 && i == 0) zs *= bars.row_scale[units & 1][128 * m + r];
-                float s[4][32];
+                float s[2][32];
+                tmem_ld32(t_s, s[0]);
+                tmem_ld32(t_s + 32, s[1]);
+                const int kb = u.key + kTileKeys * (walk.t0 + i);
+                uint32_t bits[2];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, s[c]);
+                for (int c = 0; c < 2; ++c) bits[c] = bars.words[(loads + (i >> 1)) % kWords][2 * (i & 1) + c];
+                const bool edge = kb < all_lo || kb + kTileKeys - 1 > all_hi || (bits[0] & bits[1]) != ~0u;
                 tmem_ld_wait();
-                const int kb = u.key + 128 * (walk.t0 + i);
-                uint32_t bits[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) bits[c] = bars.words[(tiles + i) % kWords][c];
-                const bool edge = kb < all_lo || kb + 127 > all_hi || (bits[0] & bits[1] & bits[2] & bits[3]) != ~0u;
                 float f = zs;
-                if (!(zs > 0.f)) {  // the maximum below is that of s
+                if (__builtin_expect(!(zs > 0.f), 0)) {  // the maximum below is that of s
                     f = 1.f;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) s[c][j] *= zs;
                 }
-                if (edge) {
+                if (__builtin_expect(edge, 0)) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 2; ++c) {
                         bits[c] &= range_bits(c, kb, mine.lo, mine.hi);
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (!(bits[c] >> j & 1)) s[c][j] = -INFINITY;
                     }
                 }
-                float mx[8];
+                float mx[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) mx[j] = s[j / 2][j % 2 * 16];
+                for (int j = 0; j < 4; ++j) mx[j] = fmaxf(s[j / 2][j % 2 * 16], s[j / 2][j % 2 * 16 + 1]);
 #pragma unroll
-                for (int k = 1; k < 16; k += 2)
+                for (int k = 2; k < 16; k += 2)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        mx[j] = k < 15 ? fmaxf(fmaxf(mx[j], s[j / 2][j % 2 * 16 + k]), s[j / 2][j % 2 * 16 + k + 1]) : fmaxf(mx[j], s[j / 2][j % 2 * 16 + k]);
-                const float most = f * fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+                    for (int j = 0; j < 4; ++j) mx[j] = fmaxf(fmaxf(mx[j], s[j / 2][j % 2 * 16 + k]), s[j / 2][j % 2 * 16 + k + 1]);
+                const float most = f * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 const bool raise = most > ref + C::kSlack || (ref == -INFINITY && most > -INFINITY);
                 if (__any_sync(0xffffffffu, raise)) {
                     float lower = 1.f;
@@ -561,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
                         sum *= lower;
                     }
                     if (i > 0) {
-                        if (!(ok = warp_wait(wait, &bars.pv_done[m], (n_pv + i - 1) & 1))) break;
+                        if (!(ok = ended(i - 1))) break;
                         tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < D / 16; ++c) {
@@ -577,61 +673,47 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
                 }
                 const float base = ref == -INFINITY ? 0.f : ref - C::kShift;
                 float part[4] = {0.f, 0.f, 0.f, 0.f};
+                float p[32];
 #pragma unroll
-                for (int c = 0; c < 4; c += 2) {
-                    float p[32];
-#pragma unroll
-                    for (int j = 0; j < 64; j += 2) {
-                        const float x = ex2(s[c + j / 32][j % 32] * f - base), y = ex2(s[c + j / 32][j % 32 + 1] * f - base);
-                        part[j / 2 % 2 * 2] += x;
-                        part[j / 2 % 2 * 2 + 1] += y;
-                        p[j / 2] = __uint_as_float(C::kE4M3 ? pack_f16x2(x, y) : pack_bf16x2(x, y));
-                    }
-                    tmem_st32(t_s + 16 * c, p);
+                for (int j = 0; j < 64; j += 2) {
+                    const float x = ex2(s[j / 32][j % 32] * f - base), y = ex2(s[j / 32][j % 32 + 1] * f - base);
+                    part[j / 2 % 2 * 2] += x;
+                    part[j / 2 % 2 * 2 + 1] += y;
+                    p[j / 2] = __uint_as_float(C::kE4M3 ? pack_f16x2(x, y) : pack_bf16x2(x, y));
                 }
+                tmem_st32(t_s, p);
                 sum += (part[0] + part[1]) + (part[2] + part[3]);
                 tmem_st_wait();
-                if (edge) {
-                    // values that only some rows attend to have to be numbers
-                    const int at = stage + 2 * C::kParts * i + C::kParts;
-                    uint32_t bad = 0;
+                if (__builtin_expect(edge, 0)) {
+                    const int at = stage + 2 * C::kParts * (i >> 1) + C::kParts;
+                    bool numbers = true;
                     for (int k = 0; ok && k < C::kParts; ++k) {
                         ok = warp_wait(wait, &bars.full[(at + k) % C::kStages], (at + k) / C::kStages & 1);
-                        const uint32_t v_at = smem_addr(ring) + (uint32_t)((at + k) % C::kStages) * C::kStage;
-#pragma unroll
-                        for (int e = 0; e < C::kDims / 8; ++e) {
-                            uint32_t x[4];
-                            lds128(x, v_at + e / 8 * kSlab + sw128_offset(r, e % 8 * 8));
-#pragma unroll
-                            for (int w = 0; w < 4; ++w)
-                                bad |= C::kE4M3 ? ((x[w] & 0x7c007c00u) + 0x04000400u) & 0x80008000u : ((x[w] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-                        }
+                        numbers = numbers && all_numbers<KIND, D>(smem_addr(ring) + (uint32_t)((at + k) % C::kStages) * C::kStage, (i & 1) * kTileKeys, r);
                     }
                     bool tainted = false;
-                    if (!(ok = ok && group_any(wait, bars, m, votes, bad != 0, tainted))) break;
+                    if (!(ok = ok && group_any(wait, bars, m, votes, !numbers, tainted))) break;
                     if (tainted) {
-                        if (!(ok = i == 0 || warp_wait(wait, &bars.pv_done[m], (n_pv + i - 1) & 1))) break;
+                        if (!(ok = i == 0 || ended(i - 1))) break;
                         tc_fence_after();
-                        add_masked<KIND, D>(t_s, t_o, ring, at, bits, i == 0);
+                        add_masked<KIND, D>(t_s, t_o, ring, at, (i & 1) * kTileKeys, bits[0], bits[1], i == 0);
                     }
-                    if (r == 0) bars.skip[which] = tainted;
+                    if (r == 0) bars.skip[m][place] = tainted;
                 } else if (r == 0) {
-                    bars.skip[which] = 0;
+                    bars.skip[m][place] = 0;
                 }
-                // the product before this one has ended, as S by turns does not say: a wait tells a product's end from the one before only
-                if (i > 0 && !(ok = warp_wait(wait, &bars.pv_done[m], (n_pv + i - 1) & 1))) break;
                 tc_fence_before();
-                mbar_arrive(&bars.p_full[which]);
+                mbar_arrive(&bars.p_full[m][place]);
             }
             if (!ok) break;
             if (n > 0) {
-                if (!(ok = warp_wait(wait, &bars.pv_done[m], (n_pv + n - 1) & 1))) break;
+                if (!(ok = warp_wait(wait, &bars.pv_done[m][(done + n - 1) & 1], (done + n - 1) >> 1 & 1))) break;
                 tc_fence_after();
             }
-            stage += 2 * C::kParts * n;
-            tiles += n;
+            stage += 2 * C::kParts * ((n + 1) / 2);
+            loads += (n + 1) / 2;
             units += n > 0;
-            n_pv += n;
+            done += n;
             // ---- the row's end in this CTA
             const bool there = r < rows;
             if (walk.whole()) {
