@@ -1,6 +1,6 @@
 // k_paged_prefill.cu -- softmax attention of new tokens over the paged cache: the plan before the attention
 // kernels, and the join of rows that were cut between CTAs after them (paged_prefill.cuh has the scheme).
-#include "paged_prefill.cuh"
+#include "paged_prefill_tc.cuh"
 
 namespace gdn {
 namespace prefill {
@@ -197,7 +197,16 @@ cudaError_t launch_paged_prefill(const PrefillArgs &args, cudaStream_t stream) {
     const int tile = row_tile(a.c.dtype, a.c.d), grid = kMaxCtas;
     cudaError_t e = launch_kernel(false, plan_kernel, 1, kPlanThreads, 0, stream, a, tile, key_tile(a.c.dtype), grid);
     if (e != cudaSuccess) return e;
-    e = a.c.dtype == GDN_BF16 ? launch_bf16(a, grid, stream) : a.c.dtype == GDN_E4M3 ? launch_e4m3(a, grid, stream) : launch_f32(a, grid, stream);
+    if (a.c.dtype == GDN_F32) {
+        e = launch_f32(a, grid, stream);
+    } else {
+        // tokens of a page that lie together in every tile of 64 keys: a TMA box from 8 on, the rows of a swizzle pattern
+        int box = 64;
+        while (a.c.page % box) box /= 2;
+        CUtensorMap maps[2];
+        const bool tma = box >= 8 && a.max_pages > 0 && make_tmap_cache(&maps[0], a.c, a.c.k, box) && make_tmap_cache(&maps[1], a.c, a.c.v, box);
+        e = a.c.dtype == GDN_BF16 ? (tma ? launch_bf16_tma : launch_bf16)(a, grid, box, maps, stream) : (tma ? launch_e4m3_tma : launch_e4m3)(a, grid, box, maps, stream);
+    }
     if (e != cudaSuccess) return e;
     const int dims = kJoinThreads / kJoinRows * 8;
     const int64_t rows = (int64_t)a.n * (a.Hq / a.c.Hkv);

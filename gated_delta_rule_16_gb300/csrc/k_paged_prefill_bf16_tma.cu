@@ -1,0 +1,12 @@
+// k_paged_prefill_bf16_tma.cu -- softmax attention of new tokens over the paged cache: the tensor-core kernel for bf16 caches, keys and values by TMA.
+#include "paged_prefill_tc.cuh"
+
+namespace gdn {
+namespace prefill {
+
+cudaError_t launch_bf16_tma(const PrefillArgs &a, int grid, int box, const CUtensorMap (&maps)[2], cudaStream_t stream) {
+    return launch_tc<GDN_BF16, true>(a, grid, box, maps, stream);
+}
+
+}  // namespace prefill
+}  // namespace gdn

@@ -9,6 +9,8 @@
 // has the same number of tiles, and one row over 131072 is shared by all of them.
 #pragma once
 
+#include <cuda.h>
+
 #include "paged.cuh"
 
 namespace gdn {
@@ -114,8 +116,10 @@ struct Walk {
 };
 
 // prefill kernels: a.ws holds the View; launched as programmatic dependents of the plan
-cudaError_t launch_bf16(const PrefillArgs &a, int grid, cudaStream_t stream);
-cudaError_t launch_e4m3(const PrefillArgs &a, int grid, cudaStream_t stream);
+cudaError_t launch_bf16(const PrefillArgs &a, int grid, int box, const CUtensorMap (&maps)[2], cudaStream_t stream);
+cudaError_t launch_bf16_tma(const PrefillArgs &a, int grid, int box, const CUtensorMap (&maps)[2], cudaStream_t stream);
+cudaError_t launch_e4m3(const PrefillArgs &a, int grid, int box, const CUtensorMap (&maps)[2], cudaStream_t stream);
+cudaError_t launch_e4m3_tma(const PrefillArgs &a, int grid, int box, const CUtensorMap (&maps)[2], cudaStream_t stream);
 cudaError_t launch_f32(const PrefillArgs &a, int grid, cudaStream_t stream);
 
 }  // namespace prefill

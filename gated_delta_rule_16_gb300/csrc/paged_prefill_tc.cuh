@@ -9,8 +9,11 @@
 //   warps 0-3, 4-7   softmax of the unit's first and second 128 rows, a thread per row.  Each has two S tiles: the tensor core makes
 //                    one while the other is worked on, so that neither waits for the other's latency (with one S tile of 128 keys a
 //                    tile took 4600 clocks of 2048 in the tensor core);
-//   warps 8-11       copy keys and values into a ring of shared memory, in the 128-byte swizzle, 16 bytes at a time by cp.async: any
-//                    page size and any strides cost the same, and what is not attended to is filled with zeros;
+//   warp 14          copies keys and values into a ring of shared memory, in the 128-byte swizzle, by TMA: one box to a slab and as many tokens
+//                    as lie together whatever the page (16 for pages of 16 or 48, 64 for pages of 64).  8-bit values go to a ring of their own,
+//                    from which warps 8-11 convert them to f16;
+//   warps 8-11       load q.  Pages of which no 8 tokens lie together (pages of 1, say) are copied by them, 16 bytes at a time by cp.async, at
+//                    a sixth of the tokens per instruction;
 //   warps 12, 13     issue the products of the first and second row tile.  Between two batches of MMAs a warp has some tens of
 //                    instructions to go through, which beside the busy softmax warps take hundreds of clocks, more than the tensor core has queued:
 //                    the other warp's batches fill the gap.
@@ -21,6 +24,7 @@
 
 #include "paged_prefill.cuh"
 #include "tc.cuh"
+#include "tmap.cuh"
 
 namespace gdn {
 namespace prefill {
@@ -54,6 +58,11 @@ struct Cfg {
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool real) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void tma_load_4d_at(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+                 : "memory");
 }
 __device__ __forceinline__ void mma_commit_at(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -169,6 +178,7 @@ struct Waiter {
 struct Bars {
     static constexpr int kMaxStages = 10;
     uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t raw_full[8], raw_empty[8];  // of 8-bit stages
     uint64_t q_full, q_empty;
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // of a group's two S tiles
     uint64_t joint[2], drain[2];    // joint: a group's votes
@@ -206,20 +216,26 @@ __device__ __forceinline__ uint32_t range_bits(int part, int kb, int lo, int hi)
 }
 
 // Whether half of a key's values in a ring stage are finite: thread r of a group has key r % 64 of a tile's, and its first or second half.
-// Values that only some rows attend to have to be.
+// Values that only some rows attend to have to be; those of a key that none does (`live` false) become zeros.
 template <gdn_dtype KIND, int D>
-__device__ __noinline__ bool all_numbers(uint32_t stage, int key0, int r) {
+__device__ __noinline__ bool all_numbers(uint32_t stage, int key0, int r, bool live) {
     using C = Cfg<KIND, D>;
     uint32_t bad = 0;
 #pragma unroll 4
     for (int e = 0; e < C::kDims / 16; ++e) {
         const int piece = (r >> 6) * (C::kDims / 16) + e;
-        uint32_t x[4];
-        lds128(x, stage + piece / 8 * kSlab + sw128_offset(key0 + (r & 63), piece % 8 * 8));
+        const uint32_t at = stage + piece / 8 * kSlab + sw128_offset(key0 + (r & 63), piece % 8 * 8);
+        if (live) {
+            uint32_t x[4];
+            lds128(x, at);
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
-            bad |= C::kE4M3 ? ((x[w] & 0x7c007c00u) + 0x04000400u) & 0x80008000u : ((x[w] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+            for (int w = 0; w < 4; ++w)
+                bad |= C::kE4M3 ? ((x[w] & 0x7c007c00u) + 0x04000400u) & 0x80008000u : ((x[w] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+        } else {
+            sts128(at, 0, 0, 0, 0);
+        }
     }
+    if (!live) fence_async_smem();
     return bad == 0;
 }
 
@@ -279,8 +295,9 @@ __device__ __noinline__ void add_masked(uint32_t t_p, uint32_t t_o, const uint8_
     }
 }
 
-template <gdn_dtype KIND, int D>
-__global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) {
+// TMA: keys and values come by TMA, in boxes of `box` tokens of one page.
+template <gdn_dtype KIND, int D, bool TMA>
+__global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, int box) {
     using C = Cfg<KIND, D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     Bars &bars = *reinterpret_cast<Bars *>(smem + C::kSmem);
@@ -293,8 +310,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
 
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(&bars.full[i], C::kE4M3 ? 128 : 128 + 4);
+            mbar_init(&bars.full[i], C::kE4M3 ? 128 : TMA ? 1 : 128 + 4);
             mbar_init(&bars.empty[i], C::kTiles);
+        }
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(&bars.raw_full[i], 1);
+            mbar_init(&bars.raw_empty[i], 128);
         }
         mbar_init(&bars.q_full, 128);
         mbar_init(&bars.q_empty, C::kTiles);
@@ -336,6 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
         // e4m3: 8-bit values of the oldest stage become f16; a thread reads what it copied itself
         auto convert = [&] {
             const int n = stage_out;
+            if (TMA && !warp_wait(wait, &bars.raw_full[n % (C::kRaw ? C::kRaw : 1)], n / (C::kRaw ? C::kRaw : 1) & 1)) return false;
             if (!free_stage(n)) return false;
             const uint32_t from = raw_at + n % (C::kRaw ? C::kRaw : 1) * C::kRawStage, to = ring_at + n % C::kStages * C::kStage;
 #pragma unroll
@@ -349,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
             }
             fence_async_smem();
             mbar_arrive(&bars.full[n % C::kStages]);
+            if (TMA) mbar_arrive(&bars.raw_empty[n % (C::kRaw ? C::kRaw : 1)]);
             ++stage_out;
             return true;
         };
@@ -377,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
             }
         };
         auto settle = [&] {  // e4m3: everything issued has been converted
-            if constexpr (C::kE4M3) {
+            if constexpr (C::kE4M3 && !TMA) {
                 cp_wait<0>();
                 while (stage_out < stage_in)
                     if (!convert()) return false;
@@ -438,6 +461,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
                 cell = key - page * a.c.page;
                 return key >= lo && key <= end ? table[page] : -1;
             };
+            if constexpr (TMA) {
+                // bf16: q is all there is to do; e4m3: the unit's stages too, q after the first keys
+                for (int i = 0; ok && i < (C::kE4M3 ? 2 * C::kParts * n : 1); ++i) {
+                    if (i == (C::kE4M3 ? C::kParts : 0) && !(ok = load_q(u, walk.h))) break;
+                    if constexpr (C::kE4M3) ok = convert();
+                }
+                continue;
+            }
             int cell_next, page_next = entry(begin + pt, cell_next);
             for (int t = 0; ok && t < n; ++t) {
                 const int page = page_next, cell = cell_next;
@@ -474,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
             // copies by cp.async and the tensor core see shared memory through different proxies
             auto ready = [&](uint32_t bar, uint32_t parity) {
                 if (!warp_wait(wait, bar, parity)) return false;
-                if constexpr (!C::kE4M3) fence_async_smem();
+                if constexpr (!C::kE4M3 && !TMA) fence_async_smem();
                 return true;
             };
             auto commit = [&](uint32_t bar) {
@@ -552,7 +583,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
                 for (int i = 0; i <= n; ++i) {
                     if (i < n) {
                         if (!(i & 1) && !(ok = stages_ready(k_place))) break;
-                        if (i == 0 && !(ok = ready(smem_addr(&bars.q_full), units & 1))) break;
+                        if (i == 0) {
+                            if (!(ok = warp_wait(wait, smem_addr(&bars.q_full), units & 1))) break;
+                            if constexpr (!C::kE4M3) fence_async_smem();  // q is copied by cp.async
+                        }
                         tc_fence_after();
                         qk((done + i) & 1, i & 1);
                         if ((i & 1) || i == n - 1) {
@@ -576,6 +610,63 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
             }
             commit(smem_addr(&bars.drain[m]));
             mbar_wait(&bars.drain[m], 0);
+        }
+        if (TMA && warp == 14) {
+            // ---- copies by TMA ----------------------------------------------------------------------------
+            constexpr int kRing = C::kE4M3 ? C::kRaw : C::kStages;
+            constexpr uint32_t kBytes = C::kE4M3 ? C::kRawStage : C::kStage;
+            const int boxes = 128 / box, shift = 31 - __clz(box);
+            const uint32_t ring_at = smem_addr(ring) + (C::kE4M3 ? C::kStages * C::kStage : 0);
+            int slot = 0, tiles = 0;
+            uint32_t turn = 0;
+            bool ok = true;
+            while (ok && walk.next()) {
+                const Unit u = walk.u;
+                if (walk.t0 == walk.t1) continue;
+                const int first = u.first + u.row / group, last = u.first + (u.row + u.rows - 1) / group;
+                const int lo = reach_of((int64_t)first + u.shift, a.window, room).lo, hi = reach_of((int64_t)last + u.shift, a.window, room).hi;
+                const int32_t *table = a.table + u.b * a.table_stride;
+                const int begin = u.key + kTileKeys * walk.t0, end = min(hi, u.key + kTileKeys * walk.t1 - 1), n = (walk.t1 - walk.t0 + 1) / 2;
+                // lane l has the l-th box of 128 keys
+                auto entry = [&](int key, int &cell) {
+                    const int page = key / a.c.page;
+                    cell = key - page * a.c.page;
+                    return lane < boxes && key + box > lo && key <= end ? table[page] : -1;
+                };
+                int cell_next, page_next = entry(begin + lane * box, cell_next);
+                for (int t = 0; ok && t < n; ++t) {
+                    const int cell = cell_next, page = page_next >= 0 && page_next < a.c.pages ? page_next : -1;  // outside the pool TMA fills with zeros
+                    if (t + 1 < n) page_next = entry(begin + 128 * (t + 1) + lane * box, cell_next);
+                    const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t word = __ballot_sync(0xffffffffu, there >> ((32 * c + lane) >> shift) & 1) & range_bits(c, begin + 128 * t, lo, end);
+                        if (lane == 0) bars.words[tiles % kWords][c] = word;
+                    }
+                    ++tiles;
+#pragma unroll 1
+                    for (int part = 0; part < 2 * C::kParts; ++part) {
+                        uint64_t *bar = C::kE4M3 ? &bars.raw_full[slot] : &bars.full[slot];
+                        if (turn > 0 && !(ok = warp_wait(wait, C::kE4M3 ? &bars.raw_empty[slot] : &bars.empty[slot], (turn - 1) & 1))) break;
+                        if (lane == 0) mbar_arrive_expect_tx(bar, kBytes);
+                        __syncwarp();
+                        if (lane < boxes) {
+                            const CUtensorMap *map = part < C::kParts ? &k_map : &v_map;
+                            const int x = part % C::kParts * C::kDims;
+                            const uint32_t dst = ring_at + slot * kBytes + lane * box * (C::kE4M3 ? C::kDims : 128);
+#pragma unroll
+                            for (int slab = 0; slab < (C::kE4M3 ? 1 : C::kSlabs); ++slab) tma_load_4d_at(dst + slab * kSlab, map, x + 64 * slab, cell, walk.h, page, smem_addr(bar));
+                        }
+                        if (++slot == kRing) slot = 0, ++turn;
+                    }
+                }
+            }
+            // what was asked for has to arrive before the memory may go
+            for (int i = 0; i < kRing; ++i) {
+                const int s = (slot + i) % kRing;
+                const uint32_t last = turn - (s >= slot);  // of the slot's turns
+                if (turn > 0 || s < slot) warp_wait(wait, C::kE4M3 ? &bars.raw_full[s] : &bars.full[s], last & 1);
+            }
         }
         __syncwarp();
     } else {
@@ -687,9 +778,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
                 if (__builtin_expect(edge, 0)) {
                     const int at = stage + 2 * C::kParts * (i >> 1) + C::kParts;
                     bool numbers = true;
+                    const bool live = bars.words[(loads + (i >> 1)) % kWords][2 * (i & 1) + (r >> 5 & 1)] >> (r & 31) & 1;
                     for (int k = 0; ok && k < C::kParts; ++k) {
                         ok = warp_wait(wait, &bars.full[(at + k) % C::kStages], (at + k) / C::kStages & 1);
-                        numbers = numbers && all_numbers<KIND, D>(smem_addr(ring) + (uint32_t)((at + k) % C::kStages) * C::kStage, (i & 1) * kTileKeys, r);
+                        numbers = numbers && all_numbers<KIND, D>(smem_addr(ring) + (uint32_t)((at + k) % C::kStages) * C::kStage, (i & 1) * kTileKeys, r, live);
                     }
                     bool tainted = false;
                     if (!(ok = ok && group_any(wait, bars, m, votes, !numbers, tainted))) break;
@@ -760,25 +852,43 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a) 
     }
 }
 
-template <gdn_dtype KIND, int D>
-cudaError_t launch_tc(const PrefillArgs &a, int grid, cudaStream_t stream) {
+// A cache tensor as a map of (dim, cell, head, page), boxes of `box` cells and the dims of a swizzled row, or of an 8-bit stage.
+inline bool make_tmap_cache(CUtensorMap *map, const gdn_kv_cache &c, const void *base, int box) {
+    auto enc = tmap_encoder();
+    if (!enc) return false;
+    const int bytes = c.dtype == GDN_E4M3 ? 1 : 2;
+    const cuuint64_t dims[4] = {(cuuint64_t)c.d, (cuuint64_t)c.page, (cuuint64_t)c.Hkv, (cuuint64_t)c.pages};
+    const int64_t step[3] = {c.stride_token, c.stride_head, c.stride_page};
+    cuuint64_t strides[3];
+    for (int i = 0; i < 3; ++i) {
+        strides[i] = (cuuint64_t)(dims[i + 1] == 1 ? c.d : step[i]) * bytes;  // of one element any will do
+        if (strides[i] == 0 || strides[i] >> 40) return false;
+    }
+    const cuuint32_t boxes[4] = {(cuuint32_t)(bytes == 1 ? (c.d < 128 ? c.d : 128) : 64), (cuuint32_t)box, 1, 1}, each[4] = {1, 1, 1, 1};
+    return enc(map, bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, boxes, each,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, bytes == 1 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <gdn_dtype KIND, int D, bool TMA>
+cudaError_t launch_tc(const PrefillArgs &a, int grid, int box, const CUtensorMap (&maps)[2], cudaStream_t stream) {
     using C = Cfg<KIND, D>;
     constexpr int kSmem = (int)(C::kSmem + sizeof(Bars));
     // the warp groups' shares of registers are what a block of 128 to a thread has: with fewer they would wait for ever
     static const int regs = [] {
         cudaFuncAttributes attr;
-        return cudaFuncGetAttributes(&attr, prefill_tc_kernel<KIND, D>) == cudaSuccess ? attr.numRegs : 0;
+        return cudaFuncGetAttributes(&attr, prefill_tc_kernel<KIND, D, TMA>) == cudaSuccess ? attr.numRegs : 0;
     }();
     if (regs != 128) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<KIND, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    return e != cudaSuccess ? e : launch_kernel(true, prefill_tc_kernel<KIND, D>, grid, kThreads, kSmem, stream, a);
+    const cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<KIND, D, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    return e != cudaSuccess ? e : launch_kernel(true, prefill_tc_kernel<KIND, D, TMA>, grid, kThreads, kSmem, stream, a, maps[0], maps[1], box);
 }
-template <gdn_dtype KIND>
-cudaError_t launch_tc(const PrefillArgs &a, int grid, cudaStream_t stream) {
+template <gdn_dtype KIND, bool TMA>
+cudaError_t launch_tc(const PrefillArgs &a, int grid, int box, const CUtensorMap (&maps)[2], cudaStream_t stream) {
     switch (a.c.d) {
-        case 64: return launch_tc<KIND, 64>(a, grid, stream);
-        case 128: return launch_tc<KIND, 128>(a, grid, stream);
-        default: return launch_tc<KIND, 256>(a, grid, stream);
+        case 64: return launch_tc<KIND, 64, TMA>(a, grid, box, maps, stream);
+        case 128: return launch_tc<KIND, 128, TMA>(a, grid, box, maps, stream);
+        default: return launch_tc<KIND, 256, TMA>(a, grid, box, maps, stream);
     }
 }
 
