@@ -179,7 +179,7 @@ struct Bars {
     static constexpr int kMaxStages = 10;
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t raw_full[8], raw_empty[8];  // of 8-bit stages
-    uint64_t q_full, q_empty;
+    uint64_t q_full[2], q_empty[2];  // of a row tile
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // of a group's two S tiles
     uint64_t joint[2], drain[2];    // joint: a group's votes
     uint32_t words[kWords][4];      // real keys of a stage
@@ -206,6 +206,20 @@ __device__ __forceinline__ bool group_any(const Waiter &wait, Bars &bars, int gr
     if ((threadIdx.x & 127) == 0) *(volatile int *)&bars.vote[group][(turn + 2) % 3] = 0;
     ++turn;
     return ok;
+}
+
+// Four lanes' 16-byte pieces of four rows change places: lane q of the four gets piece q of each of their rows.
+__device__ __forceinline__ void transpose4(uint4 (&a)[4], int lane) {
+    auto swap = [&](uint4 x, int with) {
+        return make_uint4(__shfl_xor_sync(0xffffffffu, x.x, with), __shfl_xor_sync(0xffffffffu, x.y, with), __shfl_xor_sync(0xffffffffu, x.z, with),
+                          __shfl_xor_sync(0xffffffffu, x.w, with));
+    };
+    auto pick = [](bool first, const uint4 &x, const uint4 &y) { return make_uint4(first ? x.x : y.x, first ? x.y : y.y, first ? x.z : y.z, first ? x.w : y.w); };
+    const bool odd = lane & 1, high = lane & 2;
+    uint4 x = swap(pick(odd, a[0], a[1]), 1), y = swap(pick(odd, a[2], a[3]), 1);
+    a[0] = pick(odd, x, a[0]), a[1] = pick(odd, a[1], x), a[2] = pick(odd, y, a[2]), a[3] = pick(odd, a[3], y);
+    x = swap(pick(high, a[0], a[2]), 2), y = swap(pick(high, a[1], a[3]), 2);
+    a[0] = pick(high, x, a[0]), a[2] = pick(high, a[2], x), a[1] = pick(high, y, a[1]), a[3] = pick(high, a[3], y);
 }
 
 // Bits of keys kb + 32 part .. inside [lo, hi].
@@ -317,8 +331,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
             mbar_init(&bars.raw_full[i], 1);
             mbar_init(&bars.raw_empty[i], 128);
         }
-        mbar_init(&bars.q_full, 128);
-        mbar_init(&bars.q_empty, C::kTiles);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.q_full[i], 128);
+            mbar_init(&bars.q_empty[i], 1);
+        }
         for (int i = 0; i < 2; ++i) {
             for (int j = 0; j < 2; ++j) {
                 mbar_init(&bars.s_full[i][j], 1);
@@ -350,7 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
         const int pt = tid - 256, pw = pt >> 5;
         constexpr int kChunks = C::kDims * (C::kE4M3 ? 1 : 2) / 16, kAtOnce = 32 / kChunks, kSteps = 32 / kAtOnce;  // 16-byte pieces of a row; rows per copy
         const int chunk = lane % kChunks, sub = lane / kChunks;
-        int stage_in = 0, stage_out = 0, units = 0, tiles = 0;  // stages issued, stages converted (e4m3)
+        int stage_in = 0, stage_out = 0, tiles = 0;  // stages issued, stages converted (e4m3)
+        int units = 0, units1 = 0;                    // units, and those with a second row tile
         bool ok = true;
         const uint32_t ring_at = smem_addr(ring), raw_at = smem_addr(ring + C::kStages * C::kStage);
         auto free_stage = [&](int n) { return n < C::kStages || warp_wait(wait, &bars.empty[n % C::kStages], (n / C::kStages - 1) & 1); };
@@ -407,46 +424,56 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
             }
             return true;
         };
-        // the unit's rows of q; rows behind its last are zeros
+        // the unit's rows of q, a tile of 128 after the other; rows behind the last are zeros.  A row is (token, head of the group): a lane
+        // counts its own up instead of dividing for each, which made a unit's beginning 6 us longer
+        constexpr int kLanes = D / 8, kRowStep = 4 * (32 / kLanes);  // 16 bytes to a lane; rows that the warps have at a time
+        const int piece = lane % kLanes, step_token = kRowStep / group, step_head = kRowStep % group;
+        const int64_t step = step_token * a.q_tok + step_head * a.q_head, carry = a.q_tok - group * a.q_head;
         auto load_q = [&](const Unit &u, int h) {
             if (!settle()) return false;
-            if (units > 0 && !warp_wait(wait, &bars.q_empty, (units - 1) & 1)) return false;
-            constexpr int kLanes = D / 8, kGo = 32 / kLanes;  // 16 bytes to a lane; rows that a warp has at a time
-            const int rows = u.rows <= 128 ? 128 : 128 * C::kTiles;
-            const int piece = lane % kLanes;
+            int r = pw * (32 / kLanes) + lane / kLanes, head = (u.row + r) % group;
+            const uint16_t *src = (const uint16_t *)a.q + ((int64_t)u.first + (u.row + r) / group) * a.q_tok + (int64_t)(h * group + head) * a.q_head + 8 * piece;
+#pragma unroll 1
+            for (int m = 0; m < C::kTiles && 128 * m < u.rows; ++m) {
+                const int uses = m ? units1 : units;
+                if (uses > 0 && !warp_wait(wait, &bars.q_empty[m], (uses - 1) & 1)) return false;
+                const uint32_t dst = smem_addr(q_smem) + m * C::kQTile + piece / 8 * kSlab;
 #pragma unroll 4
-            for (int r = pw * kGo + lane / kLanes; r < rows; r += 4 * kGo) {
-                const int rr = u.row + min(r, u.rows - 1);
-                const uint8_t *src = (const uint8_t *)a.q + 2 * (((int64_t)u.first + rr / group) * a.q_tok + (int64_t)(h * group + rr % group) * a.q_head) + 16 * piece;
-                const uint32_t dst = smem_addr(q_smem) + r / 128 * C::kQTile + piece / 8 * kSlab + sw128_offset(r % 128, piece % 8 * 8);
-                if constexpr (!C::kE4M3) {
-                    cp16(dst, src, r < u.rows);
+                for (int i = 0; i < 128 / kRowStep; ++i, r += kRowStep) {
+                    const bool there = r < u.rows;
+                    const uint32_t to = dst + sw128_offset(r & 127, piece % 8 * 8);
+                    if constexpr (!C::kE4M3) {
+                        cp16(to, there ? src : (const uint16_t *)a.q, there);
+                    } else {
+                        // f16 of q times a power of two that takes the row's largest to 2^14 or so: 8 bits of any value down to 2^-30 of it,
+                        // and what it loses below is lost in the fp32 sum too
+                        const uint4 x = there ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                        uint32_t most = 0;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) most = max(most, max(w[j] & 0x7fffu, w[j] >> 16 & 0x7fffu));
+#pragma unroll
+                        for (int off = kLanes / 2; off; off >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
+                        const int e = min((int)(most >> 7), 254), lift = min(141 - e, 126);
+                        const float f = __uint_as_float((uint32_t)(127 + lift) << 23);
+                        uint32_t y[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) y[j] = pack_f16x2(__uint_as_float(w[j] << 16) * f, __uint_as_float(w[j] & 0xffff0000u) * f);
+                        sts128(to, y[0], y[1], y[2], y[3]);
+                        if (piece == 0) bars.row_scale[uses & 1][r] = __uint_as_float((uint32_t)(127 - lift) << 23);
+                    }
+                    src += step;
+                    if ((head += step_head) >= group) head -= group, src += carry;
+                }
+                if constexpr (C::kE4M3) {
+                    fence_async_smem();
+                    mbar_arrive(&bars.q_full[m]);
                 } else {
-                    // f16 of q times a power of two that takes the row's largest to 2^14 or so: 8 bits of any value down to 2^-30 of it,
-                    // and what it loses below is lost in the fp32 sum too
-                    uint4 x = r < u.rows ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t most = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) most = max(most, max(w[i] & 0x7fffu, w[i] >> 16 & 0x7fffu));
-#pragma unroll
-                    for (int off = kLanes / 2; off; off >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
-                    const int e = min((int)(most >> 7), 254), lift = min(141 - e, 126);
-                    const float f = __uint_as_float((uint32_t)(127 + lift) << 23);
-                    uint32_t y[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) y[i] = pack_f16x2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
-                    sts128(dst, y[0], y[1], y[2], y[3]);
-                    if (piece == 0) bars.row_scale[units & 1][r] = __uint_as_float((uint32_t)(127 - lift) << 23);
+                    cp_arrive(&bars.q_full[m]);
                 }
             }
-            if constexpr (C::kE4M3) {
-                fence_async_smem();
-                mbar_arrive(&bars.q_full);
-            } else {
-                cp_arrive(&bars.q_full);
-            }
             ++units;
+            units1 += u.rows > 128;
             return true;
         };
         while (ok && walk.next()) {
@@ -500,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
             const uint32_t full_at = smem_addr(&bars.full), empty_at = smem_addr(&bars.empty), s_at = smem_addr(&bars.s_full), p_at = smem_addr(&bars.p_full),
                            pv_at = smem_addr(&bars.pv_done);
             const int m = warp - 12;
-            int units = 0, done = 0;  // units, and tiles of this group, before this piece; tiles take a group's two places by turns
+            int units = 0, done = 0;  // units and tiles of this row tile before this piece; tiles take a group's two places by turns
             bool ok = true;
             // copies by cp.async and the tensor core see shared memory through different proxies
             auto ready = [&](uint32_t bar, uint32_t parity) {
@@ -540,15 +567,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
                 const int n = walk.t1 - walk.t0;
                 if (n == 0) continue;
                 if (m == 1 && walk.u.rows <= 128) {  // nothing to do but to say so, stage by stage
-                    if (!(ok = warp_wait(wait, smem_addr(&bars.q_full), units & 1))) break;
-                    if (leader) mbar_arrive(&bars.q_empty);
                     for (int i = 0; ok && i < (n + 1) / 2; ++i)
                         for (Place *at : {&k_place, &v_place}) {
                             if (!(ok = warp_wait(wait, full_at + 8 * at->slot, at->parity))) break;
                             if (leader) mbar_arrive(&bars.empty[at->slot]);
                             at->step(2);
                         }
-                    ++units;
                     continue;
                 }
                 // S = Q K^T of a row tile and half of a stage's keys
@@ -584,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
                     if (i < n) {
                         if (!(i & 1) && !(ok = stages_ready(k_place))) break;
                         if (i == 0) {
-                            if (!(ok = warp_wait(wait, smem_addr(&bars.q_full), units & 1))) break;
+                            if (!(ok = warp_wait(wait, smem_addr(&bars.q_full[m]), units & 1))) break;
                             if constexpr (!C::kE4M3) fence_async_smem();  // q is copied by cp.async
                         }
                         tc_fence_after();
@@ -593,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
                             release_stages(k_place);
                             k_place.step(2 * C::kParts);
                         }
-                        if (i == n - 1) commit(smem_addr(&bars.q_empty));
+                        if (i == n - 1) commit(smem_addr(&bars.q_empty[m]));
                     }
                     if (i > 0) {
                         const int j = i - 1;
@@ -684,7 +708,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
             if (m == 1 && !two) {  // the first group has all of it
                 stage += 2 * C::kParts * ((n + 1) / 2);
                 loads += (n + 1) / 2;
-                units += n > 0;
                 continue;
             }
             const int rows = min(128, u.rows - 128 * m);
@@ -813,18 +836,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
                 float inv = none ? 0.f : 1.f / sum;
                 if (a.c.v_scale) inv *= a.c.v_scale[walk.h];
                 const int64_t out = (int64_t)token * a.Hq + head;
-                uint4 *o_at = (uint4 *)((__nv_bfloat16 *)a.o + out * D);
+                // a thread has a row, whose pieces alone would be 32 places to a store: four lanes write 64 bytes of a row together
+                __nv_bfloat16 *to[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int64_t row = __shfl_sync(0xffffffffu, out, (lane & ~3) + k);
+                    to[k] = (lane & ~3) + k + 32 * (warp & 3) < rows ? (__nv_bfloat16 *)a.o + row * D + 8 * (lane & 3) : nullptr;
+                }
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     float o[32];
                     tmem_ld32(t_o + 32 * c, o);
                     tmem_ld_wait();
-                    uint32_t w[16];
+                    uint4 w[4];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) w[j] = none ? 0u : pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv);
-                    if (there)
+                    for (int j = 0; j < 4; ++j)
+                        w[j] = none ? make_uint4(0, 0, 0, 0)
+                                    : make_uint4(pack_bf16x2(o[8 * j] * inv, o[8 * j + 1] * inv), pack_bf16x2(o[8 * j + 2] * inv, o[8 * j + 3] * inv),
+                                                 pack_bf16x2(o[8 * j + 4] * inv, o[8 * j + 5] * inv), pack_bf16x2(o[8 * j + 6] * inv, o[8 * j + 7] * inv));
+                    transpose4(w, lane);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) o_at[4 * c + j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                    for (int k = 0; k < 4; ++k)
+                        if (to[k]) *(uint4 *)(to[k] + 32 * c) = w[k];
                 }
                 if (there && a.lse) a.lse[out] = none ? -INFINITY : (ref - C::kShift + log2f(sum)) * 0.6931471805599453f;
             } else {
