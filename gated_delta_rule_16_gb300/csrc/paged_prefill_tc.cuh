@@ -14,9 +14,10 @@
 //                    from which warps 8-11 convert them to f16;
 //   warps 8-11       load q.  Pages of which no 8 tokens lie together (pages of 1, say) are copied by them, 16 bytes at a time by cp.async, at
 //                    a sixth of the tokens per instruction;
-//   warps 12, 13     issue the products of the first and second row tile.  Between two batches of MMAs a warp has some tens of
-//                    instructions to go through, which beside the busy softmax warps take hundreds of clocks, more than the tensor core has queued:
-//                    the other warp's batches fill the gap.
+//   warps 12, 13     issue the scores' products of the first and second row tile, warp 15 those with the values.  Between two batches of MMAs
+//                    a warp has some tens of instructions to go through, which beside the busy softmax warps take hundreds of clocks,
+//                    more than the tensor core has queued: the other warps' batches fill the gap.  (One warp for all of them: a pair of tiles
+//                    took 2900 clocks; a warp for each row tile 2100.)
 // With 256 dims O fills the tensor memory of two row tiles, and a unit has one.
 #pragma once
 
@@ -181,7 +182,7 @@ struct Bars {
     uint64_t raw_full[8], raw_empty[8];  // of 8-bit stages
     uint64_t q_full[2], q_empty[2];  // of a row tile
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // of a group's two S tiles
-    uint64_t joint[2], drain[2];    // joint: a group's votes
+    uint64_t joint[2], drain[3];    // joint: a group's votes
     uint32_t words[kWords][4];      // real keys of a stage
     float row_scale[2][256];        // e4m3: of q's rows, by turns
     int vote[2][3];                 // of a group, by turns
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
             mbar_init(&bars.joint[i], 128);
             for (int j = 0; j < 3; ++j) bars.vote[i][j] = 0;
         }
-        for (int i = 0; i < 2; ++i) mbar_init(&bars.drain[i], 1);
+        for (int i = 0; i < 3; ++i) mbar_init(&bars.drain[i], 1);
         bars.gave_up = 0;
         fence_mbar_init();
     }
@@ -517,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
     } else if (warpgroup == 3) {
         // ---- products -------------------------------------------------------------------------------------
         regs_less<48>();
-        if (warp < 12 + C::kTiles) {
+        if (warp < 12 + C::kTiles || warp == 15) {
             // the whole warp goes along, so that descriptors are uniform values, and one lane issues: with one lane in a branch of
             // its own an MMA took four times as long to issue as to run
             const bool leader = elect_one();
@@ -526,8 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
             const uint64_t q_desc = kmajor_desc(smem_addr(q_smem), 0, kSlab), k_desc = kmajor_desc(smem_addr(ring), 0, kSlab), v_desc = mnmajor_desc(smem_addr(ring), 0, kSlab);
             const uint32_t full_at = smem_addr(&bars.full), empty_at = smem_addr(&bars.empty), s_at = smem_addr(&bars.s_full), p_at = smem_addr(&bars.p_full),
                            pv_at = smem_addr(&bars.pv_done);
-            const int m = warp - 12;
-            int units = 0, done = 0;  // units and tiles of this row tile before this piece; tiles take a group's two places by turns
+            int units = 0, done[2] = {0, 0};  // units, and tiles of a row tile, before this piece; tiles take a row tile's two places by turns
             bool ok = true;
             // copies by cp.async and the tensor core see shared memory through different proxies
             auto ready = [&](uint32_t bar, uint32_t parity) {
@@ -555,85 +555,93 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
                 }
                 return there;
             };
-            auto release_stages = [&](Place at) {
-                commit(empty_at + 8 * at.slot);
-                if constexpr (C::kParts == 2) {
+            auto release_stages = [&](Place at, int times) {
+#pragma unroll
+                for (int part = 0; part < C::kParts; ++part) {
+                    for (int i = 0; i < times; ++i) commit(empty_at + 8 * at.slot);
                     at.step(1);
-                    commit(empty_at + 8 * at.slot);
                 }
             };
-            Place k_place = {0, 0}, v_place = {C::kParts, 0};
-            while (ok && walk.next()) {
-                const int n = walk.t1 - walk.t0;
-                if (n == 0) continue;
-                if (m == 1 && walk.u.rows <= 128) {  // nothing to do but to say so, stage by stage
-                    for (int i = 0; ok && i < (n + 1) / 2; ++i)
-                        for (Place *at : {&k_place, &v_place}) {
-                            if (!(ok = warp_wait(wait, full_at + 8 * at->slot, at->parity))) break;
-                            if (leader) mbar_arrive(&bars.empty[at->slot]);
-                            at->step(2);
+            if (warp < 15) {
+                const int m = warp - 12;
+                Place at = {0, 0};
+                while (ok && walk.next()) {
+                    const int n = walk.t1 - walk.t0;
+                    if (n == 0) continue;
+                    if (m == 1 && walk.u.rows <= 128) {  // nothing to do but to say so, stage by stage
+                        for (int i = 0; ok && i < (n + 1) / 2; ++i) {
+                            if (!(ok = warp_wait(wait, full_at + 8 * at.slot, at.parity))) break;
+                            if (leader) mbar_arrive(&bars.empty[at.slot]);
+                            at.step(2);
                         }
-                    continue;
-                }
-                // S = Q K^T of a row tile and half of a stage's keys
-                auto qk = [&](int place, int half) {
-                    Place at = k_place;
-#pragma unroll
-                    for (int part = 0; part < C::kParts; ++part) {
-                        const uint64_t k = k_desc + (uint32_t)(at.slot * (int)(C::kStage >> 4) + half * (int)(kSlab >> 5));
-#pragma unroll
-                        for (int slab = 0; slab < C::kSlabs; ++slab)
-                            mma4_ss(leader, tmem + 128 * m + 64 * place, q_desc + ((m * C::kQTile + (part * C::kSlabs + slab) * kSlab) >> 4), k + (slab * kSlab >> 4), id_qk, part + slab > 0);
-                        at.step(1);
+                        continue;
                     }
-                    commit(s_at + 16 * m + 8 * place);
-                };
-                auto pv = [&](int tile, int half, bool more) {
-                    const int place = tile & 1;
-                    if (!warp_wait(wait, p_at + 16 * m + 8 * place, tile >> 1 & 1)) return false;
-                    tc_fence_after();
-                    if (!*(volatile int *)&bars.skip[m][place]) {
-                        Place at = v_place;
-#pragma unroll
-                        for (int part = 0; part < C::kParts; ++part) {
-                            mma4_ts(leader, tmem + C::kO + m * D + part * C::kDims, tmem + 128 * m + 64 * place, v_desc + (uint32_t)(at.slot * (int)(C::kStage >> 4) + half * (int)(kSlab >> 5)), id_pv, more);
-                            at.step(1);
-                        }
-                    }
-                    commit(pv_at + 16 * m + 8 * place);
-                    return true;
-                };
-                // the scores of a tile are asked for before the weights of the one before are waited for
-                for (int i = 0; i <= n; ++i) {
-                    if (i < n) {
-                        if (!(i & 1) && !(ok = stages_ready(k_place))) break;
+#pragma unroll 1
+                    for (int i = 0; i < n; ++i) {
+                        const int tile = done[0] + i, place = tile & 1, half = i & 1;
+                        if (!half && !(ok = stages_ready(at))) break;
                         if (i == 0) {
                             if (!(ok = warp_wait(wait, smem_addr(&bars.q_full[m]), units & 1))) break;
                             if constexpr (!C::kE4M3) fence_async_smem();  // q is copied by cp.async
                         }
+                        // the weights that lie over the scores of two tiles before have been used
+                        if (tile >= 2 && !(ok = warp_wait(wait, pv_at + 16 * m + 8 * place, ((tile >> 1) - 1) & 1))) break;
                         tc_fence_after();
-                        qk((done + i) & 1, i & 1);
-                        if ((i & 1) || i == n - 1) {
-                            release_stages(k_place);
-                            k_place.step(2 * C::kParts);
+                        Place from = at;
+#pragma unroll
+                        for (int part = 0; part < C::kParts; ++part) {
+                            const uint64_t k = k_desc + (uint32_t)(from.slot * (int)(C::kStage >> 4) + half * (int)(kSlab >> 5));
+#pragma unroll
+                            for (int slab = 0; slab < C::kSlabs; ++slab)
+                                mma4_ss(leader, tmem + 128 * m + 64 * place, q_desc + ((m * C::kQTile + (part * C::kSlabs + slab) * kSlab) >> 4), k + (slab * kSlab >> 4), id_qk, part + slab > 0);
+                            from.step(1);
                         }
-                        if (i == n - 1) commit(smem_addr(&bars.q_empty[m]));
-                    }
-                    if (i > 0) {
-                        const int j = i - 1;
-                        if (!(j & 1) && !(ok = stages_ready(v_place))) break;
-                        if (!(ok = pv(done + j, j & 1, j > 0))) break;
-                        if ((j & 1) || j == n - 1) {
-                            release_stages(v_place);
-                            v_place.step(2 * C::kParts);
+                        commit(s_at + 16 * m + 8 * place);
+                        if (half || i == n - 1) {
+                            release_stages(at, 1);
+                            at.step(2 * C::kParts);
                         }
                     }
+                    commit(smem_addr(&bars.q_empty[m]));
+                    done[0] += n;
+                    ++units;
                 }
-                done += n;
-                ++units;
+            } else {
+                Place at = {C::kParts, 0};
+                while (ok && walk.next()) {
+                    const int n = walk.t1 - walk.t0, row_tiles = walk.u.rows > 128 ? 2 : 1;
+                    if (n == 0) continue;
+#pragma unroll 1
+                    for (int i = 0; ok && i < n; ++i) {
+                        const int half = i & 1;
+                        if (!half && !(ok = stages_ready(at))) break;
+#pragma unroll
+                        for (int m = 0; m < C::kTiles; ++m) {
+                            if (m >= row_tiles) break;
+                            const int tile = done[m] + i, place = tile & 1;
+                            if (!(ok = warp_wait(wait, p_at + 16 * m + 8 * place, tile >> 1 & 1))) break;
+                            tc_fence_after();
+                            if (!*(volatile int *)&bars.skip[m][place]) {
+                                Place from = at;
+#pragma unroll
+                                for (int part = 0; part < C::kParts; ++part) {
+                                    mma4_ts(leader, tmem + C::kO + m * D + part * C::kDims, tmem + 128 * m + 64 * place, v_desc + (uint32_t)(from.slot * (int)(C::kStage >> 4) + half * (int)(kSlab >> 5)), id_pv, i > 0);
+                                    from.step(1);
+                                }
+                            }
+                            commit(pv_at + 16 * m + 8 * place);
+                        }
+                        if (half || i == n - 1) {
+                            release_stages(at, C::kTiles);
+                            at.step(2 * C::kParts);
+                        }
+                    }
+                    done[0] += n;
+                    if (row_tiles == 2) done[1] += n;
+                }
             }
-            commit(smem_addr(&bars.drain[m]));
-            mbar_wait(&bars.drain[m], 0);
+            commit(smem_addr(&bars.drain[warp == 15 ? 2 : warp - 12]));
+            mbar_wait(&bars.drain[warp == 15 ? 2 : warp - 12], 0);
         }
         if (TMA && warp == 14) {
             // ---- copies by TMA ----------------------------------------------------------------------------
