@@ -74,13 +74,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PrefillArgs a, int t
             const int rows = rows_of(lo, u.first);
             u.row = (int)(i - v.first[lo]) * tile;
             u.rows = min(tile, rows - u.row);
-            const int64_t shift = (int64_t)a.lens[lo] - a.cu[lo + 1];
-            u.shift = (int)max(min(shift, (int64_t)INT32_MAX), (int64_t)INT32_MIN);
-            const Reach r0 = reach_of((int64_t)u.first + u.row / group + u.shift, a.window, room);
-            const Reach r1 = reach_of((int64_t)u.first + (u.row + u.rows - 1) / group + u.shift, a.window, room);
+            u.shift = max(a.lens[lo], 0) - a.cu[lo + 1];  // with a row at all cu is positive, and its positions are below its length
+            auto reach = [&](int row) { return reach_of(u.first + a.group.quotient(u.row + row) + u.shift, a.window, room); };
+            const Reach r0 = reach(0), r1 = reach(u.rows - 1);
+            u.lo = r0.lo;
+            u.hi = r1.hi;
             u.key = r0.lo / keys * keys;
             u.tiles = r1.hi >= r0.lo ? (r1.hi - u.key) / keys + 1 : 0;
-            u.pad = 0;
+            u.all_hi[0] = r0.hi;
+            u.all_lo[0] = reach(min(u.rows, 128) - 1).lo;
+            u.all_hi[1] = reach(min(u.rows - 1, 128)).hi;
+            u.all_lo[1] = r1.lo;
+            u.pad[0] = u.pad[1] = u.pad[2] = 0;
             v.unit[i] = u;
             mine = u.tiles + kPad;
         }
@@ -164,10 +169,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(PrefillArgs a, int t
         x[0] += f * lo.x, x[1] += f * lo.y, x[2] += f * lo.z, x[3] += f * lo.w;
         x[4] += f * hi.x, x[5] += f * hi.y, x[6] += f * hi.z, x[7] += f * hi.w;
     }
-    const int group = a.Hq / a.c.Hkv, rr = u.row + row;
+    int head;
+    const int token = u.first + a.group.quotient(u.row + row, head);
     float inv = sum == 0.f ? 0.f : 1.f / sum;
     if (a.c.v_scale) inv *= a.c.v_scale[r.x];
-    const int64_t out = ((int64_t)u.first + rr / group) * a.Hq + r.x * group + rr % group;
+    const int64_t out = (int64_t)token * a.Hq + r.x * (int)a.group.by + head;
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = sum == 0.f ? 0.f : x[i] * inv;
     if constexpr (sizeof(T) == 4) {
@@ -194,6 +200,8 @@ cudaError_t launch_paged_prefill(const PrefillArgs &args, cudaStream_t stream) {
     using namespace prefill;
     PrefillArgs a = args;
     if (a.max_pages == 0) a.c.k = a.c.v = (void *)a.q;  // an address for copies of no bytes
+    a.group = divisor(a.Hq / a.c.Hkv);
+    a.page = divisor(a.c.page);
     const int tile = row_tile(a.c.dtype, a.c.d), grid = kMaxCtas;
     cudaError_t e = launch_kernel(false, plan_kernel, 1, kPlanThreads, 0, stream, a, tile, key_tile(a.c.dtype), grid);
     if (e != cudaSuccess) return e;

@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_f32_kernel(PrefillArgs a)
     __shared__ uint32_t ok_bits[kWarps];
     float *const qs = sm, *const ks = qs + kRows * C::kPitchK, *const vs = ks + kKeys * C::kPitchK;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
-    const int group = a.Hq / a.c.Hkv, room = a.max_pages * a.c.page;
+    const int group = (int)a.group.by, room = a.max_pages * a.c.page;
     View view;
     layout(a.ws, a.B, a.n, a.Hq, a.c.Hkv, D, kRows, &view);
     pdl_wait();
@@ -60,9 +60,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_f32_kernel(PrefillArgs a)
 
     while (walk.next()) {
         const Unit u = walk.u;
-        const int first = u.first + u.row / group, last = u.first + (u.row + u.rows - 1) / group;
-        const int lo = reach_of((int64_t)first + u.shift, a.window, room).lo, hi = reach_of((int64_t)last + u.shift, a.window, room).hi;
-        const int all_lo = reach_of((int64_t)last + u.shift, a.window, room).lo, all_hi = reach_of((int64_t)first + u.shift, a.window, room).hi;
+        const int lo = u.lo, hi = u.hi, all_lo = u.all_lo[0], all_hi = u.all_hi[0];
         const int32_t *table = a.table + u.b * a.table_stride;
         // this thread's two rows
         int64_t out[2];
@@ -70,10 +68,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_f32_kernel(PrefillArgs a)
         bool there[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int r = 16 * warp + g + 8 * e, rr = u.row + min(r, u.rows - 1), token = u.first + rr / group;
+            int head;
+            const int r = 16 * warp + g + 8 * e, token = u.first + a.group.quotient(u.row + min(r, u.rows - 1), head);
             there[e] = r < u.rows;
-            out[e] = (int64_t)token * a.Hq + walk.h * group + rr % group;
-            reach[e] = reach_of((int64_t)token + u.shift, a.window, room);
+            out[e] = (int64_t)token * a.Hq + walk.h * group + head;
+            reach[e] = reach_of(token + u.shift, a.window, room);
         }
         // ---- copies: warp w has keys 4 w .. 4 w + 3 of a tile; lanes 0 to 3 know where they are
         int64_t row = 0;
@@ -83,9 +82,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_f32_kernel(PrefillArgs a)
             real = false;
             row = 0;
             if (lane < 4 && key >= lo && key <= hi) {
-                const int at = key / a.c.page, page = table[at];
+                int cell;
+                const int page = table[a.page.quotient(key, cell)];
                 real = page >= 0 && page < a.c.pages;
-                if (real) row = page * a.c.stride_page + (key - at * a.c.page) * a.c.stride_token + walk.h * a.c.stride_head;
+                if (real) row = page * a.c.stride_page + cell * a.c.stride_token + walk.h * a.c.stride_head;
             }
             const uint32_t bits = __ballot_sync(0xffffffffu, real);
             if (lane == 0) ok_bits[warp] = bits;
@@ -104,8 +104,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_f32_kernel(PrefillArgs a)
         const int n = walk.t1 - walk.t0;
         if (n > 0) {
             for (int r = warp; r < kRows; r += kWarps) {
-                const int rr = u.row + min(r, u.rows - 1);
-                const float *src = (const float *)a.q + ((int64_t)u.first + rr / group) * a.q_tok + (int64_t)(walk.h * group + rr % group) * a.q_head;
+                int head;
+                const int token = u.first + a.group.quotient(u.row + min(r, u.rows - 1), head);
+                const float *src = (const float *)a.q + token * a.q_tok + (walk.h * group + head) * a.q_head;
                 for (int c = lane; c < D / 4; c += 32) cp16(paged::smem_addr(qs + r * C::kPitchK) + 16 * c, src + 4 * c, r < u.rows);
             }
             find(walk.t0);

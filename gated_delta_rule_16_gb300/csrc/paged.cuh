@@ -67,6 +67,24 @@ struct RopeArgs {
     int heads_per_cta;                 // set by the launch
 };
 
+// n / by for 0 <= n < 2^31, with l = ceil(log2 by): (n mul) >> (31 + l), mul = ceil(2^(31 + l) / by).
+struct Divisor {
+    uint32_t by, mul, shift;
+#ifdef __CUDACC__
+    __device__ __forceinline__ int quotient(int n) const { return (int)((uint64_t)(uint32_t)n * mul >> shift); }
+    __device__ __forceinline__ int quotient(int n, int &rest) const {
+        const int q = quotient(n);
+        rest = n - q * (int)by;
+        return q;
+    }
+#endif
+};
+inline Divisor divisor(uint32_t by) {
+    uint32_t l = 0;
+    while ((uint64_t)1 << l < by) ++l;
+    return {by, (uint32_t)((((uint64_t)1 << (31 + l)) + by - 1) / by), 31 + l};
+}
+
 struct PrefillArgs {
     gdn_kv_cache c;
     int B, n, Hq;
@@ -80,6 +98,7 @@ struct PrefillArgs {
     void *o;
     float *lse;  // may be NULL
     void *ws;
+    Divisor group, page;  // set by the launch
 };
 
 struct LogprobArgs {

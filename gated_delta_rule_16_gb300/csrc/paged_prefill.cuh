@@ -18,12 +18,16 @@ namespace prefill {
 
 constexpr int kMaxCtas = 152;  // of a wave: one per SM
 
-struct Unit {       // 32 bytes
-    int b, first;   // request; its first row of q
-    int row, rows;  // of the request's (token, head of the group) rows: the first, and how many
-    int shift;      // position of a token: its row of q + shift
-    int key, tiles; // first key, a multiple of the tile; tiles of keys
-    int pad;
+// What the kernels need of a unit is worked out once, in the plan: instructions that a CTA goes through once come from afar, some 250
+// clocks to every eight of them, and with the arithmetic repeated by each kind of warp the first product was asked for 9 us after the start.
+struct alignas(16) Unit {
+    int b, first;             // request; its first row of q
+    int row, rows;            // of the request's (token, head of the group) rows: the first, and how many
+    int shift;                // position of a token: its row of q + shift
+    int key, tiles;           // first key, a multiple of the tile; tiles of keys
+    int lo, hi;               // keys that any row attends to: [lo, hi]
+    int all_lo[2], all_hi[2]; // of the two tiles of 128 rows: keys that all of its rows attend to
+    int pad[3];
 };
 
 struct View {
@@ -71,10 +75,9 @@ inline __host__ __device__ int64_t split_at(int64_t total, int ctas, int i) { re
 
 // Keys [lo, hi] that a token attends to.
 struct Reach { int lo, hi; };
-__device__ __forceinline__ Reach reach_of(int64_t pos, int window, int room) {
-    const int64_t hi = pos < room ? pos : room - 1;
-    const int64_t lo = window > 0 && pos >= window ? pos - window + 1 : 0;
-    return {(int)(lo < room ? lo : room), (int)(hi < -1 ? -1 : hi)};
+__device__ __forceinline__ Reach reach_of(int pos, int window, int room) {
+    const int lo = window > 0 && pos >= window ? pos - window + 1 : 0;
+    return {min(lo, room), max(min(pos, room - 1), -1)};
 }
 
 // What a CTA does, one piece of a unit after the other.  Every thread that walks it sees the same pieces.

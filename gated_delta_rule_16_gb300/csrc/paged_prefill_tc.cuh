@@ -184,7 +184,8 @@ struct Bars {
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // of a group's two S tiles
     uint64_t joint[2], drain[3];    // joint: a group's votes
     uint32_t words[kWords][4];      // real keys of a stage
-    float row_scale[2][256];        // e4m3: of q's rows, by turns
+    int8_t lift[3][256];            // e4m3: exponents that q's rows were lifted by, of three units by turns: q of one is loaded while the next one's
+                                    // first scores are made and the softmax may still begin the one before
     int vote[2][3];                 // of a group, by turns
     int skip[2][2];                 // the group has added this tile's P V itself
     int gave_up;
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
     Bars &bars = *reinterpret_cast<Bars *>(smem + C::kSmem);
     uint8_t *const q_smem = smem, *const ring = smem + C::kTiles * C::kQTile;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warpgroup = warp >> 2;
-    const int group = a.Hq / a.c.Hkv, room = a.max_pages * a.c.page;
+    const int group = (int)a.group.by, room = a.max_pages * a.c.page;
     const Waiter wait = {&bars.gave_up};
     View view;
     layout(a.ws, a.B, a.n, a.Hq, a.c.Hkv, D, 128 * C::kTiles, &view);
@@ -428,12 +429,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
         // the unit's rows of q, a tile of 128 after the other; rows behind the last are zeros.  A row is (token, head of the group): a lane
         // counts its own up instead of dividing for each, which made a unit's beginning 6 us longer
         constexpr int kLanes = D / 8, kRowStep = 4 * (32 / kLanes);  // 16 bytes to a lane; rows that the warps have at a time
-        const int piece = lane % kLanes, step_token = kRowStep / group, step_head = kRowStep % group;
+        const int piece = lane % kLanes, step_token = a.group.quotient(kRowStep), step_head = kRowStep - step_token * group;
         const int64_t step = step_token * a.q_tok + step_head * a.q_head, carry = a.q_tok - group * a.q_head;
         auto load_q = [&](const Unit &u, int h) {
             if (!settle()) return false;
-            int r = pw * (32 / kLanes) + lane / kLanes, head = (u.row + r) % group;
-            const uint16_t *src = (const uint16_t *)a.q + ((int64_t)u.first + (u.row + r) / group) * a.q_tok + (int64_t)(h * group + head) * a.q_head + 8 * piece;
+            int r = pw * (32 / kLanes) + lane / kLanes, head;
+            const int token = u.first + a.group.quotient(u.row + r, head);
+            const uint16_t *src = (const uint16_t *)a.q + token * a.q_tok + (h * group + head) * a.q_head + 8 * piece;
 #pragma unroll 1
             for (int m = 0; m < C::kTiles && 128 * m < u.rows; ++m) {
                 const int uses = m ? units1 : units;
@@ -461,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
 #pragma unroll
                         for (int j = 0; j < 4; ++j) y[j] = pack_f16x2(__uint_as_float(w[j] << 16) * f, __uint_as_float(w[j] & 0xffff0000u) * f);
                         sts128(to, y[0], y[1], y[2], y[3]);
-                        if (piece == 0) bars.row_scale[uses & 1][r] = __uint_as_float((uint32_t)(127 - lift) << 23);
+                        if (piece == 0) bars.lift[uses % 3][r] = (int8_t)lift;
                     }
                     src += step;
                     if ((head += step_head) >= group) head -= group, src += carry;
@@ -480,15 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
         while (ok && walk.next()) {
             const Unit u = walk.u;
             if (walk.t0 == walk.t1) continue;
-            const int first = u.first + u.row / group, last = u.first + (u.row + u.rows - 1) / group;
-            const int lo = reach_of((int64_t)first + u.shift, a.window, room).lo, hi = reach_of((int64_t)last + u.shift, a.window, room).hi;
-            const int32_t *table = a.table + u.b * a.table_stride;
-            const int begin = u.key + kTileKeys * walk.t0, end = min(hi, u.key + kTileKeys * walk.t1 - 1), n = (walk.t1 - walk.t0 + 1) / 2;
-            auto entry = [&](int key, int &cell) {  // the key's page, -1 where it has none
-                const int page = key / a.c.page;
-                cell = key - page * a.c.page;
-                return key >= lo && key <= end ? table[page] : -1;
-            };
+            const int n = (walk.t1 - walk.t0 + 1) / 2;
             if constexpr (TMA) {
                 // bf16: q is all there is to do; e4m3: the unit's stages too, q after the first keys
                 for (int i = 0; ok && i < (C::kE4M3 ? 2 * C::kParts * n : 1); ++i) {
@@ -497,6 +491,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
                 }
                 continue;
             }
+            const int32_t *table = a.table + u.b * a.table_stride;
+            const int lo = u.lo, begin = u.key + kTileKeys * walk.t0, end = min(u.hi, u.key + kTileKeys * walk.t1 - 1);
+            auto entry = [&](int key, int &cell) {  // the key's page, -1 where it has none
+                const int page = a.page.quotient(key, cell);
+                return key >= lo && key <= end ? table[page] : -1;
+            };
             int cell_next, page_next = entry(begin + pt, cell_next);
             for (int t = 0; ok && t < n; ++t) {
                 const int page = page_next, cell = cell_next;
@@ -655,14 +655,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
             while (ok && walk.next()) {
                 const Unit u = walk.u;
                 if (walk.t0 == walk.t1) continue;
-                const int first = u.first + u.row / group, last = u.first + (u.row + u.rows - 1) / group;
-                const int lo = reach_of((int64_t)first + u.shift, a.window, room).lo, hi = reach_of((int64_t)last + u.shift, a.window, room).hi;
                 const int32_t *table = a.table + u.b * a.table_stride;
-                const int begin = u.key + kTileKeys * walk.t0, end = min(hi, u.key + kTileKeys * walk.t1 - 1), n = (walk.t1 - walk.t0 + 1) / 2;
+                const int lo = u.lo, begin = u.key + kTileKeys * walk.t0, end = min(u.hi, u.key + kTileKeys * walk.t1 - 1), n = (walk.t1 - walk.t0 + 1) / 2;
                 // lane l has the l-th box of 128 keys
                 auto entry = [&](int key, int &cell) {
-                    const int page = key / a.c.page;
-                    cell = key - page * a.c.page;
+                    const int page = a.page.quotient(key, cell);
                     return lane < boxes && key + box > lo && key <= end ? table[page] : -1;
                 };
                 int cell_next, page_next = entry(begin + lane * box, cell_next);
@@ -719,12 +716,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
                 continue;
             }
             const int rows = min(128, u.rows - 128 * m);
-            const int rr = u.row + 128 * m + min(r, rows - 1);
-            const int token = u.first + rr / group, head = walk.h * group + rr % group;
-            const Reach mine = reach_of((int64_t)token + u.shift, a.window, room);
-            const int first = u.first + (u.row + 128 * m) / group, last = u.first + (u.row + 128 * m + rows - 1) / group;
+            int head;
+            const int token = u.first + a.group.quotient(u.row + 128 * m + min(r, rows - 1), head);
+            const Reach mine = reach_of(token + u.shift, a.window, room);
             // keys that all rows attend to
-            const int all_lo = reach_of((int64_t)last + u.shift, a.window, room).lo, all_hi = reach_of((int64_t)first + u.shift, a.window, room).hi;
+            const int all_lo = m ? u.all_lo[1] : u.all_lo[0], all_hi = m ? u.all_hi[1] : u.all_hi[0];
             const uint32_t t_o = tmem + lanes + C::kO + m * D;
             float ref = -INFINITY, sum = 0.f, zs = a.scale * log2e;
             if (a.c.k_scale) zs *= a.c.k_scale[walk.h];
@@ -735,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
                 auto ended = [&](int j) { return warp_wait(wait, &bars.pv_done[m][(done + j) & 1], (done + j) >> 1 & 1); };
                 if (!(ok = warp_wait(wait, &bars.s_full[m][place], (done + i) >> 1 & 1))) break;
                 tc_fence_after();
-                if (C::kE4M3 && i == 0) zs *= bars.row_scale[units & 1][128 * m + r];
+                if (C::kE4M3 && i == 0) zs *= __uint_as_float((uint32_t)(127 - bars.lift[units % 3][128 * m + r]) << 23);
                 float s[2][32];
                 tmem_ld32(t_s, s[0]);
                 tmem_ld32(t_s + 32, s[1]);
@@ -843,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
                 const bool none = n == 0 || (ref == -INFINITY && sum == 0.f);  // NaN is not nothing
                 float inv = none ? 0.f : 1.f / sum;
                 if (a.c.v_scale) inv *= a.c.v_scale[walk.h];
-                const int64_t out = (int64_t)token * a.Hq + head;
+                const int64_t out = (int64_t)token * a.Hq + walk.h * group + head;
                 // a thread has a row, whose pieces alone would be 32 places to a store: four lanes write 64 bytes of a row together
                 __nv_bfloat16 *to[4];
 #pragma unroll
