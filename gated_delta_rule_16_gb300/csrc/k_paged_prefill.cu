@@ -35,11 +35,11 @@ __device__ int64_t scan(int64_t x, int64_t *buf, int64_t &all) {
 }
 
 // One CTA: a thread per request counts its units, a thread per unit finds its request, rows and keys, a thread per CTA its run.
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(PrefillArgs a, int tile, int keys, int grid) {
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(PrefillArgs a, int tile, int keys, int grid, int pad) {
     __shared__ int64_t buf[32];
     __shared__ int64_t held[kHeldUnits];
     View v;
-    layout(a.ws, a.B, a.n, a.Hq, a.c.Hkv, a.c.d, tile, &v);
+    layout(a.ws, a.B, a.n, a.Hq, a.c.Hkv, a.c.d, tile, grid, &v);
     const int tid = threadIdx.x, group = a.Hq / a.c.Hkv, room = a.max_pages * a.c.page;
     pdl_trigger();
     auto rows_of = [&](int b, int &first) {
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PrefillArgs a, int t
             u.all_lo[1] = r1.lo;
             u.pad[0] = u.pad[1] = u.pad[2] = 0;
             v.unit[i] = u;
-            mine = u.tiles + kPad;
+            mine = u.tiles + pad;
         }
         int64_t all;
         const int64_t incl = cost + scan(mine, buf, all);
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PrefillArgs a, int t
     __syncthreads();
     const int64_t *ends = units <= kHeldUnits ? held : v.ends;
     const int64_t total = cost * a.c.Hkv;
-    const int ctas = (int)max((int64_t)1, min((int64_t)grid, total / kMinRun));
+    const int ctas = (int)max((int64_t)1, min((int64_t)grid, total / (pad + 1)));
     for (int i = tid; i <= grid; i += kPlanThreads) {
         int4 run = make_int4(-1, 0, 0, 0);
         if (i == ctas || total == 0) run = i <= ctas ? make_int4(a.c.Hkv, 0, 0, 0) : run;
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PrefillArgs a, int t
                 else lo = mid + 1;
             }
             const int64_t begin = lo ? ends[lo - 1] : 0;
-            run = make_int4((int)head, lo, (int)(rest - begin), (int)(ends[lo] - begin) - kPad);
+            run = make_int4((int)head, lo, (int)(rest - begin), (int)(ends[lo] - begin) - pad);
         }
         v.runs[i] = run;
     }
@@ -134,9 +134,9 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // blocks of dims.  A thread has 8 dims of a row.
 constexpr int kJoinRows = 32, kJoinThreads = 256;
 template <typename T>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(PrefillArgs a, int tile) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(PrefillArgs a, int tile, int grid) {
     View v;
-    layout(a.ws, a.B, a.n, a.Hq, a.c.Hkv, a.c.d, tile, &v);
+    layout(a.ws, a.B, a.n, a.Hq, a.c.Hkv, a.c.d, tile, grid, &v);
     pdl_wait();
     const int edge = blockIdx.x + 1;
     auto inside = [&](const int4 &r) { return r.x >= 0 && r.z > 0 && r.z < r.w; };
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(PrefillArgs a, int t
     const int4 before = v.runs[edge - 1];
     if (inside(before) && before.x == r.x && before.y == r.y) return;
     int parts = 2;
-    for (; edge + parts - 1 <= kMaxCtas; ++parts) {
+    for (; edge + parts - 1 <= grid; ++parts) {
         const int4 next = v.runs[edge + parts - 1];
         if (!inside(next) || next.x != r.x || next.y != r.y) break;
     }
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(PrefillArgs a, int t
 }  // namespace prefill
 
 size_t paged_prefill_workspace_bytes(const gdn_kv_cache &c, int B, int n, int Hq) {
-    return prefill::layout(nullptr, B, n, Hq, c.Hkv, c.d, prefill::row_tile(c.dtype, c.d), nullptr);
+    return prefill::layout(nullptr, B, n, Hq, c.Hkv, c.d, prefill::row_tile(c.dtype, c.d), prefill::wave(c.dtype, c.d), nullptr);
 }
 
 cudaError_t launch_paged_prefill(const PrefillArgs &args, cudaStream_t stream) {
@@ -202,8 +202,8 @@ cudaError_t launch_paged_prefill(const PrefillArgs &args, cudaStream_t stream) {
     if (a.max_pages == 0) a.c.k = a.c.v = (void *)a.q;  // an address for copies of no bytes
     a.group = divisor(a.Hq / a.c.Hkv);
     a.page = divisor(a.c.page);
-    const int tile = row_tile(a.c.dtype, a.c.d), grid = kMaxCtas;
-    cudaError_t e = launch_kernel(false, plan_kernel, 1, kPlanThreads, 0, stream, a, tile, key_tile(a.c.dtype), grid);
+    const int tile = row_tile(a.c.dtype, a.c.d), grid = wave(a.c.dtype, a.c.d);
+    cudaError_t e = launch_kernel(false, plan_kernel, 1, kPlanThreads, 0, stream, a, tile, key_tile(a.c.dtype), grid, unit_pad(a.c.dtype));
     if (e != cudaSuccess) return e;
     if (a.c.dtype == GDN_F32) {
         e = launch_f32(a, grid, stream);
@@ -219,8 +219,8 @@ cudaError_t launch_paged_prefill(const PrefillArgs &args, cudaStream_t stream) {
     const int dims = kJoinThreads / kJoinRows * 8;
     const int64_t rows = (int64_t)a.n * (a.Hq / a.c.Hkv);
     const dim3 blocks(grid - 1, (unsigned)((min((int64_t)tile, rows) + kJoinRows - 1) / kJoinRows), a.c.d / dims);
-    return a.c.dtype == GDN_F32 ? launch_kernel(true, join_kernel<float>, blocks, kJoinThreads, 0, stream, a, tile)
-                                : launch_kernel(true, join_kernel<__nv_bfloat16>, blocks, kJoinThreads, 0, stream, a, tile);
+    return a.c.dtype == GDN_F32 ? launch_kernel(true, join_kernel<float>, blocks, kJoinThreads, 0, stream, a, tile, grid)
+                                : launch_kernel(true, join_kernel<__nv_bfloat16>, blocks, kJoinThreads, 0, stream, a, tile, grid);
 }
 
 }  // namespace gdn

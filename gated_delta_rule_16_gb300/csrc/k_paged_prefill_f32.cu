@@ -43,7 +43,7 @@ __device__ __forceinline__ void mma_split(float (&c)[4], const uint32_t (&ah)[4]
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) prefill_f32_kernel(PrefillArgs a) {
+__global__ void __launch_bounds__(kThreads, D < 256 ? 2 : 1) prefill_f32_kernel(PrefillArgs a) {
     using C = Cfg<D>;
     extern __shared__ __align__(16) float sm[];
     __shared__ uint32_t ok_bits[kWarps];
@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_f32_kernel(PrefillArgs a)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
     const int group = (int)a.group.by, room = a.max_pages * a.c.page;
     View view;
-    layout(a.ws, a.B, a.n, a.Hq, a.c.Hkv, D, kRows, &view);
+    layout(a.ws, a.B, a.n, a.Hq, a.c.Hkv, D, kRows, gridDim.x, &view);
     pdl_wait();
     pdl_trigger();
     Walk walk;

@@ -16,7 +16,7 @@
 namespace gdn {
 namespace prefill {
 
-constexpr int kMaxCtas = 152;  // of a wave: one per SM
+constexpr int kMaxCtas = 304;  // of a wave, at most two per SM
 
 // What the kernels need of a unit is worked out once, in the plan: instructions that a CTA goes through once come from afar, some 250
 // clocks to every eight of them, and with the arithmetic repeated by each kind of warp the first product was asked for 9 us after the start.
@@ -37,14 +37,14 @@ struct View {
     Unit *unit;
     int64_t *ends;    // running sum of the units' costs
     int32_t *first;   // of each request: its first unit
-    float2 *ml;       // [2 kMaxCtas][rows of a unit] reference and sum of a part
-    float *o;         // [2 kMaxCtas][d / 4][rows of a unit][4]
+    float2 *ml;       // [2 CTAs][rows of a unit] reference and sum of a part
+    float *o;         // [2 CTAs][d / 4][rows of a unit][4]
 };
 
 inline __host__ __device__ int64_t unit_capacity(int B, int64_t rows, int tile) { return rows / tile + 1 + B; }
 
 // Byte offsets of View's parts; returns the size.
-inline __host__ __device__ size_t layout(void *ws, int B, int n, int Hq, int Hkv, int d, int tile, View *v) {
+inline __host__ __device__ size_t layout(void *ws, int B, int n, int Hq, int Hkv, int d, int tile, int ctas, View *v) {
     const int64_t units = unit_capacity(B, (int64_t)n * (Hq / Hkv), tile);
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -59,8 +59,8 @@ inline __host__ __device__ size_t layout(void *ws, int B, int n, int Hq, int Hkv
     x.unit = (Unit *)take(units * sizeof(Unit));
     x.ends = (int64_t *)take(units * sizeof(int64_t));
     x.first = (int32_t *)take(((size_t)B + 1) * sizeof(int32_t));
-    x.ml = (float2 *)take((size_t)2 * kMaxCtas * tile * sizeof(float2));
-    x.o = (float *)take((size_t)2 * kMaxCtas * tile * d * sizeof(float));
+    x.ml = (float2 *)take((size_t)2 * ctas * tile * sizeof(float2));
+    x.o = (float *)take((size_t)2 * ctas * tile * d * sizeof(float));
     if (v) *v = x;
     return at;
 }
@@ -68,8 +68,12 @@ inline __host__ __device__ size_t layout(void *ws, int B, int n, int Hq, int Hkv
 // Rows and keys of a tile: what the kernels are built for.
 inline __host__ __device__ int row_tile(gdn_dtype kind, int d) { return kind == GDN_F32 || d == 256 ? 128 : 256; }
 inline __host__ __device__ int key_tile(gdn_dtype kind) { return kind == GDN_F32 ? 32 : 64; }
-// A unit costs its tiles and this many more, for its beginning and end; a CTA takes a run of kMinRun at least.
-constexpr int kPad = 2, kMinRun = 4;
+// A unit costs its tiles and this many more, for its beginning and end (8-bit caches: most of all for q's conversion, in turn with the keys'),
+// and a CTA takes one more than that at least.  With 2, 3, 4, 6, 8: 8192 bf16 tokens at once 506, 502, 506, 512, 516 us; 8-bit chunks over
+// 16000 tokens 346, 333, 324, 319, 301.
+inline __host__ __device__ int unit_pad(gdn_dtype kind) { return kind == GDN_E4M3 ? 8 : 3; }
+// CTAs of a wave: one per SM, two where the registers of the warp-MMA kernel allow.
+inline __host__ __device__ int wave(gdn_dtype kind, int d) { return kind == GDN_F32 && d < 256 ? kMaxCtas : kMaxCtas / 2; }
 
 inline __host__ __device__ int64_t split_at(int64_t total, int ctas, int i) { return total / ctas * i + total % ctas * i / ctas; }
 

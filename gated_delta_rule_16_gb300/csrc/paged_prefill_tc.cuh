@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
     const int group = (int)a.group.by, room = a.max_pages * a.c.page;
     const Waiter wait = {&bars.gave_up};
     View view;
-    layout(a.ws, a.B, a.n, a.Hq, a.c.Hkv, D, 128 * C::kTiles, &view);
+    layout(a.ws, a.B, a.n, a.Hq, a.c.Hkv, D, 128 * C::kTiles, gridDim.x, &view);
 
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
@@ -835,7 +835,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
             done += n;
             // ---- the row's end in this CTA
             const bool there = r < rows;
-            if (walk.whole()) {
+            if (32 * (warp & 3) >= rows) {
+                // none of this warp's
+            } else if (walk.whole()) {
                 const bool none = n == 0 || (ref == -INFINITY && sum == 0.f);  // NaN is not nothing
                 float inv = none ? 0.f : 1.f / sum;
                 if (a.c.v_scale) inv *= a.c.v_scale[walk.h];
