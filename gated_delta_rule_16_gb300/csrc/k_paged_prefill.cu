@@ -203,7 +203,7 @@ cudaError_t launch_paged_prefill(const PrefillArgs &args, cudaStream_t stream) {
     a.group = divisor(a.Hq / a.c.Hkv);
     a.page = divisor(a.c.page);
     const int tile = row_tile(a.c.dtype, a.c.d), grid = wave(a.c.dtype, a.c.d);
-    cudaError_t e = launch_kernel(false, plan_kernel, 1, kPlanThreads, 0, stream, a, tile, key_tile(a.c.dtype), grid, unit_pad(a.c.dtype));
+    cudaError_t e = launch_kernel(false, plan_kernel, 1, kPlanThreads, 0, stream, a, tile, key_tile(a.c.dtype, a.c.d), grid, unit_pad(a.c.dtype));
     if (e != cudaSuccess) return e;
     if (a.c.dtype == GDN_F32) {
         e = launch_f32(a, grid, stream);

@@ -2,7 +2,7 @@
 // parts of cut rows lie, shared by the kernels that k_paged_prefill*.cu instantiate.
 //
 // A unit is a tile of rows (new token t, query head of one KV head's group, in this order) of one request with all the keys
-// they attend to, in tiles of 64 keys (32-bit storage: 32).  The units of all requests are laid end to end, once for each KV head, and the CTAs of one
+// they attend to, in tiles of 64 keys (32-bit storage: 32 or 16).  The units of all requests are laid end to end, once for each KV head, and the CTAs of one
 // wave get equal runs of key tiles; a unit cut by a CTA's edge leaves unnormalised fp32 parts that a last launch joins in
 // the keys' order.  Lengths are only known on the GPU, so a first launch of one CTA lists the units and finds the runs.  Causal rows
 // make units of 1 to hundreds of tiles, and equal runs need no luck with their order: of 8192 tokens at once every CTA
@@ -67,13 +67,13 @@ inline __host__ __device__ size_t layout(void *ws, int B, int n, int Hq, int Hkv
 
 // Rows and keys of a tile: what the kernels are built for.
 inline __host__ __device__ int row_tile(gdn_dtype kind, int d) { return kind == GDN_F32 || d == 256 ? 128 : 256; }
-inline __host__ __device__ int key_tile(gdn_dtype kind) { return kind == GDN_F32 ? 32 : 64; }
+inline __host__ __device__ int key_tile(gdn_dtype kind, int d) { return kind != GDN_F32 ? 64 : d == 256 ? 16 : 32; }
 // A unit costs its tiles and this many more, for its beginning and end (8-bit caches: most of all for q's conversion, in turn with the keys'),
 // and a CTA takes one more than that at least.  With 2, 3, 4, 6, 8: 8192 bf16 tokens at once 506, 502, 506, 512, 516 us; 8-bit chunks over
 // 16000 tokens 346, 333, 324, 319, 301.
 inline __host__ __device__ int unit_pad(gdn_dtype kind) { return kind == GDN_E4M3 ? 8 : 3; }
 // CTAs of a wave: one per SM, two where the registers of the warp-MMA kernel allow.
-inline __host__ __device__ int wave(gdn_dtype kind, int d) { return kind == GDN_F32 && d < 256 ? kMaxCtas : kMaxCtas / 2; }
+inline __host__ __device__ int wave(gdn_dtype kind, int d) { return kind == GDN_F32 && d == 64 ? kMaxCtas : kMaxCtas / 2; }
 
 inline __host__ __device__ int64_t split_at(int64_t total, int ctas, int i) { return total / ctas * i + total % ctas * i / ctas; }
 
