@@ -3,7 +3,7 @@
     python examples/hybrid_decode.py [--steps N] [--cache bf16|f32|e4m3] [--temperature T]
 
 Prompts of different lengths are prefilled (gdn_prefill_dense per request; the attention layer writes all prompts' keys
-and values with one gdn_kv_append and attends every prompt token as a row of its own with gdn_paged_decode), then
+and values with one gdn_kv_append and attends all prompts' tokens with one gdn_paged_prefill), then
 every step adds one token to each request: gdn_page_tables, gdn_decode_step, gdn_kv_append, gdn_paged_decode and
 gdn_sample.  Weights are random; projections are plain matrix products.
 """
@@ -72,7 +72,7 @@ def serve(model, prompts, steps, cache="bf16", page=16, temperature=0.0, top_k=5
 
     # ---- prompts: all requests' tokens in one list
     x = model.embed[torch.tensor([t for p in prompts for t in p], device=dev)]
-    slots, positions, seq_lens, _, counts = gdn.gdn_page_tables(i32(lens), free, table, page=page, n_slots=sum(lens))
+    slots, _, seq_lens, cu_new, counts = gdn.gdn_page_tables(i32(lens), free, table, page=page, n_slots=sum(lens))
     q, k, v, beta, a = model.delta_inputs(x)
     states, outs, at = [], [], 0
     for n in lens:
@@ -86,8 +86,7 @@ def serve(model, prompts, steps, cache="bf16", page=16, temperature=0.0, top_k=5
     x = model.add_delta(x, torch.cat(outs))
     q, k, v = model.attention_inputs(x)
     gdn.gdn_kv_append(k, v, slots, k_cache, v_cache, **scales)
-    rows = torch.repeat_interleave(torch.arange(B, device=dev), torch.tensor(lens, device=dev))
-    o, _ = gdn.gdn_paged_decode(q, k_cache, v_cache, table[rows], positions + 1, **scales)
+    o, _ = gdn.gdn_paged_prefill(q, k_cache, v_cache, table, seq_lens, cu_new, **scales)
     x = model.add_attention(x, o)
     x = x[torch.tensor(lens, device=dev).cumsum(0) - 1]
 

@@ -48,7 +48,7 @@ __device__ __forceinline__ uint4 split2(float x, float y) {
     return r;
 }
 __device__ __forceinline__ uint4 lds(const float *p) { return *reinterpret_cast<const uint4 *>(p); }
-__device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
+__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7fffffffu) < 0x7f7ff000u; }  // and so is its high term, rounded to 11 bits
 
 // c += a b in three products, the small ones first
 __device__ __forceinline__ void mma_split(float (&c)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], const uint4 &b) {
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) prefill_f32_kernel(
                         for (int j = 0; j < 2; ++j) {
                             // hi + lo: to 2^-22 of the value, or what it has of NaN and infinity
                             const float *at = vs + ((k >> 1) * C::kPitchV + 8 * i + 2 * q4 + j) * 4 + (k & 1);
-                            const float v = finite(at[2]) ? at[0] + at[2] : at[2];
+                            const float v = at[2] == 0.f ? at[0] : at[0] + at[2];
                             if (bits[0] >> k & 1) o[i][j] += p[0] * v;
                             if (bits[1] >> k & 1) o[i][2 + j] += p[1] * v;
                         }

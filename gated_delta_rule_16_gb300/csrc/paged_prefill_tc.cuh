@@ -23,6 +23,8 @@
 
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "paged_prefill.cuh"
 #include "tc.cuh"
 #include "tmap.cuh"
@@ -914,11 +916,14 @@ cudaError_t launch_tc(const PrefillArgs &a, int grid, int box, const CUtensorMap
     using C = Cfg<KIND, D>;
     constexpr int kSmem = (int)(C::kSmem + sizeof(Bars));
     // the warp groups' shares of registers are what a block of 128 to a thread has: with fewer they would wait for ever
-    static const int regs = [] {
+    static std::atomic<int> regs{0};
+    if (regs.load(std::memory_order_relaxed) == 0) {
         cudaFuncAttributes attr;
-        return cudaFuncGetAttributes(&attr, prefill_tc_kernel<KIND, D, TMA>) == cudaSuccess ? attr.numRegs : 0;
-    }();
-    if (regs != 128) return cudaErrorInvalidConfiguration;
+        const cudaError_t e = cudaFuncGetAttributes(&attr, prefill_tc_kernel<KIND, D, TMA>);
+        if (e != cudaSuccess) return e;
+        regs.store(attr.numRegs, std::memory_order_relaxed);
+    }
+    if (regs.load(std::memory_order_relaxed) != 128) return cudaErrorInvalidConfiguration;
     const cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<KIND, D, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     return e != cudaSuccess ? e : launch_kernel(true, prefill_tc_kernel<KIND, D, TMA>, grid, kThreads, kSmem, stream, a, maps[0], maps[1], box);
 }

@@ -118,6 +118,8 @@ def gdn_paged_prefill_status(workspace, stream=None) -> int:
     """Status of the gdn_paged_prefill call that used a workspace last (synchronises the stream): 0, or 10 (GDN_ERR_TIMEOUT)
     if a wait inside a kernel ran out, with the outputs not valid."""
     buf = workspace.buf if isinstance(workspace, Workspace) else workspace
+    if buf is None:
+        raise ValueError("no call has used the workspace")
     dev = _cuda(buf, "workspace")
     with torch.cuda.device(dev):
         return int(load().gdn_paged_prefill_status(buf.data_ptr(), _handle(dev, stream)))
