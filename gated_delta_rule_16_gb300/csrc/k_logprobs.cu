@@ -110,8 +110,8 @@ template <typename T> __device__ __forceinline__ void pairs_of(const uint4 &u, u
 }
 __device__ __forceinline__ float value(const float *p) { return *p; }
 __device__ __forceinline__ float value(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void cp16(void *dst, const void *src, bool real) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "r"(real ? 16 : 0) : "memory");
+__device__ __forceinline__ void cp16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -258,16 +258,21 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(LogprobArgs a, in
     Sums sums = {kLowest, 0.f, 0.f};
     constexpr uint32_t kNone = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;  // -inf, which has no weight
     const uint4 none = make_uint4(kNone, kNone, kNone, kNone);
-    auto vec_at = [&](int batch, int v) { return ((int64_t)batch * ctas + cta) * kBatch + v * kThreads + tid; };
-    auto slot_of = [&](int batch, int v) -> uint4 & { return slots[(batch % kAhead * kVecs + v) * kThreads + tid]; };
+    auto vec_at = [&](int batch, int v) { return (batch * ctas + cta) * kBatch + v * kThreads + tid; };  // below 2^30
+    auto slot_of = [&](int batch, int v) -> uint4 & { return slots[((batch & (kAhead - 1)) * kVecs + v) * kThreads + tid]; };
     auto copy = [&](int batch) {
-        if (batch < batches)
+        if (batch < batches) {
+            const int first = (batch * ctas + cta) * kBatch;
+            if (first + kBatch <= vecs) {
 #pragma unroll
-            for (int v = 0; v < kVecs; ++v) {
-                const int64_t i = vec_at(batch, v);
-                if (i < vecs) cp16(&slot_of(batch, v), xv + i, true);
-                else slot_of(batch, v) = none;
+                for (int v = 0; v < kVecs; ++v) cp16(&slot_of(batch, v), xv + first + tid + v * kThreads);
+            } else {
+#pragma unroll
+                for (int v = 0; v < kVecs; ++v)
+                    if (vec_at(batch, v) < vecs) cp16(&slot_of(batch, v), xv + vec_at(batch, v));
+                    else slot_of(batch, v) = none;
             }
+        }
         cp_commit();
     };
 #pragma unroll
@@ -325,12 +330,16 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(LogprobArgs a, in
             // logit i of the thread's kEach, and its index
             const int from = batch == batches ? (tid < head ? tid : tail + tid - head) : head + ((batch * ctas + cta) * kBatch + tid) * N;
             auto key_at = [&](int i) { return key_of(value((const T *)&slot_of(batch, i / N) + i % N), from + i / N * (kThreads * N) + i % N); };
-            uint32_t real = 0;
-            if (batch == batches) real = from < a.V;
-            else
+            auto real_of = [&] {
+                uint32_t real = 0;
+                if (batch == batches) real = from < a.V;
+                else
 #pragma unroll
-                for (int v = 0; v < kVecs; ++v) real |= vec_at(batch, v) < vecs ? ((1u << N) - 1) << (v * N) : 0u;
+                    for (int v = 0; v < kVecs; ++v) real |= vec_at(batch, v) < vecs ? ((1u << N) - 1) << (v * N) : 0u;
+                return real;
+            };
             if (batch == 0) {
+                const uint32_t real = real_of();
                 int at = -1;
                 float best = 0.f;
 #pragma unroll
@@ -354,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(LogprobArgs a, in
                         unpair(in[v][j], lo, hi);
                         which |= (lo < least ? 0u : 1u << (v * N + 2 * j)) | (hi < least ? 0u : 2u << (v * N + 2 * j));  // NaN is looked at too
                     }
-                which &= real;
+                which &= real_of();
 #pragma unroll 1
                 while (which) {
                     const int i = __ffs(which) - 1;
@@ -367,8 +376,7 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(LogprobArgs a, in
                 }
             }
             // (of two blocks completed by one warp at once the later)
-            const int block = (int)__reduce_max_sync(0xffffffffu, (unsigned)(full + 1)) - 1;
-            if (block >= 0) raise_from_block(s, a.top, block);
+            if (__any_sync(0xffffffffu, full >= 0)) raise_from_block(s, a.top, (int)__reduce_max_sync(0xffffffffu, (unsigned)(full + 1)) - 1);
             if (batch == 0) {
                 __syncthreads();
                 if (s.count <= kList) cut(s, a.top);
