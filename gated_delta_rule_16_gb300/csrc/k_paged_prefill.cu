@@ -1,5 +1,9 @@
 // k_paged_prefill.cu -- softmax attention of new tokens over the paged cache: the plan before the attention
 // kernels, and the join of rows that were cut between CTAs after them (paged_prefill.cuh has the scheme).
+//
+// Both are latency.  The plan is one CTA's scans and searches, 6 to 8 us by itself with cold caches (every instruction of it comes from
+// afar once); the attention kernel's CTAs start beside it and set up their barriers and tensor memory meanwhile.  The join reads at most 40 MB of
+// parts: 4 us where there are few, 16 us (cold) for 151 cut units of 256 rows of 128 dims, 3 % of a call that has so many.
 #include "paged_prefill_tc.cuh"
 
 namespace gdn {

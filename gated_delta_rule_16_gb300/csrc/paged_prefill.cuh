@@ -69,9 +69,9 @@ inline __host__ __device__ size_t layout(void *ws, int B, int n, int Hq, int Hkv
 inline __host__ __device__ int row_tile(gdn_dtype kind, int d) { return kind == GDN_F32 || d == 256 ? 128 : 256; }
 inline __host__ __device__ int key_tile(gdn_dtype kind, int d) { return kind != GDN_F32 ? 64 : d == 256 ? 16 : 32; }
 // A unit costs its tiles and this many more, for its beginning and end (8-bit caches: most of all for q's conversion, in turn with the keys'),
-// and a CTA takes one more than that at least.  With 2, 3, 4, 6, 8: 8192 bf16 tokens at once 506, 502, 506, 512, 516 us; 8-bit chunks over
-// 16000 tokens 346, 333, 324, 319, 301.
-inline __host__ __device__ int unit_pad(gdn_dtype kind) { return kind == GDN_E4M3 ? 8 : 3; }
+// and a CTA takes one more than that at least.  8192 bf16 tokens at once: 484 us with 2, 476 with 3, 479 with 4; 8-bit chunks of up to 512
+// tokens over 16000: 329 with 3, 314 with 5, 299 with 8, 290 with 10, 294 with 12.
+inline __host__ __device__ int unit_pad(gdn_dtype kind) { return kind == GDN_E4M3 ? 10 : 3; }
 // CTAs of a wave: one per SM, two where the registers of the warp-MMA kernel allow.
 inline __host__ __device__ int wave(gdn_dtype kind, int d) { return kind == GDN_F32 && d == 64 ? kMaxCtas : kMaxCtas / 2; }
 

@@ -19,6 +19,17 @@
 //                    more than the tensor core has queued: the other warps' batches fill the gap.  (One warp for all of them: a pair of tiles
 //                    took 2900 clocks; a warp for each row tile 2100.)
 // With 256 dims O fills the tensor memory of two row tiles, and a unit has one.
+//
+// What bounds it.  8192 bf16 tokens at once (32 query and 8 KV heads of 128): 476 us, 1155 TFLOP/s, 60 % of a large library product; 2048 tokens
+// over 131072: 1600 us, 1360 TFLOP/s, with the clock at 1.55 GHz under the power limit; 8-bit chunks over 16000: 290 us, 960 TFLOP/s; 256 dims in a
+// window of 4096: 331 us, 880 TFLOP/s.  A pair of S tiles takes about 1850 clocks of which the tensor core works 1280 (the scores' product, 64 keys
+// wide, reads q and k from shared memory at its full rate, 48 clocks to an MMA instead of 32).  The rest is the chain from a tile's scores over its softmax (950) and
+// product to the scores two tiles on, with four waits of 200 to 400 clocks in it; tensor memory holds no third S tile beside two O of 128 dims.  With
+// 256 dims it is also the copies: 64 KB for every 64 keys of 128 rows, and a ring of little more than two tiles.
+// Tried and not kept: S of 128 keys, one to a row tile (1900 us for the long chunk), one warp issuing both products of a row tile in turn (1880 us and
+// 454 us for 256 dims: what it issues next waits behind what the tensor core has not begun), a warp for each row tile's products with the values and three instead of
+// four to load q (8192 tokens 552 us), four S tiles and scores 128 keys wide for 256 dims (347 us), polling instead of suspended waits
+// (549 us, as the waiting warps take issue slots), keys and values by cp.async where TMA can take them (573 us).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -85,6 +96,22 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
 __device__ __forceinline__ uint32_t f16_of_e4m3(uint32_t x) {  // both values of the low half: exact
     uint32_t r;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)x));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -199,6 +226,11 @@ static_assert(sizeof(Bars) <= 3 * 1024, "shared memory");
 // A warp's waits succeed or fail for all of its lanes.
 template <typename Bar> __device__ __forceinline__ bool warp_wait(const Waiter &wait, Bar bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait(bar, parity));
+}
+// One arrival for a warp, after what all of its lanes did: 32 of them on one address take as many turns.
+__device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
 }
 // Whether any thread of a group says x, in `any`; false: a wait ran out.  `turn` counts the group's votes.
 __device__ __forceinline__ bool group_any(const Waiter &wait, Bars &bars, int group, int &turn, bool x, bool &any) {
@@ -328,12 +360,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
 
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(&bars.full[i], C::kE4M3 ? 128 : TMA ? 1 : 128 + 4);
+            mbar_init(&bars.full[i], C::kE4M3 ? 4 : TMA ? 1 : 128 + 4);
             mbar_init(&bars.empty[i], C::kTiles);
         }
         for (int i = 0; i < 8; ++i) {
             mbar_init(&bars.raw_full[i], 1);
-            mbar_init(&bars.raw_empty[i], 128);
+            mbar_init(&bars.raw_empty[i], 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.q_full[i], 128);
@@ -342,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
         for (int i = 0; i < 2; ++i) {
             for (int j = 0; j < 2; ++j) {
                 mbar_init(&bars.s_full[i][j], 1);
-                mbar_init(&bars.p_full[i][j], 128);
+                mbar_init(&bars.p_full[i][j], 4);
                 mbar_init(&bars.pv_done[i][j], 1);
                 bars.skip[i][j] = 0;
             }
@@ -391,8 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
                 sts128(at + sw128_offset(key, chunk % 4 * 16 + 8), f16_of_e4m3(x[2]), f16_of_e4m3(x[2] >> 16), f16_of_e4m3(x[3]), f16_of_e4m3(x[3] >> 16));
             }
             fence_async_smem();
-            mbar_arrive(&bars.full[n % C::kStages]);
-            if (TMA) mbar_arrive(&bars.raw_empty[n % (C::kRaw ? C::kRaw : 1)]);
+            warp_arrive(&bars.full[n % C::kStages], lane);
+            if (TMA && lane == 0) mbar_arrive(&bars.raw_empty[n % (C::kRaw ? C::kRaw : 1)]);
             ++stage_out;
             return true;
         };
@@ -443,32 +475,41 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
                 const int uses = m ? units1 : units;
                 if (uses > 0 && !warp_wait(wait, &bars.q_empty[m], (uses - 1) & 1)) return false;
                 const uint32_t dst = smem_addr(q_smem) + m * C::kQTile + piece / 8 * kSlab;
-#pragma unroll 4
-                for (int i = 0; i < 128 / kRowStep; ++i, r += kRowStep) {
-                    const bool there = r < u.rows;
-                    const uint32_t to = dst + sw128_offset(r & 127, piece % 8 * 8);
-                    if constexpr (!C::kE4M3) {
-                        cp16(to, there ? src : (const uint16_t *)a.q, there);
-                    } else {
+                constexpr int kBatch = C::kE4M3 ? 8 : 4;  // rows of a lane whose loads are on their way together
+#pragma unroll 1
+                for (int i = 0; i < 128 / kRowStep; i += kBatch) {
+                    uint4 x[C::kE4M3 ? kBatch : 1];
+#pragma unroll
+                    for (int j = 0; j < kBatch; ++j) {
+                        const int row = r + j * kRowStep;
+                        const bool there = row < u.rows;
+                        if constexpr (C::kE4M3) x[j] = there ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
+                        else cp16(dst + sw128_offset(row & 127, piece % 8 * 8), there ? src : (const uint16_t *)a.q, there);
+                        src += step;
+                        if ((head += step_head) >= group) head -= group, src += carry;
+                    }
+                    if constexpr (C::kE4M3) {
                         // f16 of q times a power of two that takes the row's largest to 2^14 or so: 8 bits of any value down to 2^-30 of it,
                         // and what it loses below is lost in the fp32 sum too
-                        const uint4 x = there ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
-                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                        uint32_t most = 0;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) most = max(most, max(w[j] & 0x7fffu, w[j] >> 16 & 0x7fffu));
+                        for (int j = 0; j < kBatch; ++j) {
+                            const int row = r + j * kRowStep;
+                            const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+                            uint32_t most = 0;
 #pragma unroll
-                        for (int off = kLanes / 2; off; off >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
-                        const int e = min((int)(most >> 7), 254), lift = min(141 - e, 126);
-                        const float f = __uint_as_float((uint32_t)(127 + lift) << 23);
-                        uint32_t y[4];
+                            for (int k = 0; k < 4; ++k) most = max(most, max(w[k] & 0x7fffu, w[k] >> 16 & 0x7fffu));
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) y[j] = pack_f16x2(__uint_as_float(w[j] << 16) * f, __uint_as_float(w[j] & 0xffff0000u) * f);
-                        sts128(to, y[0], y[1], y[2], y[3]);
-                        if (piece == 0) bars.lift[uses % 3][r] = (int8_t)lift;
+                            for (int off = kLanes / 2; off; off >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
+                            const int e = min((int)(most >> 7), 254), lift = min(141 - e, 126);
+                            const float f = __uint_as_float((uint32_t)(127 + lift) << 23);
+                            uint32_t y[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) y[k] = pack_f16x2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
+                            sts128(dst + sw128_offset(row & 127, piece % 8 * 8), y[0], y[1], y[2], y[3]);
+                            if (piece == 0) bars.lift[uses % 3][row] = (int8_t)lift;
+                        }
                     }
-                    src += step;
-                    if ((head += step_head) >= group) head -= group, src += carry;
+                    r += kBatch * kRowStep;
                 }
                 if constexpr (C::kE4M3) {
                     fence_async_smem();
@@ -792,17 +833,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
                     }
                 }
                 const float base = ref == -INFINITY ? 0.f : ref - C::kShift;
-                float part[4] = {0.f, 0.f, 0.f, 0.f};
+                // two at once: a product and a sum to each instruction
+                const uint64_t f2 = pair(f, f), base2 = pair(-base, -base);
+                uint64_t part[2] = {0, 0};
                 float p[32];
 #pragma unroll
                 for (int j = 0; j < 64; j += 2) {
-                    const float x = ex2(s[j / 32][j % 32] * f - base), y = ex2(s[j / 32][j % 32 + 1] * f - base);
-                    part[j / 2 % 2 * 2] += x;
-                    part[j / 2 % 2 * 2 + 1] += y;
+                    float x, y;
+                    unpair(fma2(pair(s[j / 32][j % 32], s[j / 32][j % 32 + 1]), f2, base2), x, y);
+                    x = ex2(x), y = ex2(y);
+                    part[j / 2 % 2] = add2(part[j / 2 % 2], pair(x, y));
                     p[j / 2] = __uint_as_float(C::kE4M3 ? pack_f16x2(x, y) : pack_bf16x2(x, y));
                 }
                 tmem_st32(t_s, p);
-                sum += (part[0] + part[1]) + (part[2] + part[3]);
+                float even, odd;
+                unpair(add2(part[0], part[1]), even, odd);
+                sum += even + odd;
                 tmem_st_wait();
                 if (__builtin_expect(edge, 0)) {
                     const int at = stage + 2 * C::kParts * (i >> 1) + C::kParts;
@@ -824,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
                     bars.skip[m][place] = 0;
                 }
                 tc_fence_before();
-                mbar_arrive(&bars.p_full[m][place]);
+                warp_arrive(&bars.p_full[m][place], lane);
             }
             if (!ok) break;
             if (n > 0) {

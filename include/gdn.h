@@ -471,9 +471,11 @@ GDN_API gdn_status gdn_qk_rope(int32_t n, int32_t Hq, int32_t Hkv, int32_t d, gd
  * Everything else is as in gdn_paged_decode: heads, strides, types, what is never
  * used, where non-finite values reach (a later token's do not reach the rows before it).
  * Weights exp(z - max z) enter the product with V in the bits of o's type or more:
- * 8 with a GDN_BF16 cache, 11 with a GDN_E4M3 one, 22 with a GDN_F32 one.
- * Workspace: gdn_paged_prefill_workspace_bytes(cache, B, n, Hq), 256-byte aligned;
- * its contents need no set-up.  The call is several launches: host threads that
+ * 8 with a GDN_BF16 cache; 11 with a GDN_E4M3 one, or 2^-36 of the largest where that
+ * is coarser; 22 with a GDN_F32 one.  cu_new does not decrease; where it does, rows
+ * of [0, n) hold the attention of some request that names them, or stay as they were.
+ * Workspace: gdn_paged_prefill_workspace_bytes(cache, B, n, Hq), 256-byte aligned (41 MB
+ * at most, and 76 bytes for every 128 rows and request); its contents need no set-up.  The call is several launches: host threads that
  * share a stream need a workspace each, and so do two captured graphs that may run
  * at the same time.  gdn_paged_prefill_status synchronises `stream` and reports
  * the call that used the workspace last (GDN_ERR_TIMEOUT: a wait inside a kernel ran
