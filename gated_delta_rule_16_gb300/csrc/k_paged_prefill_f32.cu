@@ -16,9 +16,6 @@ namespace gdn {
 namespace prefill {
 namespace {
 
-using paged::cp16;
-using paged::cp_commit;
-using paged::cp_wait;
 using paged::exp2_fast;
 using paged::mma_tf32;
 using paged::split_tf32;

@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) * D > 512 ? 3 : 4) qk_rope
     for (int i = tid; i < a.pairs; i += kThreads) freq[i] = turns(a.freqs[i]);
     __syncthreads();
     const int t = blockIdx.x * kSlots + slot;
-    const bool real = t < a.n;
+    const bool real = (unsigned)t < (unsigned)a.n;  // the last CTA's groups may pass 2^31
     const int64_t pos = real ? a.positions[t] : 0;
 
     float cs[C][N], sn[C][N];

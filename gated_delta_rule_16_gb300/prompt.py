@@ -48,10 +48,13 @@ def gdn_qk_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e-
     kv_heads = k.shape[1]
     qs, ks = _rows(q, "q", q.dtype, (n, heads, d), dev), _rows(k, "k", q.dtype, (n, kv_heads, d), dev)
     if q_out is None:
-        q_out = paged._empty((n, heads, d), dtype=q.dtype, device=q.device)
+        q_out, qo = paged._empty((n, heads, d), dtype=q.dtype, device=q.device), (heads * d, d)
+    else:
+        qo = _rows(q_out, "q_out", q.dtype, (n, heads, d), dev)
     if k_out is None:
-        k_out = paged._empty((n, kv_heads, d), dtype=q.dtype, device=q.device)
-    qo, ko = _rows(q_out, "q_out", q.dtype, (n, heads, d), dev), _rows(k_out, "k_out", q.dtype, (n, kv_heads, d), dev)
+        k_out, ko = paged._empty((n, kv_heads, d), dtype=q.dtype, device=q.device), (kv_heads * d, d)
+    else:
+        ko = _rows(k_out, "k_out", q.dtype, (n, kv_heads, d), dev)
     pairs = freqs.numel()
     _call("gdn_qk_rope", dev, n, heads, kv_heads, d, code, q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1],
           _want(positions, "positions", _I32, (n,), dev), _want(freqs, "freqs", _F64, (pairs,), dev), pairs, int(interleaved), mscale,

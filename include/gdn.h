@@ -467,7 +467,8 @@ GDN_API gdn_status gdn_qk_rope(int32_t n, int32_t Hq, int32_t Hkv, int32_t d, gd
  *   o[t,h] = sum_j p_j v_j,  p = softmax_j(scale * <q[t,h], k_j>),
  *   lse[t,h] = log sum_j exp(scale * <q[t,h], k_j>)           (lse may be NULL).
  * A row left without a token gets o = 0 and lse = -inf.  Rows of no request are not
- * written (a captured step's rows behind cu_new[B]); rows of two requests hold either's.
+ * written (a captured step's rows behind cu_new[B]); rows of two requests hold either's.  o and
+ * lse overlap no input.
  * Everything else is as in gdn_paged_decode: heads, strides, types, what is never
  * used, where non-finite values reach (a later token's do not reach the rows before it).
  * Weights exp(z - max z) enter the product with V in the bits of o's type or more:
@@ -478,8 +479,9 @@ GDN_API gdn_status gdn_qk_rope(int32_t n, int32_t Hq, int32_t Hkv, int32_t d, gd
  * at most, and 76 bytes for every 128 rows and request); its contents need no set-up.  The call is several launches: host threads that
  * share a stream need a workspace each, and so do two captured graphs that may run
  * at the same time.  gdn_paged_prefill_status synchronises `stream` and reports
- * the call that used the workspace last (GDN_ERR_TIMEOUT: a wait inside a kernel ran
- * out and o and lse are not valid). */
+ * the gdn_paged_prefill call that used the workspace last (GDN_ERR_TIMEOUT: a wait
+ * inside a kernel ran out and o and lse are not valid); no other kind of call may have
+ * used it since. */
 GDN_API size_t gdn_paged_prefill_workspace_bytes(const gdn_kv_cache *cache, int32_t B, int32_t n, int32_t Hq);
 GDN_API gdn_status gdn_paged_prefill(const gdn_kv_cache *cache, int32_t B, int32_t n, int32_t Hq, gdn_dtype dtype,
                                      const void *q, int64_t q_stride_token, int64_t q_stride_head,

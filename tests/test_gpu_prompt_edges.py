@@ -1,5 +1,7 @@
 """The prompt chunk's operators at their edges: concurrent calls, layouts that TMA cannot describe, long lists of requests, rows
 that are masked almost everywhere.  References and tolerances are those of test_gpu_prompt.py."""
+from concurrent.futures import ThreadPoolExecutor
+
 import pytest
 import torch
 
@@ -202,3 +204,48 @@ def test_prompt_calls_captured_in_one_graph_and_replayed():
         g.replay()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert gdn.gdn_paged_prefill_status(ws) == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_attend_more_units_than_the_plan_holds_in_shared_memory(kind):
+    r = torch.Generator().manual_seed(5)
+    Case([(int(c), int(n)) for c, n in torch.randint(0, 5, (2600, 2), generator=r)] + [(40, 2)], kind=kind, d=64, page=8, heads=2, kv_heads=2).check()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_attend_queries_past_32_bits(kind):
+    c = Case([(70, 20), (0, 13)], kind=kind, heads=4, kv_heads=2)
+    want = c.check()
+    far = torch.empty(34 * 2 ** 27, dtype=c.q.dtype, device=dev()).as_strided(c.q.shape, (2 ** 27, 2 ** 25, 1))  # of 33 rows of 2^27
+    far.copy_(c.q)
+    c.q = far
+    assert all(torch.equal(x, y) for x, y in zip(c.call(), want))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_rope_and_logprobs_past_32_bits(kind):
+    store = torch.empty(34 * 2 ** 27, dtype=TYPES[kind], device=dev())
+    far = store.as_strided((33, 4, 128), (2 ** 27, 2 ** 25, 1))
+    x = torch.randn((33, 4, 128), device=dev(), generator=gen(4)).to(TYPES[kind])
+    pos, freqs = i32(list(range(33))), torch.linspace(0, 1, 64, dtype=torch.float64, device=dev())
+    far.copy_(x)
+    want = gdn.gdn_qk_rope(x, x[:, :1], pos, freqs)[0]
+    assert torch.equal(gdn.gdn_qk_rope(far, x[:, :1], pos, freqs)[0], want)
+    assert torch.equal(gdn.gdn_qk_rope(far, x[:, :1], pos, freqs, q_out=far)[0], want)
+    rows = store.as_strided((33, 5003), (2 ** 27, 1))
+    rows.copy_(torch.randn((33, 5003), device=dev(), generator=gen(5)))
+    check_logprobs(rows, list(range(33)), 7)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_attend_threads_of_one_stream(kind):
+    # each thread's calls have a workspace of their own, whatever comes between their launches
+    cases = [Case([(900, 70 + 10 * i), (0, 300), (33, 1)], kind=kind, seed=i, heads=4, kv_heads=2) for i in range(4)]
+    want = [c.call() for c in cases]
+    torch.cuda.synchronize()
+    with ThreadPoolExecutor(len(cases)) as pool:
+        got = list(pool.map(lambda c: [c.call() for _ in range(20)], cases))
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        for x in a:
+            assert torch.equal(x[0], b[0]) and torch.equal(x[1], b[1])
