@@ -611,24 +611,29 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
                 while (ok && walk.next()) {
                     const int n = walk.t1 - walk.t0;
                     if (n == 0) continue;
-                    if (m == 1 && walk.u.rows <= 128) {  // nothing to do but to say so, stage by stage
-                        for (int i = 0; ok && i < (n + 1) / 2; ++i) {
+                    if (m == 1 && walk.u.rows <= 128) {
+                        // Nothing to do but to say so, stage by stage.  A wait tells a phase from the one before it only, copies arrive in any
+                        // order, and a stage has keys and values by turns: so the values of the units before have to have come, and
+                        // those of this one are waited for like the keys.
+                        if (done[0] > 0 && !(ok = warp_wait(wait, pv_at + 16 + 8 * ((done[0] - 1) & 1), (done[0] - 1) >> 1 & 1))) break;
+                        for (int i = 0; i < (n + 1) / 2 * 2; ++i) {
                             if (!(ok = warp_wait(wait, full_at + 8 * at.slot, at.parity))) break;
                             if (leader) mbar_arrive(&bars.empty[at.slot]);
-                            at.step(2);
+                            at.step(1);
                         }
                         continue;
                     }
 #pragma unroll 1
                     for (int i = 0; i < n; ++i) {
                         const int tile = done[0] + i, place = tile & 1, half = i & 1;
+                        // the weights that lie over the scores of two tiles before have been used; before the wait for keys, whose stage may have
+                        // held the values of two pairs before: of those it is known now that they had come
+                        if (tile >= 2 && !(ok = warp_wait(wait, pv_at + 16 * m + 8 * place, ((tile >> 1) - 1) & 1))) break;
                         if (!half && !(ok = stages_ready(at))) break;
                         if (i == 0) {
                             if (!(ok = warp_wait(wait, smem_addr(&bars.q_full[m]), units & 1))) break;
                             if constexpr (!C::kE4M3) fence_async_smem();  // q is copied by cp.async
                         }
-                        // the weights that lie over the scores of two tiles before have been used
-                        if (tile >= 2 && !(ok = warp_wait(wait, pv_at + 16 * m + 8 * place, ((tile >> 1) - 1) & 1))) break;
                         tc_fence_after();
                         Place from = at;
 #pragma unroll
@@ -675,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
                             commit(pv_at + 16 * m + 8 * place);
                         }
                         if (half || i == n - 1) {
-                            release_stages(at, C::kTiles);
+                            release_stages(at, row_tiles);  // the other row tile's warp says the rest
                             at.step(2 * C::kParts);
                         }
                     }

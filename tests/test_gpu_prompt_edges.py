@@ -249,3 +249,31 @@ def test_attend_threads_of_one_stream(kind):
     for a, b in zip(got, want):
         for x in a:
             assert torch.equal(x[0], b[0]) and torch.equal(x[1], b[1])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d,page", [(64, 64), (128, 64), (128, 16), (128, 1), (256, 64)])
+def test_attend_copies_that_come_in_any_order(kind, d, page):
+    # units of one row tile and of two take turns over contexts that no cache holds: a stage of keys or values may come after later ones
+    sizes = [(13000, 100), (25000, 1), (9500, 1), (17000, 1), (6800, 1), (28000, 1), (5300, 70), (0, 60), (8800, 1), (30000, 130), (0, 1), (12800, 1), (64, 33), (2, 1), (22600, 1)]
+    scale = 8 if kind == "f32" or d == 256 else 1
+    c = Case([(a // scale, b) for a, b in sizes], kind=kind, heads=16, kv_heads=4, d=d, page=page)
+    ws = gdn.Workspace()
+    want = c.check(workspace=ws)
+    for _ in range(30):
+        got = c.call(workspace=ws)
+        assert gdn.gdn_paged_prefill_status(ws) == 0
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attend_units_of_one_tile_over_cold_keys(kind, d):
+    # a tile of keys and one of values to each unit, thousands in a row
+    c = Case([(0, 1 + i % 40) for i in range(3000)], kind=kind, heads=8, kv_heads=4, d=d, page=64)
+    ws = gdn.Workspace()
+    want = c.call(workspace=ws)
+    for _ in range(20):
+        got = c.call(workspace=ws)
+        assert gdn.gdn_paged_prefill_status(ws) == 0
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
