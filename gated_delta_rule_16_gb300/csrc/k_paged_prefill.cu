@@ -39,7 +39,7 @@ __device__ int64_t scan(int64_t x, int64_t *buf, int64_t &all) {
 }
 
 // One CTA: a thread per request counts its units, a thread per unit finds its request, rows and keys, a thread per CTA its run.
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(PrefillArgs a, int tile, int keys, int grid, int pad) {
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(PrefillArgs a, int tile, int keys, int grid, int pad, Weights weights) {
     __shared__ int64_t buf[32];
     __shared__ int64_t held[kHeldUnits];
     View v;
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PrefillArgs a, int t
             u.all_lo[1] = r1.lo;
             u.pad[0] = u.pad[1] = u.pad[2] = 0;
             v.unit[i] = u;
-            mine = u.tiles + pad;
+            mine = (u.rows > 128 ? weights.two : weights.one) * (u.tiles + pad);
         }
         int64_t all;
         const int64_t incl = cost + scan(mine, buf, all);
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PrefillArgs a, int t
     __syncthreads();
     const int64_t *ends = units <= kHeldUnits ? held : v.ends;
     const int64_t total = cost * a.c.Hkv;
-    const int ctas = (int)max((int64_t)1, min((int64_t)grid, total / (pad + 1)));
+    const int ctas = (int)max((int64_t)1, min((int64_t)grid, total / (weights.one * (pad + 1))));  // no two edges at the same tile
     for (int i = tid; i <= grid; i += kPlanThreads) {
         int4 run = make_int4(-1, 0, 0, 0);
         if (i == ctas || total == 0) run = i <= ctas ? make_int4(a.c.Hkv, 0, 0, 0) : run;
@@ -117,7 +117,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PrefillArgs a, int t
                 else lo = mid + 1;
             }
             const int64_t begin = lo ? ends[lo - 1] : 0;
-            run = make_int4((int)head, lo, (int)(rest - begin), (int)(ends[lo] - begin) - pad);
+            const Unit &u = v.unit[lo];
+            run = make_int4((int)head, lo, (int)(rest - begin) / (u.rows > 128 ? weights.two : weights.one), u.tiles);
         }
         v.runs[i] = run;
     }
@@ -207,7 +208,8 @@ cudaError_t launch_paged_prefill(const PrefillArgs &args, cudaStream_t stream) {
     a.group = divisor(a.Hq / a.c.Hkv);
     a.page = divisor(a.c.page);
     const int tile = row_tile(a.c.dtype, a.c.d), grid = wave(a.c.dtype, a.c.d);
-    cudaError_t e = launch_kernel(false, plan_kernel, 1, kPlanThreads, 0, stream, a, tile, key_tile(a.c.dtype, a.c.d), grid, unit_pad(a.c.dtype));
+    cudaError_t e = launch_kernel(false, plan_kernel, 1, kPlanThreads, 0, stream, a, tile, key_tile(a.c.dtype, a.c.d), grid, unit_pad(a.c.dtype),
+                                  unit_weights(a.c.dtype, a.c.d));
     if (e != cudaSuccess) return e;
     if (a.c.dtype == GDN_F32) {
         e = launch_f32(a, grid, stream);

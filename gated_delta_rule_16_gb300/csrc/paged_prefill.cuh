@@ -3,7 +3,7 @@
 //
 // A unit is a tile of rows (new token t, query head of one KV head's group, in this order) of one request with all the keys
 // they attend to, in tiles of 64 keys (32-bit storage: 32 or 16).  The units of all requests are laid end to end, once for each KV head, and the CTAs of one
-// wave get equal runs of key tiles; a unit cut by a CTA's edge leaves unnormalised fp32 parts that a last launch joins in
+// wave get equal runs of key tiles (weighed where units of one row tile take less); a unit cut by a CTA's edge leaves unnormalised fp32 parts that a last launch joins in
 // the keys' order.  Lengths are only known on the GPU, so a first launch of one CTA lists the units and finds the runs.  Causal rows
 // make units of 1 to hundreds of tiles, and equal runs need no luck with their order: of 8192 tokens at once every CTA
 // has the same number of tiles, and one row over 131072 is shared by all of them.
@@ -70,8 +70,15 @@ inline __host__ __device__ int row_tile(gdn_dtype kind, int d) { return kind == 
 inline __host__ __device__ int key_tile(gdn_dtype kind, int d) { return kind != GDN_F32 ? 64 : d == 256 ? 16 : 32; }
 // A unit costs its tiles and this many more, for its beginning and end (8-bit caches: most of all for q's conversion, in turn with the keys'),
 // and a CTA takes one more than that at least.  8192 bf16 tokens at once: 484 us with 2, 476 with 3, 479 with 4; 8-bit chunks of up to 512
-// tokens over 16000: 329 with 3, 314 with 5, 299 with 8, 290 with 10, 294 with 12.
+// tokens over 16000: 329 with 3, 314 with 5, 299 with 8, 290 with 10, 294 with 12 (279 with 10 since units of one row tile are weighed and a tile's product is waited for ahead of its keys).
 inline __host__ __device__ int unit_pad(gdn_dtype kind) { return kind == GDN_E4M3 ? 10 : 3; }
+// What a tile costs in a unit of one row tile of 128, and of two.  With 256 bytes to a bf16 row the copies take as long for one as for two:
+// 32 requests of mostly one new token, up to 4096 behind them, 85.9 us with 1:1, 87.5 with 3:4, 92.2 with 2:3.  Rows of 128 bytes or less: bf16 of 64
+// dims 76.9, 71.2 and 74.2 us, 8-bit of 128 104, 96 and 101, of 64 89.8, 84.7 and 84.3.
+struct Weights { int one, two; };
+inline __host__ __device__ Weights unit_weights(gdn_dtype kind, int d) {
+    return row_tile(kind, d) == 128 || (kind == GDN_BF16 && d == 128) ? Weights{1, 1} : Weights{3, 4};
+}
 // CTAs of a wave: one per SM, two where the registers of the warp-MMA kernel allow.
 inline __host__ __device__ int wave(gdn_dtype kind, int d) { return kind == GDN_F32 && d == 64 ? kMaxCtas : kMaxCtas / 2; }
 
