@@ -557,6 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
             }
         }
         if (ok) settle();
+        cp_commit();
         cp_wait<0>();
     } else if (warpgroup == 3) {
         // ---- products -------------------------------------------------------------------------------------
@@ -738,11 +739,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
                     }
                 }
             }
-            // what was asked for has to arrive before the memory may go
+            // what was asked for has to arrive before the memory may go, whether or not a wait has run out
             for (int i = 0; i < kRing; ++i) {
                 const int s = (slot + i) % kRing;
                 const uint32_t last = turn - (s >= slot);  // of the slot's turns
-                if (turn > 0 || s < slot) warp_wait(wait, C::kE4M3 ? &bars.raw_full[s] : &bars.full[s], last & 1);
+                if (turn > 0 || s < slot) mbar_wait(C::kE4M3 ? &bars.raw_full[s] : &bars.full[s], last & 1);
             }
         }
         __syncwarp();
