@@ -201,7 +201,11 @@ gdn_status gdn_paged_prefill(const gdn_kv_cache *cache, int32_t B, int32_t n, in
     if (dtype != (cache->dtype == GDN_E4M3 ? GDN_BF16 : cache->dtype)) return GDN_ERR_DTYPE;
     if ((int64_t)n * Hq > INT32_MAX - 255) return GDN_ERR_SHAPE;
     if ((int64_t)max_pages * cache->page > INT32_MAX - 127) return GDN_ERR_UNSUPPORTED;  // token positions are int32
-    if (B == 0 || n == 0) return GDN_OK;
+    if (B == 0 || n == 0) {
+        // a call without rows uses its workspace too: the status asked for next is this call's
+        if (!workspace || (uintptr_t)workspace % kWsAlign || workspace_bytes < sizeof(int32_t) || !device_ok()) return GDN_OK;
+        return cudaMemsetAsync(workspace, 0, sizeof(int32_t), (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    }
     // with no page in the pool or no column in the table every row is empty, but o and lse are still written
     if (cache->pages > 0 && max_pages > 0) {
         if ((st = check_cache(cache)) != GDN_OK) return st;

@@ -481,7 +481,8 @@ GDN_API gdn_status gdn_qk_rope(int32_t n, int32_t Hq, int32_t Hkv, int32_t d, gd
  * at the same time.  gdn_paged_prefill_status synchronises `stream` and reports
  * the gdn_paged_prefill call that used the workspace last (GDN_ERR_TIMEOUT: a wait
  * inside a kernel ran out and o and lse are not valid); no other kind of call may have
- * used it since. */
+ * used it since.  A call without rows (B or n 0) writes its workspace's status too, where it is
+ * given an aligned one. */
 GDN_API size_t gdn_paged_prefill_workspace_bytes(const gdn_kv_cache *cache, int32_t B, int32_t n, int32_t Hq);
 GDN_API gdn_status gdn_paged_prefill(const gdn_kv_cache *cache, int32_t B, int32_t n, int32_t Hq, gdn_dtype dtype,
                                      const void *q, int64_t q_stride_token, int64_t q_stride_head,
