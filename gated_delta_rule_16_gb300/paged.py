@@ -32,10 +32,10 @@ _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 
 class _Local(threading.local):
     """A thread's default workspaces, by device and stream.  Attention is two launches, between which another thread's
-    calls on the same stream may come."""
+    calls on the same stream may come.  Attention of new tokens has its own, whose status stays what its last call left."""
 
     def __init__(self):
-        self.ws = {}
+        self.ws, self.prefill = {}, {}
 
 
 _local = _Local()
@@ -96,10 +96,11 @@ def _on(stream, dev, fn, given, *args, **kw):
     return got
 
 
-def _workspace(ws, nbytes, dev, handle):
+def _workspace(ws, nbytes, dev, handle, own=None):
     """(address, bytes) of the caller's workspace, or of this thread, device and stream's own."""
     if ws is None:
-        own = _local.ws
+        if own is None:
+            own = _local.ws
         buf = own.get((dev, handle))
         if buf is None or buf.numel() < nbytes:
             buf = own[dev, handle] = _empty((nbytes,), dtype=torch.uint8, device=torch.device("cuda", dev))

@@ -71,7 +71,8 @@ def gdn_paged_prefill(q, k_cache, v_cache, block_table, seq_lens, cu_new, *, k_s
     Request b's tokens are rows cu_new[b] to cu_new[b + 1] (cu_new [B+1] int32) and the last of its seq_lens[b] tokens; each attends
     to those up to itself, or to the last `window` of them.  block_table [B, max_pages] int32 (its row stride may be 0); scale:
     default dim ** -0.5.  Rows behind cu_new[B] are left as they are.  Returns (o [n, heads, dim] in q's dtype, lse [n, heads]
-    fp32).  A `workspace` belongs to one call at a time; gdn_paged_prefill_status asks it whether the call ran through."""
+    fp32).  A `workspace` belongs to one call at a time (default: this thread's for the device and stream); gdn_paged_prefill_status
+    asks whether the call ran through."""
     dev = _cuda(q, "q")
     if stream is not None and _elsewhere(dev, stream):
         return _on(stream, dev, gdn_paged_prefill, (o, lse, workspace), q, k_cache, v_cache, block_table, seq_lens, cu_new,
@@ -110,17 +111,22 @@ def gdn_paged_prefill(q, k_cache, v_cache, block_table, seq_lens, cu_new, *, k_s
         if len(_ws_bytes) > 4096:  # prompts of ever other lengths
             _ws_bytes.clear()
         nbytes = _ws_bytes[key] = load().gdn_paged_prefill_workspace_bytes(c, B, n, heads)
-    ws, ws_bytes = _workspace(workspace, nbytes, dev, handle)
+    ws, ws_bytes = _workspace(workspace, nbytes, dev, handle, paged._local.prefill)
     _call("gdn_paged_prefill", dev, c, B, n, heads, code, q.data_ptr(), qs[0], qs[1], block_table.data_ptr(), ts[0], max_pages,
           _want(seq_lens, "seq_lens", _I32, (B,), dev), _want(cu_new, "cu_new", _I32, (B + 1,), dev), window,
           d ** -0.5 if scale is None else scale, o_at, lse_at, ws, ws_bytes, handle)
     return o, lse
 
 
-def gdn_paged_prefill_status(workspace, stream=None) -> int:
+def gdn_paged_prefill_status(workspace=None, stream=None) -> int:
     """Status of the gdn_paged_prefill call that used a workspace last (synchronises the stream): 0, or 10 (GDN_ERR_TIMEOUT)
-    if a wait inside a kernel ran out, with the outputs not valid."""
-    buf = workspace.buf if isinstance(workspace, Workspace) else workspace
+    if a wait inside a kernel ran out, with the outputs not valid.  Without a workspace: of this thread's last call without one on
+    the stream (default: the current one of the current device)."""
+    if workspace is None:
+        dev = torch.cuda.current_device() if stream is None else stream.device_index
+        buf = paged._local.prefill.get((dev, _handle(dev, stream)))
+    else:
+        buf = workspace.buf if isinstance(workspace, Workspace) else workspace
     if buf is None:
         raise ValueError("no call has used the workspace")
     dev = _cuda(buf, "workspace")
