@@ -1,6 +1,7 @@
 // paged_api.cu -- the extern "C" entry points of the decode-step and prompt-chunk operators (declared in
 // include/gdn.h): argument validation and launches.  No allocation, no synchronisation
 // except in the status query.
+#include "overlap.cuh"
 #include "paged.cuh"
 
 namespace gdn {
@@ -180,6 +181,18 @@ gdn_status gdn_qk_rope(int32_t n, int32_t Hq, int32_t Hkv, int32_t d, gdn_dtype 
         if (x.in == x.out && ((n > 1 && x.tok != x.out_tok) || (x.heads > 1 && x.head != x.out_head))) return GDN_ERR_UNSUPPORTED;
     }
     if (!device_ok()) return GDN_ERR_DEVICE;
+    // a row that is read after another CTA has written there, or written twice
+    const int64_t size = bytes_of(dtype);
+    Pieces in[2], out[2];
+    for (int i = 0; i < 2; ++i) {
+        const Side &x = sides[i];
+        in[i] = pieces(x.in, d * size, n, x.tok * size, x.heads, x.head * size);
+        out[i] = pieces(x.out, d * size, n, x.out_tok * size, x.heads, x.out_head * size);
+    }
+    if (overlaps_itself(out[0]) || overlaps_itself(out[1]) || overlap(out[0], out[1])) return GDN_ERR_UNSUPPORTED;
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2; ++j)
+            if (!(i == j && sides[i].in == sides[i].out) && overlap(in[i], out[j])) return GDN_ERR_UNSUPPORTED;
     const RopeArgs a = {n, Hq, Hkv, d, dtype, q, k, q_out, k_out, q_stride_token, q_stride_head, k_stride_token, k_stride_head,
                         q_out_stride_token, q_out_stride_head, k_out_stride_token, k_out_stride_head, positions, freqs,
                         pairs, interleaved, mscale, eps, q_weight, k_weight, 0};
@@ -216,8 +229,26 @@ gdn_status gdn_paged_prefill(const gdn_kv_cache *cache, int32_t B, int32_t n, in
         (((uintptr_t)block_table | (uintptr_t)seq_lens | (uintptr_t)cu_new | (uintptr_t)lse) & 3u) ||
         (uintptr_t)workspace % kWsAlign)
         return GDN_ERR_ALIGN;
-    if (workspace_bytes < gdn_paged_prefill_workspace_bytes(cache, B, n, Hq)) return GDN_ERR_WORKSPACE;
+    const size_t need = gdn_paged_prefill_workspace_bytes(cache, B, n, Hq);
+    if (workspace_bytes < need) return GDN_ERR_WORKSPACE;
     if (!device_ok()) return GDN_ERR_DEVICE;
+    // what one CTA writes while another reads; o over q itself is in order: a row's q has been read by all who need it when its o is written
+    const int64_t size = bytes_of(dtype), d = cache->d;
+    const bool in_place = o == q && (n == 1 || q_stride_token == Hq * d) && (Hq == 1 || q_stride_head == d);
+    const int64_t cell = bytes_of(cache->dtype), used = cache->pages > 0 && max_pages > 0 ? cache->pages : 0;
+    auto cells = [&](const void *x) {
+        return pieces(x, d * cell, used, cache->stride_page * cell, cache->page, cache->stride_token * cell, cache->Hkv, cache->stride_head * cell);
+    };
+    const Pieces in[] = {pieces(q, in_place ? 0 : d * size, n, q_stride_token * size, Hq, q_stride_head * size),
+                         pieces(block_table, used ? 4ll * max_pages : 0, B, 4 * table_stride, 1, 0), pieces(seq_lens, 4ll * B), pieces(cu_new, 4 * (B + 1ll)),
+                         cells(cache->k), cells(cache->v)};
+    const Pieces out[] = {pieces(o, n * Hq * d * size), pieces(lse, lse ? 4ll * n * Hq : 0), pieces(workspace, (int64_t)need)};
+    for (const Pieces &x : out) {
+        for (const Pieces &y : in)
+            if (overlap(x, y)) return GDN_ERR_UNSUPPORTED;
+        for (const Pieces &y : out)
+            if (&x < &y && overlap(x, y)) return GDN_ERR_UNSUPPORTED;
+    }
     PrefillArgs a = {*cache, B, n, Hq, q, q_stride_token, q_stride_head, block_table, table_stride,
                      cache->pages > 0 ? max_pages : 0, window, seq_lens, cu_new, scale, o, lse, workspace};
     if (a.max_pages == 0) a.c.k_scale = a.c.v_scale = nullptr;

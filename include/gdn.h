@@ -449,8 +449,8 @@ GDN_API gdn_status gdn_sample(int32_t B, int32_t V, gdn_dtype dtype, const void 
  * freqs [pairs] fp64 in radians per token (finite); positions any int32.  Angles are
  * products of whole numbers modulo a turn: they lose nothing at far positions beyond
  * what freqs itself, in 53 bits, leaves open.  q_out may be q, and k_out k, with
- * the same strides (other strides there are GDN_ERR_UNSUPPORTED); apart from that
- * outputs do not overlap inputs.  d is 64, 128 or 256; Hq or Hkv may be 0, whose
+ * the same strides; apart from that outputs that share memory with q, k, one another or
+ * themselves are GDN_ERR_UNSUPPORTED (slices of one projection do not).  d is 64, 128 or 256; Hq or Hkv may be 0, whose
  * pointers are not looked at. */
 GDN_API gdn_status gdn_qk_rope(int32_t n, int32_t Hq, int32_t Hkv, int32_t d, gdn_dtype dtype, const void *q,
                                int64_t q_stride_token, int64_t q_stride_head, const void *k, int64_t k_stride_token,
@@ -467,8 +467,9 @@ GDN_API gdn_status gdn_qk_rope(int32_t n, int32_t Hq, int32_t Hkv, int32_t d, gd
  *   o[t,h] = sum_j p_j v_j,  p = softmax_j(scale * <q[t,h], k_j>),
  *   lse[t,h] = log sum_j exp(scale * <q[t,h], k_j>)           (lse may be NULL).
  * A row left without a token gets o = 0 and lse = -inf.  Rows of no request are not
- * written (a captured step's rows behind cu_new[B]); rows of two requests hold either's.  o and
- * lse overlap no input.
+ * written (a captured step's rows behind cu_new[B]); rows of two requests hold either's.  o may
+ * be q where q is contiguous; apart from that o, lse and the workspace share no memory with
+ * one another or an input (GDN_ERR_UNSUPPORTED).
  * Everything else is as in gdn_paged_decode: heads, strides, types, what is never
  * used, where non-finite values reach (a later token's do not reach the rows before it).
  * Weights exp(z - max z) enter the product with V in the bits of o's type or more:

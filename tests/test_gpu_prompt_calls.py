@@ -1,10 +1,10 @@
-"""What a program meets around the prompt chunk's calls: the status of calls without rows.  References and
+"""What a program meets around the prompt chunk's calls: the status of calls without rows, outputs that share memory.  References and
 tolerances are those of test_gpu_prompt.py."""
 import pytest
 import torch
 
 import gated_delta_rule_16_gb300 as gdn
-from test_gpu_prompt import KINDS, Case, _built, i32  # noqa: F401
+from test_gpu_prompt import KINDS, Case, _built, dev, i32  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -26,3 +26,77 @@ def test_status_after_a_call_without_rows(kind, used):
         assert (ws.buf[4:] == 0xFF).all()
     c.check(workspace=ws)
     assert gdn.gdn_paged_prefill_status(ws) == 0
+
+
+# ---- outputs that share memory -------------------------------------------------------------------
+def refused(fn, *tensors):
+    """The call is GDN_ERR_UNSUPPORTED and writes nothing."""
+    before = [t.clone() for t in tensors]
+    with pytest.raises(gdn.GdnError) as e:
+        fn()
+    assert e.value.status == 6
+    torch.cuda.synchronize()
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(tensors, before))
+
+
+def test_rope_outputs_that_share_memory():
+    n, d = 40, 128
+    buf = torch.randn((n + 2, 16, d), device=dev()).bfloat16()
+    q, k = buf[:n, :8], buf[:n, 8:10]
+    pos, freqs = i32(list(range(n))), 0.5 ** torch.arange(64, dtype=torch.float64, device=dev())
+    go = lambda q_out=None, k_out=None, q=q, k=k: gdn.gdn_qk_rope(q, k, pos, freqs, q_out=q_out, k_out=k_out)
+    want = go()
+    refused(lambda: go(buf[1:n + 1, :8]), buf)            # q, a token on
+    refused(lambda: go(buf[:n, 1:9]), buf)                # a head on
+    refused(lambda: go(buf[:n, 3:11]), buf)               # over some of q and of k
+    refused(lambda: go(buf[:n, 9:].as_strided((n, 8, d), (16 * d, d - 64, 1))), buf)  # heads over one another, and k
+    refused(lambda: go(k_out=buf[:n, 7:9]), buf)
+    refused(lambda: go(buf[:n, :8], q=buf[:n, :8], k=buf[:n, 4:6]), buf)   # in place over what k is
+    refused(lambda: go(buf[:n, :2], buf[:n, 8:10], q=k, k=q[:, :2]), buf)  # each over the other
+    refused(lambda: go(buf[:n, 10:11].expand(n, 8, d)), buf)  # every head to one place
+    refused(lambda: go(buf[:1, 10:].as_strided((n, 6, d), (0, d, 1)), q=q[:, :6]), buf)
+    out = torch.zeros((n, 9, d), dtype=torch.bfloat16, device=dev())
+    refused(lambda: go(out[:, :8], out[:, 7:9]), out)
+    # what shares no byte: slices of the projection itself, and one buffer for both outputs
+    got = go(buf[:n, 10:16], q=q[:, :6])
+    assert torch.equal(got[0], want[0][:, :6]) and torch.equal(got[1], want[1])
+    wide = torch.zeros((n, 10, d), dtype=torch.bfloat16, device=dev())
+    got = go(wide[:, :8], wide[:, 8:])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    major = torch.zeros((10, n, d), dtype=torch.bfloat16, device=dev()).transpose(0, 1)
+    got = go(major[:, :8], major[:, 8:])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    got = go(q, k)
+    assert got[0] is q and torch.equal(q, want[0]) and torch.equal(k, want[1])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_attend_outputs_that_share_memory(kind):
+    c = Case([(300, 50), (9, 30)], kind=kind, heads=8, kv_heads=2)
+    n, heads, d = c.q.shape
+    want, want_lse = c.check()
+    buf = torch.zeros((n + 3, heads, d), dtype=c.qkind, device=dev())
+    buf[:n] = c.q
+    at = lambda x, shape: x.reshape(-1)[:shape.numel()].view(shape)
+    q, c.q = c.q, buf[:n]
+    refused(lambda: c.call(o=buf[1:n + 1]), buf)
+    refused(lambda: c.call(lse=at(buf.view(torch.float32), want_lse.shape)), buf)
+    if kind == "bf16":
+        refused(lambda: c.call(o=at(c.k, q.shape)), c.k)
+        refused(lambda: c.call(o=at(c.v, q.shape)), c.v)
+    o = torch.zeros(2 * q.numel(), dtype=c.qkind, device=dev())
+    refused(lambda: c.call(o=at(o, q.shape), lse=at(o.view(torch.float32)[8:], want_lse.shape)), o)
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device=dev())
+    refused(lambda: c.call(o=at(ws.view(c.qkind), q.shape), workspace=ws), ws)
+    wide = torch.zeros((n, heads + 3, d), dtype=c.qkind, device=dev())
+    wide[:, :heads] = q
+    c.q = wide[:, :heads]
+    refused(lambda: c.call(o=wide.view(-1)[:q.numel()].view(q.shape)), wide)
+    # in place, where the layouts are one; rows that are cut and joined too
+    c.q = buf[:n]
+    got, got_lse = c.call(o=buf[:n])
+    assert torch.equal(got, want) and torch.equal(got_lse, want_lse) and not buf[n:].any()
+    long = Case([(9000, 3), (0, 700)], kind=kind, heads=4, kv_heads=1, page=64)
+    want, want_lse = long.call()
+    got, got_lse = long.call(o=long.q)
+    assert torch.equal(got, want) and torch.equal(got_lse, want_lse)
