@@ -1,5 +1,5 @@
-"""What a program meets around the prompt chunk's calls: the status of calls without rows, outputs that share memory.  References and
-tolerances are those of test_gpu_prompt.py."""
+"""What a program meets around the prompt chunk's calls: the status of calls without rows, outputs that share memory, the end of
+fp32's range.  References and tolerances are those of test_gpu_prompt.py."""
 import pytest
 import torch
 
@@ -100,3 +100,28 @@ def test_attend_outputs_that_share_memory(kind):
     want, want_lse = long.call()
     got, got_lse = long.call(o=long.q)
     assert torch.equal(got, want) and torch.equal(got_lse, want_lse)
+
+
+# ---- the end of fp32's range ---------------------------------------------------------------------
+@pytest.mark.parametrize("call", ["decode", "prefill"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_fp32_magnitudes_count_as_infinite_from_the_documented_one_on(call, d, sign):
+    # 2^128 - 2^116 is what rounds to infinity in the 11 bits of a high tf32 term; the number before it does not
+    border = torch.tensor(0x7f7ff000, dtype=torch.int32).view(torch.float32).double().item()
+    assert border == 2.0 ** 128 - 2.0 ** 116
+    for bits, finite in ((0x7f7fefff, True), (0x7f7ff000, False), (0x7f7ff7ff, False), (0x7f7fffff, False)):
+        c = Case([(0, 1)], kind="f32", heads=2, kv_heads=1, d=d)
+        x = sign * torch.tensor(bits, dtype=torch.int32).view(torch.float32).item()
+        at = int(c.table[0, 0]), 0, 0
+        c.v[at][5] = x
+        go = lambda: gdn.gdn_paged_decode(c.q, c.k, c.v, c.table, c.lens) if call == "decode" else c.call()
+        o, lse = go()
+        assert bool(o[..., 5].isfinite().all()) == finite and lse.isfinite().all()
+        if finite:
+            # one token has a weight of 1: two terms of 11 bits each, and one rounding
+            assert ((o[0, :, 5].double() / x - 1).abs() <= 2.0 ** -22 + 2.0 ** -24).all()
+        c.v[at][5] = 1.0
+        c.k[at][3], c.q[..., 3] = x, 2.0 ** -120
+        o, lse = go()
+        assert bool(lse.isfinite().all()) == finite
