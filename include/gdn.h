@@ -467,15 +467,17 @@ GDN_API gdn_status gdn_qk_rope(int32_t n, int32_t Hq, int32_t Hkv, int32_t d, gd
  *   o[t,h] = sum_j p_j v_j,  p = softmax_j(scale * <q[t,h], k_j>),
  *   lse[t,h] = log sum_j exp(scale * <q[t,h], k_j>)           (lse may be NULL).
  * A row left without a token gets o = 0 and lse = -inf.  Rows of no request are not
- * written (a captured step's rows behind cu_new[B]); rows of two requests hold either's.  o may
+ * written (a captured step's rows behind cu_new[B]).  o may
  * be q where q is contiguous; apart from that o, lse and the workspace share no memory with
  * one another or an input (GDN_ERR_UNSUPPORTED).
  * Everything else is as in gdn_paged_decode: heads, strides, types, what is never
  * used, where non-finite values reach (a later token's do not reach the rows before it).
  * Weights exp(z - max z) enter the product with V in the bits of o's type or more:
  * 8 with a GDN_BF16 cache; 11 with a GDN_E4M3 one, or 2^-36 of the largest where that
- * is coarser; 22 with a GDN_F32 one.  cu_new does not decrease; where it does, rows
- * of [0, n) hold the attention of some request that names them, or stay as they were.
+ * is coarser; 22 with a GDN_F32 one.  cu_new does not decrease.  Where it does, nothing
+ * but rows of [0, n) that a request names is written: one that several name holds pieces of
+ * their attentions, in o and lse apart, and where the requests' rows are more than n in all,
+ * some stay as they were.
  * Workspace: gdn_paged_prefill_workspace_bytes(cache, B, n, Hq), 256-byte aligned (41 MB
  * at most, and 76 bytes for every 128 rows and request); its contents need no set-up.  The call is several launches: host threads that
  * share a stream need a workspace each, and so do two captured graphs that may run

@@ -1,5 +1,7 @@
 """What a program meets around the prompt chunk's calls: the status of calls without rows, outputs that share memory, the end of
-fp32's range.  References and tolerances are those of test_gpu_prompt.py."""
+fp32's range, lists of requests in any order.  References and tolerances are those of test_gpu_prompt.py."""
+import copy
+
 import pytest
 import torch
 
@@ -125,3 +127,59 @@ def test_fp32_magnitudes_count_as_infinite_from_the_documented_one_on(call, d, s
         c.k[at][3], c.q[..., 3] = x, 2.0 ** -120
         o, lse = go()
         assert bool(lse.isfinite().all()) == finite
+
+
+# ---- lists of requests ---------------------------------------------------------------------------
+class Guarded:
+    """o and lse inside larger buffers of 7."""
+
+    def __init__(self, c, rows=40):
+        n, heads, d = c.q.shape
+        self.rows, self.all_o = rows, torch.full((n + 2 * rows, heads, d), 7.0, dtype=c.qkind, device=dev())
+        self.all_lse = torch.full((n + 2 * rows, heads), 7.0, device=dev())
+        self.o, self.lse = self.all_o[rows:rows + n], self.all_lse[rows:rows + n]
+
+    def untouched(self):
+        return all((x[:self.rows] == 7).all() and (x[-self.rows:] == 7).all() for x in (self.all_o, self.all_lse))
+
+
+def alone(c, b, lo, hi):
+    """(o, lse and their bounds) of the rows [lo, hi) that request b names, as if it were the only one."""
+    x = copy.copy(c)
+    x.table, x.cu = c.table[b:b + 1], i32([lo, hi])
+    x.lens = i32([max(0, int(c.lens[b])) - int(c.cu[b + 1]) + hi])
+    return x.ref()
+
+
+LISTS = [[0, 20, 15, 50], [60, 10, 2 ** 31 - 1, 5], [-7, 1000, 0, 95], [0, 100, 100, 100], [100, 0, 100, 0], [30, 30, 30, 30], [90, 100, 0, 20],
+         [5, 5, -2 ** 31, 2 ** 31 - 1]]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("cu", LISTS)
+@pytest.mark.parametrize("repeat", [1, 5])
+def test_attend_lists_of_requests_in_no_order(kind, cu, repeat):
+    c = Case([(50, 20), (30, 40), (0, 30)], kind=kind, heads=4, kv_heads=2, behind=10)
+    n = c.q.shape[0]
+    cu = cu + (cu[1:] if cu[0] == 0 else cu) * (repeat - 1)
+    B = len(cu) - 1
+    c.table, c.lens = c.table.repeat(-(-B // 3), 1)[:B].contiguous(), c.lens.repeat(-(-B // 3))[:B].contiguous()
+    c.cu = i32(cu)
+    ws, out = gdn.Workspace(), Guarded(c)
+    c.call(o=out.o, lse=out.lse, workspace=ws)
+    assert gdn.gdn_paged_prefill_status(ws) == 0 and out.untouched()
+    owners, fine_o, fine_lse = torch.zeros(n, dtype=torch.int64, device=dev()), (out.o == 7).clone(), (out.lse == 7).clone()
+    stayed = fine_o.flatten(1).all(1) & fine_lse.all(1)
+    close = lambda x, y, far: (x == y) | ((x - y).abs() <= far)
+    for b in range(B):
+        lo, hi = min(max(cu[b], 0), n), min(cu[b + 1], n)
+        if hi <= lo:
+            continue
+        o, lse, o_far, lse_far = (x[lo:hi] for x in alone(c, b, lo, hi))
+        owners[lo:hi] += 1
+        fine_o[lo:hi] |= close(out.o[lo:hi].double(), o, o_far)
+        fine_lse[lo:hi] |= close(out.lse[lo:hi].double(), lse, lse_far)
+    assert stayed[owners == 0].all()                     # rows of no request
+    assert fine_o.all() and fine_lse.all()               # every piece is that of a request that names the row
+    if int(owners.sum()) <= n:
+        assert not stayed[owners > 0].any()
