@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import gated_delta_rule_16_gb300 as gdn
-from test_gpu_prompt import KINDS, Case, _built, dev, i32  # noqa: F401
+from test_gpu_prompt import INF, KINDS, Case, _built, dev, i32, same  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -183,3 +183,33 @@ def test_attend_lists_of_requests_in_no_order(kind, cu, repeat):
     assert fine_o.all() and fine_lse.all()               # every piece is that of a request that names the row
     if int(owners.sum()) <= n:
         assert not stayed[owners > 0].any()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_attend_lse_of_requests_that_share_a_table_row(kind):
+    c = Case([(64, 32)], heads=4, kv_heads=2, kind=kind)
+    want, want_lse, o_far, lse_far = c.ref()
+    o, lse = gdn.gdn_paged_prefill(c.q, c.k, c.v, c.table.expand(2, -1), i32([80, 96]), i32([0, 16, 32]), **c.scales)
+    same(o.double(), want, o_far)
+    same(lse.double(), want_lse, lse_far)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_attend_lse_of_a_sequence_longer_than_its_table(kind):
+    c = Case([(300, 150), (40, 30), (0, 20)], kind=kind)
+    c.lens.copy_(i32([10 ** 6, 10, -5]))
+    c.table[0, -1] = -1
+    o, lse = c.check()
+    assert (lse[150:170] == -INF).all() and (lse[180:] == -INF).all() and lse[:150].isfinite().all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_attend_lse_of_rows_behind_others_that_stay(kind):
+    c = Case([(40, 20), (3, 4)], kind=kind, behind=10)
+    c.cu += 5  # rows 0 to 4 are nobody's
+    out = Guarded(c)
+    want, want_lse, o_far, lse_far = c.ref()
+    c.call(o=out.o, lse=out.lse)
+    same(out.o[5:29].double(), want[5:29], o_far[5:29])
+    same(out.lse[5:29].double(), want_lse[5:29], lse_far[5:29])
+    assert out.untouched() and all((x[:5] == 7).all() and (x[29:] == 7).all() for x in (out.o, out.lse))
