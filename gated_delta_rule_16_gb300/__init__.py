@@ -47,4 +47,5 @@ from .prompt import (  # noqa: F401
     gdn_paged_prefill,
     gdn_paged_prefill_status,
     gdn_qk_rope,
+    gdn_selftest_paged_prefill_wait,
 )

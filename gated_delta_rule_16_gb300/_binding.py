@@ -29,7 +29,7 @@ EXPORTS = ("gdn_workspace_bytes", "gdn_select_events", "gdn_events_status", "gdn
            "gdn_workspace_bytes_ex", "gdn_events_bytes", "gdn_events_carve", "gdn_noalloc_status",
            "gdn_select_events_gamma", "gdn_page_tables", "gdn_page_tables_status", "gdn_kv_append",
            "gdn_paged_decode", "gdn_paged_decode_workspace_bytes", "gdn_sample", "gdn_qk_rope", "gdn_paged_prefill",
-           "gdn_paged_prefill_workspace_bytes", "gdn_paged_prefill_status", "gdn_logprobs")
+           "gdn_paged_prefill_workspace_bytes", "gdn_paged_prefill_status", "gdn_logprobs", "gdn_selftest_paged_prefill_wait")
 STAGES = ("select", "prefix", "intra", "wbuild", "scan_runs", "scan_chain", "scan", "output", "selector")
 
 
@@ -151,6 +151,8 @@ def load(path: str | None = None):
             lib.gdn_paged_prefill.restype = i32
             lib.gdn_paged_prefill_status.argtypes = [vp, vp]
             lib.gdn_paged_prefill_status.restype = i32
+            lib.gdn_selftest_paged_prefill_wait.argtypes = [i32]
+            lib.gdn_selftest_paged_prefill_wait.restype = i32
             lib.gdn_logprobs.argtypes = [i32, i32, i32, vp, i64, vp, i32, vp, vp, vp, vp, vp]
             lib.gdn_logprobs.restype = i32
             lib.gdn_version.argtypes = []

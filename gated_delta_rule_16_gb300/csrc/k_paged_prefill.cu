@@ -219,7 +219,8 @@ cudaError_t launch_paged_prefill(const PrefillArgs &args, cudaStream_t stream) {
         while (a.c.page % box) box /= 2;
         CUtensorMap maps[2];
         const bool tma = box >= 8 && a.max_pages > 0 && make_tmap_cache(&maps[0], a.c, a.c.k, box) && make_tmap_cache(&maps[1], a.c, a.c.v, box);
-        e = a.c.dtype == GDN_BF16 ? (tma ? launch_bf16_tma : launch_bf16)(a, grid, box, maps, stream) : (tma ? launch_e4m3_tma : launch_e4m3)(a, grid, box, maps, stream);
+        if (a.lost_ns) e = (a.c.dtype == GDN_BF16 ? launch_lost_bf16 : launch_lost_e4m3)(a, tma, grid, box, maps, stream);
+        else e = a.c.dtype == GDN_BF16 ? (tma ? launch_bf16_tma : launch_bf16)(a, grid, box, maps, stream) : (tma ? launch_e4m3_tma : launch_e4m3)(a, grid, box, maps, stream);
     }
     if (e != cudaSuccess) return e;
     const int dims = kJoinThreads / kJoinRows * 8;

@@ -1,0 +1,12 @@
+// k_paged_prefill_lost_e4m3.cu -- softmax attention of new tokens over the paged cache: the self-test of the tensor-core kernel's waits, 8-bit caches.
+#include "paged_prefill_tc.cuh"
+
+namespace gdn {
+namespace prefill {
+
+cudaError_t launch_lost_e4m3(const PrefillArgs &a, bool tma, int grid, int box, const CUtensorMap (&maps)[2], cudaStream_t stream) {
+    return tma ? launch_tc<GDN_E4M3, true, true>(a, grid, box, maps, stream) : launch_tc<GDN_E4M3, false, true>(a, grid, box, maps, stream);
+}
+
+}  // namespace prefill
+}  // namespace gdn

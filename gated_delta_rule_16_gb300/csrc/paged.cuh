@@ -99,6 +99,7 @@ struct PrefillArgs {
     float *lse;  // may be NULL
     void *ws;
     Divisor group, page;  // set by the launch
+    uint32_t lost_ns;     // self-test of waits, not 0: after 128 keys a CTA's copies wait so long for what never comes
 };
 
 struct LogprobArgs {

@@ -13,6 +13,9 @@ inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 int bytes_of(gdn_dtype t) { return t == GDN_E4M3 ? 1 : (t == GDN_BF16 ? 2 : 4); }
 
+// Of this thread's gdn_paged_prefill calls: gdn_selftest_paged_prefill_wait
+thread_local uint32_t lost_ns = 0;
+
 // A stride that keeps 16-byte pieces aligned.
 bool stride_ok(int64_t s, gdn_dtype t) { return s >= 0 && s * bytes_of(t) % 16 == 0; }
 
@@ -251,8 +254,15 @@ gdn_status gdn_paged_prefill(const gdn_kv_cache *cache, int32_t B, int32_t n, in
     }
     PrefillArgs a = {*cache, B, n, Hq, q, q_stride_token, q_stride_head, block_table, table_stride,
                      cache->pages > 0 ? max_pages : 0, window, seq_lens, cu_new, scale, o, lse, workspace};
+    a.lost_ns = lost_ns;
     if (a.max_pages == 0) a.c.k_scale = a.c.v_scale = nullptr;
     return launch_paged_prefill(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_selftest_paged_prefill_wait(int32_t limit_ms) {
+    if (limit_ms < 0 || limit_ms > 2000) return GDN_ERR_SHAPE;
+    lost_ns = (uint32_t)limit_ms * 1000000u;
+    return GDN_OK;
 }
 
 gdn_status gdn_paged_prefill_status(const void *workspace, void *stream) {

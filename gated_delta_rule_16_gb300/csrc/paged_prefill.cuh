@@ -134,6 +134,8 @@ cudaError_t launch_bf16(const PrefillArgs &a, int grid, int box, const CUtensorM
 cudaError_t launch_bf16_tma(const PrefillArgs &a, int grid, int box, const CUtensorMap (&maps)[2], cudaStream_t stream);
 cudaError_t launch_e4m3(const PrefillArgs &a, int grid, int box, const CUtensorMap (&maps)[2], cudaStream_t stream);
 cudaError_t launch_e4m3_tma(const PrefillArgs &a, int grid, int box, const CUtensorMap (&maps)[2], cudaStream_t stream);
+cudaError_t launch_lost_bf16(const PrefillArgs &a, bool tma, int grid, int box, const CUtensorMap (&maps)[2], cudaStream_t stream);  // self-test of waits
+cudaError_t launch_lost_e4m3(const PrefillArgs &a, bool tma, int grid, int box, const CUtensorMap (&maps)[2], cudaStream_t stream);
 cudaError_t launch_f32(const PrefillArgs &a, int grid, cudaStream_t stream);
 
 }  // namespace prefill

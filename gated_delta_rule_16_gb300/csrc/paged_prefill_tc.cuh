@@ -191,12 +191,12 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
 }
 struct Waiter {
     volatile int *gave_up;
-    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity, uint64_t limit_ns = kWaitLimitNs) const {
         if (try_wait(bar, parity)) return true;
         const uint64_t since = globaltimer();
 #pragma unroll 1
         while (!try_wait(bar, parity))
-            if (*gave_up || globaltimer() - since > kWaitLimitNs) {
+            if (*gave_up || globaltimer() - since > limit_ns) {
                 *gave_up = 1;
                 return false;
             }
@@ -219,6 +219,7 @@ struct Bars {
     int skip[2][2];                 // the group has added this tile's P V itself
     int gave_up;
     uint32_t tmem;
+    uint64_t never;                 // self-test: nothing arrives
 };
 
 static_assert(sizeof(Bars) <= 3 * 1024, "shared memory");
@@ -345,8 +346,9 @@ __device__ __noinline__ void add_masked(uint32_t t_p, uint32_t t_o, const uint8_
     }
 }
 
-// TMA: keys and values come by TMA, in boxes of `box` tokens of one page.
-template <gdn_dtype KIND, int D, bool TMA>
+// TMA: keys and values come by TMA, in boxes of `box` tokens of one page.  LOST: the self-test of waits, instances of its own, as the same few
+// instructions in the others take 2 % of a call.
+template <gdn_dtype KIND, int D, bool TMA, bool LOST>
 __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, int box) {
     using C = Cfg<KIND, D>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -382,6 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
             for (int j = 0; j < 3; ++j) bars.vote[i][j] = 0;
         }
         for (int i = 0; i < 3; ++i) mbar_init(&bars.drain[i], 1);
+        if constexpr (LOST) mbar_init(&bars.never, 1);
         bars.gave_up = 0;
         fence_mbar_init();
     }
@@ -394,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
     const uint32_t tmem = bars.tmem;
     Walk walk;
     walk.start(view, blockIdx.x);
+    auto never = [&] { return __all_sync(0xffffffffu, wait(smem_addr(&bars.never), 0, a.lost_ns)) != 0; };
     if (smem_addr(smem) & 1023u) walk.at.x = -1, bars.gave_up = 1;  // the swizzle needs aligned tiles, which shared memory without static parts is
 
     if (warpgroup == 2) {
@@ -542,6 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
             };
             int cell_next, page_next = entry(begin + pt, cell_next);
             for (int t = 0; ok && t < n; ++t) {
+                if (LOST && tiles == 1 && !(ok = never())) break;
                 const int page = page_next, cell = cell_next;
                 if (t + 1 < n) page_next = entry(begin + 128 * (t + 1) + pt, cell_next);
                 const bool real = page >= 0 && page < a.c.pages;
@@ -713,6 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(PrefillArgs a, 
                 };
                 int cell_next, page_next = entry(begin + lane * box, cell_next);
                 for (int t = 0; ok && t < n; ++t) {
+                    if (LOST && tiles == 1 && !(ok = never())) break;
                     const int cell = cell_next, page = page_next >= 0 && page_next < a.c.pages ? page_next : -1;  // outside the pool TMA fills with zeros
                     if (t + 1 < n) page_next = entry(begin + 128 * (t + 1) + lane * box, cell_next);
                     const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
@@ -963,7 +969,7 @@ inline bool make_tmap_cache(CUtensorMap *map, const gdn_kv_cache &c, const void 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <gdn_dtype KIND, int D, bool TMA>
+template <gdn_dtype KIND, int D, bool TMA, bool LOST>
 cudaError_t launch_tc(const PrefillArgs &a, int grid, int box, const CUtensorMap (&maps)[2], cudaStream_t stream) {
     using C = Cfg<KIND, D>;
     constexpr int kSmem = (int)(C::kSmem + sizeof(Bars));
@@ -971,20 +977,20 @@ cudaError_t launch_tc(const PrefillArgs &a, int grid, int box, const CUtensorMap
     static std::atomic<int> regs{0};
     if (regs.load(std::memory_order_relaxed) == 0) {
         cudaFuncAttributes attr;
-        const cudaError_t e = cudaFuncGetAttributes(&attr, prefill_tc_kernel<KIND, D, TMA>);
+        const cudaError_t e = cudaFuncGetAttributes(&attr, prefill_tc_kernel<KIND, D, TMA, LOST>);
         if (e != cudaSuccess) return e;
         regs.store(attr.numRegs, std::memory_order_relaxed);
     }
     if (regs.load(std::memory_order_relaxed) != 128) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<KIND, D, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    return e != cudaSuccess ? e : launch_kernel(true, prefill_tc_kernel<KIND, D, TMA>, grid, kThreads, kSmem, stream, a, maps[0], maps[1], box);
+    const cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<KIND, D, TMA, LOST>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    return e != cudaSuccess ? e : launch_kernel(true, prefill_tc_kernel<KIND, D, TMA, LOST>, grid, kThreads, kSmem, stream, a, maps[0], maps[1], box);
 }
-template <gdn_dtype KIND, bool TMA>
+template <gdn_dtype KIND, bool TMA, bool LOST = false>
 cudaError_t launch_tc(const PrefillArgs &a, int grid, int box, const CUtensorMap (&maps)[2], cudaStream_t stream) {
     switch (a.c.d) {
-        case 64: return launch_tc<KIND, 64, TMA>(a, grid, box, maps, stream);
-        case 128: return launch_tc<KIND, 128, TMA>(a, grid, box, maps, stream);
-        default: return launch_tc<KIND, 256, TMA>(a, grid, box, maps, stream);
+        case 64: return launch_tc<KIND, 64, TMA, LOST>(a, grid, box, maps, stream);
+        case 128: return launch_tc<KIND, 128, TMA, LOST>(a, grid, box, maps, stream);
+        default: return launch_tc<KIND, 256, TMA, LOST>(a, grid, box, maps, stream);
     }
 }
 

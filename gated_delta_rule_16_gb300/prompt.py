@@ -9,7 +9,7 @@ from __future__ import annotations
 import torch
 
 from . import paged
-from ._binding import GDN_E4M3, Workspace, load
+from ._binding import GDN_E4M3, Workspace, _check, load
 from .paged import _CODES, _F32, _I32, _cache, _call, _cuda, _elsewhere, _handle, _on, _want, _workspace
 
 _F64 = torch.float64
@@ -132,6 +132,12 @@ def gdn_paged_prefill_status(workspace=None, stream=None) -> int:
     dev = _cuda(buf, "workspace")
     with torch.cuda.device(dev):
         return int(load().gdn_paged_prefill_status(buf.data_ptr(), _handle(dev, stream)))
+
+
+def gdn_selftest_paged_prefill_wait(limit_ms: int = 0) -> None:
+    """In this thread's following gdn_paged_prefill calls a CTA's copies wait after its first 128 keys for what never comes; the wait
+    runs out after limit_ms (1 to 2000), and the status is 10.  0: as normally."""
+    _check("gdn_selftest_paged_prefill_wait", load().gdn_selftest_paged_prefill_wait(limit_ms))
 
 
 def gdn_logprobs(logits, tokens, *, top=0, logprobs=None, entropy=None, top_tokens=None, top_logprobs=None, stream=None):

@@ -494,6 +494,13 @@ GDN_API gdn_status gdn_paged_prefill(const gdn_kv_cache *cache, int32_t B, int32
                                      void *o, float *lse, void *workspace, size_t workspace_bytes, void *stream);
 GDN_API gdn_status gdn_paged_prefill_status(const void *workspace, void *stream);
 
+/* Self-test of gdn_paged_prefill's failure detection.  With limit_ms of 1 to 2000, in this host thread's
+ * following calls, a CTA's copies wait after its first 128 keys for a barrier that nothing arrives at.  The wait runs
+ * out after limit_ms, all others end with it, the kernel waits for its copies and products in flight and
+ * returns, and the status of a call with more keys is GDN_ERR_TIMEOUT (GDN_F32 caches have no such
+ * waits).  0: as normally, where any wait ends after two seconds. */
+GDN_API gdn_status gdn_selftest_paged_prefill_wait(int32_t limit_ms);
+
 /* Log probabilities of given tokens, of every row of logits [B][V] (row b at
  * b * logits_stride elements; GDN_BF16 or GDN_F32; V <= 2^30).  With m the row's largest
  * logit and Z = sum_i exp(x_i - m):

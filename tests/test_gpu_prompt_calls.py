@@ -1,6 +1,7 @@
 """What a program meets around the prompt chunk's calls: the status of calls without rows, outputs that share memory, the end of
-fp32's range, lists of requests in any order.  References and tolerances are those of test_gpu_prompt.py."""
+fp32's range, lists of requests in any order, waits that run out.  References and tolerances are those of test_gpu_prompt.py."""
 import copy
+from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 import torch
@@ -213,3 +214,56 @@ def test_attend_lse_of_rows_behind_others_that_stay(kind):
     same(out.o[5:29].double(), want[5:29], o_far[5:29])
     same(out.lse[5:29].double(), want_lse[5:29], lse_far[5:29])
     assert out.untouched() and all((x[:5] == 7).all() and (x[29:] == 7).all() for x in (out.o, out.lse))
+
+
+# ---- waits that run out --------------------------------------------------------------------------
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [64, 1])  # keys and values by TMA, and 16 bytes at a time
+def test_attend_waits_that_run_out_are_reported(kind, d, page):
+    c = Case([(500, 130), (0, 300), (40, 1), (40000, 20)], kind=kind, heads=8, kv_heads=2, d=d, page=page)
+    ws, out = gdn.Workspace(), Guarded(c)
+    want = c.call()
+    assert gdn.gdn_paged_prefill_status() == 0
+    for _ in range(3):
+        gdn.gdn_selftest_paged_prefill_wait(5)
+        try:
+            c.call(o=out.o, lse=out.lse, workspace=ws)
+            assert gdn.gdn_paged_prefill_status(ws) == 10
+            c.call(o=out.o, lse=out.lse)
+            assert gdn.gdn_paged_prefill_status() == 10
+        finally:
+            gdn.gdn_selftest_paged_prefill_wait()
+        assert out.untouched()
+        # the next call is as any other, in the same workspace
+        got = c.check(workspace=ws)
+        assert gdn.gdn_paged_prefill_status(ws) == 0 and all(torch.equal(x, y) for x, y in zip(got, want))
+        got = c.check()
+        assert gdn.gdn_paged_prefill_status() == 0 and all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_attend_wait_limits_belong_to_a_thread():
+    c = Case([(500, 130)])
+    ws = gdn.Workspace()
+    c.call(workspace=ws)
+    with ThreadPoolExecutor(1) as pool:
+        pool.submit(gdn.gdn_selftest_paged_prefill_wait, 5).result()
+        c.check(workspace=ws)
+        assert gdn.gdn_paged_prefill_status(ws) == 0
+    f = Case([(500, 130)], kind="f32")  # whose kernel waits for no barrier in memory
+    gdn.gdn_selftest_paged_prefill_wait(5)
+    try:
+        f.check(workspace=ws)
+        assert gdn.gdn_paged_prefill_status(ws) == 0
+    finally:
+        gdn.gdn_selftest_paged_prefill_wait(0)
+    short = Case([(0, 100)])  # whose keys come before copies stop
+    gdn.gdn_selftest_paged_prefill_wait(2000)
+    try:
+        short.check(workspace=ws)
+        assert gdn.gdn_paged_prefill_status(ws) == 0
+    finally:
+        gdn.gdn_selftest_paged_prefill_wait(0)
+    for bad in (-1, 2001):
+        with pytest.raises(gdn.GdnError):
+            gdn.gdn_selftest_paged_prefill_wait(bad)
