@@ -201,15 +201,20 @@ __device__ void raise_from_block(Shared &s, int top, int block) {
 constexpr int kVecs = 4, kAhead = 4, kBatch = kVecs * kThreads;  // 16-byte pieces of a thread's batch; batches on their way or worked on
 constexpr int kSmem = kAhead * kBatch * 16;
 
-// The list once more, with barriers: parts of 16 logits per thread whose keys are gathered until there are too many, then cut.
-template <typename T> __device__ __noinline__ void gather_again(Shared &s, const LogprobArgs &a, const T *x, int ctas, int cta) {
-    constexpr int kEach = 16;
-    const int tid = threadIdx.x;
+// The list once more, with barriers: parts of 16 logits per thread whose keys are gathered until there are too many, then cut.  The parts
+// are those of this CTA's batches and no others: the row's other CTAs may have come through with theirs.
+template <typename T> __device__ __noinline__ void gather_again(Shared &s, const LogprobArgs &a, const T *x, int ctas, int cta, int head, int vecs) {
+    constexpr int N = 16 / sizeof(T), kEach = 16, kParts = kVecs * N / kEach;  // of a batch
+    const int tid = threadIdx.x, tail = head + vecs * N, parts = (vecs + kBatch * ctas - 1) / (kBatch * ctas) * kParts;
     __syncthreads();
     if (tid == 0) s.count = 0;
     __syncthreads();
-    for (int64_t base = (int64_t)cta * kThreads * kEach; base < a.V; base += (int64_t)ctas * kThreads * kEach) {
-        auto index = [&](int i) { return base + i * kThreads + tid; };
+    for (int part = 0; part < parts + (cta == 0); ++part) {  // the last has the row's ends, in the first CTA
+        auto index = [&](int i) {  // a.V or more: none
+            if (part == parts) return i > 0 ? a.V : tid < head ? tid : tail + tid - head;
+            const int vec = (part / kParts * ctas + cta) * kBatch + (part % kParts * (kEach / N) + i / N) * kThreads + tid;
+            return vec < vecs ? head + vec * N + i % N : a.V;
+        };
         uint32_t left = 0;  // those that found no place
         bool many = false;
         auto gather = [&](uint32_t which) {
@@ -218,7 +223,7 @@ template <typename T> __device__ __noinline__ void gather_again(Shared &s, const
             many = false;
             for (int i = 0; i < kEach; ++i) {
                 if (!(which >> i & 1) || index(i) >= a.V) continue;
-                const u64 key = key_of(value(x + index(i)), (int)index(i));
+                const u64 key = key_of(value(x + index(i)), index(i));
                 if (key < threshold) continue;
                 const int to = atomicAdd(&s.count, 1);
                 if (to < kList) s.list[to] = key;
@@ -232,7 +237,7 @@ template <typename T> __device__ __noinline__ void gather_again(Shared &s, const
             if (__syncthreads_or(left != 0)) {
                 u64 key = 0;
                 for (int i = 0; i < kEach; ++i)
-                    if (index(i) < a.V) key = max(key, key_of(value(x + index(i)), (int)index(i)));
+                    if (index(i) < a.V) key = max(key, key_of(value(x + index(i)), index(i)));
                 raise_threshold(s, a.top, key);
             }
             cut(s, a.top);
@@ -395,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(LogprobArgs a, in
     if (lane == 0) s.part[warp] = sums;
     __syncthreads();
     if (a.top > 0) {
-        if (s.count > kList) gather_again(s, a, x, ctas, cta);
+        if (s.count > kList) gather_again(s, a, x, ctas, cta, head, vecs);
         cut(s, a.top);
     }
     if (tid == 0) {
