@@ -11,14 +11,15 @@
 // top-th of these 64.  So 100 to 200 of 100000 logits are gathered, no barrier is met on the way (one per batch cost more
 // than all else together), and a batch whose maximum, which the sums need
 // anyway, is below T costs nothing more.  At the end the list is cut by comparing all with all.  If more were brought than it holds (rising
-// logits, say), the row is gone over again with barriers: T is raised from the maxima of each part that brings too many.
+// logits, say, or some 1500 of them in bf16, of which not all threads have one to start T from), the CTA goes over its share again with
+// barriers: T is raised from the maxima of each part that brings too many.
 //
 // What bounds it: the row is read once from HBM, at 4 bytes for some 8 instructions per logit.  A thread copies its own 64 bytes of a batch to
 // shared memory by cp.async, three batches ahead, and reads them back when it gets there: no barrier, no registers held by loads on their
 // way, and a logit that the gathering wants is looked up by its number.  One row takes a cluster of CTAs where rows
 // are few, as many as the GPU has room for, each with a share of every batch.  2047 rows of 100003 fp32 logits: 122 us without top tokens (6.7 TB/s, 99 %
 // of a copy), 130 with 5, 146 with 20 (84 %), 178 with 32: what is gathered takes some 70 instructions each, in warps of their own, and the list's
-// cuts; in bf16 70, 112, 129 and 150 us (409 MB), as the instructions per logit count more.  4 rows of 131072 bf16 logits with 5: 11 us, half of it
+// cuts; in bf16 71, 112, 130 and 149 us (409 MB), as the instructions per logit count more.  4 rows of 131072 bf16 logits with 5: 11 us, half of it
 // the clusters' two joins and the cuts.
 #include <cooperative_groups.h>
 

@@ -2,8 +2,8 @@
 //
 // Every operand is split into two tf32 terms of 11 bits, x = hi + lo to 2^-22 of x, and a product of two takes three warp MMAs
 // (lo hi, hi lo, hi hi); the tensor core's sums run over 32 terms of each only, longer ones are fp32 additions, which round where the
-// tensor core cuts.  An m16n8k8 takes 8 clocks of an SM quarter's tensor core (measured, 300 TFLOP/s in all), so three make 100 TFLOP/s at most; 47 % of
-// that is reached, the rest waits for operands and between the tile's two barriers.  One after the other for all sums instead of three to a sum: 197 us.
+// tensor core cuts.  An m16n8k8 takes 8 clocks of an SM quarter's tensor core (measured, 300 TFLOP/s in all), so three make 100 TFLOP/s at most; 41 % of
+// that is reached (3 requests up to 2031 tokens, d 64: 188 us), the rest waits for operands and between the tile's two barriers.  One after the other for all sums instead of three to a sum: 197 us.
 // Keys and values are split once, when they come (as part of each product it took ten instructions to three MMAs: 202 us against 188 for
 // 3 requests up to 2031 tokens, d 64): a thread loads its pieces of the next tile into registers while this one is worked
 // on, and stores (hi, hi, lo, lo) of two neighbours - two dims of a key, two keys of a dim of the values - as the 16 bytes that one

@@ -21,7 +21,7 @@
 // With 256 dims O fills the tensor memory of two row tiles, and a unit has one.
 //
 // What bounds it.  8192 bf16 tokens at once (32 query and 8 KV heads of 128): 476 us, 1155 TFLOP/s, 60 % of a large library product; 2048 tokens
-// over 131072: 1600 us, 1360 TFLOP/s, with the clock at 1.55 GHz under the power limit; 8-bit chunks over 16000: 279 us, 1000 TFLOP/s; 256 dims in a
+// over 131072: 1480 us, 1470 TFLOP/s in some tens of launches, 1690 us, 1290 TFLOP/s where the power limit holds the clock at 1.54 GHz; 8-bit chunks over 16000: 279 us, 1000 TFLOP/s; 256 dims in a
 // window of 4096: 331 us, 880 TFLOP/s.  A pair of S tiles takes about 1850 clocks of which the tensor core works 1280 (the scores' product, 64 keys
 // wide, reads q and k from shared memory at its full rate, 48 clocks to an MMA instead of 32).  The rest is the chain from a tile's scores over its softmax (950) and
 // product to the scores two tiles on, with four waits of 200 to 400 clocks in it; tensor memory holds no third S tile beside two O of 128 dims.  With

@@ -479,7 +479,7 @@ GDN_API gdn_status gdn_qk_rope(int32_t n, int32_t Hq, int32_t Hkv, int32_t d, gd
  * their attentions, in o and lse apart, and where the requests' rows are more than n in all,
  * some stay as they were.
  * Workspace: gdn_paged_prefill_workspace_bytes(cache, B, n, Hq), 256-byte aligned (41 MB
- * at most, and 76 bytes for every 128 rows and request); its contents need no set-up.  The call is several launches: host threads that
+ * at most, and 76 bytes for every request and every 128 of the n Hq / Hkv rows of a KV head); its contents need no set-up.  The call is several launches: host threads that
  * share a stream need a workspace each, and so do two captured graphs that may run
  * at the same time.  gdn_paged_prefill_status synchronises `stream` and reports
  * the gdn_paged_prefill call that used the workspace last (GDN_ERR_TIMEOUT: a wait
@@ -512,7 +512,8 @@ GDN_API gdn_status gdn_selftest_paged_prefill_wait(int32_t limit_ms);
  * last.  A row with a NaN or +inf has NaN for every result but top_tokens, where
  * +inf comes first and NaN last; a row of -inf alone has log probabilities of -inf and
  * entropy 0.  Sums are fp32 in a fixed order that depends on B, V and the row's
- * alignment: the same call gives the same bits.  No workspace. */
+ * alignment: the same call gives the same bits.  Outputs share no memory with inputs or one another.
+ * No workspace. */
 GDN_API gdn_status gdn_logprobs(int32_t B, int32_t V, gdn_dtype dtype, const void *logits, int64_t logits_stride,
                                 const int32_t *tokens, int32_t top, float *logprobs, float *entropy,
                                 int32_t *top_tokens, float *top_logprobs, void *stream);
