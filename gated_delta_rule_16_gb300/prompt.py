@@ -70,8 +70,8 @@ def gdn_paged_prefill(q, k_cache, v_cache, block_table, seq_lens, cu_new, *, k_s
 
     Request b's tokens are rows cu_new[b] to cu_new[b + 1] (cu_new [B+1] int32) and the last of its seq_lens[b] tokens; each attends
     to those up to itself, or to the last `window` of them.  block_table [B, max_pages] int32 (its row stride may be 0); scale:
-    default dim ** -0.5.  Rows behind cu_new[B] are left as they are.  Returns (o [n, heads, dim] in q's dtype, lse [n, heads]
-    fp32).  A `workspace` belongs to one call at a time (default: this thread's for the device and stream); gdn_paged_prefill_status
+    default dim ** -0.5.  Rows behind cu_new[B] are left as they are.  o may be q where q is contiguous.  Returns (o [n, heads, dim] in q's
+    dtype, lse [n, heads] fp32).  A `workspace` belongs to one call at a time (default: this thread's for the device and stream); gdn_paged_prefill_status
     asks whether the call ran through."""
     dev = _cuda(q, "q")
     if stream is not None and _elsewhere(dev, stream):
